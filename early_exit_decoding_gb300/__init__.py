@@ -31,8 +31,10 @@ EXPORTS = (
     "rl_kv_set_profiling", "rl_kv_profile", "rl_kv_timeline", "rl_lm_head_static", "rl_kv_set_decode_path",
     "rl_kv_decode_path", "rl_save_exit_layers", "rl_load_exit_layers", "rl_exit_kv_cosine",
     "rl_kv_set_wait_limit", "rl_debug_fail_allocations", "rl_model_offload_backbone",
-    "rl_model_memory",
+    "rl_model_memory", "rl_token_logprobs", "rl_window_attention", "rl_shared_prefix_workspace",
+    "rl_shared_prefix_attention",
 )
+RL_DT_F32, RL_DT_BF16, RL_DT_F16 = range(3)
 RL_PATH_AUTO, RL_PATH_STEP, RL_PATH_FUSED, RL_PATH_GENERIC = range(4)
 KERNEL_KINDS = ("embed", "qkv", "attention", "group_sums", "o_proj", "norm", "gate_up", "down",
                 "layer_end", "lm_head", "argmax", "decode_step")
@@ -57,6 +59,13 @@ class rl_weights(ctypes.Structure):
 class rl_exit_policy(ctypes.Structure):
     _fields_ = [("mode", ctypes.c_int32), ("tau", ctypes.c_float),
                 ("d_schedule", ctypes.c_void_p), ("schedule_len", ctypes.c_int32)]
+
+
+class rl_attn_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "kv_dtype", "q_dtype", "batch", "q_len", "n_q_heads", "n_kv_heads", "head_dim",
+        "kv_capacity")] + [("scale", ctypes.c_float)] + [(n, ctypes.c_int64 * 3) for n in (
+            "q_stride", "out_stride", "k_stride", "v_stride")]
 
 
 class RiverError(RuntimeError):
@@ -106,6 +115,12 @@ def _load():
         "rl_model_memory": (I, [P, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]),
         "rl_debug_fail_allocations": (I, [ctypes.c_int64]),
         "rl_load_exit_layers": (I, [P, ctypes.c_char_p, P]),
+        "rl_token_logprobs": (I, [P, I, I, I, ctypes.c_int64, P, I, I, P, P, P, P, P, P, P]),
+        "rl_window_attention": (I, [ctypes.POINTER(rl_attn_desc), P, P, P, P, P, I, I, P, P, P, P]),
+        "rl_shared_prefix_workspace": (I, [ctypes.POINTER(rl_attn_desc), I, ctypes.POINTER(ctypes.c_uint64)]),
+        "rl_shared_prefix_attention": (I, [ctypes.POINTER(rl_attn_desc), P, P, P, I,
+                                           ctypes.POINTER(ctypes.c_int64), P, P, P, P, P, P,
+                                           ctypes.c_uint64, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -311,6 +326,36 @@ def rl_kv_profile(kv, stream=None, cap=1024):
     return [(KERNEL_KINDS[k[i]], ly[i], pa[i], ms[i], by[i]) for i in range(n.value)]
 
 
+def rl_token_logprobs(d_logits, dtype, rows, vocab, row_stride, d_tokens, n_tok, top_k, d_lse,
+                      d_entropy, d_logprob, d_top_ids, d_top_logprobs, d_err=None, stream=None):
+    _check(_lib.rl_token_logprobs(_ptr(d_logits), dtype, rows, vocab, row_stride, _ptr(d_tokens), n_tok,
+                                  top_k, _ptr(d_lse), _ptr(d_entropy), _ptr(d_logprob), _ptr(d_top_ids),
+                                  _ptr(d_top_logprobs), _ptr(d_err), _stream(stream)))
+
+
+def rl_window_attention(desc, d_q, d_k, d_v, d_kv_len, d_q_len, window, sinks, d_out, d_lse,
+                        d_err=None, stream=None):
+    _check(_lib.rl_window_attention(ctypes.byref(desc), _ptr(d_q), _ptr(d_k), _ptr(d_v), _ptr(d_kv_len),
+                                    _ptr(d_q_len), window, sinks, _ptr(d_out), _ptr(d_lse), _ptr(d_err),
+                                    _stream(stream)))
+
+
+def rl_shared_prefix_workspace(desc, prefix_len):
+    """Workspace bytes of rl_shared_prefix_attention."""
+    n = ctypes.c_uint64()
+    _check(_lib.rl_shared_prefix_workspace(ctypes.byref(desc), prefix_len, ctypes.byref(n)))
+    return n.value
+
+
+def rl_shared_prefix_attention(desc, d_q, d_k_prefix, d_v_prefix, prefix_len, prefix_stride, d_k, d_v,
+                               d_kv_len, d_out, d_lse, d_ws, ws_bytes, d_err=None, stream=None):
+    st = (ctypes.c_int64 * 4)(*prefix_stride)
+    _check(_lib.rl_shared_prefix_attention(ctypes.byref(desc), _ptr(d_q), _ptr(d_k_prefix),
+                                           _ptr(d_v_prefix), prefix_len, st, _ptr(d_k), _ptr(d_v),
+                                           _ptr(d_kv_len), _ptr(d_out), _ptr(d_lse), _ptr(d_ws), ws_bytes,
+                                           _ptr(d_err), _stream(stream)))
+
+
 # --------------------------------------------------------------- conveniences
 
 class _DevArray:
@@ -508,6 +553,189 @@ def decode_step(model: Model, kv: KVCache, tokens, policy: Policy, out=None, str
     return o
 
 
+def _refuse(msg, status=RL_ERR_INVALID_ARG):
+    raise RiverError(status, msg)
+
+
+def _dtype_code(t):
+    import torch
+    return {torch.float32: RL_DT_F32, torch.bfloat16: RL_DT_BF16, torch.float16: RL_DT_F16}.get(t.dtype)
+
+
+def _operands(name, first, **others):
+    """Checks that every tensor (None: absent) is on ``first``'s CUDA device and
+    needs no gradient (the operators have no backward pass)."""
+    import torch
+    dev = first.device
+    grad = torch.is_grad_enabled()
+    for n, t in (("", first), *others.items()):
+        if t is None:
+            continue
+        if not t.is_cuda or t.device != dev:
+            _refuse(f"{name}: {n or 'the first operand'} is on {t.device}, not on one CUDA device with the others")
+        if grad and t.requires_grad:
+            _refuse(f"{name}: {n or 'the first operand'} requires a gradient; the operator has no backward pass",
+                    RL_ERR_UNSUPPORTED)
+    return dev
+
+
+def _buffer(o, key, shape, dtype, dev, name, stream):
+    """``o[key]``, checked against (shape, dtype), or a new tensor put there
+    (taken on the stream that writes it)."""
+    import torch
+    t = o.get(key)
+    if t is None:
+        with torch.cuda.stream(stream):
+            t = o[key] = torch.empty(shape, dtype=dtype, device=dev)
+    elif tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or \
+            (key != "out" and not t.is_contiguous()):
+        _refuse(f"{name}: out[{key!r}] must be {dtype} {tuple(shape)} on {dev}"
+                + ("" if key == "out" else ", contiguous"))
+    return t
+
+
+def _on_device(dev, stream, call):
+    """``call(stream)`` with ``dev`` current; ``stream`` None: the device's current stream."""
+    import torch
+    if dev.index == torch.cuda.current_device():
+        return call(stream)
+    with torch.cuda.device(dev):
+        return call(stream)
+
+
+def _int32(name, key, t, shape):
+    import torch
+    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        _refuse(f"{name}: {key} must be contiguous int32 {tuple(shape)}")
+
+
+def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None):
+    """Log-probabilities of given tokens, entropy and top alternatives of
+    ``logits [R][V]`` (fp32, bf16 or fp16 CUDA, rows any stride apart).
+    ``tokens``: int32 [R] or [R][n].  Returns a dict: ``lse`` and ``entropy``
+    [R], ``logprob`` (tokens' shape), ``top_ids`` int32 and ``top_logprobs``
+    [R][top_k]; buffers present in ``out`` are used.  ``err``: int32 [1] that
+    collects RL_DEVERR_* bits.  See rl_token_logprobs."""
+    import torch
+    name = "token_logprobs"
+    dt = _dtype_code(logits)
+    if logits.dim() != 2 or dt is None or 0 in logits.shape or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        _refuse(f"{name}: logits must be fp32, bf16 or fp16 [R][V] with contiguous rows")
+    dev = _operands(name, logits, tokens=tokens, err=err)
+    R, V = logits.shape
+    if not 0 <= top_k <= min(32, V):
+        _refuse(f"{name}: top_k {top_k} outside [0, {min(32, V)}]")
+    n = 0
+    if tokens is not None:
+        n = 1 if tokens.dim() == 1 else tokens.shape[-1]
+        _int32(name, "tokens", tokens, (R,) if tokens.dim() == 1 else (R, n))
+    if err is not None:
+        _int32(name, "err", err, (1,))
+    o = {} if out is None else dict(out)
+    lse = _buffer(o, "lse", (R,), torch.float32, dev, name, stream)
+    ent = _buffer(o, "entropy", (R,), torch.float32, dev, name, stream)
+    lp = _buffer(o, "logprob", tokens.shape, torch.float32, dev, name, stream) if n else None
+    ids = _buffer(o, "top_ids", (R, top_k), torch.int32, dev, name, stream) if top_k else None
+    tlp = _buffer(o, "top_logprobs", (R, top_k), torch.float32, dev, name, stream) if top_k else None
+    ld = logits.stride(0) if R > 1 else V
+    _on_device(dev, stream, lambda s: rl_token_logprobs(logits, dt, R, V, ld, tokens if n else None, n, top_k,
+                                                        lse, ent, lp, ids, tlp, err, s))
+    return o
+
+
+def _attn_desc(name, q, k, v, out, scale):
+    """rl_attn_desc of q, out [B][T][Hq][hd] and k, v [B][Hkv][S][hd]."""
+    for n, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        if t.dim() != 4 or 0 in t.shape or t.stride(3) != 1:
+            _refuse(f"{name}: {n} must have four axes, none empty, with a contiguous last one")
+    B, T, Hq, hd = q.shape
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != hd or v.dtype != k.dtype or out.dtype != k.dtype:
+        _refuse(f"{name}: q {tuple(q.shape)}, k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype} do not fit")
+    d = rl_attn_desc(_dtype_code(k) or RL_DT_F32, RL_DT_F32 if _dtype_code(q) is None else _dtype_code(q), B, T, Hq,
+                     k.shape[1], hd, k.shape[2], 0.0 if scale is None else float(scale))
+    if _dtype_code(q) is None or _dtype_code(k) is None:
+        _refuse(f"{name}: q {q.dtype}, k {k.dtype}: fp32, bf16 or fp16 expected")
+    if scale is not None and d.scale == 0.0:
+        _refuse(f"{name}: scale 0")
+
+    def strides(t, n):
+        # an axis of one entry has no stride that matters
+        return [0 if t.shape[i] == 1 else t.stride(i) for i in range(n)]
+
+    d.q_stride[:] = strides(q, 3)
+    d.out_stride[:] = strides(out, 3)
+    d.k_stride[:] = strides(k, 3)
+    d.v_stride[:] = strides(v, 3)
+    return d
+
+
+def window_attention(q, k, v, kv_len, window, sinks=0, q_len=None, scale=None, out=None, err=None, stream=None):
+    """Causal attention over the last ``window`` keys and the first ``sinks``.
+    ``q [B][T][Hq][hd]`` (k's type, or fp32), ``k``, ``v`` [B][Hkv][S][hd] bf16
+    or fp16 (KVCache.view's layout), ``kv_len`` int32 [B], ``q_len`` int32 [B]
+    or None (T each): the queries are the last q_len of a sequence's kv_len
+    rows.  Returns a dict: ``out`` (q's shape, k's type) and ``lse`` fp32
+    [B][T][Hq]; buffers present in ``out`` are used, their rows t >= q_len[b]
+    left as they were.  See rl_window_attention."""
+    import torch
+    name = "window_attention"
+    dev = _operands(name, q, k=k, v=v, kv_len=kv_len, q_len=q_len, err=err)
+    o = {} if out is None else dict(out)
+    res = _buffer(o, "out", q.shape, k.dtype, dev, name, stream)
+    d = _attn_desc(name, q, k, v, res, scale)
+    lse = _buffer(o, "lse", q.shape[:3], torch.float32, dev, name, stream)
+    _int32(name, "kv_len", kv_len, (q.shape[0],))
+    if q_len is not None:
+        _int32(name, "q_len", q_len, (q.shape[0],))
+    if err is not None:
+        _int32(name, "err", err, (1,))
+    _on_device(dev, stream, lambda s: rl_window_attention(d, q, k, v, kv_len, q_len, int(window), int(sinks), res,
+                                                          lse, err, s))
+    return o
+
+
+def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out=None, workspace=None, err=None,
+                            stream=None):
+    """One decode step's attention of a batch behind one shared prefix.
+    ``q [B][Hq][hd]``, ``k_prefix``, ``v_prefix`` [Hkv][P][hd], the sequences'
+    own ``k``, ``v`` [B][Hkv][S][hd] with ``kv_len`` int32 [B] rows in use.
+    Returns a dict: ``out`` [B][Hq][hd] (k's type), ``lse`` fp32 [B][Hq];
+    buffers present in ``out`` are used.  ``workspace``: a uint8 tensor of
+    rl_shared_prefix_workspace bytes; None takes one from PyTorch's allocator
+    for this call.  See rl_shared_prefix_attention."""
+    import torch
+    name = "shared_prefix_attention"
+    dev = _operands(name, q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, kv_len=kv_len, workspace=workspace,
+                    err=err)
+    if q.dim() != 3:
+        _refuse(f"{name}: q must be [B][Hq][hd]")
+    o = {} if out is None else dict(out)
+    res = _buffer(o, "out", q.shape, k.dtype, dev, name, stream)
+    d = _attn_desc(name, q[:, None], k, v, res[:, None], scale)
+    lse = _buffer(o, "lse", q.shape[:2], torch.float32, dev, name, stream)
+    _int32(name, "kv_len", kv_len, (q.shape[0],))
+    if err is not None:
+        _int32(name, "err", err, (1,))
+    if k_prefix.dim() != 3 or k_prefix.shape != v_prefix.shape or k_prefix.dtype != k.dtype or \
+            v_prefix.dtype != k.dtype or k_prefix.shape[0] != k.shape[1] or k_prefix.shape[2] != k.shape[3] or \
+            k_prefix.stride(2) != 1 or v_prefix.stride(2) != 1:
+        _refuse(f"{name}: k_prefix and v_prefix must be {k.dtype} [{k.shape[1]}][P][{k.shape[3]}] with a contiguous last axis")
+    P = k_prefix.shape[1]
+    ps = [0 if t.shape[i] == 1 else t.stride(i) for t in (k_prefix, v_prefix) for i in (0, 1)]
+
+    def call(s):
+        ws = workspace
+        n = rl_shared_prefix_workspace(d, P)
+        if ws is None:
+            with torch.cuda.stream(s):
+                ws = torch.empty((n,), dtype=torch.uint8, device=dev)
+        rl_shared_prefix_attention(d, q, k_prefix, v_prefix, P, ps, k, v, kv_len, res, lse, ws,
+                                   ws.numel() * ws.element_size(), err, s)
+
+    _on_device(dev, stream, call)
+    return o
+
+
 def quantize_exit_layers(model: Model, stream=None):
     model.quantize_exit_layers(stream)
 
@@ -517,4 +745,5 @@ def kv_cache_alloc(model: Model, max_batch, max_seq):
 
 
 __all__ = [*EXPORTS, "Model", "KVCache", "Policy", "RiverError", "prefill", "decode_step",
-           "quantize_exit_layers", "kv_cache_alloc", "LIB_PATH"]
+           "quantize_exit_layers", "kv_cache_alloc", "token_logprobs", "window_attention",
+           "shared_prefix_attention", "rl_attn_desc", "LIB_PATH"]

@@ -1,0 +1,303 @@
+// Stand-alone attention operators over caller-owned caches: sliding window
+// with sinks (rl_window_attention) and a batch behind one shared prefix
+// (rl_shared_prefix_attention).
+//
+// For a query row at position p:  out = sum_j w_j v_j / sum_j w_j with
+// w_j = exp(scale q.k_j - m) over the keys j it sees and m their largest
+// score;  lse = m + ln sum_j w_j.  Running maximum and sum, one pass.
+//
+// Simplest form: one warp per (sequence, query row, head), one key at a time.
+#include <float.h>
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include "dev_common.cuh"
+#include "internal.h"
+
+namespace river {
+
+namespace {
+
+using namespace dev;
+
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(uint32_t v) {
+  if constexpr (F16)
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+  else
+    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
+}
+template <bool F16>
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+  }
+}
+
+// Length of sequence b, clamped to the rows laid out for it.
+__device__ __forceinline__ int seq_len(const AttnOpArgs& a, int b, bool report) {
+  int n = a.kv_len ? a.kv_len[(long long)b * a.kv_len_step] + a.kv_len_add : a.kv_len_add;
+  if (n < 0 || n > a.cap) {
+    if (report && a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
+    n = n < 0 ? 0 : a.cap;
+  }
+  return n;
+}
+__device__ __forceinline__ int query_len(const AttnOpArgs& a, int b, bool report) {
+  int n = a.q_len ? a.q_len[b] : a.Tq;
+  if (n < 0 || n > a.Tq) {
+    if (report && a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
+    n = n < 0 ? 0 : a.Tq;
+  }
+  return n;
+}
+
+// Running softmax of one row held by a warp: lane holds dims
+// 2 * lane + 64 * i, i < HD / 64.
+template <int HD, bool F16>
+struct RowAcc {
+  float2 q[HD / 64], o[HD / 64];
+  float m = -INFINITY, l = 0.f;
+  __device__ __forceinline__ void load_q(const AttnOpArgs& a, int b, int t, int h, int lane) {
+    const long long at = b * a.qs[0] + t * a.qs[1] + h * a.qs[2] + 2 * lane;
+#pragma unroll
+    for (int i = 0; i < HD / 64; ++i) {
+      if (a.q_f32) {
+        const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + 64 * i);
+        q[i] = unpack2<F16>(pack2<F16>(f.x, f.y));
+      } else {
+        q[i] = unpack2<F16>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at + 64 * i));
+      }
+      o[i] = make_float2(0.f, 0.f);
+    }
+  }
+  __device__ __forceinline__ void keys(const KeySrc& s, int b, int hk, int j0, int j1, float scale, int lane) {
+    const long long kb = b * s.ks[0] + hk * s.ks[1] + 2 * lane, vb = b * s.vs[0] + hk * s.vs[1] + 2 * lane;
+    for (int j = j0; j < j1; ++j) {
+      float d = 0.f;
+      uint32_t vv[HD / 64];
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i) {
+        const float2 k = unpack2<F16>(
+            *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(s.k) + kb + j * s.ks[2] + 64 * i));
+        vv[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(s.v) + vb + j * s.vs[2] + 64 * i);
+        d += q[i].x * k.x + q[i].y * k.y;
+      }
+      d = warp_sum(d) * scale;
+      const float mn = fmaxf(m, d), mu = mn == -INFINITY ? 0.f : mn;
+      const float c = __expf(m - mu), e = __expf(d - mu);
+      l = l * c + e;
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i) {
+        const float2 v = unpack2<F16>(vv[i]);
+        o[i].x = o[i].x * c + e * v.x;
+        o[i].y = o[i].y * c + e * v.y;
+      }
+      m = mn;
+    }
+  }
+  __device__ __forceinline__ void store(const AttnOpArgs& a, int b, int t, int h, int lane) {
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const long long at = b * a.os[0] + t * a.os[1] + h * a.os[2] + 2 * lane;
+#pragma unroll
+    for (int i = 0; i < HD / 64; ++i)
+      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + 64 * i) =
+          pack2<F16>(o[i].x * inv, o[i].y * inv);
+    if (lane == 0 && a.lse)
+      a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+  }
+};
+
+template <int HD, bool F16>
+__global__ void __launch_bounds__(128) k_attn_rows(AttnOpArgs a) {
+  const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31;
+  if (row >= (long long)a.B * a.Tq * a.Hq) return;
+  const int h = (int)(row % a.Hq), t = (int)(row / a.Hq % a.Tq), b = (int)(row / a.Hq / a.Tq);
+  const bool report = lane == 0 && h == 0 && t == 0;
+  const int n = seq_len(a, b, report), ql = query_len(a, b, report);
+  if (t >= ql) return;
+  const int hk = h / (a.Hq / a.Hkv);
+  RowAcc<HD, F16> r;
+  r.load_q(a, b, t, h, lane);
+  if (a.P > 0) r.keys(a.pre, 0, hk, 0, a.P, a.scale, lane);
+  const int p = n - ql + t;
+  const int lo = max(0, p - a.window + 1);
+  r.keys(a.kv, b, hk, 0, min(min(a.sinks, lo), p + 1), a.scale, lane);
+  r.keys(a.kv, b, hk, lo, p + 1, a.scale, lane);
+  r.store(a, b, t, h, lane);
+}
+
+template <int HD, bool F16>
+cudaError_t launch_rows(const AttnOpArgs& a, cudaStream_t s) {
+  const long long rows = (long long)a.B * a.Tq * a.Hq;
+  k_attn_rows<HD, F16><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
+  if (a.hd == 64) return a.f16 ? launch_rows<64, true>(a, s) : launch_rows<64, false>(a, s);
+  return a.f16 ? launch_rows<128, true>(a, s) : launch_rows<128, false>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s) { return launch_any(a, s); }
+
+size_t shared_prefix_ws_bytes(int B, int Hq, int hd) { return (size_t)B * Hq * (hd + 4) * sizeof(float); }
+
+cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s) { return launch_any(a, s); }
+
+}  // namespace river
+
+using namespace river;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+bool strides_ok(const int64_t* st, int n, int es, int64_t most) {
+  for (int i = 0; i < n; ++i)
+    if (st[i] < 0 || st[i] * es % 16 != 0 || st[i] >= most) return false;
+  return true;
+}
+
+// The checks the two operators share; fills `o` from the descriptor.
+rl_status check_desc(const char* who, const rl_attn_desc* a, AttnOpArgs* o) {
+  auto bad = [&](rl_status st, const char* what) {
+    char msg[256];
+    snprintf(msg, sizeof(msg), "%s: %s", who, what);
+    return set_error(st, msg);
+  };
+  if (!a) return bad(RL_ERR_INVALID_ARG, "the descriptor is NULL");
+  if (a->kv_dtype != RL_DT_BF16 && a->kv_dtype != RL_DT_F16)
+    return bad(RL_ERR_UNSUPPORTED, "kv_dtype must be RL_DT_BF16 or RL_DT_F16");
+  if (a->q_dtype != a->kv_dtype && a->q_dtype != RL_DT_F32)
+    return bad(RL_ERR_UNSUPPORTED, "q_dtype must be kv_dtype or RL_DT_F32");
+  if (a->batch < 1 || a->q_len < 1 || a->n_q_heads < 1 || a->n_kv_heads < 1 || a->kv_capacity < 1)
+    return bad(RL_ERR_INVALID_ARG, "batch, q_len, heads and kv_capacity must be >= 1");
+  if (a->head_dim != 64 && a->head_dim != 128) return bad(RL_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (a->n_q_heads % a->n_kv_heads) return bad(RL_ERR_UNSUPPORTED, "n_q_heads must be a multiple of n_kv_heads");
+  if ((long long)a->batch * a->q_len * a->n_q_heads >= (1ll << 31))
+    return bad(RL_ERR_UNSUPPORTED, "batch * q_len * n_q_heads must be below 2^31");
+  if (!(a->scale >= 0.f) || a->scale > 1e6f) return bad(RL_ERR_INVALID_ARG, "scale must be in [0, 1e6]");
+  const int qe = a->q_dtype == RL_DT_F32 ? 4 : 2;
+  if (!strides_ok(a->q_stride, 3, qe, 1ll << 59) || !strides_ok(a->out_stride, 3, 2, 1ll << 59))
+    return bad(RL_ERR_UNSUPPORTED, "q and out strides must be whole multiples of 16 bytes");
+  if (!strides_ok(a->k_stride, 3, 2, 1ll << 39) || !strides_ok(a->v_stride, 3, 2, 1ll << 39))
+    return bad(RL_ERR_UNSUPPORTED, "k and v strides must be whole multiples of 16 bytes, below 2^39 elements");
+  memset(o, 0, sizeof(*o));
+  o->q_f32 = a->q_dtype == RL_DT_F32;
+  o->f16 = a->kv_dtype == RL_DT_F16;
+  o->B = a->batch;
+  o->Tq = a->q_len;
+  o->Hq = a->n_q_heads;
+  o->Hkv = a->n_kv_heads;
+  o->hd = a->head_dim;
+  o->cap = a->kv_capacity;
+  o->scale = a->scale > 0.f ? a->scale : 1.f / sqrtf((float)a->head_dim);
+  for (int i = 0; i < 3; ++i) {
+    o->qs[i] = a->q_stride[i];
+    o->os[i] = a->out_stride[i];
+    o->kv.ks[i] = a->k_stride[i];
+    o->kv.vs[i] = a->v_stride[i];
+  }
+  o->kv_len_step = 1;
+  return RL_OK;
+}
+
+}  // namespace
+
+extern "C" rl_status rl_window_attention(const rl_attn_desc* a, const void* d_q, const void* d_k,
+                                         const void* d_v, const int32_t* d_kv_len,
+                                         const int32_t* d_q_len, int32_t window, int32_t sinks,
+                                         void* d_out, float* d_lse, int32_t* d_err, rl_stream_t stream) {
+  AttnOpArgs o;
+  const rl_status st = check_desc("rl_window_attention", a, &o);
+  if (st != RL_OK) return st;
+  if (!d_q || !d_k || !d_v || !d_kv_len || !d_out)
+    return set_error(RL_ERR_INVALID_ARG, "rl_window_attention: NULL argument");
+  if (window < 1 || sinks < 0)
+    return set_error(RL_ERR_INVALID_ARG, "rl_window_attention: window must be >= 1 and sinks >= 0");
+  if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_out))
+    return set_error(RL_ERR_UNSUPPORTED, "rl_window_attention: q, k, v and out must start on 16-byte boundaries");
+  if (d_out == d_q || d_out == d_k || d_out == d_v)
+    return set_error(RL_ERR_INVALID_ARG, "rl_window_attention: out overlaps an input");
+  o.q = d_q;
+  o.out = d_out;
+  o.lse = d_lse;
+  o.kv.k = d_k;
+  o.kv.v = d_v;
+  o.kv_len = d_kv_len;
+  o.q_len = d_q_len;
+  o.window = window < o.cap ? window : o.cap;  // no two positions are further apart
+  o.sinks = sinks < o.cap ? sinks : o.cap;
+  o.err = d_err;
+  const cudaError_t e = launch_window_attention(o, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_error(RL_ERR_CUDA, cudaGetErrorString(e));
+  return RL_OK;
+}
+
+extern "C" rl_status rl_shared_prefix_workspace(const rl_attn_desc* a, int32_t prefix_len, uint64_t* bytes) {
+  AttnOpArgs o;
+  const rl_status st = check_desc("rl_shared_prefix_workspace", a, &o);
+  if (st != RL_OK) return st;
+  if (!bytes || prefix_len < 0)
+    return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_workspace: bytes is NULL or prefix_len below 0");
+  *bytes = shared_prefix_ws_bytes(o.B, o.Hq, o.hd);
+  return RL_OK;
+}
+
+extern "C" rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const void* d_q,
+                                                const void* d_k_prefix, const void* d_v_prefix,
+                                                int32_t prefix_len, const int64_t prefix_stride[4],
+                                                const void* d_k, const void* d_v,
+                                                const int32_t* d_kv_len, void* d_out, float* d_lse,
+                                                void* d_ws, uint64_t ws_bytes, int32_t* d_err,
+                                                rl_stream_t stream) {
+  AttnOpArgs o;
+  const rl_status st = check_desc("rl_shared_prefix_attention", a, &o);
+  if (st != RL_OK) return st;
+  if (o.Tq != 1) return set_error(RL_ERR_UNSUPPORTED, "rl_shared_prefix_attention: q_len must be 1");
+  if (!d_q || !d_k || !d_v || !d_kv_len || !d_out || !d_ws)
+    return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: NULL argument");
+  if (prefix_len < 0 || (prefix_len > 0 && (!d_k_prefix || !d_v_prefix || !prefix_stride)))
+    return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: prefix_len below 0, or a prefix argument NULL");
+  if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_out) || !aligned16(d_ws))
+    return set_error(RL_ERR_UNSUPPORTED,
+                     "rl_shared_prefix_attention: q, k, v, out and the workspace must start on 16-byte boundaries");
+  if (d_out == d_q || d_out == d_k || d_out == d_v)
+    return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: out overlaps an input");
+  if (ws_bytes < shared_prefix_ws_bytes(o.B, o.Hq, o.hd))
+    return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: workspace too small");
+  if (prefix_len > 0) {
+    if (!aligned16(d_k_prefix) || !aligned16(d_v_prefix) || !strides_ok(prefix_stride, 4, 2, 1ll << 39))
+      return set_error(RL_ERR_UNSUPPORTED,
+                       "rl_shared_prefix_attention: the prefix must start on 16-byte boundaries, strides whole "
+                       "multiples of 16 bytes below 2^39 elements");
+    o.pre.k = d_k_prefix;
+    o.pre.v = d_v_prefix;
+    o.pre.ks[1] = prefix_stride[0];
+    o.pre.ks[2] = prefix_stride[1];
+    o.pre.vs[1] = prefix_stride[2];
+    o.pre.vs[2] = prefix_stride[3];
+    o.P = prefix_len;
+  }
+  o.q = d_q;
+  o.out = d_out;
+  o.lse = d_lse;
+  o.kv.k = d_k;
+  o.kv.v = d_v;
+  o.kv_len = d_kv_len;
+  o.window = o.cap;
+  o.err = d_err;
+  o.ws = d_ws;
+  const cudaError_t e = launch_shared_prefix_attention(o, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return set_error(RL_ERR_CUDA, cudaGetErrorString(e));
+  return RL_OK;
+}

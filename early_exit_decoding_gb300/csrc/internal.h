@@ -447,6 +447,52 @@ __host__ __device__ inline int step_attn_chunks(int ctx, int B, int Hkv, int hd,
 void launch_bf16_tile_layout(const bf16* w, int N, int Kp, bf16* out, cudaStream_t s);
 
 // ---------------------------------------------------------------------------
+// Stand-alone operators: token log-probabilities (logprobs.cu) and the two
+// attentions of attn_ops.cu.
+// ---------------------------------------------------------------------------
+struct LogprobArgs {
+  const void* x;            // logits [rows][ld]
+  int dtype;                // RL_DT_*
+  int rows, V;
+  long long ld;
+  const int* tokens;        // [rows][n_tok], nullable
+  int n_tok, top_k;
+  float *lse, *entropy, *logprob;  // nullable
+  int* top_ids;
+  float* top_lp;
+  int* err;                 // nullable
+};
+cudaError_t launch_logprobs(const LogprobArgs& a, cudaStream_t s);
+
+// Keys of one source: base + b * st[0] + head * st[1] + token * st[2] (elements).
+struct KeySrc {
+  const void *k, *v;
+  long long ks[3], vs[3];
+};
+struct AttnOpArgs {
+  const void* q;
+  int q_f32, f16;           // q is fp32; k, v and out are fp16 (else bf16)
+  long long qs[3], os[3];   // sequence, query row, head
+  void* out;
+  float* lse;               // [B][Tq][Hq], nullable
+  KeySrc kv;
+  int B, Tq, Hq, Hkv, hd, cap;
+  const int* kv_len;        // length of sequence b: kv_len[b * kv_len_step] + kv_len_add (null: kv_len_add)
+  int kv_len_step, kv_len_add;
+  const int* q_len;         // null: Tq rows each
+  int window, sinks;
+  float scale;              // natural-log units
+  int* err;                 // nullable
+  // shared prefix (P > 0): its keys come before the sequence's own
+  KeySrc pre;
+  int P;
+  void* ws;                 // shared-prefix partials
+};
+cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s);
+size_t shared_prefix_ws_bytes(int B, int Hq, int hd);
+cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s);
+
+// ---------------------------------------------------------------------------
 // What the allocation-free LM-head entry point needs from the model, and the
 // runtime's error message setter (both defined in api.cu).
 // ---------------------------------------------------------------------------

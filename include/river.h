@@ -387,6 +387,108 @@ RL_API rl_status rl_lm_head_static(const rl_model* m, const float* d_h, int32_t 
                                    float* d_logits, int32_t* d_next_token, int32_t* d_err,
                                    rl_stream_t stream);
 
+/* Element types of the stand-alone operators below. */
+enum { RL_DT_F32 = 0, RL_DT_BF16 = 1, RL_DT_F16 = 2 };
+
+/* rl_token_logprobs: what a model's answer says about tokens, from rows of
+ * logits (rl_prefill's and rl_decode_step's, or any other): with
+ * m = max_i x_i and s = sum_i exp(x_i - m) of a row of `vocab` logits,
+ *   lse       = m + ln s
+ *   entropy   = ln s - (sum_i (x_i - m) exp(x_i - m)) / s         (nats)
+ *   logprob_t = (x_t - m) - ln s      for each of the row's n_tok given tokens
+ *   top k     = the top_k largest logits' ids and logprobs, largest first,
+ *               equal logits by the lower id.
+ * The pages have no counterpart (an adjacent page routes tokens by entropy).
+ *   d_logits      [rows][vocab], `dtype` RL_DT_F32 / BF16 / F16, rows
+ *                 row_stride >= vocab elements apart (any alignment)
+ *   d_tokens      [rows][n_tok] int32 (NULL when n_tok is 0)
+ *   d_lse, d_entropy  [rows] fp32 (each may be NULL)
+ *   d_logprob     [rows][n_tok] fp32 (NULL when n_tok is 0)
+ *   d_top_ids, d_top_logprobs  [rows][top_k] int32 / fp32 (NULL when top_k is 0)
+ *   d_err         [1] int32, may be NULL: RL_DEVERR_* bits are ORed into it
+ * Logits of -infinity (ids that may not be produced) have probability 0 and
+ * add nothing to the entropy.  A token id outside [0, vocab) sets
+ * RL_DEVERR_TOKEN and gets NaN.  A row with a NaN or +infinity gives NaN for
+ * lse, entropy and logprobs; NaN orders above +infinity, -0 equals +0.  A row
+ * of -infinity alone: lse -infinity, entropy and logprobs NaN.
+ * Sums are fp32; the results do not depend on the number of SMs in use and
+ * repeat bit for bit.  No workspace, one launch.  RL_ERR_INVALID_ARG for a
+ * missing buffer, a size below 1, row_stride < vocab, n_tok outside [0, 256],
+ * top_k outside [0, min(32, vocab)] or an unknown dtype. */
+RL_API rl_status rl_token_logprobs(const void* d_logits, int32_t dtype, int32_t rows, int32_t vocab,
+                                   int64_t row_stride, const int32_t* d_tokens, int32_t n_tok,
+                                   int32_t top_k, float* d_lse, float* d_entropy, float* d_logprob,
+                                   int32_t* d_top_ids, float* d_top_logprobs, int32_t* d_err,
+                                   rl_stream_t stream);
+
+/* Shapes of the stand-alone attention operators.  Strides are in elements;
+ * the innermost (head_dim) axis is contiguous.  Requirements: head_dim 64 or
+ * 128; n_q_heads a multiple of n_kv_heads (query head h reads KV head
+ * h / (n_q_heads / n_kv_heads)); q, k, v and out start on 16-byte boundaries
+ * and their strides are whole multiples of 16 bytes (RL_ERR_UNSUPPORTED
+ * otherwise); k and v strides are below 2^39 elements.  A k or v stride of 0
+ * over sequences or KV heads shares one copy between them. */
+typedef struct {
+  int32_t kv_dtype;     /* of k, v and out: RL_DT_BF16 or RL_DT_F16 */
+  int32_t q_dtype;      /* kv_dtype, or RL_DT_F32 (rounded to kv_dtype when read) */
+  int32_t batch, q_len; /* sequences; query rows laid out for each */
+  int32_t n_q_heads, n_kv_heads, head_dim;
+  int32_t kv_capacity;  /* token rows laid out in k and v for each sequence */
+  float scale;          /* of q.k; 0 means 1 / sqrt(head_dim) */
+  int64_t q_stride[3];  /* sequence, query row, head */
+  int64_t out_stride[3];
+  int64_t k_stride[3];  /* sequence, KV head, token row (rl_kv_view's layout: Hkv*T*hd, T*hd, hd) */
+  int64_t v_stride[3];
+} rl_attn_desc;
+
+/* rl_window_attention: causal attention over a sliding window, with a few
+ * first tokens that stay visible (sinks), for prompts, drafts and single
+ * tokens.  Sequence b holds kv_len[b] token rows of k and v, its q_len[b]
+ * queries among them as the last ones: query row t stands at position
+ * p = kv_len[b] - q_len[b] + t and sees the keys j with
+ *   0 <= j <= p  and  (p - j < window  or  j < sinks);
+ *   out = sum_j softmax_j(scale q.k_j) v_j,   lse = ln sum_j exp(scale q.k_j).
+ *   d_kv_len  [batch] int32 (device);  d_q_len [batch] int32, NULL: q_len rows each
+ *   d_out     out_stride layout, kv_dtype;  d_lse [batch][q_len][n_q_heads] fp32, may be NULL
+ *   d_err     [1] int32, may be NULL: RL_DEVERR_* bits are ORed into it
+ * A row that sees no key (p < 0) gets 0 and lse -infinity.  Rows t >= q_len[b]
+ * of out and lse are left as they were.  Keys a row does not see have no part
+ * in its result, whatever they hold (NaN and infinity included).  A length
+ * outside [0, kv_capacity] or [0, q_len] sets RL_DEVERR_CAPACITY and is
+ * clamped.  A window of at least kv_capacity is plain causal attention.
+ * Scores, softmax statistics and sums are fp32; the weights are rounded to
+ * kv_dtype for the product with v.  No workspace, one launch, results repeat
+ * bit for bit.  out must not overlap q, k or v.  The first call on a device
+ * sets the kernels up: make it before any stream capture on the device.
+ * RL_ERR_INVALID_ARG for a NULL buffer, a size or window below 1, sinks
+ * below 0; RL_ERR_UNSUPPORTED for a shape outside rl_attn_desc's. */
+RL_API rl_status rl_window_attention(const rl_attn_desc* a, const void* d_q, const void* d_k,
+                                     const void* d_v, const int32_t* d_kv_len, const int32_t* d_q_len,
+                                     int32_t window, int32_t sinks, void* d_out, float* d_lse,
+                                     int32_t* d_err, rl_stream_t stream);
+
+/* rl_shared_prefix_attention: one decode step's attention of a batch whose
+ * sequences all start with the same prefix (one prompt, many continuations):
+ * the prefix's keys are read once for all sequences, then each sequence's own.
+ * Query b (a->q_len must be 1) sees prefix rows 0 .. prefix_len - 1 and rows
+ * 0 .. kv_len[b] - 1 of its own k and v; out and lse as rl_window_attention.
+ *   d_k_prefix, d_v_prefix  one copy for the batch; prefix_stride: {KV head,
+ *                           token row} of k, then of v, under the strides' rules above
+ *   d_ws  workspace of rl_shared_prefix_workspace bytes (16-byte aligned), in
+ *         use until the call's work on the stream is done: calls that may
+ *         overlap need one each
+ * A sequence that sees no key gets 0 and lse -infinity; a kv_len outside
+ * [0, kv_capacity] sets RL_DEVERR_CAPACITY and is clamped.  prefix_len 0 is
+ * allowed (the prefix pointers are then not read).  Errors as
+ * rl_window_attention; RL_ERR_INVALID_ARG also for a workspace too small. */
+RL_API rl_status rl_shared_prefix_workspace(const rl_attn_desc* a, int32_t prefix_len, uint64_t* bytes);
+RL_API rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const void* d_q,
+                                            const void* d_k_prefix, const void* d_v_prefix,
+                                            int32_t prefix_len, const int64_t prefix_stride[4],
+                                            const void* d_k, const void* d_v, const int32_t* d_kv_len,
+                                            void* d_out, float* d_lse, void* d_ws, uint64_t ws_bytes,
+                                            int32_t* d_err, rl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -557,56 +557,75 @@ def _refuse(msg, status=RL_ERR_INVALID_ARG):
     raise RiverError(status, msg)
 
 
-def _dtype_code(t):
-    import torch
-    return {torch.float32: RL_DT_F32, torch.bfloat16: RL_DT_BF16, torch.float16: RL_DT_F16}.get(t.dtype)
+def _dtype_code(dtype):
+    """RL_DT_* of a torch dtype; None for any other."""
+    if not _DTYPES:
+        import torch
+        _DTYPES.update({torch.float32: RL_DT_F32, torch.bfloat16: RL_DT_BF16, torch.float16: RL_DT_F16})
+    return _DTYPES.get(dtype)
 
 
-def _operands(name, first, **others):
-    """Checks that every tensor (None: absent) is on ``first``'s CUDA device and
-    needs no gradient (the operators have no backward pass)."""
+_DTYPES = {}
+
+
+def _operands(name, tensors):
+    """The one CUDA device (index) of the tensors (None: absent), none of which
+    may need a gradient (the operators have no backward pass)."""
     import torch
-    dev = first.device
+    dev = -1
     grad = torch.is_grad_enabled()
-    for n, t in (("", first), *others.items()):
+    for t in tensors:
         if t is None:
             continue
-        if not t.is_cuda or t.device != dev:
-            _refuse(f"{name}: {n or 'the first operand'} is on {t.device}, not on one CUDA device with the others")
+        d = t.get_device()
+        if d < 0 or (dev >= 0 and d != dev):
+            _refuse(f"{name}: every operand must be on one CUDA device (found {t.device})")
+        dev = d
         if grad and t.requires_grad:
-            _refuse(f"{name}: {n or 'the first operand'} requires a gradient; the operator has no backward pass",
-                    RL_ERR_UNSUPPORTED)
+            _refuse(f"{name}: an operand requires a gradient; the operator has no backward pass", RL_ERR_UNSUPPORTED)
     return dev
 
 
-def _buffer(o, key, shape, dtype, dev, name, stream):
+def _buffer(o, key, shape, like, dtype, stream, name):
     """``o[key]``, checked against (shape, dtype), or a new tensor put there
     (taken on the stream that writes it)."""
-    import torch
     t = o.get(key)
     if t is None:
-        with torch.cuda.stream(stream):
-            t = o[key] = torch.empty(shape, dtype=dtype, device=dev)
-    elif tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.device != dev or \
+        if stream is None:
+            t = like.new_empty(shape, dtype=dtype)
+        else:
+            import torch
+            with torch.cuda.stream(stream):
+                t = like.new_empty(shape, dtype=dtype)
+        o[key] = t
+    elif tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.get_device() != like.get_device() or \
             (key != "out" and not t.is_contiguous()):
-        _refuse(f"{name}: out[{key!r}] must be {dtype} {tuple(shape)} on {dev}"
+        _refuse(f"{name}: out[{key!r}] must be {dtype} {tuple(shape)} on {like.device}"
                 + ("" if key == "out" else ", contiguous"))
     return t
 
 
-def _on_device(dev, stream, call):
-    """``call(stream)`` with ``dev`` current; ``stream`` None: the device's current stream."""
+def _run(dev, stream, fn, *args):
+    """The library call ``fn(*args, stream)`` with device ``dev`` current;
+    ``stream`` None: that device's current stream."""
     import torch
-    if dev.index == torch.cuda.current_device():
-        return call(stream)
-    with torch.cuda.device(dev):
-        return call(stream)
+    cur = torch.cuda.current_device()
+    if cur != dev:
+        with torch.cuda.device(dev):
+            return _run(dev, stream, fn, *args)
+    status = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    if status != RL_OK:
+        _check(status)
 
 
 def _int32(name, key, t, shape):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        _refuse(f"{name}: {key} must be contiguous int32 {tuple(shape)}")
+    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        _refuse(f"{name}: {key} must be contiguous int32 {shape}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
 
 
 def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None):
@@ -618,10 +637,10 @@ def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None
     collects RL_DEVERR_* bits.  See rl_token_logprobs."""
     import torch
     name = "token_logprobs"
-    dt = _dtype_code(logits)
-    if logits.dim() != 2 or dt is None or 0 in logits.shape or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    dt = _dtype_code(logits.dtype)
+    if logits.dim() != 2 or dt is None or logits.numel() == 0 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         _refuse(f"{name}: logits must be fp32, bf16 or fp16 [R][V] with contiguous rows")
-    dev = _operands(name, logits, tokens=tokens, err=err)
+    dev = _operands(name, (logits, tokens, err))
     R, V = logits.shape
     if not 0 <= top_k <= min(32, V):
         _refuse(f"{name}: top_k {top_k} outside [0, {min(32, V)}]")
@@ -632,40 +651,45 @@ def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None
     if err is not None:
         _int32(name, "err", err, (1,))
     o = {} if out is None else dict(out)
-    lse = _buffer(o, "lse", (R,), torch.float32, dev, name, stream)
-    ent = _buffer(o, "entropy", (R,), torch.float32, dev, name, stream)
-    lp = _buffer(o, "logprob", tokens.shape, torch.float32, dev, name, stream) if n else None
-    ids = _buffer(o, "top_ids", (R, top_k), torch.int32, dev, name, stream) if top_k else None
-    tlp = _buffer(o, "top_logprobs", (R, top_k), torch.float32, dev, name, stream) if top_k else None
-    ld = logits.stride(0) if R > 1 else V
-    _on_device(dev, stream, lambda s: rl_token_logprobs(logits, dt, R, V, ld, tokens if n else None, n, top_k,
-                                                        lse, ent, lp, ids, tlp, err, s))
+    f32 = torch.float32
+    lse = _buffer(o, "lse", (R,), logits, f32, stream, name)
+    ent = _buffer(o, "entropy", (R,), logits, f32, stream, name)
+    lp = _buffer(o, "logprob", tokens.shape, logits, f32, stream, name) if n else None
+    ids = _buffer(o, "top_ids", (R, top_k), logits, torch.int32, stream, name) if top_k else None
+    tlp = _buffer(o, "top_logprobs", (R, top_k), logits, f32, stream, name) if top_k else None
+    _run(dev, stream, _lib.rl_token_logprobs, logits.data_ptr(), dt, R, V, logits.stride(0) if R > 1 else V,
+         _addr(tokens) if n else None, n, top_k, lse.data_ptr(), ent.data_ptr(), _addr(lp), _addr(ids), _addr(tlp),
+         _addr(err))
     return o
+
+
+def _strides(d, t):
+    """Strides of the first three axes into the descriptor's field; an axis of
+    one entry has no stride that matters."""
+    s, n = t.stride(), t.shape
+    d[0] = s[0] if n[0] > 1 else 0
+    d[1] = s[1] if n[1] > 1 else 0
+    d[2] = s[2] if n[2] > 1 else 0
 
 
 def _attn_desc(name, q, k, v, out, scale):
     """rl_attn_desc of q, out [B][T][Hq][hd] and k, v [B][Hkv][S][hd]."""
-    for n, t in (("q", q), ("k", k), ("v", v), ("out", out)):
-        if t.dim() != 4 or 0 in t.shape or t.stride(3) != 1:
-            _refuse(f"{name}: {n} must have four axes, none empty, with a contiguous last one")
+    for t in (q, k, v, out):
+        if t.dim() != 4 or t.numel() == 0 or t.stride(3) != 1:
+            _refuse(f"{name}: q, k, v and out must have their axes, none empty, with a contiguous last one")
     B, T, Hq, hd = q.shape
-    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != hd or v.dtype != k.dtype or out.dtype != k.dtype:
-        _refuse(f"{name}: q {tuple(q.shape)}, k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype} do not fit")
-    d = rl_attn_desc(_dtype_code(k) or RL_DT_F32, RL_DT_F32 if _dtype_code(q) is None else _dtype_code(q), B, T, Hq,
-                     k.shape[1], hd, k.shape[2], 0.0 if scale is None else float(scale))
-    if _dtype_code(q) is None or _dtype_code(k) is None:
-        _refuse(f"{name}: q {q.dtype}, k {k.dtype}: fp32, bf16 or fp16 expected")
-    if scale is not None and d.scale == 0.0:
-        _refuse(f"{name}: scale 0")
-
-    def strides(t, n):
-        # an axis of one entry has no stride that matters
-        return [0 if t.shape[i] == 1 else t.stride(i) for i in range(n)]
-
-    d.q_stride[:] = strides(q, 3)
-    d.out_stride[:] = strides(out, 3)
-    d.k_stride[:] = strides(k, 3)
-    d.v_stride[:] = strides(v, 3)
+    _, Hkv, S, _ = k.shape
+    qc, kc = _dtype_code(q.dtype), _dtype_code(k.dtype)
+    if k.shape != v.shape or k.shape[0] != B or k.shape[3] != hd or v.dtype != k.dtype or out.dtype != k.dtype or \
+            qc is None or kc is None:
+        _refuse(f"{name}: q {tuple(q.shape)} {q.dtype}, k {tuple(k.shape)} {k.dtype}, v {tuple(v.shape)} {v.dtype} do not fit")
+    if scale is not None and not scale > 0.0:
+        _refuse(f"{name}: scale must be above 0")
+    d = rl_attn_desc(kc, qc, B, T, Hq, Hkv, hd, S, 0.0 if scale is None else scale)
+    _strides(d.q_stride, q)
+    _strides(d.out_stride, out)
+    _strides(d.k_stride, k)
+    _strides(d.v_stride, v)
     return d
 
 
@@ -679,18 +703,18 @@ def window_attention(q, k, v, kv_len, window, sinks=0, q_len=None, scale=None, o
     left as they were.  See rl_window_attention."""
     import torch
     name = "window_attention"
-    dev = _operands(name, q, k=k, v=v, kv_len=kv_len, q_len=q_len, err=err)
+    dev = _operands(name, (q, k, v, kv_len, q_len, err))
     o = {} if out is None else dict(out)
-    res = _buffer(o, "out", q.shape, k.dtype, dev, name, stream)
+    res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
     d = _attn_desc(name, q, k, v, res, scale)
-    lse = _buffer(o, "lse", q.shape[:3], torch.float32, dev, name, stream)
-    _int32(name, "kv_len", kv_len, (q.shape[0],))
+    lse = _buffer(o, "lse", q.shape[:3], q, torch.float32, stream, name)
+    _int32(name, "kv_len", kv_len, (d.batch,))
     if q_len is not None:
-        _int32(name, "q_len", q_len, (q.shape[0],))
+        _int32(name, "q_len", q_len, (d.batch,))
     if err is not None:
         _int32(name, "err", err, (1,))
-    _on_device(dev, stream, lambda s: rl_window_attention(d, q, k, v, kv_len, q_len, int(window), int(sinks), res,
-                                                          lse, err, s))
+    _run(dev, stream, _lib.rl_window_attention, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), kv_len.data_ptr(),
+         _addr(q_len), window, sinks, res.data_ptr(), lse.data_ptr(), _addr(err))
     return o
 
 
@@ -705,34 +729,27 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
     for this call.  See rl_shared_prefix_attention."""
     import torch
     name = "shared_prefix_attention"
-    dev = _operands(name, q, k_prefix=k_prefix, v_prefix=v_prefix, k=k, v=v, kv_len=kv_len, workspace=workspace,
-                    err=err)
+    dev = _operands(name, (q, k_prefix, v_prefix, k, v, kv_len, workspace, err))
     if q.dim() != 3:
         _refuse(f"{name}: q must be [B][Hq][hd]")
     o = {} if out is None else dict(out)
-    res = _buffer(o, "out", q.shape, k.dtype, dev, name, stream)
+    res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
     d = _attn_desc(name, q[:, None], k, v, res[:, None], scale)
-    lse = _buffer(o, "lse", q.shape[:2], torch.float32, dev, name, stream)
-    _int32(name, "kv_len", kv_len, (q.shape[0],))
+    lse = _buffer(o, "lse", q.shape[:2], q, torch.float32, stream, name)
+    _int32(name, "kv_len", kv_len, (d.batch,))
     if err is not None:
         _int32(name, "err", err, (1,))
     if k_prefix.dim() != 3 or k_prefix.shape != v_prefix.shape or k_prefix.dtype != k.dtype or \
-            v_prefix.dtype != k.dtype or k_prefix.shape[0] != k.shape[1] or k_prefix.shape[2] != k.shape[3] or \
+            v_prefix.dtype != k.dtype or k_prefix.shape[0] != d.n_kv_heads or k_prefix.shape[2] != d.head_dim or \
             k_prefix.stride(2) != 1 or v_prefix.stride(2) != 1:
-        _refuse(f"{name}: k_prefix and v_prefix must be {k.dtype} [{k.shape[1]}][P][{k.shape[3]}] with a contiguous last axis")
+        _refuse(f"{name}: k_prefix and v_prefix must be {k.dtype} [{d.n_kv_heads}][P][{d.head_dim}] with a contiguous last axis")
     P = k_prefix.shape[1]
-    ps = [0 if t.shape[i] == 1 else t.stride(i) for t in (k_prefix, v_prefix) for i in (0, 1)]
-
-    def call(s):
-        ws = workspace
-        n = rl_shared_prefix_workspace(d, P)
-        if ws is None:
-            with torch.cuda.stream(s):
-                ws = torch.empty((n,), dtype=torch.uint8, device=dev)
-        rl_shared_prefix_attention(d, q, k_prefix, v_prefix, P, ps, k, v, kv_len, res, lse, ws,
-                                   ws.numel() * ws.element_size(), err, s)
-
-    _on_device(dev, stream, call)
+    ps = (ctypes.c_int64 * 4)(*(t.stride(i) if t.shape[i] > 1 else 0 for t in (k_prefix, v_prefix) for i in (0, 1)))
+    if workspace is None:
+        workspace = _buffer({}, "workspace", (rl_shared_prefix_workspace(d, P),), q, torch.uint8, stream, name)
+    _run(dev, stream, _lib.rl_shared_prefix_attention, d, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), P, ps,
+         k.data_ptr(), v.data_ptr(), kv_len.data_ptr(), res.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+         workspace.numel() * workspace.element_size(), _addr(err))
     return o
 
 

@@ -12,106 +12,14 @@
 #include <stdio.h>
 #include <string.h>
 
-#include "dev_common.cuh"
-#include "internal.h"
+#include "attn_ops.cuh"
 
 namespace river {
 
 namespace {
 
 using namespace dev;
-
-template <bool F16>
-__device__ __forceinline__ float2 unpack2(uint32_t v) {
-  if constexpr (F16)
-    return __half22float2(*reinterpret_cast<const __half2*>(&v));
-  else
-    return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&v));
-}
-template <bool F16>
-__device__ __forceinline__ uint32_t pack2(float x, float y) {
-  if constexpr (F16) {
-    const __half2 h = __floats2half2_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  } else {
-    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
-    return *reinterpret_cast<const uint32_t*>(&h);
-  }
-}
-
-// Length of sequence b, clamped to the rows laid out for it.
-__device__ __forceinline__ int seq_len(const AttnOpArgs& a, int b, bool report) {
-  int n = a.kv_len ? a.kv_len[(long long)b * a.kv_len_step] + a.kv_len_add : a.kv_len_add;
-  if (n < 0 || n > a.cap) {
-    if (report && a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
-    n = n < 0 ? 0 : a.cap;
-  }
-  return n;
-}
-__device__ __forceinline__ int query_len(const AttnOpArgs& a, int b, bool report) {
-  int n = a.q_len ? a.q_len[b] : a.Tq;
-  if (n < 0 || n > a.Tq) {
-    if (report && a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
-    n = n < 0 ? 0 : a.Tq;
-  }
-  return n;
-}
-
-// Running softmax of one row held by a warp: lane holds dims
-// 2 * lane + 64 * i, i < HD / 64.
-template <int HD, bool F16>
-struct RowAcc {
-  float2 q[HD / 64], o[HD / 64];
-  float m = -INFINITY, l = 0.f;
-  __device__ __forceinline__ void load_q(const AttnOpArgs& a, int b, int t, int h, int lane) {
-    const long long at = b * a.qs[0] + t * a.qs[1] + h * a.qs[2] + 2 * lane;
-#pragma unroll
-    for (int i = 0; i < HD / 64; ++i) {
-      if (a.q_f32) {
-        const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at + 64 * i);
-        q[i] = unpack2<F16>(pack2<F16>(f.x, f.y));
-      } else {
-        q[i] = unpack2<F16>(*reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) + at + 64 * i));
-      }
-      o[i] = make_float2(0.f, 0.f);
-    }
-  }
-  __device__ __forceinline__ void keys(const KeySrc& s, int b, int hk, int j0, int j1, float scale, int lane) {
-    const long long kb = b * s.ks[0] + hk * s.ks[1] + 2 * lane, vb = b * s.vs[0] + hk * s.vs[1] + 2 * lane;
-    for (int j = j0; j < j1; ++j) {
-      float d = 0.f;
-      uint32_t vv[HD / 64];
-#pragma unroll
-      for (int i = 0; i < HD / 64; ++i) {
-        const float2 k = unpack2<F16>(
-            *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(s.k) + kb + j * s.ks[2] + 64 * i));
-        vv[i] = *reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(s.v) + vb + j * s.vs[2] + 64 * i);
-        d += q[i].x * k.x + q[i].y * k.y;
-      }
-      d = warp_sum(d) * scale;
-      const float mn = fmaxf(m, d), mu = mn == -INFINITY ? 0.f : mn;
-      const float c = __expf(m - mu), e = __expf(d - mu);
-      l = l * c + e;
-#pragma unroll
-      for (int i = 0; i < HD / 64; ++i) {
-        const float2 v = unpack2<F16>(vv[i]);
-        o[i].x = o[i].x * c + e * v.x;
-        o[i].y = o[i].y * c + e * v.y;
-      }
-      m = mn;
-    }
-  }
-  __device__ __forceinline__ void store(const AttnOpArgs& a, int b, int t, int h, int lane) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    const long long at = b * a.os[0] + t * a.os[1] + h * a.os[2] + 2 * lane;
-#pragma unroll
-    for (int i = 0; i < HD / 64; ++i)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + 64 * i) =
-          pack2<F16>(o[i].x * inv, o[i].y * inv);
-    if (lane == 0 && a.lse)
-      a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
-  }
-};
+using namespace attn;
 
 template <int HD, bool F16>
 __global__ void __launch_bounds__(128) k_attn_rows(AttnOpArgs a) {
@@ -126,10 +34,7 @@ __global__ void __launch_bounds__(128) k_attn_rows(AttnOpArgs a) {
   RowAcc<HD, F16> r;
   r.load_q(a, b, t, h, lane);
   if (a.P > 0) r.keys(a.pre, 0, hk, 0, a.P, a.scale, lane);
-  const int p = n - ql + t;
-  const int lo = max(0, p - a.window + 1);
-  r.keys(a.kv, b, hk, 0, min(min(a.sinks, lo), p + 1), a.scale, lane);
-  r.keys(a.kv, b, hk, lo, p + 1, a.scale, lane);
+  r.window(a, b, t, hk, n, ql, lane);
   r.store(a, b, t, h, lane);
 }
 
@@ -147,9 +52,12 @@ cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s) { return launch_any(a, s); }
+cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s) {
+  if (a.Tq * (a.Hq / a.Hkv) <= 64) return launch_attn_decode(a, false, s);
+  return launch_any(a, s);
+}
 
-size_t shared_prefix_ws_bytes(int B, int Hq, int hd) { return (size_t)B * Hq * (hd + 4) * sizeof(float); }
+size_t shared_prefix_ws_bytes(int B, int Hq, int hd) { return (size_t)B * Hq * ws_entry(hd) * sizeof(float); }
 
 cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s) { return launch_any(a, s); }
 
@@ -208,6 +116,8 @@ rl_status check_desc(const char* who, const rl_attn_desc* a, AttnOpArgs* o) {
     o->kv.vs[i] = a->v_stride[i];
   }
   o->kv_len_step = 1;
+  if (a->kv_capacity > 1 && (a->k_stride[2] == 0 || a->v_stride[2] == 0))
+    return bad(RL_ERR_UNSUPPORTED, "k and v token strides must not be 0");
   return RL_OK;
 }
 

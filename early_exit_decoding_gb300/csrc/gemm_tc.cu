@@ -773,6 +773,7 @@ void launch_rope_table(const float* inv_freq, int half, int Tmax, float2* out, c
 }
 
 bool tc_gemm_available() { return encode_fn() != nullptr; }
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() { return encode_fn(); }
 
 // Shared-memory opt-in of every instantiation (once per process and device,
 // before any launch or graph capture).

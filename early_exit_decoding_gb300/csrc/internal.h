@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -115,6 +116,8 @@ void launch_gemv(const GemvArgs& a, int sm_count, cudaStream_t s);
 // epilogues; returns at once when the layer takes the W4 path.
 // ---------------------------------------------------------------------------
 bool tc_gemm_available();
+// The driver's cuTensorMapEncodeTiled (null if it cannot be found).
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 cudaError_t tc_gemm_init();
 bool make_tmap_bf16(CUtensorMap* map, const void* base, int inner, int rows, int ld, int box_rows);
 bool make_weight_tmap(CUtensorMap* map, const bf16* w, int N, int Kp);
@@ -450,6 +453,10 @@ void launch_bf16_tile_layout(const bf16* w, int N, int Kp, bf16* out, cudaStream
 // Stand-alone operators: token log-probabilities (logprobs.cu) and the two
 // attentions of attn_ops.cu.
 // ---------------------------------------------------------------------------
+constexpr int kOpDevices = 64;  // devices the operators' per-device set-up covers
+// SMs of device `dev` (looked up once).
+cudaError_t device_sm_count(int dev, int* out);
+
 struct LogprobArgs {
   const void* x;            // logits [rows][ld]
   int dtype;                // RL_DT_*

@@ -411,8 +411,7 @@ enum { RL_DT_F32 = 0, RL_DT_BF16 = 1, RL_DT_F16 = 2 };
  * RL_DEVERR_TOKEN and gets NaN.  A row with a NaN or +infinity gives NaN for
  * lse, entropy and logprobs; NaN orders above +infinity, -0 equals +0.  A row
  * of -infinity alone: lse -infinity, entropy and logprobs NaN.
- * Sums are fp32; the results do not depend on the number of SMs in use and
- * repeat bit for bit.  No workspace, one launch.  RL_ERR_INVALID_ARG for a
+ * Sums are fp32 and repeat bit for bit.  No workspace, one launch.  RL_ERR_INVALID_ARG for a
  * missing buffer, a size below 1, row_stride < vocab, n_tok outside [0, 256],
  * top_k outside [0, min(32, vocab)] or an unknown dtype. */
 RL_API rl_status rl_token_logprobs(const void* d_logits, int32_t dtype, int32_t rows, int32_t vocab,
@@ -427,7 +426,8 @@ RL_API rl_status rl_token_logprobs(const void* d_logits, int32_t dtype, int32_t 
  * h / (n_q_heads / n_kv_heads)); q, k, v and out start on 16-byte boundaries
  * and their strides are whole multiples of 16 bytes (RL_ERR_UNSUPPORTED
  * otherwise); k and v strides are below 2^39 elements.  A k or v stride of 0
- * over sequences or KV heads shares one copy between them. */
+ * over sequences or KV heads shares one copy between them; the token rows'
+ * stride may be 0 only if there is one. */
 typedef struct {
   int32_t kv_dtype;     /* of k, v and out: RL_DT_BF16 or RL_DT_F16 */
   int32_t q_dtype;      /* kv_dtype, or RL_DT_F32 (rounded to kv_dtype when read) */

@@ -3,16 +3,19 @@
 //
 // With m = max x, s = sum exp(x - m) and t = sum (x - m) exp(x - m):
 //   lse = m + ln s,  entropy = ln s - t / s,  logprob_i = (x_i - m) - ln s.
-// One pass over the row.  Every thread keeps its own (m, s, t): a tile of 16
-// (fp32) or 32 (bf16, fp16) logits a thread raises m by the tile's maximum
-// first, s' = a s and t' = a (t + (m - m') s) with a = exp(m - m'), then adds
+// One pass over the row.  Every warp has its own ring of 2 KB tiles filled by
+// bulk copies (192 KB in flight a SM without a register held for them; plain
+// loads prefetched into registers spilled and gave 5.3 TB/s).  Every thread
+// keeps its own (m, s, t): a tile of 16 (fp32) or 32 (bf16, fp16) logits a
+// thread raises m by the tile's maximum first, s' = a s and t' = a (t + (m - m') s) with a = exp(m - m'), then adds
 // the tile's terms; threads, warps and the CTAs of a cluster join theirs by
 // the same rule in a fixed order, so results repeat bit for bit.
 //
 // Top k (k <= 32): every warp keeps the candidates above its threshold in a
 // list in shared memory, as 64-bit keys (ordered value, then the lower id).
-// The first threshold is the k-th largest of the 32 lanes' maxima in the
-// first tile (at least k logits reach it); a full list is cut to its k
+// The first threshold is the k-th largest of the four largest thread maxima of
+// each of the 8 warps' first tiles (at least k logits reach it: for k = 20
+// about 1 % of random logits do); a full list is cut to its k
 // largest, the last of which is the next threshold.  A tile none of whose
 // logits reaches the threshold costs one comparison a thread and one vote.
 // The warps' lists are merged in order, then the CTAs'.
@@ -35,12 +38,18 @@ namespace {
 
 using namespace dev;
 
-constexpr int kLpThreads = 512;
+constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kLpVecs = 4;       // 16-byte loads of a thread's tile
-constexpr int kLpCap = 128;      // candidates a warp's list holds
+constexpr int kLpResident = 4;   // CTAs a SM holds
+constexpr int kLpVecs = 4;       // 16-byte vectors of a thread's tile
+constexpr int kLpTile = 32 * kLpVecs;           // vectors of a warp's tile
+constexpr int kLpStages = 3;     // tiles of a warp's ring
+constexpr int kLpRing = kLpWarps * kLpStages * kLpTile * 16;
+constexpr int kLpCap = 96;       // candidates a warp's list holds (4 CTAs' shared memory fits an SM)
 constexpr int kLpMaxSplit = 16;  // CTAs of a row's cluster
+constexpr unsigned long long kLpWaitNs = 2000000000ull;
 constexpr float kLog2e = 1.4426950408889634f;
+static_assert(kLpWarps == 8 && kLpVecs == 4, "the first threshold takes four values of each of 8 warps");
 
 // Unsigned keys that order values as documented: NaN above +infinity, -0 as
 // +0; the low half orders equal values by the lower id.
@@ -52,12 +61,9 @@ __device__ __forceinline__ unsigned long long order_key(float x, int id) {
   return ((unsigned long long)order_bits(x) << 32) | (0xffffffffu - (uint32_t)id);
 }
 __device__ __forceinline__ unsigned long long warp_max_u64(unsigned long long v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long w = __shfl_xor_sync(0xffffffffu, v, o);
-    v = w > v ? w : v;
-  }
-  return v;
+  const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32));
+  const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(v >> 32) == hi ? (uint32_t)v : 0u);
+  return ((unsigned long long)hi << 32) | lo;
 }
 // Maximum that a NaN survives.
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -76,10 +82,9 @@ struct Elem;
 template <>
 struct Elem<float> {
   static constexpr int kVec = 4;
-  static constexpr uint32_t kNegInf = 0xff800000u;
+  static constexpr uint32_t kNegInf = 0xff800000u;  // -infinity in every element
   static __device__ __forceinline__ float get(const uint4& v, int e) { return __uint_as_float(u4get(v, e)); }
   static __device__ __forceinline__ float load(const float* p) { return *p; }
-  static __device__ __forceinline__ void set(uint32_t (&w)[4], int e, const float* p) { w[e] = __float_as_uint(*p); }
 };
 template <>
 struct Elem<bf16> {
@@ -90,10 +95,6 @@ struct Elem<bf16> {
     return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
   }
   static __device__ __forceinline__ float load(const bf16* p) { return __bfloat162float(*p); }
-  static __device__ __forceinline__ void set(uint32_t (&w)[4], int e, const bf16* p) {
-    const uint32_t b = *reinterpret_cast<const uint16_t*>(p);
-    w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | (b << 16) : (w[e >> 1] & 0xffff0000u) | b;
-  }
 };
 template <>
 struct Elem<__half> {
@@ -104,10 +105,6 @@ struct Elem<__half> {
     return __half2float(__ushort_as_half((unsigned short)((e & 1) ? w >> 16 : w & 0xffffu)));
   }
   static __device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
-  static __device__ __forceinline__ void set(uint32_t (&w)[4], int e, const __half* p) {
-    const uint32_t b = *reinterpret_cast<const uint16_t*>(p);
-    w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | (b << 16) : (w[e >> 1] & 0xffff0000u) | b;
-  }
 };
 
 // Partial sums of a part of a row: s and t relative to m.
@@ -148,6 +145,21 @@ __device__ __forceinline__ float value_of(unsigned long long key) {
 // Keeps the k largest keys of the list, largest first.
 __device__ __noinline__ void cut_list(Cand& c, int k, int lane) {
   __syncwarp();
+  if (c.cnt <= 32) {  // one key a lane: its place is the number of larger ones
+    const unsigned long long v = lane < c.cnt ? c.list[lane] : 0ull;
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) rank += __shfl_sync(0xffffffffu, v, i) > v;
+    __syncwarp();
+    if (v != 0 && rank < k) c.list[rank] = v;
+    c.cnt = min(k, c.cnt);
+    __syncwarp();
+    if (c.cnt == k) {
+      c.thr = c.list[k - 1];
+      c.thr_f = value_of(c.thr);
+    }
+    return;
+  }
   unsigned long long v[kLpCap / 32];
 #pragma unroll
   for (int i = 0; i < kLpCap / 32; ++i) v[i] = lane + 32 * i < c.cnt ? c.list[lane + 32 * i] : 0ull;
@@ -170,108 +182,185 @@ __device__ __noinline__ void cut_list(Cand& c, int k, int lane) {
   __syncwarp();
 }
 
+// The lanes' logits v at ids `id` that may be candidates join the list.
+__device__ __noinline__ void push(Cand& c, float v, int id, bool may, int k, int lane) {
+  const unsigned long long key = order_key(v, id);
+  const bool take = may && key > c.thr;
+  const unsigned mask = __ballot_sync(0xffffffffu, take);
+  if (take) c.list[c.cnt + __popc(mask & ((1u << lane) - 1))] = key;
+  c.cnt += __popc(mask);
+  if (c.cnt > kLpCap - 32) cut_list(c, k, lane);
+}
+
+// Adds one logit to a part whose m is already at least as large.
+__device__ __forceinline__ void add(Part& p, float x, float mu) {
+  const float d = max_nan(x - mu, -1e30f), e = ex2(d * kLog2e);
+  p.s += e;
+  p.t = fmaf(d, e, p.t);
+}
+
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads, 2) k_logprobs(LogprobArgs a, int split) {
+__global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __grid_constant__ LogprobArgs a, int split) {
   using E = Elem<T>;
-  constexpr int VEC = E::kVec, N = kLpVecs * VEC;
+  constexpr int VEC = E::kVec;
+  extern __shared__ __align__(16) unsigned char ring_all[];
+  __shared__ __align__(8) uint64_t full[kLpWarps][kLpStages];
   __shared__ Part s_part[kLpWarps];
   __shared__ Part s_cta;
   __shared__ unsigned long long s_list[kTop ? kLpWarps : 1][kTop ? kLpCap : 1];
+  __shared__ uint32_t s_w[32];  // the warps' four largest lane maxima
   __shared__ unsigned long long s_top[kTop ? 32 : 1];
-  __shared__ unsigned long long s_all[kTop ? kLpMaxSplit : 1][kTop ? 32 : 1];
 
   const int row = blockIdx.x / split, part = blockIdx.x % split;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const T* x = static_cast<const T*>(a.x) + (long long)row * a.ld;
   const int V = a.V, k = a.top_k;
 
-  // The row in 16-byte vectors: vector 0 holds the first logit at element
-  // `mis`; the first and last vector may reach outside the row.
-  const int mis = (int)((reinterpret_cast<uintptr_t>(x) & 15) / sizeof(T));
-  const T* xv = x - mis;
-  const int nvec = (int)(((long long)V + mis + VEC - 1) / VEC);
+  // The row's whole 16-byte vectors [0, nvec) start `head` logits in; this
+  // CTA's part of them is [v0, v1), dealt out to its warps in tiles of 2 KB.
+  // The logits in front (part 0) and behind (last part) are `edge`, one a lane
+  // of warp 0.
+  const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
+  const int nvec = (V - head) / VEC;
   const int v0 = (int)((long long)nvec * part / split), v1 = (int)((long long)nvec * (part + 1) / split);
-
-  auto fetch = [&](int v) -> uint4 {
-    uint32_t w[4] = {E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf};
-    if (v < v1) {
-      const long long e0 = (long long)v * VEC - mis;
-      if (e0 >= 0 && e0 + VEC <= V) return __ldcs(reinterpret_cast<const uint4*>(xv + (long long)v * VEC));
-#pragma unroll
-      for (int e = 0; e < VEC; ++e)
-        if (e0 + e >= 0 && e0 + e < V) E::set(w, e, x + e0 + e);
+  const T* xv = x + head;
+  const int ntile = (v1 - v0 + kLpTile - 1) / kLpTile;
+  unsigned char* ring = ring_all + warp * kLpStages * kLpTile * 16;
+  auto issue = [&](int i, int st) {  // tile i of the part into stage st
+    const int at = v0 + i * kLpTile, n = min(kLpTile, v1 - at);
+    mbar_expect_tx(&full[warp][st], n * 16);
+    bulk_g2s(ring + st * kLpTile * 16, xv + (long long)at * VEC, n * 16, &full[warp][st]);
+  };
+  if (lane == 0) {
+    for (int i = 0; i < kLpStages; ++i) mbar_init(&full[warp][i], 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    for (int i = 0; i < kLpStages; ++i)
+      if (warp + i * kLpWarps < ntile) issue(warp + i * kLpWarps, i);
+  }
+  // the given tokens' logits, one a thread (part 0; n_tok <= 256)
+  float tokv = NAN;
+  if (part == 0 && tid < a.n_tok) {
+    const int tok = a.tokens[(long long)row * a.n_tok + tid];
+    if (tok >= 0 && tok < V)
+      tokv = E::load(x + tok);
+    else if (a.err)
+      atomicOr(a.err, RL_DEVERR_TOKEN);
+  }
+  Part p{-INFINITY, 0.f, 0.f};
+  int edge = -1;  // id of this lane's edge logit
+  float edge_v = -INFINITY;
+  if (warp == 0) {
+    const int tail = head + nvec * VEC + lane - 16;
+    if (part == 0 && lane < head) edge = lane;
+    if (part == split - 1 && lane >= 16 && tail < V) edge = tail;
+    if (edge >= 0) {
+      edge_v = E::load(x + edge);
+      p.m = fmaxf(p.m, edge_v);
+      add(p, edge_v, pivot(p.m));
     }
-    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  __syncwarp();
+
+  bool ok = true;
+  auto wait = [&](int st, int ph) {
+    const bool got = mbar_wait_for(&full[warp][st], ph, kLpWaitNs);
+    if (!__all_sync(0xffffffffu, got) && ok) {
+      ok = false;
+      if (lane == 0 && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
+    }
+  };
+  auto vec = [&](int i, int st, int j) {  // this lane's vector j of tile i
+    return v0 + i * kLpTile + j * 32 + lane < v1
+               ? *reinterpret_cast<const uint4*>(ring + (st * kLpTile + j * 32 + lane) * 16)
+               : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
+  };
+  auto vec_max = [&](const uint4& v) {
+    float m = E::get(v, 0);
+#pragma unroll
+    for (int e = 1; e < VEC; ++e) m = max_nan(m, E::get(v, e));
+    return m;
   };
 
-  Part p{-INFINITY, 0.f, 0.f};
   Cand c{kTop ? s_list[warp] : nullptr, 0ull, -INFINITY, 0};
-  bool first = true;
-  uint4 nxt[kLpVecs];
-#pragma unroll
-  for (int j = 0; j < kLpVecs; ++j) nxt[j] = fetch(v0 + j * kLpThreads + tid);
-  for (int base = v0; base < v1; base += kLpVecs * kLpThreads) {
-    uint4 cur[kLpVecs];
-#pragma unroll
-    for (int j = 0; j < kLpVecs; ++j) cur[j] = nxt[j];
-    if (base + kLpVecs * kLpThreads < v1) {
-#pragma unroll
-      for (int j = 0; j < kLpVecs; ++j) nxt[j] = fetch(base + (kLpVecs + j) * kLpThreads + tid);
+  if constexpr (kTop) {
+    uint32_t o = 0;
+    if (warp < ntile) {
+      wait(0, 0);
+      o = order_bits(max_nan(max_nan(vec_max(vec(warp, 0, 0)), vec_max(vec(warp, 0, 1))),
+                             max_nan(vec_max(vec(warp, 0, 2)), vec_max(vec(warp, 0, 3)))));
     }
-    float tm = E::get(cur[0], 0);
 #pragma unroll
-    for (int i = 1; i < N; ++i) tm = max_nan(tm, E::get(cur[i / VEC], i % VEC));
-    const float mn = fmaxf(p.m, tm);
-    if (mn > p.m) rebase(p, mn);
-    const float mu = pivot(p.m);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float d = max_nan(E::get(cur[i / VEC], i % VEC) - mu, -1e30f);
-      const float e = ex2(d * kLog2e);
-      p.s += e;
-      p.t = fmaf(d, e, p.t);
-    }
-    if constexpr (kTop) {
-      if (first) {
-        // the k-th largest of the lanes' maxima: at least k logits reach it
-        first = false;
-        const uint32_t o = order_bits(tm);
-        int rank = 0;
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint32_t q = __shfl_sync(0xffffffffu, o, i);
-          rank += q > o || (q == o && i < lane);
-        }
-        const unsigned who = __ballot_sync(0xffffffffu, rank == k - 1);
-        const uint32_t ok = __shfl_sync(0xffffffffu, o, __ffs(who) - 1);
-        c.thr = ((unsigned long long)ok << 32) - 1;
-        c.thr_f = value_of((unsigned long long)ok << 32);
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = __reduce_max_sync(0xffffffffu, o);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, o == w)) - 1) {
+        s_w[4 * warp + i] = w;
+        o = 0;
       }
-      if (__any_sync(0xffffffffu, !(tm < c.thr_f))) {
-#pragma unroll 1
-        for (int j = 0; j < kLpVecs; ++j) {
-          uint4 cv = cur[0];
-          if (j == 1) cv = cur[1];
-          if (j == 2) cv = cur[2];
-          if (j == 3) cv = cur[3];
-          const long long e0 = (long long)(base + j * kLpThreads + tid) * VEC - mis;
-          const bool in = base + j * kLpThreads + tid < v1;
+    }
+    __syncthreads();
+    const uint32_t mine = s_w[lane];
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t q = __shfl_sync(0xffffffffu, mine, i);
+      rank += q > mine || (q == mine && i < lane);
+    }
+    const unsigned who = __ballot_sync(0xffffffffu, rank == k - 1);
+    const uint32_t kth = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+    if (kth) {
+      c.thr = ((unsigned long long)kth << 32) - 1;
+      c.thr_f = value_of((unsigned long long)kth << 32);
+    }
+    if (warp == 0) push(c, edge_v, edge, edge >= 0, k, lane);
+  }
+
+  // After a wait that gave up nothing is copied or computed any more; the
+  // copies already in flight are still waited for (`stop`).
+  int st = 0, ph = 0, stop = ok ? ntile : min(ntile, warp + kLpStages * kLpWarps);
+  for (int i = warp; i < stop; i += kLpWarps) {
+    const bool was = ok;
+    wait(st, ph);
+    if (was && !ok) stop = min(ntile, i + kLpStages * kLpWarps);
+    if (ok) {
+      uint4 cur[kLpVecs];
+      float vm[kLpVecs];  // largest of each vector
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float v = E::get(cv, e);
-            const unsigned long long key = order_key(v, (int)(e0 + e));
-            const bool take = in && key > c.thr && e0 + e >= 0 && e0 + e < V;
-            const unsigned mask = __ballot_sync(0xffffffffu, take);
-            if (mask) {
-              if (take) c.list[c.cnt + __popc(mask & ((1u << lane) - 1))] = key;
-              c.cnt += __popc(mask);
-              if (c.cnt > kLpCap - 32) cut_list(c, k, lane);
+      for (int j = 0; j < kLpVecs; ++j) cur[j] = vec(i, st, j);
+#pragma unroll
+      for (int j = 0; j < kLpVecs; ++j) vm[j] = vec_max(cur[j]);
+      const float tm = max_nan(max_nan(vm[0], vm[1]), max_nan(vm[2], vm[3]));
+      const float mn = fmaxf(p.m, tm);
+      if (mn > p.m) rebase(p, mn);
+      const float mu = pivot(p.m);
+#pragma unroll
+      for (int j = 0; j < kLpVecs; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) add(p, E::get(cur[j], e), mu);
+      if constexpr (kTop) {
+        if (__any_sync(0xffffffffu, !(tm < c.thr_f))) {
+#pragma unroll 1
+          for (int j = 0; j < kLpVecs; ++j) {
+            const uint4 w = vec(i, st, j);
+            if (!__any_sync(0xffffffffu, !(vec_max(w) < c.thr_f))) continue;
+            const int at = v0 + i * kLpTile + j * 32 + lane;
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) {
+              const float v = E::get(w, e);
+              const bool hit = at < v1 && !(v < c.thr_f);
+              if (__any_sync(0xffffffffu, hit)) push(c, v, head + at * VEC + e, hit, k, lane);
             }
           }
         }
       }
     }
+    __syncwarp();
+    if (ok && lane == 0 && i + kLpStages * kLpWarps < ntile) issue(i + kLpStages * kLpWarps, st);
+    if (++st == kLpStages) {
+      st = 0;
+      ph ^= 1;
+    }
   }
+  if (!ok) p.s = NAN;  // a copy did not arrive (reported): no result
 
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1)
@@ -303,6 +392,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_logprobs(LogprobArgs a, int s
     if (lane == 0) s_cta = p;
     if constexpr (kTop) merge([&](int i) { return s_list[i]; }, kLpWarps, s_top);
   }
+  __shared__ float s_res[2];
   if (split > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (part == 0 && warp == 0) {
@@ -324,6 +414,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_logprobs(LogprobArgs a, int s
         p = join(p, Part{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
                          __shfl_xor_sync(0xffffffffu, p.t, o)});
       if constexpr (kTop) {
+        // (the warps' lists are merged: their memory takes the CTAs')
+        auto s_all = reinterpret_cast<unsigned long long(*)[32]>(&s_list[0][0]);
+        static_assert(kLpMaxSplit * 32 <= kLpWarps * kLpCap, "the CTAs' lists must fit");
         for (int i = 0; i < split; ++i) {
           if (lane < k) {
             unsigned long long v;
@@ -339,37 +432,35 @@ __global__ void __launch_bounds__(kLpThreads, 2) k_logprobs(LogprobArgs a, int s
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (part != 0) return;
   }
-  if (warp != 0) return;
-  const float m = __shfl_sync(0xffffffffu, p.m, 0), s = __shfl_sync(0xffffffffu, p.s, 0), t = __shfl_sync(0xffffffffu, p.t, 0);
-  // no distribution: nothing above -infinity (s 0), or a NaN or +infinity (s NaN)
-  const float ln_s = s == 0.f ? NAN : logf(s);
-  if (lane == 0) {
-    if (a.lse) a.lse[row] = s == 0.f ? -INFINITY : m + ln_s;
-    if (a.entropy) a.entropy[row] = ln_s - t / s;
-  }
-  for (int i = lane; i < a.n_tok; i += 32) {
-    const int tok = a.tokens[(long long)row * a.n_tok + i];
-    float v = NAN;
-    if (tok >= 0 && tok < V)
-      v = (E::load(x + tok) - m) - ln_s;
-    else if (a.err)
-      atomicOr(a.err, RL_DEVERR_TOKEN);
-    a.logprob[(long long)row * a.n_tok + i] = v;
-  }
-  if constexpr (kTop) {
-    if (lane < k) {
-      const int id = (int)(0xffffffffu - (uint32_t)s_top[lane]);
-      a.top_ids[(long long)row * k + lane] = id;
-      a.top_lp[(long long)row * k + lane] = (E::load(x + id) - m) - ln_s;
+  if (warp == 0) {
+    const float m = __shfl_sync(0xffffffffu, p.m, 0), s = __shfl_sync(0xffffffffu, p.s, 0);
+    // no distribution: nothing above -infinity (s 0), or a NaN or +infinity (s NaN)
+    const float ln_s = s == 0.f ? NAN : logf(s);
+    if (lane == 0) {
+      s_res[0] = m;
+      s_res[1] = ln_s;
+      if (a.lse) a.lse[row] = s == 0.f ? -INFINITY : m + ln_s;
+      if (a.entropy) a.entropy[row] = ln_s - p.t / s;
     }
+    if constexpr (kTop) {
+      if (lane < k) {
+        const unsigned long long key = s_top[lane];
+        a.top_ids[(long long)row * k + lane] = (int)(0xffffffffu - (uint32_t)key);
+        a.top_lp[(long long)row * k + lane] = (value_of(key) - m) - ln_s;
+      }
+    }
+  }
+  if (a.n_tok > 0) {
+    __syncthreads();
+    if (tid < a.n_tok) a.logprob[(long long)row * a.n_tok + tid] = (tokv - s_res[0]) - s_res[1];
   }
 }
 
-// CTAs a row is split over: one while the rows fill the GPU's resident CTAs
-// (two a SM); else as many as keep them busy, not below one tile each.
+// CTAs a row is split over: one while the rows fill the GPU's resident CTAs;
+// else as many as do, not below one tile a warp.
 int pick_split(int rows, long long vecs, int sm_count) {
   int s = 1;
-  while (s < kLpMaxSplit && rows * s * 2 <= 2 * sm_count && vecs > (long long)s * kLpThreads * kLpVecs) s *= 2;
+  while (s < kLpMaxSplit && rows * s * 2 <= kLpResident * sm_count && vecs > (long long)s * kLpWarps * kLpTile) s *= 2;
   return s;
 }
 
@@ -387,7 +478,8 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
     static bool done[kOpDevices] = {};
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kLpRing);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
@@ -396,6 +488,7 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.rows * split);
   cfg.blockDim = dim3(kLpThreads);
+  cfg.dynamicSmemBytes = kLpRing;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -5,8 +5,7 @@
 // For a query row at position p:  out = sum_j w_j v_j / sum_j w_j with
 // w_j = exp(scale q.k_j - m) over the keys j it sees and m their largest
 // score;  lse = m + ln sum_j w_j.  Running maximum and sum, one pass.
-//
-// Simplest form: one warp per (sequence, query row, head), one key at a time.
+// Few query rows go to attn_decode.cu, many to attn_rows_tc.cu.
 #include <float.h>
 #include <math.h>
 #include <stdio.h>
@@ -16,50 +15,24 @@
 
 namespace river {
 
-namespace {
-
-using namespace dev;
 using namespace attn;
-
-template <int HD, bool F16>
-__global__ void __launch_bounds__(128) k_attn_rows(AttnOpArgs a) {
-  const long long row = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-  const int lane = threadIdx.x & 31;
-  if (row >= (long long)a.B * a.Tq * a.Hq) return;
-  const int h = (int)(row % a.Hq), t = (int)(row / a.Hq % a.Tq), b = (int)(row / a.Hq / a.Tq);
-  const bool report = lane == 0 && h == 0 && t == 0;
-  const int n = seq_len(a, b, report), ql = query_len(a, b, report);
-  if (t >= ql) return;
-  const int hk = h / (a.Hq / a.Hkv);
-  RowAcc<HD, F16> r;
-  r.load_q(a, b, t, h, lane);
-  if (a.P > 0) r.keys(a.pre, 0, hk, 0, a.P, a.scale, lane);
-  r.window(a, b, t, hk, n, ql, lane);
-  r.store(a, b, t, h, lane);
-}
-
-template <int HD, bool F16>
-cudaError_t launch_rows(const AttnOpArgs& a, cudaStream_t s) {
-  const long long rows = (long long)a.B * a.Tq * a.Hq;
-  k_attn_rows<HD, F16><<<(unsigned)((rows + 3) / 4), 128, 0, s>>>(a);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
-  if (a.hd == 64) return a.f16 ? launch_rows<64, true>(a, s) : launch_rows<64, false>(a, s);
-  return a.f16 ? launch_rows<128, true>(a, s) : launch_rows<128, false>(a, s);
-}
-
-}  // namespace
 
 cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s) {
   if (a.Tq * (a.Hq / a.Hkv) <= 64) return launch_attn_decode(a, false, s);
-  return launch_any(a, s);
+  return launch_attn_rows_tc(a, false, s);
 }
 
 size_t shared_prefix_ws_bytes(int B, int Hq, int hd) { return (size_t)B * Hq * ws_entry(hd) * sizeof(float); }
 
-cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s) { return launch_any(a, s); }
+// The prefix for all rows first, then each sequence's own keys; the second
+// kernel starts beside the first and takes the prefix's part at its end.
+cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s) {
+  if (a.P > 0) {
+    const cudaError_t e = launch_attn_rows_tc(a, true, s);
+    if (e != cudaSuccess) return e;
+  }
+  return launch_attn_decode(a, false, s);
+}
 
 }  // namespace river
 

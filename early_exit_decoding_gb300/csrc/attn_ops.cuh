@@ -172,5 +172,8 @@ __host__ __device__ constexpr int ws_entry(int hd) { return hd + 4; }
 
 // Few query rows against long key ranges (attn_decode.cu).
 cudaError_t launch_attn_decode(const AttnOpArgs& a, bool pdl, cudaStream_t s);
+// Many query rows on the tensor cores (attn_rows_tc.cu): a prompt's window, or
+// (prefix) every sequence's rows against a.pre into a.ws.
+cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s);
 
 }  // namespace river

@@ -1,0 +1,568 @@
+// Many query rows against one key range on the 5th-generation tensor cores:
+// prompts under a sliding window, and the rows of all sequences against a
+// shared prefix.
+//
+// A CTA takes 256 query rows (query position x the heads that share a KV
+// head; for a prefix, sequence x those heads) as two M = 128 tiles and walks
+// the keys any of them sees in tiles of 128:
+//   S = Q K^T          tcgen05.mma, Q and K in shared memory, S in TMEM
+//   w = exp2(S - m)    one thread a row; w rounded to the cache's type, in TMEM over S
+//   O += w V           tcgen05.mma, w from TMEM, V as it lies ([key][dim]: the
+//                      N-major operand), O in TMEM
+// The two tiles share every K and V tile in shared memory (one alone would
+// need 128 bytes a clock from L2 at full tensor rate) and alternate: while
+// one's rows are in the softmax the other's products run.
+//   warps 0-3, 4-7  softmax of tile 0 and 1      warp 8  TMA (K, V in turn)
+//   warp 9          MMA issue
+// The running maximum follows lazily: O and the sum are rescaled only when a
+// row's maximum grew by more than 2^8 since the last time (weights then stay
+// below 2^8, far inside both types; the sum is fp32), so most tiles touch O
+// with the tensor core alone.
+//
+// Keys are dealt out over a cluster of S CTAs when the row tiles alone do not
+// fill the GPU; its CTAs join their (maximum, sum, O) through distributed
+// shared memory in a fixed order.
+#include <mutex>
+
+#include "attn_ops.cuh"
+
+namespace river {
+
+namespace {
+
+using namespace dev;
+using namespace attn;
+
+constexpr int kThreads = 320;
+constexpr int kRowsCta = 256;
+constexpr int kKeys = 128;       // keys of a tile
+constexpr int kMaxSplit = 16;
+constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.f;     // log2 growth of a maximum that is let pass
+
+template <int HD>
+constexpr int kTileBytes = kKeys * HD * 2;  // a Q, K or V tile: HD / 64 blocks of 128 rows x 128 bytes
+template <int HD>
+constexpr int kStages = HD == 128 ? 4 : 8;
+template <int HD>
+constexpr int kSmem = (2 + kStages<HD>)*kTileBytes<HD> + 1024;
+
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+  // rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart, 128-byte swizzle
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr) {
+  // 64 elements of N a row (128 bytes), the next 64 one block (128 rows) on,
+  // 8 rows of K 1024 bytes apart, 128-byte swizzle
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((kKeys * 128) >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// kind::f16, fp32 accumulate, M = 128.
+__host__ __device__ constexpr uint32_t idesc(bool f16, int n, bool b_n_major) {
+  return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(128 >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(id), "r"(acc)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define RL_R8(r, i) "=f"(r[i]), "=f"(r[i + 1]), "=f"(r[i + 2]), "=f"(r[i + 3]), "=f"(r[i + 4]), "=f"(r[i + 5]), "=f"(r[i + 6]), "=f"(r[i + 7])
+#define RL_I8(r, i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
+// 32 consecutive fp32 columns of this thread's lane (complete after ld_wait).
+__device__ __forceinline__ void tmem_ld32(uint32_t at, float* r) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : RL_R8(r, 0), RL_R8(r, 8), RL_R8(r, 16), RL_R8(r, 24)
+      : "r"(at));
+}
+// Waits for this thread's TMEM loads; the values pass through, so that no use
+// of them moves ahead of the wait.
+template <int N>
+__device__ __forceinline__ void ld_wait(float* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+f"(r[i]));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+      "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(at),
+      RL_I8(r, 0), RL_I8(r, 8), RL_I8(r, 16), RL_I8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+struct Bars {
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], full[8], empty[8], drain;
+};
+
+template <int HD, bool F16, bool PREFIX>
+__global__ void __launch_bounds__(kThreads, 1)
+    k_attn_rows_tc(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnOpArgs a, int split, int tiles) {
+  constexpr int NST = kStages<HD>, TB = kTileBytes<HD>;
+  extern __shared__ unsigned char smem_dyn[];
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~(uintptr_t)1023);
+  unsigned char* sq = smem;            // [2] Q tiles
+  unsigned char* ring = smem + 2 * TB; // K_0, V_0, K_1, V_1, ...
+  __shared__ __align__(8) Bars bar;
+  __shared__ uint32_t s_tmem;
+  __shared__ volatile int s_fail;
+  __shared__ float s_m[kRowsCta], s_l[kRowsCta];  // a row's maximum (log2 units) and sum
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int part = blockIdx.x % split, rep = a.Hq / a.Hkv;
+  int id = blockIdx.x / split;
+  // later tiles of a prompt see more keys: first come, first served from the end
+  const int row0 = (tiles - 1 - id / (PREFIX ? a.Hkv : a.Hkv * a.B)) * kRowsCta;
+  id %= PREFIX ? a.Hkv : a.Hkv * a.B;
+  const int hk = id % a.Hkv, b = PREFIX ? 0 : id / a.Hkv;
+  int n, ql, nrow, p0 = 0, lo = 0, hi, sink_end = 0;
+  if constexpr (PREFIX) {
+    n = hi = a.P;
+    ql = a.B;
+    nrow = min(kRowsCta, a.B * rep - row0);
+  } else {
+    const bool report = part == 0 && tid == 0 && hk == 0 && row0 == 0;
+    n = seq_len(a, b, report);
+    ql = query_len(a, b, report);
+    nrow = max(0, min(kRowsCta, ql * rep - row0));
+    // keys any row sees: [0, sink_end) and [lo, hi)
+    p0 = max(n - ql + row0 / rep, 0);
+    const int p1 = nrow ? n - ql + (row0 + nrow - 1) / rep : -1;
+    hi = max(p1 + 1, 0);
+    if (hi > 0) lo = max(0, p0 - a.window + 1);
+    sink_end = min(a.sinks, lo);
+    if (sink_end == lo) lo = sink_end = 0;
+  }
+  const int su = (sink_end + kKeys - 1) / kKeys;
+  const int all = su + (hi - lo + kKeys - 1) / kKeys;
+  const int j0 = (int)((long long)all * part / split), nt = (int)((long long)all * (part + 1) / split) - j0;
+  auto key0 = [&](int j) { return j < su ? j * kKeys : lo + (j - su) * kKeys; };
+  auto count = [&](int j) { return min(kKeys, (j < su ? sink_end : hi) - key0(j)); };
+  const int ngrp = nrow > 128 ? 2 : 1;
+
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 128);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.o_full[i], 1);
+    }
+    for (int i = 0; i < NST; ++i) {
+      mbar_init(&bar.full[i], 1);
+      mbar_init(&bar.empty[i], 1);
+    }
+    mbar_init(&bar.drain, 1);
+    s_fail = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = s_tmem;
+  // false: gave up (this wait or another's); nobody computes any more
+  auto wait = [&](uint64_t* w, uint32_t ph) {
+    if (mbar_try(w, ph)) return true;
+    unsigned long long t0, t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+    for (;;) {
+      for (int i = 0; i < 64; ++i)
+        if (mbar_try(w, ph)) return true;
+      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+      if (s_fail || t - t0 > kWaitNs) {
+        s_fail = 1;
+        return false;
+      }
+    }
+  };
+  const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + 128};
+
+  if (warp == 8) {
+    if (lane == 0) {
+      int i = 0;
+      bool go = true;
+      for (; i < 2 * nt && go; ++i) {
+        const int st = i % NST;
+        if (i >= NST && !wait(&bar.empty[st], ((i / NST) - 1) & 1)) {
+          go = false;
+          break;
+        }
+        mbar_expect_tx(&bar.full[st], TB);
+        const int j = key0(j0 + (i >> 1));
+        if (i & 1)
+          tma_load_5d(ring + st * TB, &maps.v, j, hk * maps.vh, b * maps.vb, &bar.full[st]);
+        else
+          tma_load_5d(ring + st * TB, &maps.k, j, hk * maps.kh, b * maps.kb, &bar.full[st]);
+      }
+      if (!go || s_fail)  // the copies in flight still land before anybody leaves
+        for (int q = max(0, i - NST); q < i; ++q) mbar_wait_for(&bar.full[q % NST], (q / NST) & 1, kWaitNs);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    if (lane == 0 && nt > 0) {
+      constexpr uint32_t idS = idesc(F16, kKeys, false), idO = idesc(F16, HD, true);
+      auto scores = [&](int g, int j) {  // S_g = Q_g K_j^T
+        const uint32_t q = smem_u32(sq + g * TB), k = smem_u32(ring + (2 * j % NST) * TB);
+#pragma unroll
+        for (int ks = 0; ks < HD / 16; ++ks) {
+          const uint32_t off = (ks >> 2) * (kKeys * 128) + (ks & 3) * 32;
+          mma_ss(tS[g], desc_k_major(q + off), desc_k_major(k + off), idS, ks != 0);
+        }
+        commit(&bar.s_full[g]);
+      };
+      auto values = [&](int g, int j) {  // O_g += w_g V_j
+        const uint32_t v = smem_u32(ring + ((2 * j + 1) % NST) * TB);
+#pragma unroll
+        for (int ks = 0; ks < kKeys / 16; ++ks)
+          mma_ts(tO[g], tS[g] + ks * 8, desc_n_major(v + ks * 2048), idO, j != 0 || ks != 0);
+      };
+      bool go = wait(&bar.full[0], 0);
+      for (int g = 0; g < ngrp && go; ++g) {
+        go = wait(&bar.q_full[g], 0);
+        if (!go) break;
+        fence_after();
+        scores(g, 0);
+      }
+      if (go) commit(&bar.empty[0]);
+      for (int j = 0; j < nt && go; ++j) {
+        const int iv = 2 * j + 1, ik = 2 * j + 2;
+        if (!(go = wait(&bar.full[iv % NST], (iv / NST) & 1))) break;
+        for (int g = 0; g < ngrp; ++g) {
+          if (!(go = wait(&bar.p_full[g], j & 1))) break;
+          fence_after();
+          values(g, j);
+          if (g == ngrp - 1) commit(&bar.empty[iv % NST]);
+          if (j + 1 < nt) {
+            if (g == 0 && !(go = wait(&bar.full[ik % NST], (ik / NST) & 1))) break;
+            scores(g, j + 1);
+            if (g == ngrp - 1) commit(&bar.empty[ik % NST]);
+          } else {
+            commit(&bar.o_full[g]);
+          }
+        }
+      }
+      if (!go) {  // what was issued still completes before TMEM is given back
+        commit(&bar.drain);
+        mbar_wait_for(&bar.drain, 0, kWaitNs);
+      }
+    }
+    __syncwarp();
+  }
+
+  const int g = warp >> 2, r = tid & 127;  // softmax: tile and row
+  float m = -INFINITY, l = 0.f;            // m in units of raw scores
+  const float sc = a.scale * kLog2e;
+  const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
+  const int i_row = row0 + g * 128 + r;    // (query, head in group)
+  if (warp < 8 && g < ngrp && nt > 0) {
+    // Q rows to shared memory as the TMA would lay them; rows past the last are 0
+    for (int it = tid & 127; it < 128 * (HD / 8); it += 128) {
+      const int qr = it / (HD / 8), ch = it % (HD / 8), i = row0 + g * 128 + qr;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (g * 128 + qr < nrow) {
+        const int t = i / rep;
+        const long long at = (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)t * a.qs[1]) +
+                             (long long)(hk * rep + i % rep) * a.qs[2] + ch * 8;
+        if (a.q_f32) {
+          const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+          const float4 x = f[0], y = f[1];
+          v = make_uint4(pack2<F16>(x.x, x.y), pack2<F16>(x.z, x.w), pack2<F16>(y.x, y.y), pack2<F16>(y.z, y.w));
+        } else {
+          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+        }
+      }
+      *reinterpret_cast<uint4*>(sq + g * TB + (ch >> 3) * (128 * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = v;
+    }
+    fence_proxy_async_smem();
+    mbar_arrive(&bar.q_full[g]);
+
+    const int p = PREFIX ? 0 : n - ql + i_row / rep;  // this row's position
+    // positions of the tile's first and last row that count
+    const int pa = PREFIX ? 0 : max(n - ql + (row0 + g * 128) / rep, 0);
+    const int pz = PREFIX ? 0 : n - ql + (row0 + min(nrow, g * 128 + 128) - 1) / rep;
+    bool go = true;
+    for (int j = 0; j < nt; ++j) {
+      const int k0 = key0(j0 + j), cnt = count(j0 + j);
+      if (!(go = wait(&bar.s_full[g], j & 1))) break;
+      fence_after();
+      float s[kKeys];
+#pragma unroll
+      for (int c = 0; c < kKeys; c += 32) tmem_ld32(tS[g] + lane_at + c, s + c);
+      ld_wait<kKeys>(s);
+      if (PREFIX) {
+        if (cnt < kKeys) {
+#pragma unroll
+          for (int c = 0; c < kKeys; ++c)
+            if (c >= cnt) s[c] = -INFINITY;
+        }
+      } else if (cnt < kKeys || k0 + kKeys - 1 > pa || (pz - k0 >= a.window && k0 + kKeys > a.sinks)) {
+        // keys this row sees: below `end`, and from `beg` on or below `snk`
+        const int end = min(cnt, p - k0 + 1), beg = p - a.window + 1 - k0, snk = a.sinks - k0;
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+          if (c >= end || (c < beg && c >= snk)) s[c] = -INFINITY;
+      }
+      float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kKeys; ++c) x[c & 3] = fmaxf(x[c & 3], s[c]);
+      const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      if (__any_sync(0xffffffffu, mx * sc > m * sc + kLazy || (m == -INFINITY && mx > m))) {
+        const float mn = fmaxf(m, mx);
+        const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
+        l *= f;
+        m = mn;
+        if (j > 0) {
+          // the products of the tiles before are complete (S_j was issued after them)
+#pragma unroll
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            uint32_t u[32];
+            tmem_ld32(tO[g] + lane_at + c, o);
+            ld_wait<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+            tmem_st32(tO[g] + lane_at + c, u);
+          }
+        }
+      }
+      const float ms = m == -INFINITY ? 0.f : m * sc;
+      float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float u = ex2(fmaf(s[h * 64 + 2 * c], sc, -ms)), v = ex2(fmaf(s[h * 64 + 2 * c + 1], sc, -ms));
+          y[(2 * c) & 3] += u;
+          y[(2 * c + 1) & 3] += v;
+          w[c] = pack2<F16>(u, v);
+        }
+        tmem_st32(tS[g] + lane_at + h * 32, w);
+      }
+      l += (y[0] + y[1]) + (y[2] + y[3]);
+      if (cnt < kKeys) {
+        // V rows behind the range may hold anything: 0 * NaN must not happen
+        const int iv = 2 * j + 1;
+        if (!(go = wait(&bar.full[iv % NST], (iv / NST) & 1))) break;
+        unsigned char* sv = ring + (iv % NST) * TB;
+        for (int it = tid & 127; it < (kKeys - cnt) * (HD / 8); it += 128) {
+          const int kr = cnt + it / (HD / 8), ch = it % (HD / 8);
+          *reinterpret_cast<uint4*>(sv + (ch >> 3) * (kKeys * 128) + kr * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+      }
+      st_wait();
+      fence_before();
+      mbar_arrive(&bar.p_full[g]);
+    }
+    // (the last tile's: the ring, which the other tile's products still read,
+    // is written over below)
+    if (go) go = wait(&bar.o_full[PREFIX || split > 1 ? ngrp - 1 : g], 0);
+    fence_after();
+    if (!go) l = NAN;
+  }
+  auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
+  const bool direct = !PREFIX && split == 1;
+  if (warp < 8) {
+    const bool mine = g * 128 + r < nrow;
+    const bool have = g < ngrp && nt > 0;
+    if (direct) {
+      const int t = i_row / rep, h = hk * rep + i_row % rep;
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      bool fin = true;
+      uint16_t* dst = static_cast<uint16_t*>(a.out) + (mine ? b * a.os[0] + t * a.os[1] + h * a.os[2] : 0);
+#pragma unroll
+      for (int c = 0; c < HD; c += 32) {
+        float o[32];
+        if (have) {
+          tmem_ld32(tO[g] + lane_at + c, o);
+          ld_wait<32>(o);
+        }
+#pragma unroll
+        for (int e = 0; e < 32; e += 8) {
+          uint32_t w[4];
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const float u = have ? o[e + 2 * q] * inv : 0.f, v = have ? o[e + 2 * q + 1] * inv : 0.f;
+            // (a row that sees no key has l 0; its O may hold anything)
+            const float u0 = l == 0.f ? 0.f : u, v0 = l == 0.f ? 0.f : v;
+            fin = fin && isfinite(u0) && isfinite(v0);
+            w[q] = pack2<F16>(u0, v0);
+          }
+          if (mine) *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      if (mine && a.lse)
+        a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
+      // rows of different masks shared V's tiles: one that is not finite may
+      // owe that to a key it does not see (0 * infinity)
+      unsigned bad = __ballot_sync(0xffffffffu, mine && !fin);
+      if (s_fail) bad = 0;
+      while (bad) {
+        const int i = row0 + g * 128 + (warp & 3) * 32 + __ffs(bad) - 1;
+        bad &= bad - 1;
+        exact_row<HD, F16>(a, b, i / rep, hk * rep + i % rep, n, ql, lane);
+      }
+    } else {
+      // to shared memory over the drained ring: rows of HD floats, 16-byte
+      // chunk c of row q at c ^ (q mod chunks)
+      constexpr int CH = HD / 4;
+      s_m[g * 128 + r] = have && l != 0.f ? m * sc : -INFINITY;
+      s_l[g * 128 + r] = l;
+      if (have) {
+        float4* dst = reinterpret_cast<float4*>(ring) + (g * 128 + r) * CH;
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          tmem_ld32(tO[g] + lane_at + c, o);
+          ld_wait<32>(o);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) dst[((c + e) / 4) ^ (r & (CH - 1))] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+        }
+      }
+    }
+  }
+  if (!direct) {
+    if (split > 1)
+      cluster_barrier();
+    else
+      __syncthreads();
+    constexpr int CH = HD / 4;
+    // one row a warp, dealt out over the cluster's warps 0 .. 7; lane has the
+    // 16-byte chunk `lane` (HD 64: the lower 16 lanes)
+    for (int q = part * 8 + warp; warp < 8 && q < nrow; q += split * 8) {
+      float cm = -INFINITY, cl = 0.f;
+      if (lane < split) {
+        cm = cluster_ld(cluster_addr(&s_m[q], lane));
+        cl = cluster_ld(cluster_addr(&s_l[q], lane));
+      }
+      const float top = warp_max(cm), f = weight(cm, top);
+      const float sum = warp_sum(cm == -INFINITY ? cl : f * cl);
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+      const int c = lane & (CH - 1);
+      for (int k = 0; k < split; ++k) {
+        const float fk = __shfl_sync(0xffffffffu, f, k);
+        if (fk == 0.f) continue;
+        const uint32_t src = cluster_addr(reinterpret_cast<float4*>(ring) + q * CH + (c ^ (q & (CH - 1))), k);
+        const float2 u = cluster_ld2(src), v = cluster_ld2(src + 8);
+        acc.x += fk * u.x;
+        acc.y += fk * u.y;
+        acc.z += fk * v.x;
+        acc.w += fk * v.y;
+      }
+      const int i = row0 + q, t = i / rep, h = hk * rep + i % rep;
+      if constexpr (PREFIX) {
+        float* e = static_cast<float*>(a.ws) + ((long long)t * a.Hq + h) * ws_entry(HD);
+        if (lane < CH) reinterpret_cast<float4*>(e)[c] = acc;
+        if (lane == 0) {
+          e[HD] = top;
+          e[HD + 1] = sum;
+        }
+      } else {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const bool fin = isfinite(acc.x * inv) && isfinite(acc.y * inv) && isfinite(acc.z * inv) && isfinite(acc.w * inv);
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2] + c * 4;
+        if (lane < CH)
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
+        if (lane == 0 && a.lse)
+          a.lse[((long long)b * a.Tq + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        if (!__all_sync(0xffffffffu, fin) && !s_fail) exact_row<HD, F16>(a, b, t, h, n, ql, lane);
+      }
+    }
+    if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
+  }
+  fence_before();
+  __syncthreads();
+  if (tid == 0 && s_fail && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
+  if (warp == 9) {
+    fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
+  }
+}
+
+template <int HD, bool F16, bool PREFIX>
+cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = device_sm_count(dev, &sms);
+  if (e != cudaSuccess) return e;
+  auto kern = k_attn_rows_tc<HD, F16, PREFIX>;
+  {
+    static std::mutex mu;
+    static bool done[kOpDevices] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<HD>);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+  }
+  KvMaps maps;
+  const bool got = PREFIX ? make_kv_maps(&maps, a.pre, a.f16 != 0, 1, a.Hkv, HD, a.P, kKeys)
+                          : make_kv_maps(&maps, a.kv, a.f16 != 0, a.B, a.Hkv, HD, a.cap, kKeys);
+  if (!got) return cudaErrorInvalidValue;
+  const int rep = a.Hq / a.Hkv;
+  const long long rows = (long long)(PREFIX ? a.B : a.Tq) * rep;
+  const int tiles = (int)((rows + kRowsCta - 1) / kRowsCta);
+  const long long ctas = (long long)tiles * a.Hkv * (PREFIX ? 1 : a.B);
+  // Splits of the keys: as many as fill the SMs (one CTA each), no CTA below one tile.
+  const long long keys = PREFIX ? a.P : min((long long)a.cap, (long long)a.window + min(a.Tq, kRowsCta / rep + 2) + a.sinks);
+  int split = 1;
+  while (split < kMaxSplit && ctas * split * 2 <= sms && (keys + kKeys - 1) / kKeys >= split * 2) split *= 2;
+  if (ctas * split >= (1ll << 31)) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(ctas * split));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem<HD>;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, split, tiles);
+}
+
+template <bool PREFIX>
+cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
+  if (a.hd == 64) return a.f16 ? launch<64, true, PREFIX>(a, s) : launch<64, false, PREFIX>(a, s);
+  return a.f16 ? launch<128, true, PREFIX>(a, s) : launch<128, false, PREFIX>(a, s);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s) {
+  return prefix ? launch_any<true>(a, s) : launch_any<false>(a, s);
+}
+
+}  // namespace river

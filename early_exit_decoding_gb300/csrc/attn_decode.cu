@@ -33,7 +33,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 16;        // keys a warp takes at a time
 constexpr int kRows = 16;        // query rows of a tile
 constexpr int kMaxSplit = 16;    // CTAs of a cluster
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr int kSpin = 1 << 21;  // polls of a wait (each may suspend) before it gives up
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int HD>
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   // copies already in flight are still waited for (`stop`).
   int st = 0, ph = 0, stop = units;
   for (int u = first; u < stop; u += W) {
-    const bool got = mbar_wait_for(&full[warp][st], ph, kWaitNs);
+    const bool got = mbar_wait(&full[warp][st], ph, kSpin);
     if (!__all_sync(0xffffffffu, got) && ok) {
       ok = false;
       stop = min(units, u + NST * W);
@@ -329,15 +329,24 @@ __global__ void __launch_bounds__(kThreads, 2)
         acc[i2] = make_float2(fp * v.x, fp * v.y);
       }
     }
-    for (int c = 0; c < split; ++c) {
-      const float fc = __shfl_sync(0xffffffffu, f, c);
-      if (fc == 0.f) continue;
-      const uint32_t src = cluster_addr(reinterpret_cast<float*>(smem) + r * HD + 2 * lane, c);
+    const uint32_t own = smem_u32(reinterpret_cast<float*>(smem) + r * HD + 2 * lane);
+    for (int c0 = 0; c0 < split; c0 += 4) {  // four CTAs' loads in flight together
+      float2 v[4][HD / 64];
 #pragma unroll
-      for (int i2 = 0; i2 < HD / 64; ++i2) {
-        const float2 v = cluster_ld2(src + 256 * i2);
-        acc[i2].x += fc * v.x;
-        acc[i2].y += fc * v.y;
+      for (int c = 0; c < 4; ++c) {
+        const uint32_t src = cluster_map(own, min(c0 + c, split - 1));
+#pragma unroll
+        for (int i2 = 0; i2 < HD / 64; ++i2) v[c][i2] = cluster_ld2(src + 256 * i2);
+      }
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        const float fc = __shfl_sync(0xffffffffu, f, c0 + c);
+        if (c0 + c >= split || fc == 0.f) continue;
+#pragma unroll
+        for (int i2 = 0; i2 < HD / 64; ++i2) {
+          acc[i2].x += fc * v[c][i2].x;
+          acc[i2].y += fc * v[c][i2].y;
+        }
       }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;

@@ -13,7 +13,11 @@
 // need 128 bytes a clock from L2 at full tensor rate) and alternate: while
 // one's rows are in the softmax the other's products run.
 //   warps 0-3, 4-7  softmax of tile 0 and 1      warp 8  TMA (K, V in turn)
-//   warp 9          MMA issue
+//   warp 9          MMA issue                    warps 10, 11  idle
+// A softmax thread holds its row's 128 scores in registers: of the 168 a
+// thread the launch has, the control warps give most to them (216 + 216 + 72
+// = 3 x 168; with 168 they spilled, and with 200 KB of shared memory in use
+// spills go to L2: a tile took 5900 clocks).
 // The running maximum follows lazily: O and the sum are rescaled only when a
 // row's maximum grew by more than 2^8 since the last time (weights then stay
 // below 2^8, far inside both types; the sum is fp32), so most tiles touch O
@@ -33,11 +37,11 @@ namespace {
 using namespace dev;
 using namespace attn;
 
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
 constexpr int kRowsCta = 256;
 constexpr int kKeys = 128;       // keys of a tile
 constexpr int kMaxSplit = 16;
-constexpr unsigned long long kWaitNs = 2000000000ull;
+constexpr int kSpin = 1 << 21;   // polls of a wait (each may suspend) before it gives up
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;     // log2 growth of a maximum that is let pass
 
@@ -111,6 +115,15 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
       : "memory");
 }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Bits 0 .. n - 1.
+__device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
+// Scores whose bit is 0 become -infinity (selects on bits: as 128 conditions
+// they were branches, 6000 to 11000 clocks a masked tile).
+__device__ __forceinline__ void keep_only(float* s, uint32_t bits) {
+#pragma unroll
+  for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? s[e] : -INFINITY;
+}
 
 struct Bars {
   uint64_t q_full[2], s_full[2], p_full[2], o_full[2], full[8], empty[8], drain;
@@ -188,21 +201,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = s_tmem;
   // false: gave up (this wait or another's); nobody computes any more
   auto wait = [&](uint64_t* w, uint32_t ph) {
-    if (mbar_try(w, ph)) return true;
-    unsigned long long t0, t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
-    for (;;) {
-      for (int i = 0; i < 64; ++i)
-        if (mbar_try(w, ph)) return true;
-      asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-      if (s_fail || t - t0 > kWaitNs) {
-        s_fail = 1;
-        return false;
-      }
+    // (counted, not timed: a read of %globaltimer costs near a thousand clocks)
+    for (int i = 0; i < kSpin; ++i) {
+      if (mbar_try(w, ph)) return true;
+      if ((i & 1023) == 1023 && s_fail) return false;
     }
+    s_fail = 1;
+    return false;
   };
-  const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + 128};
+  auto wait_warp = [&](uint64_t* w, uint32_t ph) { return __all_sync(0xffffffffu, wait(w, ph)) != 0; };
+  // TMEM columns: S_0, S_1 (their weights over them), O_0, O_1
+  auto t_s = [tmem](int g) { return tmem + g * 128; };
+  auto t_o = [tmem](int g) { return tmem + 256 + g * 128; };
 
+  if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 8) {
     if (lane == 0) {
       int i = 0;
@@ -221,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_5d(ring + st * TB, &maps.k, j, hk * maps.kh, b * maps.kb, &bar.full[st]);
       }
       if (!go || s_fail)  // the copies in flight still land before anybody leaves
-        for (int q = max(0, i - NST); q < i; ++q) mbar_wait_for(&bar.full[q % NST], (q / NST) & 1, kWaitNs);
+        for (int q = max(0, i - NST); q < i; ++q) mbar_wait(&bar.full[q % NST], (q / NST) & 1, kSpin);
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -232,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
           const uint32_t off = (ks >> 2) * (kKeys * 128) + (ks & 3) * 32;
-          mma_ss(tS[g], desc_k_major(q + off), desc_k_major(k + off), idS, ks != 0);
+          mma_ss(t_s(g), desc_k_major(q + off), desc_k_major(k + off), idS, ks != 0);
         }
         commit(&bar.s_full[g]);
       };
@@ -240,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t v = smem_u32(ring + ((2 * j + 1) % NST) * TB);
 #pragma unroll
         for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_ts(tO[g], tS[g] + ks * 8, desc_n_major(v + ks * 2048), idO, j != 0 || ks != 0);
+          mma_ts(t_o(g), t_s(g) + ks * 8, desc_n_major(v + ks * 2048), idO, j != 0 || ks != 0);
       };
       bool go = wait(&bar.full[0], 0);
       for (int g = 0; g < ngrp && go; ++g) {
@@ -269,234 +281,266 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!go) {  // what was issued still completes before TMEM is given back
         commit(&bar.drain);
-        mbar_wait_for(&bar.drain, 0, kWaitNs);
+        mbar_wait(&bar.drain, 0, kSpin);
       }
     }
     __syncwarp();
   }
 
-  const int g = warp >> 2, r = tid & 127;  // softmax: tile and row
-  float m = -INFINITY, l = 0.f;            // m in units of raw scores
-  const float sc = a.scale * kLog2e;
-  const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
-  const int i_row = row0 + g * 128 + r;    // (query, head in group)
-  if (warp < 8 && g < ngrp && nt > 0) {
-    // Q rows to shared memory as the TMA would lay them; rows past the last are 0
-    for (int it = tid & 127; it < 128 * (HD / 8); it += 128) {
-      const int qr = it / (HD / 8), ch = it % (HD / 8), i = row0 + g * 128 + qr;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (g * 128 + qr < nrow) {
-        const int t = i / rep;
-        const long long at = (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)t * a.qs[1]) +
-                             (long long)(hk * rep + i % rep) * a.qs[2] + ch * 8;
-        if (a.q_f32) {
-          const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-          const float4 x = f[0], y = f[1];
-          v = make_uint4(pack2<F16>(x.x, x.y), pack2<F16>(x.z, x.w), pack2<F16>(y.x, y.y), pack2<F16>(y.z, y.w));
-        } else {
-          v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
-        }
-      }
-      *reinterpret_cast<uint4*>(sq + g * TB + (ch >> 3) * (128 * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = v;
-    }
-    fence_proxy_async_smem();
-    mbar_arrive(&bar.q_full[g]);
-
-    const int p = PREFIX ? 0 : n - ql + i_row / rep;  // this row's position
-    // positions of the tile's first and last row that count
-    const int pa = PREFIX ? 0 : max(n - ql + (row0 + g * 128) / rep, 0);
-    const int pz = PREFIX ? 0 : n - ql + (row0 + min(nrow, g * 128 + 128) - 1) / rep;
-    bool go = true;
-    for (int j = 0; j < nt; ++j) {
-      const int k0 = key0(j0 + j), cnt = count(j0 + j);
-      if (!(go = wait(&bar.s_full[g], j & 1))) break;
-      fence_after();
-      float s[kKeys];
-#pragma unroll
-      for (int c = 0; c < kKeys; c += 32) tmem_ld32(tS[g] + lane_at + c, s + c);
-      ld_wait<kKeys>(s);
-      if (PREFIX) {
-        if (cnt < kKeys) {
-#pragma unroll
-          for (int c = 0; c < kKeys; ++c)
-            if (c >= cnt) s[c] = -INFINITY;
-        }
-      } else if (cnt < kKeys || k0 + kKeys - 1 > pa || (pz - k0 >= a.window && k0 + kKeys > a.sinks)) {
-        // keys this row sees: below `end`, and from `beg` on or below `snk`
-        const int end = min(cnt, p - k0 + 1), beg = p - a.window + 1 - k0, snk = a.sinks - k0;
-#pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-          if (c >= end || (c < beg && c >= snk)) s[c] = -INFINITY;
-      }
-      float x[4] = {s[0], s[1], s[2], s[3]};
-#pragma unroll
-      for (int c = 4; c < kKeys; ++c) x[c & 3] = fmaxf(x[c & 3], s[c]);
-      const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
-      if (__any_sync(0xffffffffu, mx * sc > m * sc + kLazy || (m == -INFINITY && mx > m))) {
-        const float mn = fmaxf(m, mx);
-        const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
-        l *= f;
-        m = mn;
-        if (j > 0) {
-          // the products of the tiles before are complete (S_j was issued after them)
-#pragma unroll
-          for (int c = 0; c < HD; c += 32) {
-            float o[32];
-            uint32_t u[32];
-            tmem_ld32(tO[g] + lane_at + c, o);
-            ld_wait<32>(o);
-#pragma unroll
-            for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
-            tmem_st32(tO[g] + lane_at + c, u);
-          }
-        }
-      }
-      const float ms = m == -INFINITY ? 0.f : m * sc;
-      float y[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w[32];
-#pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float u = ex2(fmaf(s[h * 64 + 2 * c], sc, -ms)), v = ex2(fmaf(s[h * 64 + 2 * c + 1], sc, -ms));
-          y[(2 * c) & 3] += u;
-          y[(2 * c + 1) & 3] += v;
-          w[c] = pack2<F16>(u, v);
-        }
-        tmem_st32(tS[g] + lane_at + h * 32, w);
-      }
-      l += (y[0] + y[1]) + (y[2] + y[3]);
-      if (cnt < kKeys) {
-        // V rows behind the range may hold anything: 0 * NaN must not happen
-        const int iv = 2 * j + 1;
-        if (!(go = wait(&bar.full[iv % NST], (iv / NST) & 1))) break;
-        unsigned char* sv = ring + (iv % NST) * TB;
-        for (int it = tid & 127; it < (kKeys - cnt) * (HD / 8); it += 128) {
-          const int kr = cnt + it / (HD / 8), ch = it % (HD / 8);
-          *reinterpret_cast<uint4*>(sv + (ch >> 3) * (kKeys * 128) + kr * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-      }
-      st_wait();
-      fence_before();
-      mbar_arrive(&bar.p_full[g]);
-    }
-    // (the last tile's: the ring, which the other tile's products still read,
-    // is written over below)
-    if (go) go = wait(&bar.o_full[PREFIX || split > 1 ? ngrp - 1 : g], 0);
-    fence_after();
-    if (!go) l = NAN;
-  }
-  auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
-  const bool direct = !PREFIX && split == 1;
-  if (warp < 8) {
-    const bool mine = g * 128 + r < nrow;
-    const bool have = g < ngrp && nt > 0;
-    if (direct) {
-      const int t = i_row / rep, h = hk * rep + i_row % rep;
-      const float inv = l == 0.f ? 0.f : 1.f / l;
-      bool fin = true;
-      uint16_t* dst = static_cast<uint16_t*>(a.out) + (mine ? b * a.os[0] + t * a.os[1] + h * a.os[2] : 0);
-#pragma unroll
-      for (int c = 0; c < HD; c += 32) {
-        float o[32];
-        if (have) {
-          tmem_ld32(tO[g] + lane_at + c, o);
-          ld_wait<32>(o);
-        }
-#pragma unroll
-        for (int e = 0; e < 32; e += 8) {
-          uint32_t w[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const float u = have ? o[e + 2 * q] * inv : 0.f, v = have ? o[e + 2 * q + 1] * inv : 0.f;
-            // (a row that sees no key has l 0; its O may hold anything)
-            const float u0 = l == 0.f ? 0.f : u, v0 = l == 0.f ? 0.f : v;
-            fin = fin && isfinite(u0) && isfinite(v0);
-            w[q] = pack2<F16>(u0, v0);
-          }
-          if (mine) *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-      }
-      if (mine && a.lse)
-        a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
-      // rows of different masks shared V's tiles: one that is not finite may
-      // owe that to a key it does not see (0 * infinity)
-      unsigned bad = __ballot_sync(0xffffffffu, mine && !fin);
-      if (s_fail) bad = 0;
-      while (bad) {
-        const int i = row0 + g * 128 + (warp & 3) * 32 + __ffs(bad) - 1;
-        bad &= bad - 1;
-        exact_row<HD, F16>(a, b, i / rep, hk * rep + i % rep, n, ql, lane);
-      }
-    } else {
-      // to shared memory over the drained ring: rows of HD floats, 16-byte
-      // chunk c of row q at c ^ (q mod chunks)
-      constexpr int CH = HD / 4;
-      s_m[g * 128 + r] = have && l != 0.f ? m * sc : -INFINITY;
-      s_l[g * 128 + r] = l;
-      if (have) {
-        float4* dst = reinterpret_cast<float4*>(ring) + (g * 128 + r) * CH;
-#pragma unroll
-        for (int c = 0; c < HD; c += 32) {
-          float o[32];
-          tmem_ld32(tO[g] + lane_at + c, o);
-          ld_wait<32>(o);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) dst[((c + e) / 4) ^ (r & (CH - 1))] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
-        }
-      }
-    }
-  }
-  if (!direct) {
+  const bool direct = !PREFIX && split == 1;  // a CTA has all keys of its rows
+  // every warp of the cluster (of the CTA, if it is alone)
+  auto meet = [&]() {
     if (split > 1)
       cluster_barrier();
     else
-      __syncthreads();
-    constexpr int CH = HD / 4;
-    // one row a warp, dealt out over the cluster's warps 0 .. 7; lane has the
-    // 16-byte chunk `lane` (HD 64: the lower 16 lanes)
-    for (int q = part * 8 + warp; warp < 8 && q < nrow; q += split * 8) {
-      float cm = -INFINITY, cl = 0.f;
-      if (lane < split) {
-        cm = cluster_ld(cluster_addr(&s_m[q], lane));
-        cl = cluster_ld(cluster_addr(&s_l[q], lane));
+      named_sync(1, kThreads);
+  };
+  if (warp >= 8) {
+    if (!direct) {
+      meet();
+      if (split > 1) cluster_barrier();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int g = warp >> 2, r = tid & 127;  // softmax: tile and row
+    float m = -INFINITY, l = 0.f;            // m in units of raw scores
+    const float sc = a.scale * kLog2e;
+    const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = t_s(g & 1), to = t_o(g & 1);
+    const int i_row = row0 + g * 128 + r;    // (query, head in group)
+    if (g < ngrp && nt > 0) {
+      // Q rows to shared memory as the TMA would lay them; rows past the last are 0
+      // (all loads of a batch in flight before its first store)
+      constexpr int BATCH = HD / 8;
+      for (int it0 = 0; it0 < HD / 8; it0 += BATCH) {
+        uint4 v[BATCH];
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+          const int it = (it0 + e) * 128 + r, qr = it / (HD / 8), ch = it % (HD / 8), i = row0 + g * 128 + qr;
+          v[e] = make_uint4(0, 0, 0, 0);
+          if (g * 128 + qr < nrow) {
+            const int t = i / rep;
+            const long long at = (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)t * a.qs[1]) +
+                                 (long long)(hk * rep + i % rep) * a.qs[2] + ch * 8;
+            if (a.q_f32) {
+              const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+              const float4 x = f[0], y = f[1];
+              v[e] = make_uint4(pack2<F16>(x.x, x.y), pack2<F16>(x.z, x.w), pack2<F16>(y.x, y.y), pack2<F16>(y.z, y.w));
+            } else {
+              v[e] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
+            }
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < BATCH; ++e) {
+          const int it = (it0 + e) * 128 + r, qr = it / (HD / 8), ch = it % (HD / 8);
+          *reinterpret_cast<uint4*>(sq + g * TB + (ch >> 3) * (128 * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = v[e];
+        }
       }
-      const float top = warp_max(cm), f = weight(cm, top);
-      const float sum = warp_sum(cm == -INFINITY ? cl : f * cl);
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      const int c = lane & (CH - 1);
-      for (int k = 0; k < split; ++k) {
-        const float fk = __shfl_sync(0xffffffffu, f, k);
-        if (fk == 0.f) continue;
-        const uint32_t src = cluster_addr(reinterpret_cast<float4*>(ring) + q * CH + (c ^ (q & (CH - 1))), k);
-        const float2 u = cluster_ld2(src), v = cluster_ld2(src + 8);
-        acc.x += fk * u.x;
-        acc.y += fk * u.y;
-        acc.z += fk * v.x;
-        acc.w += fk * v.y;
+      fence_proxy_async_smem();
+      mbar_arrive(&bar.q_full[g]);
+
+      const int p = PREFIX ? 0 : n - ql + i_row / rep;  // this row's position
+      // positions of the tile's first and last row that count
+      const int pa = PREFIX ? 0 : max(n - ql + (row0 + g * 128) / rep, 0);
+      const int pz = PREFIX ? 0 : n - ql + (row0 + min(nrow, g * 128 + 128) - 1) / rep;
+      bool go = true;
+      for (int j = 0; j < nt; ++j) {
+        const int k0 = key0(j0 + j), cnt = count(j0 + j);
+        if (!(go = wait_warp(&bar.s_full[g], j & 1))) break;
+        fence_after();
+        float s[kKeys];
+#pragma unroll
+        for (int c = 0; c < kKeys; c += 32) tmem_ld32(ts + lane_at + c, s + c);
+        ld_wait<kKeys>(s);
+        if (PREFIX) {
+          if (cnt < kKeys) {
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32) keep_only(s + c, below(cnt - c));
+          }
+        } else if (cnt < kKeys || k0 + kKeys - 1 > pa || (pz - k0 >= a.window && k0 + kKeys > a.sinks)) {
+          // keys this row sees: below `end`, and from `beg` on or below `snk`
+          const int end = min(cnt, p - k0 + 1), beg = p - a.window + 1 - k0, snk = a.sinks - k0;
+#pragma unroll
+          for (int c = 0; c < kKeys; c += 32)
+            keep_only(s + c, below(end - c) & (~below(beg - c) | below(snk - c)));
+        }
+        float x[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int c = 4; c < kKeys; ++c) x[c & 3] = fmaxf(x[c & 3], s[c]);
+        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        if (__any_sync(0xffffffffu, mx * sc > m * sc + kLazy || (m == -INFINITY && mx > m))) {
+          const float mn = fmaxf(m, mx);
+          const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
+          l *= f;
+          m = mn;
+          if (j > 0) {
+            // the products of the tiles before are complete (S_j was issued after them)
+#pragma unroll
+            for (int c = 0; c < HD; c += 32) {
+              float o[32];
+              uint32_t u[32];
+              tmem_ld32(to + lane_at + c, o);
+              ld_wait<32>(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) u[e] = __float_as_uint(o[e] * f);
+              tmem_st32(to + lane_at + c, u);
+            }
+          }
+        }
+        const float ms = m == -INFINITY ? 0.f : m * sc;
+        float y[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const float u = ex2(fmaf(s[h * 64 + 2 * c], sc, -ms)), v = ex2(fmaf(s[h * 64 + 2 * c + 1], sc, -ms));
+            y[(2 * c) & 3] += u;
+            y[(2 * c + 1) & 3] += v;
+            w[c] = pack2<F16>(u, v);
+          }
+          tmem_st32(ts + lane_at + h * 32, w);
+        }
+        l += (y[0] + y[1]) + (y[2] + y[3]);
+        if (cnt < kKeys) {
+          // V rows behind the range may hold anything: 0 * NaN must not happen
+          const int iv = 2 * j + 1;
+          if (!(go = wait_warp(&bar.full[iv % NST], (iv / NST) & 1))) break;
+          unsigned char* sv = ring + (iv % NST) * TB;
+          for (int it = tid & 127; it < (kKeys - cnt) * (HD / 8); it += 128) {
+            const int kr = cnt + it / (HD / 8), ch = it % (HD / 8);
+            *reinterpret_cast<uint4*>(sv + (ch >> 3) * (kKeys * 128) + kr * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          fence_proxy_async_smem();
+        }
+        st_wait();
+        fence_before();
+        mbar_arrive(&bar.p_full[g]);
       }
-      const int i = row0 + q, t = i / rep, h = hk * rep + i % rep;
-      if constexpr (PREFIX) {
-        float* e = static_cast<float*>(a.ws) + ((long long)t * a.Hq + h) * ws_entry(HD);
-        if (lane < CH) reinterpret_cast<float4*>(e)[c] = acc;
-        if (lane == 0) {
-          e[HD] = top;
-          e[HD + 1] = sum;
+      // (the last tile's: the ring, which the other tile's products still read,
+      // is written over below)
+      if (go) go = wait_warp(&bar.o_full[PREFIX || split > 1 ? ngrp - 1 : g], 0);
+      fence_after();
+      if (!go) l = NAN;
+    }
+    auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
+    {
+      const bool mine = g * 128 + r < nrow;
+      const bool have = g < ngrp && nt > 0;
+      if (direct) {
+        const int t = i_row / rep, h = hk * rep + i_row % rep;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        bool fin = true;
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + (mine ? b * a.os[0] + t * a.os[1] + h * a.os[2] : 0);
+#pragma unroll
+        for (int c = 0; c < HD; c += 32) {
+          float o[32];
+          if (have) {
+            tmem_ld32(to + lane_at + c, o);
+            ld_wait<32>(o);
+          }
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            uint32_t w[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float u = have ? o[e + 2 * q] * inv : 0.f, v = have ? o[e + 2 * q + 1] * inv : 0.f;
+              // (a row that sees no key has l 0; its O may hold anything)
+              const float u0 = l == 0.f ? 0.f : u, v0 = l == 0.f ? 0.f : v;
+              fin = fin && isfinite(u0) && isfinite(v0);
+              w[q] = pack2<F16>(u0, v0);
+            }
+            if (mine) *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+        if (mine && a.lse)
+          a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
+        // rows of different masks shared V's tiles: one that is not finite may
+        // owe that to a key it does not see (0 * infinity)
+        unsigned bad = __ballot_sync(0xffffffffu, mine && !fin);
+        if (s_fail) bad = 0;
+        while (bad) {
+          const int i = row0 + g * 128 + (warp & 3) * 32 + __ffs(bad) - 1;
+          bad &= bad - 1;
+          exact_row<HD, F16>(a, b, i / rep, hk * rep + i % rep, n, ql, lane);
         }
       } else {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const bool fin = isfinite(acc.x * inv) && isfinite(acc.y * inv) && isfinite(acc.z * inv) && isfinite(acc.w * inv);
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2] + c * 4;
-        if (lane < CH)
-          *reinterpret_cast<uint2*>(dst) =
-              make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
-        if (lane == 0 && a.lse)
-          a.lse[((long long)b * a.Tq + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-        if (!__all_sync(0xffffffffu, fin) && !s_fail) exact_row<HD, F16>(a, b, t, h, n, ql, lane);
+        // to shared memory over the drained ring: rows of HD floats, 16-byte
+        // chunk c of row q at c ^ (q mod chunks)
+        constexpr int CH = HD / 4;
+        s_m[g * 128 + r] = have && l != 0.f ? m * sc : -INFINITY;
+        s_l[g * 128 + r] = l;
+        if (have) {
+          float4* dst = reinterpret_cast<float4*>(ring) + (g * 128 + r) * CH;
+#pragma unroll
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            tmem_ld32(to + lane_at + c, o);
+            ld_wait<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) dst[((c + e) / 4) ^ (r & (CH - 1))] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+        }
       }
     }
-    if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
+    if (!direct) {
+      meet();
+      constexpr int CH = HD / 4;
+      // one row a warp, dealt out over the cluster's warps 0 .. 7; lane has the
+      // 16-byte chunk `lane` (HD 64: the lower 16 lanes)
+      for (int q = part * 8 + warp; q < nrow; q += split * 8) {
+        float cm = -INFINITY, cl = 0.f;
+        if (lane < split) {
+          cm = cluster_ld(cluster_addr(&s_m[q], lane));
+          cl = cluster_ld(cluster_addr(&s_l[q], lane));
+        }
+        const float top = warp_max(cm), f = weight(cm, top);
+        const float sum = warp_sum(cm == -INFINITY ? cl : f * cl);
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int c = lane & (CH - 1);
+        const uint32_t own = smem_u32(reinterpret_cast<float4*>(ring) + q * CH + (c ^ (q & (CH - 1))));
+        for (int k0 = 0; k0 < split; k0 += 4) {  // four CTAs' loads in flight together
+          float2 u[4], v[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t src = cluster_map(own, min(k0 + k, split - 1));
+            u[k] = cluster_ld2(src);
+            v[k] = cluster_ld2(src + 8);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
+            if (k0 + k < split && fk != 0.f) {  // (a CTA without keys has written no O)
+              acc.x += fk * u[k].x;
+              acc.y += fk * u[k].y;
+              acc.z += fk * v[k].x;
+              acc.w += fk * v[k].y;
+            }
+          }
+        }
+        const int i = row0 + q, t = i / rep, h = hk * rep + i % rep;
+        if constexpr (PREFIX) {
+          float* e = static_cast<float*>(a.ws) + ((long long)t * a.Hq + h) * ws_entry(HD);
+          if (lane < CH) reinterpret_cast<float4*>(e)[c] = acc;
+          if (lane == 0) {
+            e[HD] = top;
+            e[HD + 1] = sum;
+          }
+        } else {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const bool fin = isfinite(acc.x * inv) && isfinite(acc.y * inv) && isfinite(acc.z * inv) && isfinite(acc.w * inv);
+          uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2] + c * 4;
+          if (lane < CH)
+            *reinterpret_cast<uint2*>(dst) =
+                make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
+          if (lane == 0 && a.lse)
+            a.lse[((long long)b * a.Tq + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+          if (!__all_sync(0xffffffffu, fin) && !s_fail) exact_row<HD, F16>(a, b, t, h, n, ql, lane);
+        }
+      }
+      if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
+    }
   }
   fence_before();
   __syncthreads();

@@ -70,7 +70,8 @@ __device__ __forceinline__ uint32_t load_q2(const AttnOpArgs& a, const Tile& t, 
 
 template <int HD, bool F16>
 __global__ void __launch_bounds__(kThreads, 2)
-    k_attn_decode(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnOpArgs a, int split, int tiles) {
+    k_attn_decode(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnOpArgs a, int split, int tiles,
+                  int presplit) {
   constexpr int NST = kStages<HD>, SB = kStageBytes<HD>;
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* smem =
@@ -309,24 +310,50 @@ __global__ void __launch_bounds__(kThreads, 2)
   for (int r = part * kWarps + warp; r < nrow; r += W) {
     const int i = t.row0 + r, tq = i / t.rep, h = t.hk * t.rep + i % t.rep;
     if (tq >= t.ql) continue;
-    const float* pre = a.P > 0 ? static_cast<const float*>(a.ws) + ((long long)t.b * a.Hq + h) * ws_entry(HD) : nullptr;
-    float cm = -INFINITY, cl = 0.f;
+    float cm = -INFINITY, cl = 0.f, pm = -INFINITY, pl = 0.f;
     if (lane < split) {
       cm = cluster_ld(cluster_addr(&c_m[r], lane));
       cl = cluster_ld(cluster_addr(&c_l[r], lane));
     }
-    float pm = pre ? pre[HD] : -INFINITY;
-    const float top = fmaxf(warp_max(cm), pm);
+    PrefixWs ws;
+    int pq = 0;
+    if (a.P > 0) {
+      const int pi = t.b * t.rep + i % t.rep, ptiles = (a.B * t.rep + 255) / 256;
+      pq = pi & 255;
+      ws = prefix_ws(a.ws, pi >> 8, ptiles, a.B * t.rep, t.hk, a.Hkv, 0, presplit, HD);
+      if (lane < presplit) {
+        const long long at = (long long)lane * 2 * prefix_rows(ptiles, a.B * t.rep) + pq;
+        pm = ws.m[at];
+        pl = ws.l[at];
+      }
+    }
+    const float top = warp_max(fmaxf(cm, pm));
     const float f = weight(cm, top), fp = weight(pm, top);
-    float l = warp_sum(cm == -INFINITY ? cl : f * cl);
-    if (pre) l += fp * pre[HD + 1];
+    const float l = warp_sum((cm == -INFINITY ? cl : f * cl) + (pm == -INFINITY ? pl : fp * pl));
     float2 acc[HD / 64];
 #pragma unroll
-    for (int i2 = 0; i2 < HD / 64; ++i2) {
-      acc[i2] = make_float2(0.f, 0.f);
-      if (pre && fp != 0.f) {
-        const float2 v = *reinterpret_cast<const float2*>(pre + 2 * lane + 64 * i2);
-        acc[i2] = make_float2(fp * v.x, fp * v.y);
+    for (int i2 = 0; i2 < HD / 64; ++i2) acc[i2] = make_float2(0.f, 0.f);
+    if (a.P > 0) {
+      const long long step = (long long)prefix_rows((a.B * t.rep + 255) / 256, a.B * t.rep) * HD;
+      const float* src = ws.o + pq * HD + (((2 * lane) >> 2) ^ (pq & (HD / 4 - 1) & 15)) * 4 + (2 * lane & 3);
+      for (int c0 = 0; c0 < presplit; c0 += 4) {  // four parts' loads in flight together
+        float2 v[4][HD / 64];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i2 = 0; i2 < HD / 64; ++i2)
+            v[c][i2] = *reinterpret_cast<const float2*>(src + min(c0 + c, presplit - 1) * step +
+                                                        (HD == 128 ? 64 * (i2 ^ ((pq >> 4) & 1)) : 0));
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const float fc = __shfl_sync(0xffffffffu, fp, (c0 + c) & 31);
+          if (c0 + c >= presplit || fc == 0.f) continue;
+#pragma unroll
+          for (int i2 = 0; i2 < HD / 64; ++i2) {
+            acc[i2].x += fc * v[c][i2].x;
+            acc[i2].y += fc * v[c][i2].y;
+          }
+        }
       }
     }
     const uint32_t own = smem_u32(reinterpret_cast<float*>(smem) + r * HD + 2 * lane);
@@ -398,6 +425,7 @@ cudaError_t launch(const AttnOpArgs& a, bool pdl, cudaStream_t s) {
   if (!make_kv_maps(&maps, a.kv, a.f16 != 0, a.B, a.Hkv, HD, a.cap, kUnit)) return cudaErrorInvalidValue;
   const int tiles = (a.Tq * (a.Hq / a.Hkv) + kRows - 1) / kRows;
   const long long all = (long long)a.B * a.Hkv * tiles;
+  const int presplit = a.P > 0 ? prefix_split(a.B, a.Hq / a.Hkv, a.Hkv, a.P) : 0;
   const int split = pick_split(all, (int)min((long long)a.cap, (long long)a.window + a.Tq + a.sinks), sms);
   if (all * split >= (1ll << 31)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
@@ -414,7 +442,7 @@ cudaError_t launch(const AttnOpArgs& a, bool pdl, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, a, split, tiles);
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, split, tiles, presplit);
 }
 
 }  // namespace

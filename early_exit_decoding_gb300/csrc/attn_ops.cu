@@ -22,7 +22,7 @@ cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s) {
   return launch_attn_rows_tc(a, false, s);
 }
 
-size_t shared_prefix_ws_bytes(int B, int Hq, int hd) { return (size_t)B * Hq * ws_entry(hd) * sizeof(float); }
+size_t shared_prefix_ws_bytes(int B, int Hq, int Hkv, int hd, int P) { return prefix_ws_bytes(B, Hq / Hkv, Hkv, hd, P); }
 
 // The prefix for all rows first, then each sequence's own keys; the second
 // kernel starts beside the first and takes the prefix's part at its end.
@@ -132,7 +132,7 @@ extern "C" rl_status rl_shared_prefix_workspace(const rl_attn_desc* a, int32_t p
   if (st != RL_OK) return st;
   if (!bytes || prefix_len < 0)
     return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_workspace: bytes is NULL or prefix_len below 0");
-  *bytes = shared_prefix_ws_bytes(o.B, o.Hq, o.hd);
+  *bytes = shared_prefix_ws_bytes(o.B, o.Hq, o.Hkv, o.hd, prefix_len);
   return RL_OK;
 }
 
@@ -156,7 +156,7 @@ extern "C" rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const voi
                      "rl_shared_prefix_attention: q, k, v, out and the workspace must start on 16-byte boundaries");
   if (d_out == d_q || d_out == d_k || d_out == d_v)
     return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: out overlaps an input");
-  if (ws_bytes < shared_prefix_ws_bytes(o.B, o.Hq, o.hd))
+  if (ws_bytes < shared_prefix_ws_bytes(o.B, o.Hq, o.Hkv, o.hd, prefix_len))
     return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: workspace too small");
   if (prefix_len > 0) {
     if (!aligned16(d_k_prefix) || !aligned16(d_v_prefix) || !strides_ok(prefix_stride, 4, 2, 1ll << 39))

@@ -165,9 +165,36 @@ __device__ __forceinline__ float2 cluster_ld2(uint32_t at) {
   return v;
 }
 
-// Floats of one (sequence, head)'s entry of the shared-prefix workspace: the
-// prefix's sum of weighted values, the largest score (log2 units) and the sum of weights.
-__host__ __device__ constexpr int ws_entry(int hd) { return hd + 4; }
+__device__ __forceinline__ float4 cluster_ld4(uint32_t at) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(at)
+               : "memory");
+  return v;
+}
+
+// Shared memory to global, a multiple of 16 bytes, in the issuing thread's bulk group.
+__device__ __forceinline__ void bulk_s2g(void* dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(dev::smem_u32(src)), "r"(bytes)
+               : "memory");
+}
+
+// The shared-prefix workspace: for every (tile of 256 rows, KV head, split of
+// the prefix) the rows' sums of weighted values (16-byte chunk c of row q at
+// c ^ (q mod chunks)), then for all of them the rows' largest scores (log2
+// units; -infinity: no keys) and sums of weights.
+__host__ __device__ inline int prefix_rows(int tiles, long long rows) { return tiles > 1 ? 256 : (int)((rows + 31) / 32 * 32); }
+struct PrefixWs {
+  float *o, *m, *l;
+};
+__device__ __forceinline__ PrefixWs prefix_ws(void* ws, int tile, int tiles, int rows, int hk, int Hkv, int part, int split,
+                                              int hd) {
+  const long long R = prefix_rows(tiles, rows), e = ((long long)tile * Hkv + hk) * split + part;
+  float* base = static_cast<float*>(ws);
+  float* ml = base + (long long)tiles * Hkv * split * R * hd;
+  return PrefixWs{base + e * R * hd, ml + e * 2 * R, ml + (e * 2 + 1) * R};
+}
 
 }  // namespace attn
 
@@ -176,5 +203,8 @@ cudaError_t launch_attn_decode(const AttnOpArgs& a, bool pdl, cudaStream_t s);
 // Many query rows on the tensor cores (attn_rows_tc.cu): a prompt's window, or
 // (prefix) every sequence's rows against a.pre into a.ws.
 cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s);
+constexpr int kMaxPrefixSplit = 32;
+int prefix_split(int B, int rep, int Hkv, int P);
+size_t prefix_ws_bytes(int B, int rep, int Hkv, int hd, int P);
 
 }  // namespace river

@@ -40,7 +40,7 @@ using namespace attn;
 constexpr int kThreads = 384;
 constexpr int kRowsCta = 256;
 constexpr int kKeys = 128;       // keys of a tile
-constexpr int kMaxSplit = 16;
+constexpr int kMaxSplit = 8;     // CTAs of a cluster (of 16, no more than 7 clusters fit the SMs at once)
 constexpr int kSpin = 1 << 21;   // polls of a wait (each may suspend) before it gives up
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;     // log2 growth of a maximum that is let pass
@@ -52,39 +52,46 @@ constexpr int kStages = HD == 128 ? 4 : 8;
 template <int HD>
 constexpr int kSmem = (2 + kStages<HD>)*kTileBytes<HD> + 1024;
 
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
-  // rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart, 128-byte swizzle
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-__device__ __forceinline__ uint64_t desc_n_major(uint32_t addr) {
-  // 64 elements of N a row (128 bytes), the next 64 one block (128 rows) on,
-  // 8 rows of K 1024 bytes apart, 128-byte swizzle
-  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)((kKeys * 128) >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-         ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory matrix descriptors, 128-byte swizzle: the low word holds the
+// address / 16 (and the leading byte offset), the high word is constant.
+//   K-major (Q, K): rows of 128 bytes, 8-row swizzle atoms 1024 bytes apart.
+//   N-major (V): 64 elements of N a row, the next 64 one block (128 rows) on,
+//   8 rows of K 1024 bytes apart.
+constexpr uint32_t kDescHi = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t addr) { return ((addr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t desc_n_major(uint32_t addr) {
+  return ((addr & 0x3FFFFu) >> 4) | ((uint32_t)((kKeys * 128) >> 4) << 16);
 }
 // kind::f16, fp32 accumulate, M = 128.
 __host__ __device__ constexpr uint32_t idesc(bool f16, int n, bool b_n_major) {
   return (1u << 4) | (f16 ? 0u : (1u << 7) | (1u << 10)) | (b_n_major ? 1u << 16 : 0u) | ((uint32_t)(n >> 3) << 17) |
          ((uint32_t)(128 >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t id, uint32_t acc) {
+// Every lane calls these with the same operands and the one with `el` != 0
+// issues: a single lane's branch would move each operand to the uniform
+// registers anew (32 MMAs a tile pair then cost more issue time than tensor time).
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t el) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, e;\n .reg .b64 x, y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " mov.b64 x, {%1, %6};\n mov.b64 y, {%2, %6};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(el), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t id, uint32_t acc) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t id, uint32_t acc, uint32_t el) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(id), "r"(acc)
+      "{\n .reg .pred p, e;\n .reg .b64 y;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+      " mov.b64 y, {%2, %6};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(id), "r"(acc), "r"(el), "r"(kDescHi)
       : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-               : "memory");
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t el) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(smem_u32(bar)),
+      "r"(el)
+      : "memory");
 }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -125,8 +132,30 @@ __device__ __forceinline__ void keep_only(float* s, uint32_t bits) {
   for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? s[e] : -INFINITY;
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 struct Bars {
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], full[8], empty[8], drain;
+  uint64_t s_full[2], p_full[2], o_full[2], full[8], empty[8], drain;
 };
 
 template <int HD, bool F16, bool PREFIX>
@@ -175,25 +204,63 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto count = [&](int j) { return min(kKeys, (j < su ? sink_end : hi) - key0(j)); };
   const int ngrp = nrow > 128 ? 2 : 1;
 
-  if (tid == 0) {
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&bar.q_full[i], 128);
-      mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 128);
-      mbar_init(&bar.o_full[i], 1);
+  auto load = [&](int i) {  // K (i even) or V tile i / 2 into its stage
+    const int st = i % NST, j = key0(j0 + (i >> 1));
+    mbar_expect_tx(&bar.full[st], TB);
+    if (i & 1)
+      tma_load_5d(ring + st * TB, &maps.v, j, hk * maps.vh, b * maps.vb, &bar.full[st]);
+    else
+      tma_load_5d(ring + st * TB, &maps.k, j, hk * maps.kh, b * maps.kb, &bar.full[st]);
+  };
+  if (warp == 8) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&bar.s_full[i], 1);
+        mbar_init(&bar.p_full[i], 128);
+        mbar_init(&bar.o_full[i], 1);
+      }
+      for (int i = 0; i < NST; ++i) {
+        mbar_init(&bar.full[i], 1);
+        mbar_init(&bar.empty[i], 1);
+      }
+      mbar_init(&bar.drain, 1);
+      s_fail = 0;
+      asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+      if (nt > 0) load(0);  // (the others after Q's rows, which the first scores need too)
     }
-    for (int i = 0; i < NST; ++i) {
-      mbar_init(&bar.full[i], 1);
-      mbar_init(&bar.empty[i], 1);
-    }
-    mbar_init(&bar.drain, 1);
-    s_fail = 0;
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  if (warp == 9) {
+    __syncwarp();
+  } else if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  } else if (warp < 8 && warp / 4 < ngrp && nt > 0) {
+    // Q rows to shared memory as the TMA would lay them; rows past the last are 0
+    const int g = warp / 4, r = tid & 127;
+    auto at = [&](int e) {  // 16-byte chunk e * 128 + r of the tile: its place in q
+      const int it = e * 128 + r, i = row0 + min(g * 128 + it / (HD / 8), nrow - 1), t = i / rep;
+      return (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)t * a.qs[1]) +
+             (long long)(hk * rep + i - t * rep) * a.qs[2] + it % (HD / 8) * 8;
+    };
+    auto put = [&](int e, uint4 v) {
+      const int it = e * 128 + r, qr = it / (HD / 8), ch = it % (HD / 8);
+      if (g * 128 + qr >= nrow) v = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(sq + g * TB + (ch >> 3) * (128 * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = v;
+    };
+    if (a.q_f32) {
+#pragma unroll 2
+      for (int e = 0; e < HD / 8; ++e) {
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at(e));
+        const float4 x = __ldg(f), y = __ldg(f + 1);
+        put(e, make_uint4(pack2<F16>(x.x, x.y), pack2<F16>(x.z, x.w), pack2<F16>(y.x, y.y), pack2<F16>(y.z, y.w)));
+      }
+    } else {
+      uint4 v[HD / 8];  // all loads in flight before the first store
+#pragma unroll
+      for (int e = 0; e < HD / 8; ++e) v[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at(e)));
+#pragma unroll
+      for (int e = 0; e < HD / 8; ++e) put(e, v[e]);
+    }
+    fence_proxy_async_smem();
   }
   fence_before();
   __syncthreads();
@@ -217,77 +284,76 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp >= 8) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 8) {
     if (lane == 0) {
-      int i = 0;
+      int i = 1;
       bool go = true;
-      for (; i < 2 * nt && go; ++i) {
-        const int st = i % NST;
-        if (i >= NST && !wait(&bar.empty[st], ((i / NST) - 1) & 1)) {
-          go = false;
-          break;
-        }
-        mbar_expect_tx(&bar.full[st], TB);
-        const int j = key0(j0 + (i >> 1));
-        if (i & 1)
-          tma_load_5d(ring + st * TB, &maps.v, j, hk * maps.vh, b * maps.vb, &bar.full[st]);
-        else
-          tma_load_5d(ring + st * TB, &maps.k, j, hk * maps.kh, b * maps.kb, &bar.full[st]);
+      for (; i < 2 * nt; ++i) {
+        if (i >= NST && !(go = wait(&bar.empty[i % NST], ((i / NST) - 1) & 1))) break;
+        load(i);
       }
       if (!go || s_fail)  // the copies in flight still land before anybody leaves
         for (int q = max(0, i - NST); q < i; ++q) mbar_wait(&bar.full[q % NST], (q / NST) & 1, kSpin);
     }
     __syncwarp();
   } else if (warp == 9) {
-    if (lane == 0 && nt > 0) {
+    if (nt > 0) {
       constexpr uint32_t idS = idesc(F16, kKeys, false), idO = idesc(F16, HD, true);
+      const uint32_t el = lane == 0;
+      const uint32_t q0 = desc_k_major(smem_u32(sq)), k0 = desc_k_major(smem_u32(ring)), v0 = desc_n_major(smem_u32(ring));
       auto scores = [&](int g, int j) {  // S_g = Q_g K_j^T
-        const uint32_t q = smem_u32(sq + g * TB), k = smem_u32(ring + (2 * j % NST) * TB);
+        const uint32_t q = q0 + g * (TB >> 4), k = k0 + ((2 * j) % NST) * (TB >> 4);
 #pragma unroll
         for (int ks = 0; ks < HD / 16; ++ks) {
-          const uint32_t off = (ks >> 2) * (kKeys * 128) + (ks & 3) * 32;
-          mma_ss(t_s(g), desc_k_major(q + off), desc_k_major(k + off), idS, ks != 0);
+          const uint32_t off = (ks >> 2) * (kKeys * 128 >> 4) + (ks & 3) * 2;
+          mma_ss(t_s(g), q + off, k + off, idS, ks != 0, el);
         }
-        commit(&bar.s_full[g]);
+        commit(&bar.s_full[g], el);
       };
       auto values = [&](int g, int j) {  // O_g += w_g V_j
-        const uint32_t v = smem_u32(ring + ((2 * j + 1) % NST) * TB);
+        const uint32_t v = v0 + ((2 * j + 1) % NST) * (TB >> 4);
+        mma_ts(t_o(g), t_s(g), v, idO, j != 0, el);
 #pragma unroll
-        for (int ks = 0; ks < kKeys / 16; ++ks)
-          mma_ts(t_o(g), t_s(g) + ks * 8, desc_n_major(v + ks * 2048), idO, j != 0 || ks != 0);
+        for (int ks = 1; ks < kKeys / 16; ++ks) mma_ts(t_o(g), t_s(g) + ks * 8, v + ks * (2048 >> 4), idO, 1, el);
       };
-      bool go = wait(&bar.full[0], 0);
-      for (int g = 0; g < ngrp && go; ++g) {
-        go = wait(&bar.q_full[g], 0);
-        if (!go) break;
-        fence_after();
-        scores(g, 0);
+      bool go = wait_warp(&bar.full[0], 0);
+      if (go) {
+        scores(0, 0);
+        if (ngrp == 2) scores(1, 0);
+        commit(&bar.empty[0], el);
       }
-      if (go) commit(&bar.empty[0]);
       for (int j = 0; j < nt && go; ++j) {
         const int iv = 2 * j + 1, ik = 2 * j + 2;
-        if (!(go = wait(&bar.full[iv % NST], (iv / NST) & 1))) break;
-        for (int g = 0; g < ngrp; ++g) {
-          if (!(go = wait(&bar.p_full[g], j & 1))) break;
+        const bool more = j + 1 < nt;
+        if (!(go = wait_warp(&bar.full[iv % NST], (iv / NST) & 1))) break;
+        if (more && !(go = wait_warp(&bar.full[ik % NST], (ik / NST) & 1))) break;
+        if (!(go = wait_warp(&bar.p_full[0], j & 1))) break;
+        fence_after();
+        values(0, j);
+        if (more)
+          scores(0, j + 1);
+        else
+          commit(&bar.o_full[0], el);
+        if (ngrp == 2) {
+          if (!(go = wait_warp(&bar.p_full[1], j & 1))) break;
           fence_after();
-          values(g, j);
-          if (g == ngrp - 1) commit(&bar.empty[iv % NST]);
-          if (j + 1 < nt) {
-            if (g == 0 && !(go = wait(&bar.full[ik % NST], (ik / NST) & 1))) break;
-            scores(g, j + 1);
-            if (g == ngrp - 1) commit(&bar.empty[ik % NST]);
-          } else {
-            commit(&bar.o_full[g]);
-          }
+          values(1, j);
+        }
+        commit(&bar.empty[iv % NST], el);
+        if (more) {
+          if (ngrp == 2) scores(1, j + 1);
+          commit(&bar.empty[ik % NST], el);
+        } else if (ngrp == 2) {
+          commit(&bar.o_full[1], el);
         }
       }
       if (!go) {  // what was issued still completes before TMEM is given back
-        commit(&bar.drain);
+        commit(&bar.drain, el);
         mbar_wait(&bar.drain, 0, kSpin);
       }
     }
     __syncwarp();
   }
 
-  const bool direct = !PREFIX && split == 1;  // a CTA has all keys of its rows
+  const bool direct = PREFIX || split == 1;  // no other CTA's keys are joined here
   // every warp of the cluster (of the CTA, if it is alone)
   auto meet = [&]() {
     if (split > 1)
@@ -309,37 +375,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t ts = t_s(g & 1), to = t_o(g & 1);
     const int i_row = row0 + g * 128 + r;    // (query, head in group)
     if (g < ngrp && nt > 0) {
-      // Q rows to shared memory as the TMA would lay them; rows past the last are 0
-      // (all loads of a batch in flight before its first store)
-      constexpr int BATCH = HD / 8;
-      for (int it0 = 0; it0 < HD / 8; it0 += BATCH) {
-        uint4 v[BATCH];
-#pragma unroll
-        for (int e = 0; e < BATCH; ++e) {
-          const int it = (it0 + e) * 128 + r, qr = it / (HD / 8), ch = it % (HD / 8), i = row0 + g * 128 + qr;
-          v[e] = make_uint4(0, 0, 0, 0);
-          if (g * 128 + qr < nrow) {
-            const int t = i / rep;
-            const long long at = (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)t * a.qs[1]) +
-                                 (long long)(hk * rep + i % rep) * a.qs[2] + ch * 8;
-            if (a.q_f32) {
-              const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
-              const float4 x = f[0], y = f[1];
-              v[e] = make_uint4(pack2<F16>(x.x, x.y), pack2<F16>(x.z, x.w), pack2<F16>(y.x, y.y), pack2<F16>(y.z, y.w));
-            } else {
-              v[e] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at);
-            }
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < BATCH; ++e) {
-          const int it = (it0 + e) * 128 + r, qr = it / (HD / 8), ch = it % (HD / 8);
-          *reinterpret_cast<uint4*>(sq + g * TB + (ch >> 3) * (128 * 128) + qr * 128 + (((ch & 7) ^ (qr & 7)) << 4)) = v[e];
-        }
-      }
-      fence_proxy_async_smem();
-      mbar_arrive(&bar.q_full[g]);
-
       const int p = PREFIX ? 0 : n - ql + i_row / rep;  // this row's position
       // positions of the tile's first and last row that count
       const int pa = PREFIX ? 0 : max(n - ql + (row0 + g * 128) / rep, 0);
@@ -365,10 +400,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = 0; c < kKeys; c += 32)
             keep_only(s + c, below(end - c) & (~below(beg - c) | below(snk - c)));
         }
-        float x[4] = {s[0], s[1], s[2], s[3]};
+        float x[4];
 #pragma unroll
-        for (int c = 4; c < kKeys; ++c) x[c & 3] = fmaxf(x[c & 3], s[c]);
-        const float mx = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        for (int c = 0; c < 4; ++c) x[c] = max3(s[c], s[c + 4], s[c + 8]);
+#pragma unroll
+        for (int c = 12; c + 8 <= kKeys; c += 8)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = max3(x[e], s[c + e], s[c + 4 + e]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = fmaxf(x[e], s[kKeys - 4 + e]);
+        const float mx = fmaxf(max3(x[0], x[1], x[2]), x[3]);
         if (__any_sync(0xffffffffu, mx * sc > m * sc + kLazy || (m == -INFINITY && mx > m))) {
           const float mn = fmaxf(m, mx);
           const float f = m == -INFINITY ? 0.f : ex2((m - mn) * sc);
@@ -389,20 +430,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         const float ms = m == -INFINITY ? 0.f : m * sc;
-        float y[4] = {0.f, 0.f, 0.f, 0.f};
+        float2 y[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        const float2 sc2 = make_float2(sc, sc), ms2 = make_float2(-ms, -ms);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
-            const float u = ex2(fmaf(s[h * 64 + 2 * c], sc, -ms)), v = ex2(fmaf(s[h * 64 + 2 * c + 1], sc, -ms));
-            y[(2 * c) & 3] += u;
-            y[(2 * c + 1) & 3] += v;
-            w[c] = pack2<F16>(u, v);
+            float2 u = fma2(make_float2(s[h * 64 + 2 * c], s[h * 64 + 2 * c + 1]), sc2, ms2);
+            u.x = ex2(u.x);
+            u.y = ex2(u.y);
+            y[c & 1] = add2(y[c & 1], u);
+            w[c] = pack2<F16>(u.x, u.y);
           }
           tmem_st32(ts + lane_at + h * 32, w);
         }
-        l += (y[0] + y[1]) + (y[2] + y[3]);
+        const float2 yy = add2(y[0], y[1]);
+        l += yy.x + yy.y;
         if (cnt < kKeys) {
           // V rows behind the range may hold anything: 0 * NaN must not happen
           const int iv = 2 * j + 1;
@@ -420,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       // (the last tile's: the ring, which the other tile's products still read,
       // is written over below)
-      if (go) go = wait_warp(&bar.o_full[PREFIX || split > 1 ? ngrp - 1 : g], 0);
+      if (go) go = wait_warp(&bar.o_full[PREFIX || !direct ? ngrp - 1 : g], 0);
       fence_after();
       if (!go) l = NAN;
     }
@@ -428,7 +472,35 @@ __global__ void __launch_bounds__(kThreads, 1)
     {
       const bool mine = g * 128 + r < nrow;
       const bool have = g < ngrp && nt > 0;
-      if (direct) {
+      if constexpr (PREFIX) {
+        // O, maximum and sum of the CTA's keys to the workspace, 32 rows a warp:
+        // through shared memory over the drained ring (16-byte chunk c of row q
+        // at c ^ (q mod chunks), and so in the workspace) by one bulk copy
+        constexpr int CH = HD / 4;
+        const int q0 = g * 128 + (warp & 3) * 32, rows = min(32, nrow - q0);
+        if (have && rows > 0) {
+          float4* dst = reinterpret_cast<float4*>(ring) + (q0 + lane) * CH;
+#pragma unroll
+          for (int c = 0; c < HD; c += 32) {
+            float o[32];
+            tmem_ld32(to + lane_at + c, o);
+            ld_wait<32>(o);
+#pragma unroll
+            for (int e = 0; e < 32; e += 4) dst[((c + e) / 4) ^ (lane & (CH - 1))] = make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          const PrefixWs ws = prefix_ws(a.ws, row0 / kRowsCta, tiles, a.B * rep, hk, a.Hkv, part, split, HD);
+          if (lane == 0) {
+            bulk_s2g(ws.o + (long long)q0 * HD, ring + q0 * HD * 4, rows * HD * 4);
+            asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
+          }
+          if (lane < rows) {
+            ws.m[q0 + lane] = l == 0.f ? -INFINITY : m * sc;
+            ws.l[q0 + lane] = l;
+          }
+        }
+      } else if (direct) {
         const int t = i_row / rep, h = hk * rep + i_row % rep;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         bool fin = true;
@@ -500,44 +572,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         const int c = lane & (CH - 1);
         const uint32_t own = smem_u32(reinterpret_cast<float4*>(ring) + q * CH + (c ^ (q & (CH - 1))));
-        for (int k0 = 0; k0 < split; k0 += 4) {  // four CTAs' loads in flight together
-          float2 u[4], v[4];
+        // from the next CTA on (all starting at CTA 0 would queue there), eight
+        // CTAs' loads in flight; the order is the row's own, so results repeat
+        for (int k0 = 0; k0 < split; k0 += 8) {
+          float4 v[8];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const uint32_t src = cluster_map(own, min(k0 + k, split - 1));
-            u[k] = cluster_ld2(src);
-            v[k] = cluster_ld2(src + 8);
-          }
+          for (int k = 0; k < 8; ++k)
+            if (k0 + k < split) v[k] = cluster_ld4(cluster_map(own, (part + k0 + k) % split));
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, k0 + k);
+          for (int k = 0; k < 8; ++k) {
+            const float fk = __shfl_sync(0xffffffffu, f, (part + k0 + k) % split);
             if (k0 + k < split && fk != 0.f) {  // (a CTA without keys has written no O)
-              acc.x += fk * u[k].x;
-              acc.y += fk * u[k].y;
-              acc.z += fk * v[k].x;
-              acc.w += fk * v[k].y;
+              acc.x += fk * v[k].x;
+              acc.y += fk * v[k].y;
+              acc.z += fk * v[k].z;
+              acc.w += fk * v[k].w;
             }
           }
         }
         const int i = row0 + q, t = i / rep, h = hk * rep + i % rep;
-        if constexpr (PREFIX) {
-          float* e = static_cast<float*>(a.ws) + ((long long)t * a.Hq + h) * ws_entry(HD);
-          if (lane < CH) reinterpret_cast<float4*>(e)[c] = acc;
-          if (lane == 0) {
-            e[HD] = top;
-            e[HD + 1] = sum;
-          }
-        } else {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const bool fin = isfinite(acc.x * inv) && isfinite(acc.y * inv) && isfinite(acc.z * inv) && isfinite(acc.w * inv);
-          uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2] + c * 4;
-          if (lane < CH)
-            *reinterpret_cast<uint2*>(dst) =
-                make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
-          if (lane == 0 && a.lse)
-            a.lse[((long long)b * a.Tq + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-          if (!__all_sync(0xffffffffu, fin) && !s_fail) exact_row<HD, F16>(a, b, t, h, n, ql, lane);
-        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const bool fin = isfinite(acc.x * inv) && isfinite(acc.y * inv) && isfinite(acc.z * inv) && isfinite(acc.w * inv);
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2] + c * 4;
+        if (lane < CH)
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
+        if (lane == 0 && a.lse)
+          a.lse[((long long)b * a.Tq + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        if (!__all_sync(0xffffffffu, fin) && !s_fail) exact_row<HD, F16>(a, b, t, h, n, ql, lane);
       }
       if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
     }
@@ -564,7 +626,6 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<HD>);
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
@@ -577,10 +638,14 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   const long long rows = (long long)(PREFIX ? a.B : a.Tq) * rep;
   const int tiles = (int)((rows + kRowsCta - 1) / kRowsCta);
   const long long ctas = (long long)tiles * a.Hkv * (PREFIX ? 1 : a.B);
-  // Splits of the keys: as many as fill the SMs (one CTA each), no CTA below one tile.
-  const long long keys = PREFIX ? a.P : min((long long)a.cap, (long long)a.window + min(a.Tq, kRowsCta / rep + 2) + a.sinks);
   int split = 1;
-  while (split < kMaxSplit && ctas * split * 2 <= sms && (keys + kKeys - 1) / kKeys >= split * 2) split *= 2;
+  if (PREFIX) {
+    split = prefix_split(a.B, rep, a.Hkv, a.P);
+  } else {
+    // as many as fill the SMs (one CTA each), no CTA below one tile
+    const long long keys = min((long long)a.cap, (long long)a.window + min(a.Tq, kRowsCta / rep + 2) + a.sinks);
+    while (split < kMaxSplit && ctas * split * 2 <= sms && (keys + kKeys - 1) / kKeys >= split * 2) split *= 2;
+  }
   if (ctas * split >= (1ll << 31)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ctas * split));
@@ -589,7 +654,7 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.x = PREFIX ? 1 : split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
@@ -604,6 +669,33 @@ cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
 }
 
 }  // namespace
+
+// Keys' splits of a prefix: the count with the least time by this model (clocks,
+// measured): a CTA's start and end, its tiles of 128 keys (two row tiles, or
+// one), and the workspace traffic of a part.  152 SMs are planned for, so that
+// the workspace's size does not depend on the device.
+int prefix_split(int B, int rep, int Hkv, int P) {
+  const long long rows = (long long)B * rep, tiles = (rows + kRowsCta - 1) / kRowsCta, items = tiles * Hkv;
+  const long long nt = ((long long)P + kKeys - 1) / kKeys;
+  const double tile = rows > 128 ? 3900 : 2700;
+  int best = 1;
+  double least = 0;
+  for (int s = 1; s <= kMaxPrefixSplit && s <= nt; ++s) {
+    const double t = (double)((items * s + 151) / 152) * (10000 + (double)((nt + s - 1) / s) * tile) + 130.0 * items * s;
+    if (s == 1 || t < least) {
+      best = s;
+      least = t;
+    }
+  }
+  return best;
+}
+
+size_t prefix_ws_bytes(int B, int rep, int Hkv, int hd, int P) {
+  const long long rows = (long long)B * rep;
+  const int tiles = (int)((rows + kRowsCta - 1) / kRowsCta);
+  const int split = P > 0 ? prefix_split(B, rep, Hkv, P) : 1;
+  return (size_t)tiles * Hkv * split * attn::prefix_rows(tiles, rows) * (hd + 2) * sizeof(float);
+}
 
 cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s) {
   return prefix ? launch_any<true>(a, s) : launch_any<false>(a, s);

@@ -496,7 +496,7 @@ struct AttnOpArgs {
   void* ws;                 // shared-prefix partials
 };
 cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s);
-size_t shared_prefix_ws_bytes(int B, int Hq, int hd);
+size_t shared_prefix_ws_bytes(int B, int Hq, int Hkv, int hd, int P);
 cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s);
 
 // ---------------------------------------------------------------------------

@@ -31,7 +31,7 @@ cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s) 
     const cudaError_t e = launch_attn_rows_tc(a, true, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_attn_decode(a, false, s);
+  return launch_attn_decode(a, a.P > 0, s);
 }
 
 }  // namespace river

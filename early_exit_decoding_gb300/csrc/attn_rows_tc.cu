@@ -173,6 +173,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ float s_m[kRowsCta], s_l[kRowsCta];  // a row's maximum (log2 units) and sum
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // the kernel that takes the prefix's parts may start beside the last CTAs
+  // (it waits for all of them before it reads the workspace)
+  if (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   const int part = blockIdx.x % split, rep = a.Hq / a.Hkv;
   int id = blockIdx.x / split;
   // later tiles of a prompt see more keys: first come, first served from the end

@@ -591,14 +591,14 @@ def _buffer(o, key, shape, like, dtype, stream, name):
     (taken on the stream that writes it)."""
     t = o.get(key)
     if t is None:
+        import torch
         if stream is None:
-            t = like.new_empty(shape, dtype=dtype)
+            t = torch.empty(shape, dtype=dtype, device=like.device)
         else:
-            import torch
             with torch.cuda.stream(stream):
-                t = like.new_empty(shape, dtype=dtype)
+                t = torch.empty(shape, dtype=dtype, device=like.device)
         o[key] = t
-    elif tuple(t.shape) != tuple(shape) or t.dtype != dtype or t.get_device() != like.get_device() or \
+    elif t.shape != shape or t.dtype != dtype or t.get_device() != like.get_device() or \
             (key != "out" and not t.is_contiguous()):
         _refuse(f"{name}: out[{key!r}] must be {dtype} {tuple(shape)} on {like.device}"
                 + ("" if key == "out" else ", contiguous"))
@@ -609,18 +609,18 @@ def _run(dev, stream, fn, *args):
     """The library call ``fn(*args, stream)`` with device ``dev`` current;
     ``stream`` None: that device's current stream."""
     import torch
-    cur = torch.cuda.current_device()
-    if cur != dev:
+    if torch.cuda.current_device() != dev:
         with torch.cuda.device(dev):
             return _run(dev, stream, fn, *args)
-    status = fn(*args, (torch.cuda.current_stream() if stream is None else stream).cuda_stream)
+    # (the raw handle: making a Stream object costs as much as a small launch)
+    status = fn(*args, torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream)
     if status != RL_OK:
         _check(status)
 
 
 def _int32(name, key, t, shape):
     import torch
-    if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         _refuse(f"{name}: {key} must be contiguous int32 {shape}")
 
 
@@ -664,20 +664,23 @@ def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None
 
 
 def _strides(d, t):
-    """Strides of the first three axes into the descriptor's field; an axis of
-    one entry has no stride that matters."""
+    """Strides of the outer axes into the descriptor's field (of three: the
+    middle one stays 0); an axis of one entry has no stride that matters."""
     s, n = t.stride(), t.shape
     d[0] = s[0] if n[0] > 1 else 0
-    d[1] = s[1] if n[1] > 1 else 0
-    d[2] = s[2] if n[2] > 1 else 0
+    if len(n) == 4:
+        d[1] = s[1] if n[1] > 1 else 0
+    d[2] = s[-2] if n[-2] > 1 else 0
 
 
 def _attn_desc(name, q, k, v, out, scale):
-    """rl_attn_desc of q, out [B][T][Hq][hd] and k, v [B][Hkv][S][hd]."""
+    """rl_attn_desc of q, out [B][T][Hq][hd] ([B][Hq][hd]: T is 1) and k, v
+    [B][Hkv][S][hd]."""
     for t in (q, k, v, out):
-        if t.dim() != 4 or t.numel() == 0 or t.stride(3) != 1:
+        if t.dim() != (4 if t is k or t is v else q.dim()) or t.numel() == 0 or t.stride(-1) != 1:
             _refuse(f"{name}: q, k, v and out must have their axes, none empty, with a contiguous last one")
-    B, T, Hq, hd = q.shape
+    B, Hq, hd = q.shape[0], q.shape[-2], q.shape[-1]
+    T = q.shape[1] if q.dim() == 4 else 1
     _, Hkv, S, _ = k.shape
     qc, kc = _dtype_code(q.dtype), _dtype_code(k.dtype)
     if k.shape != v.shape or k.shape[0] != B or k.shape[3] != hd or v.dtype != k.dtype or out.dtype != k.dtype or \
@@ -704,6 +707,8 @@ def window_attention(q, k, v, kv_len, window, sinks=0, q_len=None, scale=None, o
     import torch
     name = "window_attention"
     dev = _operands(name, (q, k, v, kv_len, q_len, err))
+    if q.dim() != 4:
+        _refuse(f"{name}: q must be [B][T][Hq][hd]")
     o = {} if out is None else dict(out)
     res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
     d = _attn_desc(name, q, k, v, res, scale)
@@ -734,7 +739,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
         _refuse(f"{name}: q must be [B][Hq][hd]")
     o = {} if out is None else dict(out)
     res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
-    d = _attn_desc(name, q[:, None], k, v, res[:, None], scale)
+    d = _attn_desc(name, q, k, v, res, scale)
     lse = _buffer(o, "lse", q.shape[:2], q, torch.float32, stream, name)
     _int32(name, "kv_len", kv_len, (d.batch,))
     if err is not None:

@@ -32,7 +32,7 @@ EXPORTS = (
     "rl_kv_decode_path", "rl_save_exit_layers", "rl_load_exit_layers", "rl_exit_kv_cosine",
     "rl_kv_set_wait_limit", "rl_debug_fail_allocations", "rl_model_offload_backbone",
     "rl_model_memory", "rl_token_logprobs", "rl_window_attention", "rl_shared_prefix_workspace",
-    "rl_shared_prefix_attention",
+    "rl_shared_prefix_attention", "rl_kv_set_window", "rl_kv_share_prefix", "rl_prefill_score",
 )
 RL_DT_F32, RL_DT_BF16, RL_DT_F16 = range(3)
 RL_PATH_AUTO, RL_PATH_STEP, RL_PATH_FUSED, RL_PATH_GENERIC = range(4)
@@ -115,6 +115,9 @@ def _load():
         "rl_model_memory": (I, [P, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]),
         "rl_debug_fail_allocations": (I, [ctypes.c_int64]),
         "rl_load_exit_layers": (I, [P, ctypes.c_char_p, P]),
+        "rl_kv_set_window": (I, [P, I, I]),
+        "rl_kv_share_prefix": (I, [P, I]),
+        "rl_prefill_score": (I, [P, P, P, I, I, ctypes.POINTER(rl_exit_policy), P, P, P, P, P, P, I, P, P, P]),
         "rl_token_logprobs": (I, [P, I, I, I, ctypes.c_int64, P, I, I, P, P, P, P, P, P, P]),
         "rl_window_attention": (I, [ctypes.POINTER(rl_attn_desc), P, P, P, P, P, I, I, P, P, P, P]),
         "rl_shared_prefix_workspace": (I, [ctypes.POINTER(rl_attn_desc), I, ctypes.POINTER(ctypes.c_uint64)]),
@@ -285,6 +288,21 @@ def rl_debug_fail_allocations(after):
     """Test hook: the next ``after`` library allocations succeed, later ones
     fail (RL_ERR_OOM); negative switches it off."""
     _check(_lib.rl_debug_fail_allocations(int(after)))
+
+
+def rl_kv_set_window(kv, window, sinks=0):
+    _check(_lib.rl_kv_set_window(kv, int(window), int(sinks)))
+
+
+def rl_kv_share_prefix(kv, n):
+    _check(_lib.rl_kv_share_prefix(kv, int(n)))
+
+
+def rl_prefill_score(model, kv, d_tokens, B, T, policy, d_logits, d_next_token, d_exit_layer, d_min_cos,
+                     d_logprob, d_entropy=None, top_k=0, d_top_ids=None, d_top_logprobs=None, stream=None):
+    _check(_lib.rl_prefill_score(model, kv, _ptr(d_tokens), B, T, ctypes.byref(policy), _ptr(d_logits),
+                                 _ptr(d_next_token), _ptr(d_exit_layer), _ptr(d_min_cos), _ptr(d_logprob),
+                                 _ptr(d_entropy), top_k, _ptr(d_top_ids), _ptr(d_top_logprobs), _stream(stream)))
 
 
 def rl_kv_set_decode_path(kv, path):
@@ -512,6 +530,16 @@ class KVCache:
         self._trace = t
         rl_kv_set_trace(self.handle, t)
 
+    def set_window(self, window, sinks=0):
+        """Sliding-window attention with ``sinks`` first tokens that stay
+        visible, from the next call on (0: off)."""
+        rl_kv_set_window(self.handle, window, sinks)
+
+    def share_prefix(self, n=None):
+        """The first ``n`` positions of sequence 0 (None: all so far) serve
+        every sequence of the later decode steps (0: off)."""
+        rl_kv_share_prefix(self.handle, self.position()[0] if n is None else n)
+
     def set_decode_path(self, path):
         rl_kv_set_decode_path(self.handle, path)
 
@@ -541,6 +569,24 @@ def prefill(model: Model, kv: KVCache, tokens, policy: Policy, out=None, stream=
     o = _outputs(model, B, out)
     rl_prefill(model.handle, kv.handle, tokens, B, T, policy.c(), o["logits"], o["next_token"],
                o["exit_layer"], o["min_cos"], stream)
+    return o
+
+
+def prefill_score(model: Model, kv: KVCache, tokens, policy: Policy, top_k=0, out=None, stream=None):
+    """prefill that also scores the prompt: ``logprob [B][T]`` (of token t after
+    the tokens before it, 0 for the first), ``entropy [B][T]`` and, for
+    ``top_k`` > 0, ``top_ids`` and ``top_logprobs`` [B][T][top_k] of every
+    position.  See rl_prefill_score."""
+    import torch
+    B, T = tokens.shape
+    o = _outputs(model, B, out)
+    f32 = torch.float32
+    for n, shape, dt in (("logprob", (B, T), f32), ("entropy", (B, T), f32)) + (
+            (("top_ids", (B, T, top_k), torch.int32), ("top_logprobs", (B, T, top_k), f32)) if top_k > 0 else ()):
+        o.setdefault(n, torch.empty(shape, dtype=dt, device="cuda"))
+    rl_prefill_score(model.handle, kv.handle, tokens, B, T, policy.c(), o["logits"], o["next_token"],
+                     o["exit_layer"], o["min_cos"], o["logprob"], o["entropy"], top_k, o.get("top_ids"),
+                     o.get("top_logprobs"), stream)
     return o
 
 
@@ -767,5 +813,5 @@ def kv_cache_alloc(model: Model, max_batch, max_seq):
 
 
 __all__ = [*EXPORTS, "Model", "KVCache", "Policy", "RiverError", "prefill", "decode_step",
-           "quantize_exit_layers", "kv_cache_alloc", "token_logprobs", "window_attention",
+           "quantize_exit_layers", "kv_cache_alloc", "prefill_score", "token_logprobs", "window_attention",
            "shared_prefix_attention", "rl_attn_desc", "LIB_PATH"]

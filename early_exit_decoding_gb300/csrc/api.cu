@@ -160,12 +160,14 @@ struct GraphKey {
   bool step = false;
   long long wait = 0;  // rl_kv_set_wait_limit
   int epoch = 0;       // the model's weight-placement epoch
+  int window = 0, sinks = 0;  // sliding window (0: every key)
+  int prefix = 0;             // positions shared from sequence 0
   bool operator==(const GraphKey& o) const {
     return B == o.B && mode == o.mode && tau == o.tau && sched == o.sched &&
            sched_len == o.sched_len && tokens == o.tokens && logits == o.logits &&
            next == o.next && exit == o.exit && min_cos == o.min_cos && trace == o.trace &&
            prof == o.prof && fused == o.fused && step == o.step && wait == o.wait &&
-           epoch == o.epoch;
+           epoch == o.epoch && window == o.window && sinks == o.sinks && prefix == o.prefix;
   }
 };
 
@@ -213,6 +215,10 @@ struct rl_kv {
   bool use_fused = true;
   int path_pref = RL_PATH_AUTO;  // rl_kv_set_decode_path
   long long wait_limit = 0;      // rl_kv_set_wait_limit (0: the kernels' own limits)
+  int window = 0, sinks = 0;     // rl_kv_set_window (0: off)
+  int prefix = 0;                // rl_kv_share_prefix (0: off)
+  void* prefix_ws = nullptr;     // its attention's workspace
+  size_t prefix_ws_bytes = 0;
   // persistent step kernel
   bool use_step = true;
   unsigned* bars = nullptr;           // per-CTA phase flags [n_bars], 128 bytes apart
@@ -250,6 +256,7 @@ struct rl_kv {
   int nrec = 0;
   int* d_paths = nullptr;
   int prof_pos = 0, prof_B = 1;
+  double prof_attn_keys = 0;     // keys the profiled step's attention reads per KV head
   std::vector<void*> allocs;
 
   template <typename T>
@@ -460,6 +467,10 @@ rl_status stage_layer(const rl_model* m, rl_kv* kv, int l, int w4mode, cudaStrea
   return RL_OK;
 }
 
+// Whether the next decode step's position is past its sliding window, so that
+// some key is out of sight.
+bool windowed(const rl_kv* kv) { return kv->window > 0 && kv->host_pos >= kv->window; }
+
 rl_status enqueue_pass(rl_model* m, rl_kv* kv, const StepIO& io, const Work& w, cudaStream_t s) {
   const int L = m->L, d = m->d;
   Prof pf{kv, s, kv->profiling && !io.prefill};
@@ -553,7 +564,53 @@ rl_status enqueue_pass(rl_model* m, rl_kv* kv, const StepIO& io, const Work& w, 
     at.o = w.o;
     at.ldo = m->Ko;
     pf.begin();
-    if (prefill && kv->tm_ok && attn_prefill_supported(m->Hq / m->Hkv, m->hd)) {
+    if (prefill ? (kv->window > 0 && T > kv->window) : (windowed(kv) || kv->prefix > 0)) {
+      // the stand-alone operators on this layer's cache: a sliding window past
+      // its first keys, or a step behind a shared prefix
+      AttnOpArgs op;
+      memset(&op, 0, sizeof(op));
+      op.q = w.q;
+      op.q_f32 = 1;
+      op.out = w.o;
+      op.B = io.B;
+      op.Tq = prefill ? T : 1;
+      op.Hq = m->Hq;
+      op.Hkv = m->Hkv;
+      op.hd = m->hd;
+      op.scale = 1.f / sqrtf((float)m->hd);
+      op.err = &kv->st->err;
+      op.qs[0] = (long long)op.Tq * m->Hq * m->hd;
+      op.qs[1] = (long long)m->Hq * m->hd;
+      op.qs[2] = m->hd;
+      op.os[0] = (long long)op.Tq * m->Ko;
+      op.os[1] = m->Ko;
+      op.os[2] = m->hd;
+      KeySrc cache;
+      cache.ks[0] = cache.vs[0] = (long long)m->Hkv * kv->Tmax * m->hd;
+      cache.ks[1] = cache.vs[1] = (long long)kv->Tmax * m->hd;
+      cache.ks[2] = cache.vs[2] = m->hd;
+      const int P = prefill ? 0 : kv->prefix;
+      cache.k = kv->K[l] + (size_t)P * m->hd;  // (P < max_seq: a step's own slot comes after it)
+      cache.v = kv->V[l] + (size_t)P * m->hd;
+      op.kv = cache;
+      op.cap = kv->Tmax - P;
+      op.kv_len = prefill ? nullptr : &kv->st->pos;
+      op.kv_len_add = prefill ? T : 1 - P;
+      if (P > 0) {
+        op.pre = cache;
+        op.pre.ks[0] = op.pre.vs[0] = 0;
+        op.pre.k = kv->K[l];
+        op.pre.v = kv->V[l];
+        op.P = P;
+        op.ws = kv->prefix_ws;
+        op.window = op.cap;
+        RL_CUDA(launch_shared_prefix_attention(op, s));
+      } else {
+        op.window = std::min(kv->window, kv->Tmax);
+        op.sinks = std::min(kv->sinks, kv->Tmax);
+        RL_CUDA(launch_window_attention(op, s));
+      }
+    } else if (prefill && kv->tm_ok && attn_prefill_supported(m->Hq / m->Hkv, m->hd)) {
       // the prompt: causal flash-style attention on the tensor cores
       AttnPrefillArgs ap;
       memset(&ap, 0, sizeof(ap));
@@ -997,6 +1054,8 @@ bool fused_fits(const rl_model* m, int B);
 // fused five-launches-per-layer path, or the generic path (any batch); -1
 // when the path the cache was told to use cannot run this batch.
 int decode_path(const rl_model* m, const rl_kv* kv, int B) {
+  if (windowed(kv) || kv->prefix > 0)
+    return kv->path_pref == RL_PATH_AUTO || kv->path_pref == RL_PATH_GENERIC ? RL_PATH_GENERIC : -1;
   const bool step = kv->use_step && step_fits(m, kv, B);
   const bool fused = kv->use_fused && fused_fits(m, B);
   switch (kv->path_pref) {
@@ -1817,11 +1876,45 @@ rl_status rl_kv_set_position(rl_kv* kv, int32_t pos, int32_t decode_step, rl_str
   if (!kv) return fail(RL_ERR_INVALID_ARG, "kv is NULL");
   if (pos < 0 || pos > kv->Tmax || decode_step < 0)
     return fail(RL_ERR_INVALID_ARG, "position %d outside [0, %d] or negative step", pos, kv->Tmax);
+  if (pos < kv->prefix) return fail(RL_ERR_STATE, "position %d inside the shared prefix of %d", pos, kv->prefix);
   launch_set_state(kv->st, pos, decode_step, as_stream(stream));
   RL_LAUNCHED();
   RL_TRY(reset_sync_words(kv, as_stream(stream)));
   kv->host_pos = pos;
   kv->host_step = decode_step;
+  return RL_OK;
+}
+
+rl_status rl_kv_set_window(rl_kv* kv, int32_t window, int32_t sinks) {
+  if (!kv) return fail(RL_ERR_INVALID_ARG, "kv is NULL");
+  if (window < 0 || sinks < 0) return fail(RL_ERR_INVALID_ARG, "window and sinks must be >= 0");
+  if (window > 0 && kv->prefix > 0) return fail(RL_ERR_STATE, "a prefix is shared: no window beside it");
+  if (window > 0 && !tc_gemm_available()) return fail(RL_ERR_UNSUPPORTED, "no tensor maps on this driver");
+  kv->window = window;
+  kv->sinks = window > 0 ? sinks : 0;
+  return RL_OK;
+}
+
+rl_status rl_kv_share_prefix(rl_kv* kv, int32_t n) {
+  if (!kv) return fail(RL_ERR_INVALID_ARG, "kv is NULL");
+  if (n < 0 || n > kv->host_pos)
+    return fail(RL_ERR_INVALID_ARG, "prefix of %d positions: the cache holds %d", n, kv->host_pos);
+  if (n > 0 && kv->window > 0) return fail(RL_ERR_STATE, "a window is set: no shared prefix beside it");
+  if (n > 0 && !tc_gemm_available()) return fail(RL_ERR_UNSUPPORTED, "no tensor maps on this driver");
+  if (n > 0) {
+    const rl_model* m = kv->m;
+    size_t need = 0;
+    for (int b = 1; b <= std::min(kv->maxB, kMaxBatch); ++b)
+      need = std::max(need, shared_prefix_ws_bytes(b, m->Hq, m->Hkv, m->hd, n));
+    if (need > kv->prefix_ws_bytes) {
+      char* p = nullptr;
+      RL_TRY(kv->alloc(&p, need));  // (a smaller one of before stays until the cache is freed)
+      kv->prefix_ws = p;
+      kv->prefix_ws_bytes = need;
+      kv->key = GraphKey();  // a captured step holds the old one's address
+    }
+  }
+  kv->prefix = n;
   return RL_OK;
 }
 
@@ -1855,9 +1948,66 @@ rl_status rl_kv_set_trace(rl_kv* kv, float* d_hidden) {
   return RL_OK;
 }
 
-rl_status rl_prefill(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B, int32_t T,
-                     const rl_exit_policy* policy, float* d_logits, int32_t* d_next_token,
-                     int32_t* d_exit_layer, float* d_min_cos, rl_stream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// What a scored prefill returns beside rl_prefill's outputs.
+struct ScoreOut {
+  float *logprob, *entropy;
+  int top_k;
+  int* top_ids;
+  float* top_lp;
+};
+// Rows whose logits a scored prefill holds at a time (fp32 [rows][vocab]:
+// 263 MB at a vocabulary of 128,256; enough for whole waves of the LM head's
+// 256-token tiles).
+constexpr int kScoreRows = 512;
+
+// The LM head and rl_token_logprobs over every row of a prefill (its final
+// norm's rows are in w.x_attn), `rows` at a time.
+rl_status enqueue_scores(rl_model* m, rl_kv* kv, const StepIO& io, const Work& w, const ScoreOut& score, float* logits,
+                         int rows, cudaStream_t s) {
+  const int M = io.B * io.T;
+  for (int r0 = 0; r0 < M; r0 += rows) {
+    const int n = std::min(rows, M - r0);
+    GemvArgs a = gemv_base(m, Linear(), W4_OFF, nullptr, 0);
+    a.w = m->lm_head;
+    a.N = m->V;
+    a.Kp = m->Kd;
+    a.x = w.x_attn + (size_t)r0 * m->Kd;
+    a.ldx = m->Kd;
+    a.B = n;
+    a.epi = EPI_STORE;
+    a.out = logits;
+    a.ldo = m->V;
+    a.err = &kv->st->err;
+    RL_TRY(project(m, kv, m->tm_lm, a, s));
+    LogprobArgs p;
+    memset(&p, 0, sizeof(p));
+    p.x = logits;
+    p.dtype = RL_DT_F32;
+    p.rows = n;
+    p.V = m->V;
+    p.ld = m->V;
+    p.tokens = io.tokens;
+    p.n_tok = 1;
+    p.T = io.T;
+    p.row0 = r0;
+    p.top_k = score.top_k;
+    p.entropy = score.entropy;
+    p.logprob = score.logprob;
+    p.top_ids = score.top_ids;
+    p.top_lp = score.top_lp;
+    p.err = &kv->st->err;
+    RL_CUDA(launch_logprobs(p, s));
+  }
+  return RL_OK;
+}
+
+rl_status prefill_run(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B, int32_t T,
+                      const rl_exit_policy* policy, float* d_logits, int32_t* d_next_token,
+                      int32_t* d_exit_layer, float* d_min_cos, const ScoreOut* score, rl_stream_t stream) {
   if (!m || !kv || !d_tokens || !d_logits || !d_exit_layer)
     return fail(RL_ERR_INVALID_ARG, "NULL argument");
   if (kv->m != m) return fail(RL_ERR_INVALID_ARG, "kv cache belongs to another model");
@@ -1874,6 +2024,7 @@ rl_status rl_prefill(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B,
   const size_t bytes = 3 * n_h * 4 + 2 * n_xd * 2 + n_xo * 2 + n_xf * 2 +
                        M * (2 * Gd + Go + Gf) * 4 + M * m->Hq * m->hd * 4 +
                        M * m->Hq * (m->hd + 2) * 4 + M * 4 + 32 * 256;  // + alignment slack of the carve-up
+  const size_t score_rows = score ? std::min<size_t>(M, kScoreRows) : 0;
   char* base = nullptr;
   if (alloc_injected_failure()) return fail(RL_ERR_OOM, "prefill workspace: injected allocation failure");
   RL_CUDA(cudaMallocAsync((void**)&base, bytes, s));
@@ -1900,13 +2051,48 @@ rl_status rl_prefill(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B,
   w.cosbuf = (float*)take(M * 4);
   if ((size_t)(p - base) > bytes) return fail(RL_ERR_CUDA, "prefill workspace sizing");
   StepIO io{d_tokens, B, T, policy, d_logits, d_next_token, d_exit_layer, d_min_cos, true};
-  RL_TRY(reset_sync_words(kv, s));
-  rl_status st = enqueue_pass(m, kv, io, w, s);
+  float* score_logits = nullptr;
+  if (score) {
+    const cudaError_t e = alloc_injected_failure()
+                              ? cudaErrorMemoryAllocation
+                              : cudaMallocAsync((void**)&score_logits, score_rows * m->V * sizeof(float), s);
+    if (e != cudaSuccess) {
+      cudaGetLastError();
+      cudaFreeAsync(base, s);
+      return fail(RL_ERR_OOM, "scoring workspace of %zu rows: %s", score_rows, cudaGetErrorString(e));
+    }
+  }
+  rl_status st = reset_sync_words(kv, s);
+  if (st == RL_OK) st = enqueue_pass(m, kv, io, w, s);
+  if (st == RL_OK && score) st = enqueue_scores(m, kv, io, w, *score, score_logits, (int)score_rows, s);
+  if (score_logits) cudaFreeAsync(score_logits, s);
   cudaFreeAsync(base, s);
   if (st != RL_OK) return st;
   kv->host_pos = T;
   kv->host_step = 0;
+  kv->prefix = 0;
   return RL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+rl_status rl_prefill(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B, int32_t T,
+                     const rl_exit_policy* policy, float* d_logits, int32_t* d_next_token,
+                     int32_t* d_exit_layer, float* d_min_cos, rl_stream_t stream) {
+  return prefill_run(m, kv, d_tokens, B, T, policy, d_logits, d_next_token, d_exit_layer, d_min_cos, nullptr, stream);
+}
+
+rl_status rl_prefill_score(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B, int32_t T,
+                           const rl_exit_policy* policy, float* d_logits, int32_t* d_next_token,
+                           int32_t* d_exit_layer, float* d_min_cos, float* d_logprob, float* d_entropy,
+                           int32_t top_k, int32_t* d_top_ids, float* d_top_logprobs, rl_stream_t stream) {
+  if (!d_logprob) return fail(RL_ERR_INVALID_ARG, "NULL argument");
+  if (top_k < 0 || top_k > 32 || (m && top_k > m->V) || (top_k > 0 && (!d_top_ids || !d_top_logprobs)))
+    return fail(RL_ERR_INVALID_ARG, "top_k outside [0, min(32, vocab)], or its outputs NULL");
+  const ScoreOut score{d_logprob, d_entropy, top_k, d_top_ids, d_top_logprobs};
+  return prefill_run(m, kv, d_tokens, B, T, policy, d_logits, d_next_token, d_exit_layer, d_min_cos, &score, stream);
 }
 
 rl_status rl_decode_step(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B,
@@ -1926,6 +2112,11 @@ rl_status rl_decode_step(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_
   const Work w = decode_work(kv, B);
   kv->prof_pos = kv->host_pos;
   kv->prof_B = B;
+  kv->prof_attn_keys = (double)B * (kv->host_pos + 1);
+  if (windowed(kv))
+    kv->prof_attn_keys = (double)B * (kv->window + std::min(kv->sinks, kv->host_pos + 1 - kv->window));
+  else if (kv->prefix > 0)
+    kv->prof_attn_keys = kv->prefix + (double)B * (kv->host_pos + 1 - kv->prefix);
   const int path = decode_path(m, kv, B);
   if (path < 0) return fail(RL_ERR_UNSUPPORTED, "the requested decode path does not fit batch %d", B);
   const bool step = path == RL_PATH_STEP;
@@ -1956,6 +2147,9 @@ rl_status rl_decode_step(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_
     key.step = step;
     key.wait = kv->wait_limit;
     key.epoch = m->epoch;
+    key.window = windowed(kv) ? kv->window : 0;
+    key.sinks = windowed(kv) ? kv->sinks : 0;
+    key.prefix = kv->prefix;
     if (!kv->exec || !(key == kv->key)) {
       if (step) RL_TRY(prepare_step_phases(m, kv, io, s));
       cudaGraph_t g = nullptr;
@@ -2166,8 +2360,8 @@ rl_status rl_kv_profile(rl_kv* kv, rl_stream_t stream, int32_t cap, int32_t* kin
     RL_CUDA(cudaEventElapsedTime(&t, kv->ev[2 * i], kv->ev[2 * i + 1]));
     const int path = r.gemv ? hp[i] : -1;
     double b = path == 1 ? r.bytes_w4 : r.bytes_bf;
-    if (r.attn)  // K and V rows 0..p of every sequence
-      b = 2.0 * kv->prof_B * m->Hkv * (double)(kv->prof_pos + 1) * m->hd * 2.0;
+    if (r.attn)  // K and V rows 0..p of every sequence (in its window; a shared prefix once)
+      b = 2.0 * kv->prof_attn_keys * m->Hkv * m->hd * 2.0;
     if (kinds) kinds[i] = r.kind;
     if (layers) layers[i] = r.layer;
     if (paths) paths[i] = path;

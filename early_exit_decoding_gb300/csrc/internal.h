@@ -464,6 +464,11 @@ struct LogprobArgs {
   long long ld;
   const int* tokens;        // [rows][n_tok], nullable
   int n_tok, top_k;
+  // T > 0: the rows are positions row0 .. of sequences of T tokens; row R scores
+  // tokens[R + 1] into logprob[R + 1] (not the last of a sequence), the first
+  // writes 0 to logprob[R]; every output is indexed by R
+  int T;
+  long long row0;
   float *lse, *entropy, *logprob;  // nullable
   int* top_ids;
   float* top_lp;

@@ -239,8 +239,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
   }
   // the given tokens' logits, one a thread (part 0; n_tok <= 256)
   float tokv = NAN;
-  if (part == 0 && tid < a.n_tok) {
-    const int tok = a.tokens[(long long)row * a.n_tok + tid];
+  const long long orow = row + a.row0;  // where the row's outputs go
+  const int tpos = a.T > 0 ? (int)(orow % a.T) : 0;
+  const int n_tok = a.T > 0 ? (tpos < a.T - 1) : a.n_tok;
+  const long long tok_at = a.T > 0 ? orow + 1 : orow * a.n_tok;
+  if (part == 0 && tid < n_tok) {
+    const int tok = a.tokens[tok_at + tid];
     if (tok >= 0 && tok < V)
       tokv = E::load(x + tok);
     else if (a.err)
@@ -439,20 +443,21 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
     if (lane == 0) {
       s_res[0] = m;
       s_res[1] = ln_s;
-      if (a.lse) a.lse[row] = s == 0.f ? -INFINITY : m + ln_s;
-      if (a.entropy) a.entropy[row] = ln_s - p.t / s;
+      if (a.lse) a.lse[orow] = s == 0.f ? -INFINITY : m + ln_s;
+      if (a.entropy) a.entropy[orow] = ln_s - p.t / s;
+      if (a.T > 0 && tpos == 0) a.logprob[orow] = 0.f;
     }
     if constexpr (kTop) {
       if (lane < k) {
         const unsigned long long key = s_top[lane];
-        a.top_ids[(long long)row * k + lane] = (int)(0xffffffffu - (uint32_t)key);
-        a.top_lp[(long long)row * k + lane] = (value_of(key) - m) - ln_s;
+        a.top_ids[orow * k + lane] = (int)(0xffffffffu - (uint32_t)key);
+        a.top_lp[orow * k + lane] = (value_of(key) - m) - ln_s;
       }
     }
   }
-  if (a.n_tok > 0) {
+  if (n_tok > 0) {
     __syncthreads();
-    if (tid < a.n_tok) a.logprob[(long long)row * a.n_tok + tid] = (tokv - s_res[0]) - s_res[1];
+    if (tid < n_tok) a.logprob[tok_at + tid] = (tokv - s_res[0]) - s_res[1];
   }
 }
 

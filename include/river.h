@@ -239,6 +239,29 @@ RL_API rl_status rl_kv_set_position(rl_kv* kv, int32_t pos, int32_t decode_step,
  * NULL switches it off. */
 RL_API rl_status rl_kv_set_trace(rl_kv* kv, float* d_hidden);
 
+/* Sliding-window attention for this cache: from the next call on, position p
+ * attends to the keys j <= p with p - j < window or j < sinks (the first tokens
+ * stay visible), in prefills and decode steps; the cache keeps every slot.
+ * window 0 (the default) switches it off.  While no position is past the window
+ * every path runs as without it; from then on decode steps run RL_PATH_GENERIC
+ * with the attention of rl_window_attention (a forced other path makes
+ * rl_decode_step return RL_ERR_UNSUPPORTED).  Not on the pages: long
+ * generations at a bounded cost of attention.  RL_ERR_STATE while a prefix is
+ * shared; RL_ERR_INVALID_ARG for a negative value. */
+RL_API rl_status rl_kv_set_window(rl_kv* kv, int32_t window, int32_t sinks);
+
+/* One prompt, many continuations: the first n positions of sequence 0 (n at
+ * most the cache's position) become the first n positions of every sequence.
+ * Later decode steps of any batch up to max_batch read them from sequence 0's
+ * slots, once for the whole batch, and each sequence's own slots from n on
+ * (rl_shared_prefix_attention, on RL_PATH_GENERIC); each sequence writes its
+ * own slots, so a prompt prefilled once with B = 1 serves them all.  n 0
+ * switches it off, and so does the next rl_prefill.  Takes a workspace the
+ * first time (waits for the device); make the call outside stream captures.
+ * RL_ERR_STATE while a window is set; RL_ERR_INVALID_ARG for n outside [0, position];
+ * RL_ERR_OOM (nothing changed). */
+RL_API rl_status rl_kv_share_prefix(rl_kv* kv, int32_t n);
+
 /* Which kernels run a decode step.  RL_PATH_STEP: one persistent cooperative
  * kernel per step (batch <= 8, shapes whose activations and weight ring fit in
  * shared memory, GQA ratio 1, 2 or 4, head_dim 64 or 128); RL_PATH_FUSED: five
@@ -264,6 +287,22 @@ RL_API int32_t rl_kv_decode_path(const rl_kv* kv, int32_t B);
 RL_API rl_status rl_prefill(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B, int32_t T,
                      const rl_exit_policy* policy, float* d_logits, int32_t* d_next_token,
                      int32_t* d_exit_layer, float* d_min_cos, rl_stream_t stream);
+
+/* rl_prefill that also scores the prompt: every position's distribution goes
+ * through rl_token_logprobs (the LM head runs over all positions, a few hundred
+ * rows at a time, in a workspace of the call).  Outputs as rl_prefill, and
+ *   d_logprob [B][T] fp32: entry (b, t) is the log-probability of token t after
+ *             tokens 0 .. t-1 (0 for t = 0)
+ *   d_entropy [B][T] fp32 (may be NULL): of the distribution after position t
+ *   d_top_ids, d_top_logprobs [B][T][top_k] (NULL when top_k is 0; top_k <= 32):
+ *             the most likely tokens after position t
+ * Not on the pages: it compares what exits cost in likelihood (the perplexity
+ * of a text under a policy). */
+RL_API rl_status rl_prefill_score(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B, int32_t T,
+                                  const rl_exit_policy* policy, float* d_logits, int32_t* d_next_token,
+                                  int32_t* d_exit_layer, float* d_min_cos, float* d_logprob,
+                                  float* d_entropy, int32_t top_k, int32_t* d_top_ids,
+                                  float* d_top_logprobs, rl_stream_t stream);
 
 /* decode_step (explainer sections 四, 五: token-level exit per generation
  * step, minimum over the batch): one token per sequence, d_tokens [B], at the

@@ -90,12 +90,14 @@ def cosine(a: np.ndarray, b: np.ndarray) -> np.ndarray:
     return (dot / np.maximum(na * nb, F32(1e-12))).astype(F32)
 
 
-def attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, q_pos: np.ndarray) -> np.ndarray:
+def attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, q_pos: np.ndarray, window: int = 0,
+              sinks: int = 0) -> np.ndarray:
     """Causal grouped-query attention for one sequence.
 
     q [n][Hq][hd] at positions q_pos [n]; k, v [Hkv][T][hd] for positions
     0..T-1.  Query head h reads KV head h // (Hq / Hkv).  A query at position
-    p attends to keys 0..p.  Softmax in fp32 with max subtraction.
+    p attends to keys 0..p; with window > 0 only to those less than window
+    positions back and to the first `sinks`.  Softmax in fp32 with max subtraction.
     Returns o [n][Hq][hd].
     """
     n, Hq, hd = q.shape
@@ -104,6 +106,9 @@ def attention(q: np.ndarray, k: np.ndarray, v: np.ndarray, q_pos: np.ndarray) ->
     scale = F32(1.0 / np.sqrt(hd))
     out = np.empty((n, Hq, hd), dtype=F32)
     mask = np.arange(T)[None, :] <= np.asarray(q_pos)[:, None]  # [n][T]
+    if window > 0:
+        back = np.asarray(q_pos)[:, None] - np.arange(T)[None, :]
+        mask &= (back < window) | (np.arange(T)[None, :] < sinks)
     for h in range(Hq):
         g = h // rep
         s = (q[:, h, :] @ k[g].T).astype(F32) * scale            # [n][T]
@@ -154,6 +159,7 @@ class KVState:
         self.pos = 0
         self.B = B
         self.max_seq = max_seq
+        self.window = self.sinks = 0  # sliding window (0: every key)
 
 
 class OracleModel:
@@ -236,7 +242,7 @@ class OracleModel:
         T = pos0 + n
         o = np.empty((B, n, Hq, hd), F32)
         for b in range(B):
-            o[b] = attention(q[b], st.K[l][b, :, :T], st.V[l][b, :, :T], pos)
+            o[b] = attention(q[b], st.K[l][b, :, :T], st.V[l][b, :, :T], pos, st.window, st.sinks)
         h1 = (h + (o.reshape(B, n, Hq * hd) @ W["wo"].T)).astype(F32)
         x2 = rmsnorm(h1, lw["g_ffn"], S.rms_eps)
         u = (silu((x2 @ W["wg"].T).astype(F32)) * (x2 @ W["wu"].T)).astype(F32)

@@ -242,7 +242,8 @@ class OracleModel:
         T = pos0 + n
         o = np.empty((B, n, Hq, hd), F32)
         for b in range(B):
-            o[b] = attention(q[b], st.K[l][b, :, :T], st.V[l][b, :, :T], pos, st.window, st.sinks)
+            more = (st.window, st.sinks) if st.window else ()
+            o[b] = attention(q[b], st.K[l][b, :, :T], st.V[l][b, :, :T], pos, *more)
         h1 = (h + (o.reshape(B, n, Hq * hd) @ W["wo"].T)).astype(F32)
         x2 = rmsnorm(h1, lw["g_ffn"], S.rms_eps)
         u = (silu((x2 @ W["wg"].T).astype(F32)) * (x2 @ W["wu"].T)).astype(F32)

@@ -618,17 +618,14 @@ def _operands(name, tensors):
     """The one CUDA device (index) of the tensors (None: absent), none of which
     may need a gradient (the operators have no backward pass)."""
     import torch
-    dev = -1
+    dev = tensors[0].get_device()
     grad = torch.is_grad_enabled()
     for t in tensors:
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0 or (dev >= 0 and d != dev):
-            _refuse(f"{name}: every operand must be on one CUDA device (found {t.device})")
-        dev = d
-        if grad and t.requires_grad:
-            _refuse(f"{name}: an operand requires a gradient; the operator has no backward pass", RL_ERR_UNSUPPORTED)
+        if t is not None:
+            if t.get_device() != dev or dev < 0:
+                _refuse(f"{name}: every operand must be on one CUDA device (found {t.device})")
+            if grad and t.requires_grad:
+                _refuse(f"{name}: an operand requires a gradient; the operator has no backward pass", RL_ERR_UNSUPPORTED)
     return dev
 
 
@@ -655,7 +652,7 @@ def _run(dev, stream, fn, *args):
     """The library call ``fn(*args, stream)`` with device ``dev`` current;
     ``stream`` None: that device's current stream."""
     import torch
-    if torch.cuda.current_device() != dev:
+    if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _run(dev, stream, fn, *args)
     # (the raw handle: making a Stream object costs as much as a small launch)
@@ -698,14 +695,16 @@ def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None
         _int32(name, "err", err, (1,))
     o = {} if out is None else dict(out)
     f32 = torch.float32
-    lse = _buffer(o, "lse", (R,), logits, f32, stream, name)
-    ent = _buffer(o, "entropy", (R,), logits, f32, stream, name)
-    lp = _buffer(o, "logprob", tokens.shape, logits, f32, stream, name) if n else None
-    ids = _buffer(o, "top_ids", (R, top_k), logits, torch.int32, stream, name) if top_k else None
-    tlp = _buffer(o, "top_logprobs", (R, top_k), logits, f32, stream, name) if top_k else None
+    lse = _buffer(o, "lse", (R,), logits, f32, stream, name).data_ptr()
+    ent = _buffer(o, "entropy", (R,), logits, f32, stream, name).data_ptr()
+    lp = ids = tlp = None
+    if n:
+        lp = _buffer(o, "logprob", tokens.shape, logits, f32, stream, name).data_ptr()
+    if top_k:
+        ids = _buffer(o, "top_ids", (R, top_k), logits, torch.int32, stream, name).data_ptr()
+        tlp = _buffer(o, "top_logprobs", (R, top_k), logits, f32, stream, name).data_ptr()
     _run(dev, stream, _lib.rl_token_logprobs, logits.data_ptr(), dt, R, V, logits.stride(0) if R > 1 else V,
-         _addr(tokens) if n else None, n, top_k, lse.data_ptr(), ent.data_ptr(), _addr(lp), _addr(ids), _addr(tlp),
-         _addr(err))
+         tokens.data_ptr() if n else None, n, top_k, lse, ent, lp, ids, tlp, _addr(err))
     return o
 
 
@@ -717,6 +716,23 @@ def _strides(d, t):
     if len(n) == 4:
         d[1] = s[1] if n[1] > 1 else 0
     d[2] = s[-2] if n[-2] > 1 else 0
+
+
+_PLANS = {}
+
+
+def _plan(name, scale, tensors, make):
+    """What ``make()`` derives from the tensors' shapes, strides and types alone
+    (their checks, the descriptor, a workspace's size), kept for calls of the
+    same layout."""
+    key = (name, scale, *[x for t in tensors for x in (t.shape, t.stride(), t.dtype)])
+    p = _PLANS.get(key)
+    if p is None:
+        p = make()
+        if len(_PLANS) >= 256:
+            _PLANS.clear()
+        _PLANS[key] = p
+    return p
 
 
 def _attn_desc(name, q, k, v, out, scale):
@@ -757,11 +773,12 @@ def window_attention(q, k, v, kv_len, window, sinks=0, q_len=None, scale=None, o
         _refuse(f"{name}: q must be [B][T][Hq][hd]")
     o = {} if out is None else dict(out)
     res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
-    d = _attn_desc(name, q, k, v, res, scale)
-    lse = _buffer(o, "lse", q.shape[:3], q, torch.float32, stream, name)
-    _int32(name, "kv_len", kv_len, (d.batch,))
+    d = _plan(name, scale, (q, k, v, res), lambda: _attn_desc(name, q, k, v, res, scale))
+    B, T, Hq, _ = q.shape
+    lse = _buffer(o, "lse", (B, T, Hq), q, torch.float32, stream, name)
+    _int32(name, "kv_len", kv_len, (B,))
     if q_len is not None:
-        _int32(name, "q_len", q_len, (d.batch,))
+        _int32(name, "q_len", q_len, (B,))
     if err is not None:
         _int32(name, "err", err, (1,))
     _run(dev, stream, _lib.rl_window_attention, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), kv_len.data_ptr(),
@@ -785,22 +802,27 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
         _refuse(f"{name}: q must be [B][Hq][hd]")
     o = {} if out is None else dict(out)
     res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
-    d = _attn_desc(name, q, k, v, res, scale)
-    lse = _buffer(o, "lse", q.shape[:2], q, torch.float32, stream, name)
-    _int32(name, "kv_len", kv_len, (d.batch,))
+
+    def make():
+        d = _attn_desc(name, q, k, v, res, scale)
+        if k_prefix.dim() != 3 or k_prefix.shape != v_prefix.shape or k_prefix.dtype != k.dtype or \
+                v_prefix.dtype != k.dtype or k_prefix.shape[0] != d.n_kv_heads or k_prefix.shape[2] != d.head_dim or \
+                k_prefix.stride(2) != 1 or v_prefix.stride(2) != 1:
+            _refuse(f"{name}: k_prefix and v_prefix must be {k.dtype} [{d.n_kv_heads}][P][{d.head_dim}] with a contiguous last axis")
+        ps = (ctypes.c_int64 * 4)(*(t.stride(i) if t.shape[i] > 1 else 0 for t in (k_prefix, v_prefix) for i in (0, 1)))
+        return d, ps, rl_shared_prefix_workspace(d, k_prefix.shape[1])
+
+    d, ps, need = _plan(name, scale, (q, k, v, res, k_prefix, v_prefix), make)
+    B, Hq, _ = q.shape
+    lse = _buffer(o, "lse", (B, Hq), q, torch.float32, stream, name)
+    _int32(name, "kv_len", kv_len, (B,))
     if err is not None:
         _int32(name, "err", err, (1,))
-    if k_prefix.dim() != 3 or k_prefix.shape != v_prefix.shape or k_prefix.dtype != k.dtype or \
-            v_prefix.dtype != k.dtype or k_prefix.shape[0] != d.n_kv_heads or k_prefix.shape[2] != d.head_dim or \
-            k_prefix.stride(2) != 1 or v_prefix.stride(2) != 1:
-        _refuse(f"{name}: k_prefix and v_prefix must be {k.dtype} [{d.n_kv_heads}][P][{d.head_dim}] with a contiguous last axis")
-    P = k_prefix.shape[1]
-    ps = (ctypes.c_int64 * 4)(*(t.stride(i) if t.shape[i] > 1 else 0 for t in (k_prefix, v_prefix) for i in (0, 1)))
     if workspace is None:
-        workspace = _buffer({}, "workspace", (rl_shared_prefix_workspace(d, P),), q, torch.uint8, stream, name)
-    _run(dev, stream, _lib.rl_shared_prefix_attention, d, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(), P, ps,
-         k.data_ptr(), v.data_ptr(), kv_len.data_ptr(), res.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-         workspace.numel() * workspace.element_size(), _addr(err))
+        workspace = _buffer({}, "workspace", (need,), q, torch.uint8, stream, name)
+    _run(dev, stream, _lib.rl_shared_prefix_attention, d, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
+         k_prefix.shape[1], ps, k.data_ptr(), v.data_ptr(), kv_len.data_ptr(), res.data_ptr(), lse.data_ptr(),
+         workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(err))
     return o
 
 

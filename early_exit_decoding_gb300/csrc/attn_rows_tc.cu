@@ -317,18 +317,18 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int ks = 1; ks < kKeys / 16; ++ks) mma_ts(t_o(g), t_s(g) + ks * 8, v + ks * (2048 >> 4), idO, 1, el);
       };
-      bool go = wait_warp(&bar.full[0], 0);
+      // (every lane polls; no vote: the waits are on the products' path)
+      bool go = wait(&bar.full[0], 0);
       if (go) {
         scores(0, 0);
         if (ngrp == 2) scores(1, 0);
         commit(&bar.empty[0], el);
       }
+      if (go) go = wait(&bar.full[1 % NST], 0) && (nt == 1 || wait(&bar.full[2 % NST], (2 / NST) & 1));
       for (int j = 0; j < nt && go; ++j) {
         const int iv = 2 * j + 1, ik = 2 * j + 2;
         const bool more = j + 1 < nt;
-        if (!(go = wait_warp(&bar.full[iv % NST], (iv / NST) & 1))) break;
-        if (more && !(go = wait_warp(&bar.full[ik % NST], (ik / NST) & 1))) break;
-        if (!(go = wait_warp(&bar.p_full[0], j & 1))) break;
+        if (!(go = wait(&bar.p_full[0], j & 1))) break;
         fence_after();
         values(0, j);
         if (more)
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         else
           commit(&bar.o_full[0], el);
         if (ngrp == 2) {
-          if (!(go = wait_warp(&bar.p_full[1], j & 1))) break;
+          if (!(go = wait(&bar.p_full[1], j & 1))) break;
           fence_after();
           values(1, j);
         }
@@ -344,6 +344,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (more) {
           if (ngrp == 2) scores(1, j + 1);
           commit(&bar.empty[ik % NST], el);
+          // the next tiles, while the products issued run
+          go = wait(&bar.full[(iv + 2) % NST], ((iv + 2) / NST) & 1) &&
+               (j + 2 >= nt || wait(&bar.full[(ik + 2) % NST], ((ik + 2) / NST) & 1));
         } else if (ngrp == 2) {
           commit(&bar.o_full[1], el);
         }

@@ -129,42 +129,19 @@ __device__ __forceinline__ Part join(Part x, Part y) {
   return Part{m, x.s + y.s, x.t + y.t};
 }
 
-// A warp's candidate list: `cnt` keys, of which those above `thr` matter.
-struct Cand {
-  unsigned long long* list;
-  unsigned long long thr;
-  float thr_f;
-  int cnt;
-};
-
 __device__ __forceinline__ float value_of(unsigned long long key) {
   const uint32_t o = (uint32_t)(key >> 32);
   return __uint_as_float((o & 0x80000000u) ? (o & 0x7fffffffu) : ~o);
 }
 
-// Keeps the k largest keys of the list, largest first.
-__device__ __noinline__ void cut_list(Cand& c, int k, int lane) {
+// Keeps the k largest of the list's cnt keys, largest first; returns how many.
+__device__ __noinline__ int cut_list(unsigned long long* list, int cnt, int k, int lane) {
   __syncwarp();
-  if (c.cnt <= 32) {  // one key a lane: its place is the number of larger ones
-    const unsigned long long v = lane < c.cnt ? c.list[lane] : 0ull;
-    int rank = 0;
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i) rank += __shfl_sync(0xffffffffu, v, i) > v;
-    __syncwarp();
-    if (v != 0 && rank < k) c.list[rank] = v;
-    c.cnt = min(k, c.cnt);
-    __syncwarp();
-    if (c.cnt == k) {
-      c.thr = c.list[k - 1];
-      c.thr_f = value_of(c.thr);
-    }
-    return;
-  }
   unsigned long long v[kLpCap / 32];
 #pragma unroll
-  for (int i = 0; i < kLpCap / 32; ++i) v[i] = lane + 32 * i < c.cnt ? c.list[lane + 32 * i] : 0ull;
+  for (int i = 0; i < kLpCap / 32; ++i) v[i] = lane + 32 * i < cnt ? list[lane + 32 * i] : 0ull;
   __syncwarp();
-  const int n = min(k, c.cnt);
+  const int n = min(k, cnt);
   unsigned long long last = ~0ull, mine = 0;
   for (int r = 0; r < n; ++r) {  // keys differ, so "below the last one" is the rest
     unsigned long long b = 0;
@@ -173,23 +150,50 @@ __device__ __noinline__ void cut_list(Cand& c, int k, int lane) {
     last = warp_max_u64(b);
     if (lane == r) mine = last;
   }
-  if (lane < n) c.list[lane] = mine;
-  c.cnt = n;
-  if (n == k) {
-    c.thr = last;
-    c.thr_f = value_of(last);
-  }
+  if (lane < n) list[lane] = mine;
   __syncwarp();
+  return n;
 }
 
-// The lanes' logits v at ids `id` that may be candidates join the list.
-__device__ __noinline__ void push(Cand& c, float v, int id, bool may, int k, int lane) {
-  const unsigned long long key = order_key(v, id);
-  const bool take = may && key > c.thr;
+// The k-th largest of the lanes' values (0: none).
+__device__ __forceinline__ uint32_t kth_of_lanes(uint32_t v, int k, int lane) {
+  int rank = 0;
+#pragma unroll 8
+  for (int i = 0; i < 32; ++i) {
+    const uint32_t q = __shfl_sync(0xffffffffu, v, i);
+    rank += q > v || (q == v && i < lane);
+  }
+  const unsigned who = __ballot_sync(0xffffffffu, rank == k - 1);
+  return __shfl_sync(0xffffffffu, v, __ffs(who) - 1);
+}
+
+// The lanes' keys that reach `least` in their value join sel (counted in *n,
+// beyond kLpSel counted only).
+constexpr int kLpSel = 64;
+__device__ __forceinline__ void select(unsigned long long key, uint32_t least, unsigned long long* sel, int* n, int lane) {
+  const bool take = key != 0 && (uint32_t)(key >> 32) >= least;
   const unsigned mask = __ballot_sync(0xffffffffu, take);
-  if (take) c.list[c.cnt + __popc(mask & ((1u << lane) - 1))] = key;
-  c.cnt += __popc(mask);
-  if (c.cnt > kLpCap - 32) cut_list(c, k, lane);
+  if (!mask) return;
+  int at = 0;
+  if (lane == __ffs(mask) - 1) at = atomicAdd(n, __popc(mask));
+  at = __shfl_sync(0xffffffffu, at, __ffs(mask) - 1) + __popc(mask & ((1u << lane) - 1));
+  if (take && at < kLpSel) sel[at] = key;
+}
+// One warp: the k largest of sel's n <= kLpSel keys in order, zeros behind
+// (a key's place is the number of larger ones: the order they came in is immaterial).
+__device__ __forceinline__ void rank_sel(const unsigned long long* sel, int n, int k, unsigned long long* out, int lane) {
+  const unsigned long long a = lane < n ? sel[lane] : 0ull, b = lane + 32 < n ? sel[lane + 32] : 0ull;
+  int ra = 0, rb = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const unsigned long long x = sel[i];
+    ra += x > a;
+    rb += x > b;
+  }
+  if (lane >= n && lane < k) out[lane] = 0ull;
+  if (a != 0 && ra < k) out[ra] = a;
+  if (b != 0 && rb < k) out[rb] = b;
+  __syncwarp();
 }
 
 // Adds one logit to a part whose m is already at least as large.
@@ -208,7 +212,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
   __shared__ Part s_part[kLpWarps];
   __shared__ Part s_cta;
   __shared__ unsigned long long s_list[kTop ? kLpWarps : 1][kTop ? kLpCap : 1];
-  __shared__ uint32_t s_w[32];  // the warps' four largest lane maxima
+  __shared__ uint32_t s_w[32];  // four large values of each warp
+  __shared__ unsigned long long s_sel[kTop ? kLpSel : 1];
+  __shared__ int s_n;
   __shared__ unsigned long long s_top[kTop ? 32 : 1];
 
   const int row = blockIdx.x / split, part = blockIdx.x % split;
@@ -231,6 +237,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
     mbar_expect_tx(&full[warp][st], n * 16);
     bulk_g2s(ring + st * kLpTile * 16, xv + (long long)at * VEC, n * 16, &full[warp][st]);
   };
+  if (tid == 0) s_n = 0;
   if (lane == 0) {
     for (int i = 0; i < kLpStages; ++i) mbar_init(&full[warp][i], 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -285,7 +292,33 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
     return m;
   };
 
-  Cand c{kTop ? s_list[warp] : nullptr, 0ull, -INFINITY, 0};
+  // This warp's candidates: `cnt` keys above `thr` (thr_f: its value).
+  unsigned long long* const list = s_list[kTop ? warp : 0];
+  unsigned long long thr = 0;
+  float thr_f = -INFINITY;
+  int cnt = 0;
+  auto push = [&](unsigned long long key, bool may) {
+    const bool take = may && key > thr;
+    const unsigned mask = __ballot_sync(0xffffffffu, take);
+    if (take) list[cnt + __popc(mask & ((1u << lane) - 1))] = key;
+    cnt += __popc(mask);
+    if (cnt > kLpCap - 32) {
+      cnt = cut_list(list, cnt, k, lane);  // (more than k were there)
+      thr = list[k - 1];
+      thr_f = value_of(thr);
+    }
+  };
+  // The four largest of the lanes' values to s_w.
+  auto publish4 = [&](uint32_t v) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = __reduce_max_sync(0xffffffffu, v);
+      if (lane == __ffs(__ballot_sync(0xffffffffu, v == w)) - 1) {
+        s_w[4 * warp + i] = w;
+        v = 0;
+      }
+    }
+  };
   if constexpr (kTop) {
     uint32_t o = 0;
     if (warp < ntile) {
@@ -293,29 +326,14 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
       o = order_bits(max_nan(max_nan(vec_max(vec(warp, 0, 0)), vec_max(vec(warp, 0, 1))),
                              max_nan(vec_max(vec(warp, 0, 2)), vec_max(vec(warp, 0, 3)))));
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t w = __reduce_max_sync(0xffffffffu, o);
-      if (lane == __ffs(__ballot_sync(0xffffffffu, o == w)) - 1) {
-        s_w[4 * warp + i] = w;
-        o = 0;
-      }
-    }
+    publish4(o);
     __syncthreads();
-    const uint32_t mine = s_w[lane];
-    int rank = 0;
-#pragma unroll 8
-    for (int i = 0; i < 32; ++i) {
-      const uint32_t q = __shfl_sync(0xffffffffu, mine, i);
-      rank += q > mine || (q == mine && i < lane);
-    }
-    const unsigned who = __ballot_sync(0xffffffffu, rank == k - 1);
-    const uint32_t kth = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+    const uint32_t kth = kth_of_lanes(s_w[lane], k, lane);
     if (kth) {
-      c.thr = ((unsigned long long)kth << 32) - 1;
-      c.thr_f = value_of((unsigned long long)kth << 32);
+      thr = ((unsigned long long)kth << 32) - 1;
+      thr_f = value_of((unsigned long long)kth << 32);
     }
-    if (warp == 0) push(c, edge_v, edge, edge >= 0, k, lane);
+    if (warp == 0) push(order_key(edge_v, edge), edge >= 0);
   }
 
   // After a wait that gave up nothing is copied or computed any more; the
@@ -341,17 +359,20 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
 #pragma unroll
         for (int e = 0; e < VEC; ++e) add(p, E::get(cur[j], e), mu);
       if constexpr (kTop) {
-        if (__any_sync(0xffffffffu, !(tm < c.thr_f))) {
-#pragma unroll 1
-          for (int j = 0; j < kLpVecs; ++j) {
-            const uint4 w = vec(i, st, j);
-            if (!__any_sync(0xffffffffu, !(vec_max(w) < c.thr_f))) continue;
-            const int at = v0 + i * kLpTile + j * 32 + lane;
+        if (__any_sync(0xffffffffu, !(tm < thr_f))) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float v = E::get(w, e);
-              const bool hit = at < v1 && !(v < c.thr_f);
-              if (__any_sync(0xffffffffu, hit)) push(c, v, head + at * VEC + e, hit, k, lane);
+          for (int j = 0; j < kLpVecs; ++j) {
+            const int at = v0 + i * kLpTile + j * 32 + lane;
+            uint32_t hits = 0;  // elements of the vector that may be candidates
+            if (at < v1 && !(vm[j] < thr_f)) {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e) hits |= !(E::get(cur[j], e) < thr_f) ? 1u << e : 0u;
+            }
+            while (__any_sync(0xffffffffu, hits != 0)) {
+              const int e = hits ? __ffs(hits) - 1 : 0;
+              const float v = E::load(reinterpret_cast<const T*>(ring + (st * kLpTile + j * 32 + lane) * 16) + e);
+              push(order_key(v, head + at * VEC + e), hits != 0);
+              hits &= hits - 1;
             }
           }
         }
@@ -371,11 +392,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
     p = join(p, Part{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
                      __shfl_xor_sync(0xffffffffu, p.t, o)});
   if (lane == 0) s_part[warp] = p;
-  if constexpr (kTop) {
-    cut_list(c, k, lane);
-    for (int i = c.cnt + lane; i < k; i += 32) c.list[i] = 0ull;
-  }
-  __syncthreads();
   // `src(i)`: list of k keys, largest first, zeros behind; the k largest of n lists in order
   auto merge = [&](auto src, int n, unsigned long long* out) {
     int at = 0;
@@ -387,6 +403,31 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
     }
     __syncwarp();
   };
+  // The lists' k largest: those that reach the k-th largest of four candidates
+  // of each warp (k at least do; seldom many more) are ranked by one warp.
+  if constexpr (kTop) {
+    __syncwarp();
+    unsigned long long v[kLpCap / 32];
+    uint32_t o = 0;
+#pragma unroll
+    for (int q = 0; q < kLpCap / 32; ++q) {
+      v[q] = lane + 32 * q < cnt ? list[lane + 32 * q] : 0ull;
+      o = max(o, (uint32_t)(v[q] >> 32));
+    }
+    __syncthreads();  // (every warp has read the first threshold's values)
+    publish4(o);
+    __syncthreads();
+    const uint32_t least = kth_of_lanes(s_w[lane], k, lane);
+#pragma unroll
+    for (int q = 0; q < kLpCap / 32; ++q)
+      if (32 * q < cnt) select(v[q], least, s_sel, &s_n, lane);
+    __syncthreads();
+    if (s_n > kLpSel) {
+      cnt = cut_list(list, cnt, k, lane);
+      for (int q = cnt + lane; q < k; q += 32) list[q] = 0ull;
+    }
+  }
+  __syncthreads();
   if (warp == 0) {
     p = lane < kLpWarps ? s_part[lane] : Part{-INFINITY, 0.f, 0.f};
 #pragma unroll
@@ -394,42 +435,66 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
       p = join(p, Part{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
                        __shfl_xor_sync(0xffffffffu, p.t, o)});
     if (lane == 0) s_cta = p;
-    if constexpr (kTop) merge([&](int i) { return s_list[i]; }, kLpWarps, s_top);
+    if constexpr (kTop) {
+      if (s_n <= kLpSel)
+        rank_sel(s_sel, s_n, k, s_top, lane);
+      else
+        merge([&](int i) { return s_list[i]; }, kLpWarps, s_top);
+    }
   }
   __shared__ float s_res[2];
   if (split > 1) {
     asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-    if (part == 0 && warp == 0) {
+    if (part == 0) {
       auto remote = [&](const void* q, int rank) {
         uint32_t r;
         asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(q)), "r"(rank));
         return r;
       };
-      p = Part{-INFINITY, 0.f, 0.f};
-      if (lane < split) {
-        const uint32_t at = remote(&s_cta, lane);
-        asm volatile("ld.shared::cluster.f32 %0, [%3];\nld.shared::cluster.f32 %1, [%3+4];\nld.shared::cluster.f32 %2, [%3+8];"
-                     : "=f"(p.m), "=f"(p.s), "=f"(p.t)
-                     : "r"(at)
-                     : "memory");
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1)
-        p = join(p, Part{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
-                         __shfl_xor_sync(0xffffffffu, p.t, o)});
-      if constexpr (kTop) {
-        // (the warps' lists are merged: their memory takes the CTAs')
-        auto s_all = reinterpret_cast<unsigned long long(*)[32]>(&s_list[0][0]);
-        static_assert(kLpMaxSplit * 32 <= kLpWarps * kLpCap, "the CTAs' lists must fit");
-        for (int i = 0; i < split; ++i) {
-          if (lane < k) {
-            unsigned long long v;
-            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(&s_top[lane], i)) : "memory");
-            s_all[i][lane] = v;
-          }
+      if (warp == 0) {
+        p = Part{-INFINITY, 0.f, 0.f};
+        if (lane < split) {
+          const uint32_t at = remote(&s_cta, lane);
+          asm volatile("ld.shared::cluster.f32 %0, [%3];\nld.shared::cluster.f32 %1, [%3+4];\nld.shared::cluster.f32 %2, [%3+8];"
+                       : "=f"(p.m), "=f"(p.s), "=f"(p.t)
+                       : "r"(at)
+                       : "memory");
         }
-        __syncwarp();
-        merge([&](int i) { return s_all[i]; }, split, s_top);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          p = join(p, Part{__shfl_xor_sync(0xffffffffu, p.m, o), __shfl_xor_sync(0xffffffffu, p.s, o),
+                           __shfl_xor_sync(0xffffffffu, p.t, o)});
+      }
+      if constexpr (kTop) {
+        // the CTAs' lists: one key a thread (two at most), then as the warps' above
+        auto s_all = &s_list[0][0];  // (the warps' lists are done with)
+        static_assert(kLpMaxSplit * 32 <= kLpWarps * kLpCap && kLpMaxSplit * 32 <= 2 * kLpThreads, "the CTAs' lists must fit");
+        unsigned long long v[2] = {0ull, 0ull};
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          const int at = tid + q * kLpThreads;
+          if (at < split * k)
+            asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v[q]) : "r"(remote(&s_top[at % k], at / k)) : "memory");
+        }
+        __syncthreads();  // (warp 0 has ranked the CTA's own: s_sel, s_n and the lists are free)
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (tid + q * kLpThreads < split * k) s_all[tid + q * kLpThreads] = v[q];
+        if (tid == 0) s_n = 0;
+        __syncthreads();
+        const int each = 32 / split;  // (split is a power of two up to 16)
+        const int li = lane / each, le = lane % each;
+        const uint32_t least = kth_of_lanes(le < k ? (uint32_t)(s_all[li * k + le] >> 32) : 0u, k, lane);
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+          if (q * kLpThreads + warp * 32 < split * k) select(v[q], least, s_sel, &s_n, lane);
+        __syncthreads();
+        if (warp == 0) {
+          if (s_n <= kLpSel)
+            rank_sel(s_sel, s_n, k, s_top, lane);
+          else
+            merge([&](int i) { return s_all + i * k; }, split, s_top);
+        }
       }
     }
     // nobody leaves while its shared memory may still be read

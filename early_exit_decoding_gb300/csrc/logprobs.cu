@@ -84,6 +84,9 @@ struct Elem<float> {
   static constexpr int kVec = 4;
   static constexpr uint32_t kNegInf = 0xff800000u;  // -infinity in every element
   static __device__ __forceinline__ float get(const uint4& v, int e) { return __uint_as_float(u4get(v, e)); }
+  static __device__ __forceinline__ float largest(const uint4& v) {
+    return max_nan(max_nan(get(v, 0), get(v, 1)), max_nan(get(v, 2), get(v, 3)));
+  }
   static __device__ __forceinline__ float load(const float* p) { return *p; }
 };
 template <>
@@ -94,6 +97,13 @@ struct Elem<bf16> {
     const uint32_t w = u4get(v, e >> 1);
     return __uint_as_float((e & 1) ? (w & 0xffff0000u) : (w << 16));
   }
+  static __device__ __forceinline__ float largest(const uint4& v) {  // (pairs at a time; exact)
+    uint32_t m, n;
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
+    asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+  }
   static __device__ __forceinline__ float load(const bf16* p) { return __bfloat162float(*p); }
 };
 template <>
@@ -103,6 +113,13 @@ struct Elem<__half> {
   static __device__ __forceinline__ float get(const uint4& v, int e) {
     const uint32_t w = u4get(v, e >> 1);
     return __half2float(__ushort_as_half((unsigned short)((e & 1) ? w >> 16 : w & 0xffffu)));
+  }
+  static __device__ __forceinline__ float largest(const uint4& v) {
+    uint32_t m, n;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(v.x), "r"(v.y));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(n) : "r"(v.z), "r"(v.w));
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(m) : "r"(m), "r"(n));
+    return max_nan(get(make_uint4(m, 0, 0, 0), 0), get(make_uint4(m, 0, 0, 0), 1));
   }
   static __device__ __forceinline__ float load(const __half* p) { return __half2float(*p); }
 };
@@ -196,6 +213,30 @@ __device__ __forceinline__ void rank_sel(const unsigned long long* sel, int n, i
   __syncwarp();
 }
 
+// Two fp32 operations an instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)));
+  return *reinterpret_cast<float2*>(&d);
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;"
+      : "=l"(d)
+      : "l"(*reinterpret_cast<unsigned long long*>(&a)), "l"(*reinterpret_cast<unsigned long long*>(&b)),
+        "l"(*reinterpret_cast<unsigned long long*>(&c)));
+  return *reinterpret_cast<float2*>(&d);
+}
+
 // Adds one logit to a part whose m is already at least as large.
 __device__ __forceinline__ void add(Part& p, float x, float mu) {
   const float d = max_nan(x - mu, -1e30f), e = ex2(d * kLog2e);
@@ -285,12 +326,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
                ? *reinterpret_cast<const uint4*>(ring + (st * kLpTile + j * 32 + lane) * 16)
                : make_uint4(E::kNegInf, E::kNegInf, E::kNegInf, E::kNegInf);
   };
-  auto vec_max = [&](const uint4& v) {
-    float m = E::get(v, 0);
-#pragma unroll
-    for (int e = 1; e < VEC; ++e) m = max_nan(m, E::get(v, e));
-    return m;
-  };
+  auto vec_max = [&](const uint4& v) { return E::largest(v); };
 
   // This warp's candidates: `cnt` keys above `thr` (thr_f: its value).
   unsigned long long* const list = s_list[kTop ? warp : 0];
@@ -336,6 +372,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
     if (warp == 0) push(order_key(edge_v, edge), edge >= 0);
   }
 
+  if constexpr (!kTop) {
+    // a common start keeps the warps' neighbouring tiles together in time
+    // (4096 rows of 128,256 fp32 logits: 392 -> 330 us)
+    if (warp < ntile) wait(0, 0);
+    __syncthreads();
+  }
   // After a wait that gave up nothing is copied or computed any more; the
   // copies already in flight are still waited for (`stop`).
   int st = 0, ph = 0, stop = ok ? ntile : min(ntile, warp + kLpStages * kLpWarps);
@@ -353,11 +395,21 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
       const float tm = max_nan(max_nan(vm[0], vm[1]), max_nan(vm[2], vm[3]));
       const float mn = fmaxf(p.m, tm);
       if (mn > p.m) rebase(p, mn);
-      const float mu = pivot(p.m);
+      const float2 mu = make_float2(-pivot(p.m), -pivot(p.m)), l2e = make_float2(kLog2e, kLog2e);
+      float2 s2 = make_float2(p.s, 0.f), t2 = make_float2(p.t, 0.f);
 #pragma unroll
       for (int j = 0; j < kLpVecs; ++j)
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) add(p, E::get(cur[j], e), mu);
+        for (int e = 0; e < VEC; e += 2) {  // as add(), two logits at a time
+          float2 d = add2(make_float2(E::get(cur[j], e), E::get(cur[j], e + 1)), mu);
+          d = make_float2(max_nan(d.x, -1e30f), max_nan(d.y, -1e30f));
+          float2 x = mul2(d, l2e);
+          x = make_float2(ex2(x.x), ex2(x.y));
+          s2 = add2(s2, x);
+          t2 = fma2(d, x, t2);
+        }
+      p.s = s2.x + s2.y;
+      p.t = t2.x + t2.y;
       if constexpr (kTop) {
         if (__any_sync(0xffffffffu, !(tm < thr_f))) {
 #pragma unroll
@@ -526,11 +578,12 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
   }
 }
 
-// CTAs a row is split over: one while the rows fill the GPU's resident CTAs;
-// else as many as do, not below one tile a warp.
+// CTAs a row is split over: as many as give every SM two (a cluster's start and
+// join cost about 3 us: 64 rows of 128,256 fp32 logits took 15.9 us in 4 parts,
+// 17.4 in 8; 256 rows 24.6 in one, 45 in 2), not below one tile a warp.
 int pick_split(int rows, long long vecs, int sm_count) {
   int s = 1;
-  while (s < kLpMaxSplit && rows * s * 2 <= kLpResident * sm_count && vecs > (long long)s * kLpWarps * kLpTile) s *= 2;
+  while (s < kLpMaxSplit && rows * s * 2 <= 2 * sm_count && vecs > (long long)s * kLpWarps * kLpTile) s *= 2;
   return s;
 }
 

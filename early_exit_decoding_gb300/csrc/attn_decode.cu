@@ -32,14 +32,15 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 16;        // keys a warp takes at a time
 constexpr int kRows = 16;        // query rows of a tile
-constexpr int kMaxSplit = 16;    // CTAs of a cluster
+constexpr int kMaxSplit = 12;    // CTAs of a cluster
 constexpr int kSpin = 1 << 21;  // polls of a wait (each may suspend) before it gives up
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int HD>
 constexpr int kStageBytes = 2 * kUnit * HD * 2;  // K and V rows of a unit
 template <int HD>
-constexpr int kStages = HD == 128 ? 3 : 6;
+constexpr int kStages = HD == 128 ? 2 : 4;  // (with 3 and 6 two CTAs share an SM instead of three:
+                                             // 64 ragged 4k windows 143 us, not 127)
 template <int HD>
 constexpr int kSmem = kWarps * kStages<HD> * kStageBytes<HD> + 1024;
 
@@ -69,7 +70,7 @@ __device__ __forceinline__ uint32_t load_q2(const AttnOpArgs& a, const Tile& t, 
 }
 
 template <int HD, bool F16>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, 3)
     k_attn_decode(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnOpArgs a, int split, int tiles,
                   int presplit) {
   constexpr int NST = kStages<HD>, SB = kStageBytes<HD>;
@@ -336,16 +337,16 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (a.P > 0) {
       const long long step = (long long)prefix_rows((a.B * t.rep + 255) / 256, a.B * t.rep) * HD;
       const float* src = ws.o + pq * HD + (((2 * lane) >> 2) ^ (pq & (HD / 4 - 1) & 15)) * 4 + (2 * lane & 3);
-      for (int c0 = 0; c0 < presplit; c0 += 4) {  // four parts' loads in flight together
-        float2 v[4][HD / 64];
+      for (int c0 = 0; c0 < presplit; c0 += 8) {  // eight parts' loads in flight together
+        float2 v[8][HD / 64];
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
+        for (int c = 0; c < 8; ++c)
 #pragma unroll
           for (int i2 = 0; i2 < HD / 64; ++i2)
             v[c][i2] = *reinterpret_cast<const float2*>(src + min(c0 + c, presplit - 1) * step +
                                                         (HD == 128 ? 64 * (i2 ^ ((pq >> 4) & 1)) : 0));
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < 8; ++c) {
           const float fc = __shfl_sync(0xffffffffu, fp, (c0 + c) & 31);
           if (c0 + c >= presplit || fc == 0.f) continue;
 #pragma unroll
@@ -394,13 +395,15 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
 }
 
-// CTAs a row tile's keys are split over.  Enough that the cluster's warps have
-// a few units each, and more while the tiles alone do not fill the GPU.
+// CTAs a row tile's keys are split over: as many as keep all of them within two
+// a SM, a unit for each warp.  More only queue clusters behind one another:
+// head_dim 128, window 2048, 8 KV heads: one sequence 27.9 us in 1 part, 13.7 in
+// 4, 11.1 in 8, 10.0 in 12, 11.3 in 16; 8 sequences 28.5, 16.8, 25.6, 25.4,
+// 43.1; 32 sequences 45 us in 1 part, 60 in 2.
 int pick_split(long long tiles, int keys, int sm_count) {
   const int units = (keys + kUnit - 1) / kUnit;
-  int s = 1;
-  while (s < kMaxSplit && units > s * kWarps && (tiles * s < 2ll * sm_count || units > s * kWarps * 32)) s *= 2;
-  return s;
+  const long long s = min(2ll * sm_count / tiles, (long long)(units + kWarps - 1) / kWarps);
+  return (int)max(1ll, min(s, (long long)kMaxSplit));
 }
 
 template <int HD, bool F16>

@@ -18,7 +18,10 @@ namespace river {
 using namespace attn;
 
 cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s) {
-  if (a.Tq * (a.Hq / a.Hkv) <= 64) return launch_attn_decode(a, false, s);
+  // up to 16 rows of a KV head (one m16 tile) are the few-row kernel's; with more
+  // it would read the keys once a tile (8 sequences, window 2048, head_dim 128,
+  // 4 rows: 17 us against 21; 20 rows: 28 against 23; 64 rows: 55 against 26)
+  if ((long long)a.Tq * (a.Hq / a.Hkv) <= 16) return launch_attn_decode(a, false, s);
   return launch_attn_rows_tc(a, false, s);
 }
 

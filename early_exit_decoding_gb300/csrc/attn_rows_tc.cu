@@ -626,15 +626,31 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   if (e == cudaSuccess) e = device_sm_count(dev, &sms);
   if (e != cudaSuccess) return e;
   auto kern = k_attn_rows_tc<HD, F16, PREFIX>;
+  const int* clusters = nullptr;  // that fit the GPU at once, by their CTAs (fixed once set)
   {
     static std::mutex mu;
     static bool done[kOpDevices] = {};
+    static int room[kOpDevices][kMaxSplit + 1];
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<HD>);
+      for (int c = 1; c <= kMaxSplit && !PREFIX && e == cudaSuccess; ++c) {
+        cudaLaunchConfig_t q = {};
+        q.gridDim = dim3(c);
+        q.blockDim = dim3(kThreads);
+        q.dynamicSmemBytes = kSmem<HD>;
+        cudaLaunchAttribute at[1];
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = c;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        q.attrs = at;
+        q.numAttrs = 1;
+        e = cudaOccupancyMaxActiveClusters(&room[dev][c], kern, &q);
+      }
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
+    clusters = room[dev];
   }
   KvMaps maps;
   const bool got = PREFIX ? make_kv_maps(&maps, a.pre, a.f16 != 0, 1, a.Hkv, HD, a.P, kKeys)
@@ -648,9 +664,20 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   if (PREFIX) {
     split = prefix_split(a.B, rep, a.Hkv, a.P);
   } else {
-    // as many as fill the SMs (one CTA each), no CTA below one tile
+    // the count with the least time by this model (clocks, measured): rounds of
+    // clusters, each a CTA's start and end, its tiles of 128 keys, a cluster's join
     const long long keys = min((long long)a.cap, (long long)a.window + min(a.Tq, kRowsCta / rep + 2) + a.sinks);
-    while (split < kMaxSplit && ctas * split * 2 <= sms && (keys + kKeys - 1) / kKeys >= split * 2) split *= 2;
+    const long long nt = (keys + kKeys - 1) / kKeys;
+    double least = 0;
+    for (int c = 1; c <= kMaxSplit && c <= nt; ++c) {
+      if (clusters[c] < 1) continue;
+      const double t = (double)((ctas + clusters[c] - 1) / clusters[c]) *
+                       (10000 + (double)((nt + c - 1) / c) * (rows > 128 ? 3400 : 2500) + (c > 1 ? 6000 : 0));
+      if (c == 1 || t < least) {
+        split = c;
+        least = t;
+      }
+    }
   }
   if (ctas * split >= (1ll << 31)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};

@@ -33,7 +33,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 16;        // keys a warp takes at a time
 constexpr int kRows = 16;        // query rows of a tile
 constexpr int kMaxSplit = 12;    // CTAs of a cluster
-constexpr int kSpin = 1 << 21;  // polls of a wait (each may suspend) before it gives up
+constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int HD>
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   // copies already in flight are still waited for (`stop`).
   int st = 0, ph = 0, stop = units;
   for (int u = first; u < stop; u += W) {
-    const bool got = mbar_wait(&full[warp][st], ph, kSpin);
+    const bool got = mbar_wait_lazy(&full[warp][st], ph, kWaitNs);
     if (!__all_sync(0xffffffffu, got) && ok) {
       ok = false;
       stop = min(units, u + NST * W);

@@ -53,6 +53,27 @@ __device__ __forceinline__ bool mbar_wait_for(uint64_t* b, uint32_t parity, unsi
     if (t - t0 > ns) return false;
   }
 }
+// The same for waits that are nearly always short and whose loop is on a
+// kernel's critical path: some polls first, then the timed wait (a read of the
+// clock costs near a thousand cycles), out of line.  `stop` (nullable): another
+// thread gave up.
+static __device__ __noinline__ bool mbar_wait_long(uint64_t* b, uint32_t parity, unsigned long long ns, const volatile int* stop) {
+  unsigned long long t0, t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t0));
+  for (;;) {
+    for (int i = 0; i < 256; ++i)
+      if (mbar_try(b, parity)) return true;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    if (t - t0 > ns || (stop && *stop)) return false;
+  }
+}
+__device__ __forceinline__ bool mbar_wait_lazy(uint64_t* b, uint32_t parity, unsigned long long ns,
+                                               const volatile int* stop = nullptr) {
+#pragma unroll 1
+  for (int i = 0; i < 1024; ++i)
+    if (mbar_try(b, parity)) return true;
+  return mbar_wait_long(b, parity, ns, stop);
+}
 // 16-byte asynchronous copy global -> shared (the load path of ordinary
 // loads: it also reads mapped host memory).
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {

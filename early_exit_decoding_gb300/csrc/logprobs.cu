@@ -47,7 +47,7 @@ constexpr int kLpStages = 3;     // tiles of a warp's ring
 constexpr int kLpRing = kLpWarps * kLpStages * kLpTile * 16;
 constexpr int kLpCap = 96;       // candidates a warp's list holds (4 CTAs' shared memory fits an SM)
 constexpr int kLpMaxSplit = 16;  // CTAs of a row's cluster
-constexpr int kLpSpin = 1 << 21;  // polls of a wait (each may suspend) before it gives up
+constexpr unsigned long long kLpWaitNs = 2000000000ull;  // a wait gives up after two seconds
 constexpr float kLog2e = 1.4426950408889634f;
 static_assert(kLpWarps == 8 && kLpVecs == 4, "the first threshold takes four values of each of 8 warps");
 
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
 
   bool ok = true;
   auto wait = [&](int st, int ph) {
-    const bool got = mbar_wait(&full[warp][st], ph, kLpSpin);
+    const bool got = mbar_wait_lazy(&full[warp][st], ph, kLpWaitNs);
     if (!__all_sync(0xffffffffu, got) && ok) {
       ok = false;
       if (lane == 0 && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);

@@ -711,7 +711,7 @@ cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
 int prefix_split(int B, int rep, int Hkv, int P) {
   const long long rows = (long long)B * rep, tiles = (rows + kRowsCta - 1) / kRowsCta, items = tiles * Hkv;
   const long long nt = ((long long)P + kKeys - 1) / kKeys;
-  const double tile = rows > 128 ? 3900 : 2700;
+  const double tile = rows > 128 ? 3400 : 2500;
   int best = 1;
   double least = 0;
   for (int s = 1; s <= kMaxPrefixSplit && s <= nt; ++s) {

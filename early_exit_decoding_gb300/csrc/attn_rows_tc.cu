@@ -511,7 +511,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = i_row / rep, h = hk * rep + i_row % rep;
         const float inv = l == 0.f ? 0.f : 1.f / l;
         bool fin = true;
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + (mine ? b * a.os[0] + t * a.os[1] + h * a.os[2] : 0);
+        const long long row_at = mine ? b * a.os[0] + t * a.os[1] + h * a.os[2] : -1;
+        // through shared memory (over Q, which no product reads any more), so that
+        // whole rows are written, not 16 bytes of 32 rows at a time
+        constexpr int CR = HD / 8;  // 16-byte chunks of a row; chunk c of row q at c ^ (q & 7)
+        unsigned char* stage = sq + g * TB + (warp & 3) * (32 * HD * 2);
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
           float o[32];
@@ -530,15 +534,25 @@ __global__ void __launch_bounds__(kThreads, 1)
               fin = fin && isfinite(u0) && isfinite(v0);
               w[q] = pack2<F16>(u0, v0);
             }
-            if (mine) *reinterpret_cast<uint4*>(dst + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stage + lane * (HD * 2) + ((((c + e) / 8) ^ (lane & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int q = lane / CR; q < 32; q += 32 / CR) {
+          const long long at = __shfl_sync(0xffffffffu, row_at, q);
+          const int c = lane % CR;
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + q * (HD * 2) + ((c ^ (q & 7)) << 4));
+          if (at >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c * 8) = v;
         }
         if (mine && a.lse)
           a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
         // rows of different masks shared V's tiles: one that is not finite may
         // owe that to a key it does not see (0 * infinity)
         unsigned bad = __ballot_sync(0xffffffffu, mine && !fin);
-        if (s_fail) bad = 0;
+        if (__any_sync(0xffffffffu, s_fail)) bad = 0;  // (the same for every lane: exact_row shuffles)
+        if (bad) __syncwarp();  // the rows' first values, stored by other lanes, come before the new ones
         while (bad) {
           const int i = row0 + g * 128 + (warp & 3) * 32 + __ffs(bad) - 1;
           bad &= bad - 1;
@@ -606,7 +620,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
         if (lane == 0 && a.lse)
           a.lse[((long long)b * a.Tq + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-        if (!__all_sync(0xffffffffu, fin) && !s_fail) exact_row<HD, F16>(a, b, t, h, n, ql, lane);
+        if (__any_sync(0xffffffffu, !fin) && !__any_sync(0xffffffffu, s_fail)) {
+          __syncwarp();  // (its stores come after those above)
+          exact_row<HD, F16>(a, b, t, h, n, ql, lane);
+        }
       }
       if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
     }
@@ -712,10 +729,11 @@ int prefix_split(int B, int rep, int Hkv, int P) {
   const long long rows = (long long)B * rep, tiles = (rows + kRowsCta - 1) / kRowsCta, items = tiles * Hkv;
   const long long nt = ((long long)P + kKeys - 1) / kKeys;
   const double tile = rows > 128 ? 3400 : 2500;
+  const double part = 0.5 * attn::prefix_rows((int)tiles, rows);
   int best = 1;
   double least = 0;
   for (int s = 1; s <= kMaxPrefixSplit && s <= nt; ++s) {
-    const double t = (double)((items * s + 151) / 152) * (10000 + (double)((nt + s - 1) / s) * tile) + 130.0 * items * s;
+    const double t = (double)((items * s + 151) / 152) * (10000 + (double)((nt + s - 1) / s) * tile) + part * items * s;
     if (s == 1 || t < least) {
       best = s;
       least = t;

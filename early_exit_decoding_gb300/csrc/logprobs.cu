@@ -302,9 +302,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
   int edge = -1;  // id of this lane's edge logit
   float edge_v = -INFINITY;
   if (warp == 0) {
-    const int tail = head + nvec * VEC + lane - 16;
+    const int rest = V - head - nvec * VEC;
     if (part == 0 && lane < head) edge = lane;
-    if (part == split - 1 && lane >= 16 && tail < V) edge = tail;
+    if (part == split - 1 && lane >= 16 && lane - 16 < rest) edge = V - rest + (lane - 16);
     if (edge >= 0) {
       edge_v = E::load(x + edge);
       p.m = fmaxf(p.m, edge_v);
@@ -583,7 +583,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
 // 17.4 in 8; 256 rows 24.6 in one, 45 in 2), not below one tile a warp.
 int pick_split(int rows, long long vecs, int sm_count) {
   int s = 1;
-  while (s < kLpMaxSplit && rows * s * 2 <= 2 * sm_count && vecs > (long long)s * kLpWarps * kLpTile) s *= 2;
+  while (s < kLpMaxSplit && (long long)rows * s <= sm_count && vecs > (long long)s * kLpWarps * kLpTile) s *= 2;
   return s;
 }
 

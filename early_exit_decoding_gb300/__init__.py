@@ -719,6 +719,7 @@ def _strides(d, t):
 
 
 _PLANS = {}
+_INT32_MAX = 2**31 - 1
 
 
 def _plan(name, scale, tensors, make):
@@ -782,7 +783,7 @@ def window_attention(q, k, v, kv_len, window, sinks=0, q_len=None, scale=None, o
     if err is not None:
         _int32(name, "err", err, (1,))
     _run(dev, stream, _lib.rl_window_attention, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), kv_len.data_ptr(),
-         _addr(q_len), window, sinks, res.data_ptr(), lse.data_ptr(), _addr(err))
+         _addr(q_len), min(window, _INT32_MAX), min(sinks, _INT32_MAX), res.data_ptr(), lse.data_ptr(), _addr(err))
     return o
 
 
@@ -820,6 +821,8 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
         _int32(name, "err", err, (1,))
     if workspace is None:
         workspace = _buffer({}, "workspace", (need,), q, torch.uint8, stream, name)
+    elif not workspace.is_contiguous():
+        _refuse(f"{name}: workspace must be contiguous")
     _run(dev, stream, _lib.rl_shared_prefix_attention, d, q.data_ptr(), k_prefix.data_ptr(), v_prefix.data_ptr(),
          k_prefix.shape[1], ps, k.data_ptr(), v.data_ptr(), kv_len.data_ptr(), res.data_ptr(), lse.data_ptr(),
          workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(err))

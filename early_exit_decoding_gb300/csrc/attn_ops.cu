@@ -11,6 +11,8 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "attn_ops.cuh"
 
 namespace river {
@@ -43,11 +45,27 @@ using namespace river;
 
 namespace {
 
+constexpr int kMaxTokens = 1 << 30;  // of one source: key numbers a tile further stay in 31 bits
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 bool strides_ok(const int64_t* st, int n, int es, int64_t most) {
   for (int i = 0; i < n; ++i)
     if (st[i] < 0 || st[i] * es % 16 != 0 || st[i] >= most) return false;
+  return true;
+}
+
+// Whether the rows of `row` elements at these strides (extents n) are apart:
+// from the smallest stride on, each axis steps over all that lies within it.
+bool rows_apart(const int64_t* st, const int64_t* n, int row) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int x, int y) { return st[x] < st[y]; });
+  double span = row;
+  for (int i : order) {
+    if (n[i] == 1) continue;
+    if ((double)st[i] < span) return false;
+    span += (double)st[i] * (double)(n[i] - 1);
+  }
   return true;
 }
 
@@ -67,6 +85,7 @@ rl_status check_desc(const char* who, const rl_attn_desc* a, AttnOpArgs* o) {
     return bad(RL_ERR_INVALID_ARG, "batch, q_len, heads and kv_capacity must be >= 1");
   if (a->head_dim != 64 && a->head_dim != 128) return bad(RL_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
   if (a->n_q_heads % a->n_kv_heads) return bad(RL_ERR_UNSUPPORTED, "n_q_heads must be a multiple of n_kv_heads");
+  if (a->kv_capacity > kMaxTokens) return bad(RL_ERR_UNSUPPORTED, "kv_capacity must be at most 2^30");
   if ((long long)a->batch * a->q_len * a->n_q_heads >= (1ll << 31))
     return bad(RL_ERR_UNSUPPORTED, "batch * q_len * n_q_heads must be below 2^31");
   if (!(a->scale >= 0.f) || a->scale > 1e6f) return bad(RL_ERR_INVALID_ARG, "scale must be in [0, 1e6]");
@@ -75,6 +94,8 @@ rl_status check_desc(const char* who, const rl_attn_desc* a, AttnOpArgs* o) {
     return bad(RL_ERR_UNSUPPORTED, "q and out strides must be whole multiples of 16 bytes");
   if (!strides_ok(a->k_stride, 3, 2, 1ll << 39) || !strides_ok(a->v_stride, 3, 2, 1ll << 39))
     return bad(RL_ERR_UNSUPPORTED, "k and v strides must be whole multiples of 16 bytes, below 2^39 elements");
+  const int64_t n_out[3] = {a->batch, a->q_len, a->n_q_heads};
+  if (!rows_apart(a->out_stride, n_out, a->head_dim)) return bad(RL_ERR_INVALID_ARG, "rows of out overlap");
   memset(o, 0, sizeof(*o));
   o->q_f32 = a->q_dtype == RL_DT_F32;
   o->f16 = a->kv_dtype == RL_DT_F16;
@@ -135,6 +156,8 @@ extern "C" rl_status rl_shared_prefix_workspace(const rl_attn_desc* a, int32_t p
   if (st != RL_OK) return st;
   if (!bytes || prefix_len < 0)
     return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_workspace: bytes is NULL or prefix_len below 0");
+  if (prefix_len > kMaxTokens)
+    return set_error(RL_ERR_UNSUPPORTED, "rl_shared_prefix_workspace: prefix_len must be at most 2^30");
   *bytes = shared_prefix_ws_bytes(o.B, o.Hq, o.Hkv, o.hd, prefix_len);
   return RL_OK;
 }
@@ -154,6 +177,8 @@ extern "C" rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const voi
     return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: NULL argument");
   if (prefix_len < 0 || (prefix_len > 0 && (!d_k_prefix || !d_v_prefix || !prefix_stride)))
     return set_error(RL_ERR_INVALID_ARG, "rl_shared_prefix_attention: prefix_len below 0, or a prefix argument NULL");
+  if (prefix_len > kMaxTokens)
+    return set_error(RL_ERR_UNSUPPORTED, "rl_shared_prefix_attention: prefix_len must be at most 2^30");
   if (!aligned16(d_q) || !aligned16(d_k) || !aligned16(d_v) || !aligned16(d_out) || !aligned16(d_ws))
     return set_error(RL_ERR_UNSUPPORTED,
                      "rl_shared_prefix_attention: q, k, v, out and the workspace must start on 16-byte boundaries");

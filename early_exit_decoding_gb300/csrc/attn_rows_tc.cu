@@ -10,14 +10,22 @@
 //   O += w V           tcgen05.mma, w from TMEM, V as it lies ([key][dim]: the
 //                      N-major operand), O in TMEM
 // The two tiles share every K and V tile in shared memory (one alone would
-// need 128 bytes a clock from L2 at full tensor rate) and alternate: while
+// need 64 bytes a clock from L2 at the tensor cores' rate) and alternate: while
 // one's rows are in the softmax the other's products run.
 //   warps 0-3, 4-7  softmax of tile 0 and 1      warp 8  TMA (K, V in turn)
-//   warp 9          MMA issue                    warps 10, 11  idle
+//   warp 9          MMA issue                    warps 10, 11  no work of their
+//   own: setmaxnreg counts whole warpgroups
 // A softmax thread holds its row's 128 scores in registers: of the 168 a
 // thread the launch has, the control warps give most to them (216 + 216 + 72
-// = 3 x 168; with 168 they spilled, and with 200 KB of shared memory in use
-// spills go to L2: a tile took 5900 clocks).
+// = 3 x 168; with 168 they spilled, and a tile pair took 5900 clocks, not 3300).
+//
+// What bounds it: a row tile's chain, softmax (about 1500 clocks: 128 keys
+// loaded, compared, raised and packed by each thread) -> the 16 products of
+// its values and next scores (1290; 1035 if they ran alone) -> the hand-offs
+// between the warps (500), two of them interleaved: 3300 clocks a tile pair,
+// in which the tensor cores could do 6.3 products.  8192 queries, 32 heads, 8
+// KV heads, head_dim 128: 260.8 us, 0.49 of the measured bf16 rate, of them
+// about 50 us CTAs' starts and ends.
 // The running maximum follows lazily: O and the sum are rescaled only when a
 // row's maximum grew by more than 2^8 since the last time (weights then stay
 // below 2^8, far inside both types; the sum is fp32), so most tiles touch O
@@ -361,17 +369,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   const bool direct = PREFIX || split == 1;  // no other CTA's keys are joined here
-  // every warp of the cluster (of the CTA, if it is alone)
-  auto meet = [&]() {
-    if (split > 1)
-      cluster_barrier();
-    else
-      named_sync(1, kThreads);
-  };
   if (warp >= 8) {
-    if (!direct) {
-      meet();
-      if (split > 1) cluster_barrier();
+    if (!direct) {  // (the softmax warps' two below)
+      cluster_barrier();
+      cluster_barrier();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
@@ -578,7 +579,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     if (!direct) {
-      meet();
+      cluster_barrier();
       constexpr int CH = HD / 4;
       // one row a warp, dealt out over the cluster's warps 0 .. 7; lane has the
       // 16-byte chunk `lane` (HD 64: the lower 16 lanes)
@@ -593,22 +594,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
         const int c = lane & (CH - 1);
         const uint32_t own = smem_u32(reinterpret_cast<float4*>(ring) + q * CH + (c ^ (q & (CH - 1))));
-        // from the next CTA on (all starting at CTA 0 would queue there), eight
-        // CTAs' loads in flight; the order is the row's own, so results repeat
-        for (int k0 = 0; k0 < split; k0 += 8) {
-          float4 v[8];
+        // from the next CTA on (all starting at CTA 0 would queue there), all loads
+        // in flight together; the order is the row's own, so results repeat
+        float4 v[kMaxSplit];
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (k0 + k < split) v[k] = cluster_ld4(cluster_map(own, (part + k0 + k) % split));
+        for (int k = 0; k < kMaxSplit; ++k)
+          if (k < split) v[k] = cluster_ld4(cluster_map(own, (part + k) % split));
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float fk = __shfl_sync(0xffffffffu, f, (part + k0 + k) % split);
-            if (k0 + k < split && fk != 0.f) {  // (a CTA without keys has written no O)
-              acc.x += fk * v[k].x;
-              acc.y += fk * v[k].y;
-              acc.z += fk * v[k].z;
-              acc.w += fk * v[k].w;
-            }
+        for (int k = 0; k < kMaxSplit; ++k) {
+          const float fk = __shfl_sync(0xffffffffu, f, (part + k) % split);
+          if (k < split && fk != 0.f) {  // (a CTA without keys has written no O)
+            acc.x += fk * v[k].x;
+            acc.y += fk * v[k].y;
+            acc.z += fk * v[k].z;
+            acc.w += fk * v[k].w;
           }
         }
         const int i = row0 + q, t = i / rep, h = hk * rep + i % rep;
@@ -625,7 +624,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           exact_row<HD, F16>(a, b, t, h, n, ql, lane);
         }
       }
-      if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
+      cluster_barrier();  // nobody leaves while its shared memory may still be read
     }
   }
   fence_before();

@@ -426,7 +426,13 @@ RL_API rl_status rl_lm_head_static(const rl_model* m, const float* d_h, int32_t 
                                    float* d_logits, int32_t* d_next_token, int32_t* d_err,
                                    rl_stream_t stream);
 
-/* Element types of the stand-alone operators below. */
+/* The stand-alone operators below run on the current device (buffers and
+ * stream are its own), enqueue and return, and keep nothing between calls.
+ * They may be captured into a graph; the first call of an operator on a device
+ * sets its kernels up: make it before any stream capture there.  Calls from
+ * several threads or on several streams do not disturb one another. */
+
+/* Element types of the stand-alone operators. */
 enum { RL_DT_F32 = 0, RL_DT_BF16 = 1, RL_DT_F16 = 2 };
 
 /* rl_token_logprobs: what a model's answer says about tokens, from rows of
@@ -450,9 +456,10 @@ enum { RL_DT_F32 = 0, RL_DT_BF16 = 1, RL_DT_F16 = 2 };
  * RL_DEVERR_TOKEN and gets NaN.  A row with a NaN or +infinity gives NaN for
  * lse, entropy and logprobs; NaN orders above +infinity, -0 equals +0.  A row
  * of -infinity alone: lse -infinity, entropy and logprobs NaN.
- * Sums are fp32 and repeat bit for bit.  No workspace, one launch.  RL_ERR_INVALID_ARG for a
- * missing buffer, a size below 1, row_stride < vocab, n_tok outside [0, 256],
- * top_k outside [0, min(32, vocab)] or an unknown dtype. */
+ * Sums are fp32 and repeat bit for bit.  No workspace, one launch.
+ * RL_ERR_INVALID_ARG for a missing buffer, logits off their element's
+ * alignment, a size below 1, row_stride < vocab, n_tok outside [0, 256], top_k
+ * outside [0, min(32, vocab)] or an unknown dtype. */
 RL_API rl_status rl_token_logprobs(const void* d_logits, int32_t dtype, int32_t rows, int32_t vocab,
                                    int64_t row_stride, const int32_t* d_tokens, int32_t n_tok,
                                    int32_t top_k, float* d_lse, float* d_entropy, float* d_logprob,
@@ -464,7 +471,9 @@ RL_API rl_status rl_token_logprobs(const void* d_logits, int32_t dtype, int32_t 
  * 128; n_q_heads a multiple of n_kv_heads (query head h reads KV head
  * h / (n_q_heads / n_kv_heads)); q, k, v and out start on 16-byte boundaries
  * and their strides are whole multiples of 16 bytes (RL_ERR_UNSUPPORTED
- * otherwise); k and v strides are below 2^39 elements.  A k or v stride of 0
+ * otherwise); k and v strides are below 2^39 elements, kv_capacity (and a
+ * prefix's length) at most 2^30; the rows of out are apart, each axis nested
+ * in the next larger one (RL_ERR_INVALID_ARG otherwise).  A k or v stride of 0
  * over sequences or KV heads shares one copy between them; the token rows'
  * stride may be 0 only if there is one. */
 typedef struct {
@@ -497,8 +506,7 @@ typedef struct {
  * clamped.  A window of at least kv_capacity is plain causal attention.
  * Scores, softmax statistics and sums are fp32; the weights are rounded to
  * kv_dtype for the product with v.  No workspace, one launch, results repeat
- * bit for bit.  out must not overlap q, k or v.  The first call on a device
- * sets the kernels up: make it before any stream capture on the device.
+ * bit for bit.  out must not overlap q, k or v.
  * RL_ERR_INVALID_ARG for a NULL buffer, a size or window below 1, sinks
  * below 0; RL_ERR_UNSUPPORTED for a shape outside rl_attn_desc's. */
 RL_API rl_status rl_window_attention(const rl_attn_desc* a, const void* d_q, const void* d_k,
@@ -518,8 +526,9 @@ RL_API rl_status rl_window_attention(const rl_attn_desc* a, const void* d_q, con
  *         overlap need one each
  * A sequence that sees no key gets 0 and lse -infinity; a kv_len outside
  * [0, kv_capacity] sets RL_DEVERR_CAPACITY and is clamped.  prefix_len 0 is
- * allowed (the prefix pointers are then not read).  Errors as
- * rl_window_attention; RL_ERR_INVALID_ARG also for a workspace too small. */
+ * allowed (the prefix pointers are then not read).  Two launches (one without
+ * a prefix), results repeat bit for bit.  Errors as rl_window_attention;
+ * RL_ERR_INVALID_ARG also for a workspace too small. */
 RL_API rl_status rl_shared_prefix_workspace(const rl_attn_desc* a, int32_t prefix_len, uint64_t* bytes);
 RL_API rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const void* d_q,
                                             const void* d_k_prefix, const void* d_v_prefix,

@@ -192,6 +192,66 @@ def test_window_masked_keys_have_no_part(river, T, bad):
         compare(got["out"][0, ts], got["lse"][0, ts], refs, "rows that do not see it")
 
 
+@pytest.mark.parametrize("D,dtype", [(64, FP), (128, BF)])
+def test_window_masked_keys_of_many_sequences(river, D, dtype):
+    """As above with more row tiles than the GPU holds at once (no tile's keys
+    are split): the first row sees a NaN, the other rows of its tile do not."""
+    B, T, W = 40, 64, 50
+    q, k, v = window_case(B, T, 8, 8, D, 150, dtype, 61)
+    n = torch.arange(B, dtype=torch.int32, device="cuda") + 105
+    ql = torch.full((B,), T, dtype=torch.int32, device="cuda")
+    ql[::3] = 33
+    clean = river.window_attention(q, k, v, n, W, 2, q_len=ql)
+    check_window(clean, q, k, v, n, ql, W, 2, rows=4)
+    vb = v.clone()
+    for b in range(B):
+        # the first row's oldest key in the window (below 0, with no such key: a slot behind the sequence)
+        j = int(n[b]) - int(ql[b]) - W + 1
+        vb[b, :, j, 1] = float("nan")
+    got = river.window_attention(q, k, vb, n, W, 2, q_len=ql)
+    hit = (n - ql - W + 1 >= 0)[:, None].expand(B, 8)
+    assert hit.any() and not hit.all() and torch.equal(torch.isnan(got["out"][:, 0, :, 1]), hit)
+    refs = []
+    for b in range(B):
+        for t in (0, 1 + b % 7):
+            p = int(n[b]) - int(ql[b]) + t
+            jj = torch.arange(p + 1, device="cuda")
+            jj = jj[(p - jj < W) | (jj < 2)]
+            ref = row_ref(q[b, t], k[b][:, jj], v[b][:, jj], 1 / math.sqrt(D))
+            if t == 0:  # (its other dims)
+                assert ((got["out"][b, 0].to(F64) - ref[0]).abs() <= ref[2])[:, 2:].all()
+            elif b == 8:  # (its key is a sink: every row sees it)
+                assert int(n[b]) - int(ql[b]) - W + 1 == 0 and torch.isnan(got["out"][b, t, :, 1]).all()
+            else:
+                refs.append(ref)
+    ar = torch.tensor([b for b in range(B) if b != 8], device="cuda")
+    compare(got["out"][ar, 1 + ar % 7], got["lse"][ar, 1 + ar % 7], refs, "rows that do not see it")
+
+
+def test_window_wider_than_any_length(river):
+    """Windows and sinks beyond 32 bits are plain causal attention."""
+    q, k, v = window_case(2, 3, 4, 2, 64, 90, BF, 71)
+    n = i32(90, 41)
+    want = river.window_attention(q, k, v, n, 90)
+    for w, s in ((2**31 - 1, 0), (2**32 + 5, 0), (7, 2**40)):
+        got = river.window_attention(q, k, v, n, w, s)
+        check_window(got, q, k, v, n, None, w, s)
+        assert s or (torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"]))
+
+
+def test_buffers_that_overlap_themselves(river):
+    q, k, v = window_case(2, 3, 4, 2, 64, 40, BF, 81)
+    n = i32(40, 11)
+    for out in (torch.empty((1, 3, 4, 64), dtype=BF, device="cuda").expand(2, 3, 4, 64),
+                torch.empty(2000, dtype=BF, device="cuda").as_strided((2, 3, 4, 64), (768, 256, 32, 1))):
+        with pytest.raises(river.RiverError):
+            river.window_attention(q, k, v, n, 8, out={"out": out})
+    qp, kp, vp, kq, vq = prefix_case(2, 4, 2, 64, 64, 20, BF, 91)
+    with pytest.raises(river.RiverError):
+        river.shared_prefix_attention(qp, kp, vp, kq, vq, i32(20, 3),
+                                      workspace=torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 20))
+
+
 def test_window_lengths_outside_the_buffers(river):
     q, k, v = window_case(3, 4, 4, 2, 64, 100, BF, 61)
     err = torch.zeros(1, dtype=torch.int32, device="cuda")

@@ -58,6 +58,9 @@ SHARED = [
     (dict(out_stride=(-256, 256, 64)), "UNSUPPORTED"), (dict(k_stride=(4096, 2048, 68)), "UNSUPPORTED"),
     (dict(v_stride=(1 << 39, 2048, 64)), "UNSUPPORTED"), (dict(k_stride=(4096, 2048, 0)), "UNSUPPORTED"),
     (dict(batch=1 << 20, q_len=1 << 12), "UNSUPPORTED"),
+    (dict(kv_capacity=(1 << 30) + 1), "UNSUPPORTED"), (dict(out_stride=(0, 256, 64)), "INVALID_ARG"),
+    (dict(out_stride=(256, 256, 0)), "INVALID_ARG"), (dict(out_stride=(128, 256, 64)), "INVALID_ARG"),
+    (dict(out_stride=(64, 256, 64)), "INVALID_ARG"),
     (dict(q=None), "INVALID_ARG"), (dict(k=None), "INVALID_ARG"), (dict(v=None), "INVALID_ARG"),
     (dict(kv_len=None), "INVALID_ARG"), (dict(out=None), "INVALID_ARG"), (dict(q=A + 8), "UNSUPPORTED"),
     (dict(k=A + 2), "UNSUPPORTED"), (dict(out=A + 4 * 4096 + 8), "UNSUPPORTED"), (dict(out=A), "INVALID_ARG"),
@@ -80,7 +83,7 @@ def test_window_attention_refuses(river, kw, status):
 
 
 @pytest.mark.parametrize("kw,status", [x for x in SHARED if "q_len" not in x[0]] + [
-    (dict(q_len=2), "UNSUPPORTED"), (dict(prefix=-1), "INVALID_ARG"), (dict(pk=None), "INVALID_ARG"), (dict(pv=A + 24576 + 8), "UNSUPPORTED"),
+    (dict(q_len=2, out_stride=(512, 256, 64)), "UNSUPPORTED"), (dict(prefix=-1), "INVALID_ARG"), (dict(prefix=(1 << 30) + 1), "UNSUPPORTED"), (dict(pk=None), "INVALID_ARG"), (dict(pv=A + 24576 + 8), "UNSUPPORTED"),
     (dict(ps=(1024, 65, 1024, 64)), "UNSUPPORTED"), (dict(ws=None), "INVALID_ARG"), (dict(ws_bytes=16), "INVALID_ARG"),
     (dict(ws=A + 28672 + 4), "UNSUPPORTED")])
 def test_shared_prefix_attention_refuses(river, kw, status):

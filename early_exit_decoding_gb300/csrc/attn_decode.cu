@@ -59,12 +59,17 @@ __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint3
 struct Tile {
   int b, hk, row0, rep, n, ql;
 };
+// Divisors of a launch.
+struct DecodeShape {
+  int split, tiles, presplit;
+  FastDiv by_split, by_tiles, by_heads, by_rep;  // CTAs of a cluster, row tiles, KV heads, heads a KV head
+};
 
 template <int HD, bool F16>
-__device__ __forceinline__ uint32_t load_q2(const AttnOpArgs& a, const Tile& t, int r, int dim) {
-  const int i = t.row0 + r;
-  if (i >= a.Tq * t.rep) return 0u;
-  const long long at = t.b * a.qs[0] + (i / t.rep) * a.qs[1] + (long long)(t.hk * t.rep + i % t.rep) * a.qs[2] + dim;
+__device__ __forceinline__ uint32_t load_q2(const AttnOpArgs& a, const Tile& t, const FastDiv& by_rep, int r, int dim) {
+  const int i = t.row0 + r, tq = by_rep.quot(i);
+  if (tq >= a.Tq) return 0u;
+  const long long at = t.b * a.qs[0] + tq * a.qs[1] + (long long)(t.hk * t.rep + i - tq * t.rep) * a.qs[2] + dim;
   if (a.q_f32) {
     const float2 f = *reinterpret_cast<const float2*>(static_cast<const float*>(a.q) + at);
     return pack2<F16>(f.x, f.y);
@@ -74,8 +79,8 @@ __device__ __forceinline__ uint32_t load_q2(const AttnOpArgs& a, const Tile& t, 
 
 template <int HD, bool F16>
 __global__ void __launch_bounds__(kThreads, 3)
-    k_attn_decode(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnOpArgs a, int split, int tiles,
-                  int presplit) {
+    k_attn_decode(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnOpArgs a,
+                  const __grid_constant__ DecodeShape sh) {
   constexpr int NST = kStages<HD>, SB = kStageBytes<HD>;
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* smem =
@@ -84,18 +89,23 @@ __global__ void __launch_bounds__(kThreads, 3)
   __shared__ float s_m[kWarps][kRows], s_l[kWarps][kRows];
   __shared__ float c_m[kRows], c_l[kRows];
 
-  const int part = blockIdx.x % split;
-  int id = blockIdx.x / split;
+  if (threadIdx.x == kThreads - 1) {
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+  }
+  const int split = sh.split, presplit = sh.presplit;
+  const int id = sh.by_split.quot(blockIdx.x), head = sh.by_tiles.quot(id);
+  const int part = blockIdx.x - id * split;
   Tile t;
-  t.rep = a.Hq / a.Hkv;
-  t.row0 = (id % tiles) * kRows;
-  id /= tiles;
-  t.hk = id % a.Hkv;
-  t.b = id / a.Hkv;
+  t.rep = sh.by_rep.d;
+  t.row0 = (id - head * sh.tiles) * kRows;
+  t.b = sh.by_heads.quot(head);
+  t.hk = head - t.b * a.Hkv;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const bool report = part == 0 && tid == 0 && t.hk == 0 && t.row0 == 0;
-  t.n = seq_len(a, t.b, report);
-  t.ql = query_len(a, t.b, report);
+  const Lens len = seq_lens(a, t.b, report);
+  t.n = len.n;
+  t.ql = len.ql;
   unsigned char* ring = smem + warp * NST * SB;
   if (lane == 0) {
     for (int i = 0; i < NST; ++i) mbar_init(&full[warp][i], 1);
@@ -104,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 3)
   __syncwarp();
 
   // Keys any row of the tile sees: [0, sink_end) and [lo, hi).
-  const int t0 = t.row0 / t.rep, t1 = min((t.row0 + kRows - 1) / t.rep, t.ql - 1);
+  const int t0 = sh.by_rep.quot(t.row0), t1 = min(sh.by_rep.quot(t.row0 + kRows - 1), t.ql - 1);
   const int p0 = max(t.n - t.ql + t0, 0), p1 = t.n - t.ql + t1;
   const bool live = t0 <= t1 && p1 >= 0;
   int lo = live ? max(0, p0 - a.window + 1) : 0;
@@ -132,13 +142,13 @@ __global__ void __launch_bounds__(kThreads, 3)
   uint32_t qf[HD / 16][4];
 #pragma unroll
   for (int ks = 0; ks < HD / 16; ++ks) {
-    qf[ks][0] = load_q2<HD, F16>(a, t, g, ks * 16 + c2);
-    qf[ks][1] = load_q2<HD, F16>(a, t, g + 8, ks * 16 + c2);
-    qf[ks][2] = load_q2<HD, F16>(a, t, g, ks * 16 + 8 + c2);
-    qf[ks][3] = load_q2<HD, F16>(a, t, g + 8, ks * 16 + 8 + c2);
+    qf[ks][0] = load_q2<HD, F16>(a, t, sh.by_rep, g, ks * 16 + c2);
+    qf[ks][1] = load_q2<HD, F16>(a, t, sh.by_rep, g + 8, ks * 16 + c2);
+    qf[ks][2] = load_q2<HD, F16>(a, t, sh.by_rep, g, ks * 16 + 8 + c2);
+    qf[ks][3] = load_q2<HD, F16>(a, t, sh.by_rep, g + 8, ks * 16 + 8 + c2);
   }
   // positions of this thread's two rows
-  const int pr0 = t.n - t.ql + (t.row0 + g) / t.rep, pr1 = t.n - t.ql + (t.row0 + g + 8) / t.rep;
+  const int pr0 = t.n - t.ql + sh.by_rep.quot(t.row0 + g), pr1 = t.n - t.ql + sh.by_rep.quot(t.row0 + g + 8);
   const bool one_mask = a.Tq == 1;  // every row sees the same keys
   const float sc = a.scale * kLog2e;
 
@@ -312,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     __syncthreads();
   if (a.P > 0) pdl_wait();  // the prefix's part of the rows is complete and visible
   for (int r = part * kWarps + warp; r < nrow; r += W) {
-    const int i = t.row0 + r, tq = i / t.rep, h = t.hk * t.rep + i % t.rep;
+    const int i = t.row0 + r, tq = sh.by_rep.quot(i), gh = i - tq * t.rep, h = t.hk * t.rep + gh;
     if (tq >= t.ql) continue;
     float cm = -INFINITY, cl = 0.f, pm = -INFINITY, pl = 0.f;
     if (lane < split) {
@@ -322,7 +332,7 @@ __global__ void __launch_bounds__(kThreads, 3)
     PrefixWs ws;
     int pq = 0;
     if (a.P > 0) {
-      const int pi = t.b * t.rep + i % t.rep, ptiles = (a.B * t.rep + 255) / 256;
+      const int pi = t.b * t.rep + gh, ptiles = (a.B * t.rep + 255) / 256;
       pq = pi & 255;
       ws = prefix_ws(a.ws, pi >> 8, ptiles, a.B * t.rep, t.hk, a.Hkv, 0, presplit, HD);
       if (lane < presplit) {
@@ -448,7 +458,8 @@ cudaError_t launch(const AttnOpArgs& a, bool pdl, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, a, split, tiles, presplit);
+  const DecodeShape sh{split, tiles, presplit, FastDiv(split), FastDiv(tiles), FastDiv(a.Hkv), FastDiv(a.Hq / a.Hkv)};
+  return cudaLaunchKernelEx(&cfg, kern, maps, a, sh);
 }
 
 }  // namespace

@@ -35,22 +35,15 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // Length of sequence b, clamped to the rows laid out for it.
-__device__ __forceinline__ int seq_len(const AttnOpArgs& a, int b, bool report) {
-  long long n = a.kv_len_add;
-  if (a.kv_len) n += a.kv_len[(long long)b * a.kv_len_step];
-  if (n < 0 || n > a.cap) {
-    if (report && a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
-    n = n < 0 ? 0 : a.cap;
-  }
-  return (int)n;
-}
-__device__ __forceinline__ int query_len(const AttnOpArgs& a, int b, bool report) {
-  int n = a.q_len ? a.q_len[b] : a.Tq;
-  if (n < 0 || n > a.Tq) {
-    if (report && a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
-    n = n < 0 ? 0 : a.Tq;
-  }
-  return n;
+struct Lens {
+  int n, ql;  // token rows of a sequence, query rows among them
+};
+__device__ __forceinline__ Lens seq_lens(const AttnOpArgs& a, int b, bool report) {
+  // (both loads before either check, which may write the error word)
+  const int kv = a.kv_len ? __ldg(a.kv_len + (long long)b * a.kv_len_step) : 0, q = a.q_len ? __ldg(a.q_len + b) : a.Tq;
+  const long long n = (long long)kv + a.kv_len_add;
+  if (report && a.err && (n < 0 || n > a.cap || q < 0 || q > a.Tq)) atomicOr(a.err, RL_DEVERR_CAPACITY);
+  return Lens{(int)max(0ll, min(n, (long long)a.cap)), max(0, min(q, a.Tq))};
 }
 
 // One row in the plain form, held by a warp: lane has dims 2 * lane + 64 * i,
@@ -124,6 +117,21 @@ __device__ __noinline__ void exact_row(const AttnOpArgs& a, int b, int t, int h,
   r.store(a, b, t, h, lane);
 }
 
+// Division of n < 2^31 by a fixed d >= 1 as a multiplication and a shift (a
+// division takes some 130 clocks, and a CTA's first copy waits for several in
+// a row): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// n / d = (mulhi(m, n) + n) >> l (Granlund and Montgomery 1994).
+struct FastDiv {
+  uint32_t m, l;
+  int d;
+  FastDiv() = default;
+  explicit FastDiv(int div) : m(0), l(0), d(div) {
+    while ((1ll << l) < div) ++l;
+    m = (uint32_t)(((1ull << 32) * ((1ull << l) - (unsigned long long)div)) / (unsigned long long)div + 1);
+  }
+  __device__ __forceinline__ int quot(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> l); }
+};
+
 // Tensor maps of one K and one V source: five axes (64 dims, token rows,
 // 64-dim blocks, KV heads, sequences), so one copy brings `rows` token rows of
 // all dims as HD / 64 blocks of rows x 128 bytes, 128-byte swizzle; rows past
@@ -135,6 +143,9 @@ struct KvMaps {
 };
 bool make_kv_maps(KvMaps* m, const KeySrc& s, bool f16, int B, int Hkv, int hd, int tokens, int rows);
 
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
 __device__ __forceinline__ void tma_load_5d(void* dst, const CUtensorMap* map, int tok, int head, int seq,
                                             uint64_t* bar) {
   asm volatile(

@@ -129,6 +129,14 @@ __device__ __forceinline__ void tmem_st32(uint32_t at, const uint32_t* r) {
       RL_I8(r, 0), RL_I8(r, 8), RL_I8(r, 16), RL_I8(r, 24)
       : "memory");
 }
+// A row tile of Q: 64-dim blocks of 128 rows (query row x heads of the group).
+__device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, int head, int row, int seq, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5, %3, %6}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(head), "r"(row), "r"(seq)
+      : "memory");
+}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Bits 0 .. n - 1.
@@ -162,13 +170,21 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// A launch's shape: divisors, and whether Q comes by TMA (its map's axes: 64
+// dims, heads, query rows, 64-dim blocks, sequences; a box is a row tile).
+struct RowsShape {
+  int split, tiles, q_tma;
+  FastDiv by_split, by_heads, by_group, by_rep;  // CTAs of a cluster, KV heads, KV heads x sequences, heads a KV head
+};
+
 struct Bars {
   uint64_t s_full[2], p_full[2], o_full[2], full[8], empty[8], drain;
 };
 
 template <int HD, bool F16, bool PREFIX>
 __global__ void __launch_bounds__(kThreads, 1)
-    k_attn_rows_tc(const __grid_constant__ KvMaps maps, const __grid_constant__ AttnOpArgs a, int split, int tiles) {
+    k_attn_rows_tc(const __grid_constant__ KvMaps maps, const __grid_constant__ CUtensorMap q_map,
+                   const __grid_constant__ AttnOpArgs a, const __grid_constant__ RowsShape sh) {
   constexpr int NST = kStages<HD>, TB = kTileBytes<HD>;
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* smem =
@@ -184,12 +200,19 @@ __global__ void __launch_bounds__(kThreads, 1)
   // the kernel that takes the prefix's parts may start beside the last CTAs
   // (it waits for all of them before it reads the workspace)
   if (PREFIX) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  const int part = blockIdx.x % split, rep = a.Hq / a.Hkv;
-  int id = blockIdx.x / split;
+  if (tid == kThreads - 1) {  // (a thread without work of its own)
+    prefetch_map(&maps.k);
+    prefetch_map(&maps.v);
+    if (sh.q_tma) prefetch_map(&q_map);
+  }
+  const int split = sh.split, tiles = sh.tiles, rep = sh.by_rep.d;
+  int id = sh.by_split.quot(blockIdx.x);
+  const int part = blockIdx.x - id * split;
   // later tiles of a prompt see more keys: first come, first served from the end
-  const int row0 = (tiles - 1 - id / (PREFIX ? a.Hkv : a.Hkv * a.B)) * kRowsCta;
-  id %= PREFIX ? a.Hkv : a.Hkv * a.B;
-  const int hk = id % a.Hkv, b = PREFIX ? 0 : id / a.Hkv;
+  const int back = sh.by_group.quot(id);
+  const int row0 = (tiles - 1 - back) * kRowsCta;
+  id -= back * sh.by_group.d;
+  const int b = sh.by_heads.quot(id), hk = id - b * sh.by_heads.d;  // (b is 0 for a prefix)
   int n, ql, nrow, p0 = 0, lo = 0, hi, sink_end = 0;
   if constexpr (PREFIX) {
     n = hi = a.P;
@@ -197,12 +220,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     nrow = min(kRowsCta, a.B * rep - row0);
   } else {
     const bool report = part == 0 && tid == 0 && hk == 0 && row0 == 0;
-    n = seq_len(a, b, report);
-    ql = query_len(a, b, report);
-    nrow = max(0, min(kRowsCta, ql * rep - row0));
+    const Lens len = seq_lens(a, b, report);
+    n = len.n;
+    ql = len.ql;
+    nrow = min(kRowsCta, ql * rep - row0);
+    if (nrow <= 0) return;  // (its whole cluster: the rows are the same)
     // keys any row sees: [0, sink_end) and [lo, hi)
-    p0 = max(n - ql + row0 / rep, 0);
-    const int p1 = nrow ? n - ql + (row0 + nrow - 1) / rep : -1;
+    p0 = max(n - ql + sh.by_rep.quot(row0), 0);
+    const int p1 = n - ql + sh.by_rep.quot(row0 + nrow - 1);
     hi = max(p1 + 1, 0);
     if (hi > 0) lo = max(0, p0 - a.window + 1);
     sink_end = min(a.sinks, lo);
@@ -217,7 +242,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   auto load = [&](int i) {  // K (i even) or V tile i / 2 into its stage
     const int st = i % NST, j = key0(j0 + (i >> 1));
-    mbar_expect_tx(&bar.full[st], TB);
+    mbar_expect_tx(&bar.full[st], i == 0 && sh.q_tma ? (1 + ngrp) * TB : TB);
     if (i & 1)
       tma_load_5d(ring + st * TB, &maps.v, j, hk * maps.vh, b * maps.vb, &bar.full[st]);
     else
@@ -237,18 +262,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&bar.drain, 1);
       s_fail = 0;
       asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-      if (nt > 0) load(0);  // (the others after Q's rows, which the first scores need too)
+      if (nt > 0) {
+        load(0);  // (the others after Q's rows, which the first scores need too)
+        if (sh.q_tma)
+          for (int g = 0; g < ngrp; ++g) {
+            const int t = sh.by_rep.quot(row0 + g * 128);
+            tma_load_q(sq + g * TB, &q_map, hk * rep, t, b, &bar.full[0]);
+          }
+      }
     }
     __syncwarp();
   } else if (warp == 9) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)), "r"(512)
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-  } else if (warp < 8 && warp / 4 < ngrp && nt > 0) {
+  } else if (warp < 8 && warp / 4 < ngrp && nt > 0 && !sh.q_tma) {
     // Q rows to shared memory as the TMA would lay them; rows past the last are 0
     const int g = warp / 4, r = tid & 127;
     auto at = [&](int e) {  // 16-byte chunk e * 128 + r of the tile: its place in q
-      const int it = e * 128 + r, i = row0 + min(g * 128 + it / (HD / 8), nrow - 1), t = i / rep;
+      const int it = e * 128 + r, i = row0 + min(g * 128 + it / (HD / 8), nrow - 1), t = sh.by_rep.quot(i);
       return (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)t * a.qs[1]) +
              (long long)(hk * rep + i - t * rep) * a.qs[2] + it % (HD / 8) * 8;
     };
@@ -382,12 +414,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_at = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = t_s(g & 1), to = t_o(g & 1);
     const int i_row = row0 + g * 128 + r;    // (query, head in group)
+    bool go = true;                          // (the same for a warp)
     if (g < ngrp && nt > 0) {
-      const int p = PREFIX ? 0 : n - ql + i_row / rep;  // this row's position
+      const int p = PREFIX ? 0 : n - ql + sh.by_rep.quot(i_row);  // this row's position
       // positions of the tile's first and last row that count
-      const int pa = PREFIX ? 0 : max(n - ql + (row0 + g * 128) / rep, 0);
-      const int pz = PREFIX ? 0 : n - ql + (row0 + min(nrow, g * 128 + 128) - 1) / rep;
-      bool go = true;
+      const int pa = PREFIX ? 0 : max(n - ql + sh.by_rep.quot(row0 + g * 128), 0);
+      const int pz = PREFIX ? 0 : n - ql + sh.by_rep.quot(row0 + min(nrow, g * 128 + 128) - 1);
       for (int j = 0; j < nt; ++j) {
         const int k0 = key0(j0 + j), cnt = count(j0 + j);
         if (!(go = wait_warp(&bar.s_full[g], j & 1))) break;
@@ -470,15 +502,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_before();
         mbar_arrive(&bar.p_full[g]);
       }
+    }
+    const bool mine = g * 128 + r < nrow;
+    long long row_at = -1;  // where the row's output goes
+    float inv = 0.f;
+    if (!PREFIX && direct && mine) {  // (while the last products run)
+      const int t = sh.by_rep.quot(i_row), h = hk * rep + i_row - t * rep;
+      row_at = b * a.os[0] + t * a.os[1] + h * a.os[2];
+      inv = l == 0.f ? 0.f : 1.f / l;
+      if (a.lse) a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
+    }
+    if (g < ngrp && nt > 0) {
       // (the last tile's: the ring, which the other tile's products still read,
       // is written over below)
-      if (go) go = wait_warp(&bar.o_full[PREFIX || !direct ? ngrp - 1 : g], 0);
+      if (!go || !wait_warp(&bar.o_full[PREFIX || !direct ? ngrp - 1 : g], 0)) l = inv = NAN;
       fence_after();
-      if (!go) l = NAN;
     }
     auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
     {
-      const bool mine = g * 128 + r < nrow;
       const bool have = g < ngrp && nt > 0;
       if constexpr (PREFIX) {
         // O, maximum and sum of the CTA's keys to the workspace, 32 rows a warp:
@@ -509,17 +550,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       } else if (direct) {
-        const int t = i_row / rep, h = hk * rep + i_row % rep;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        bool fin = true;
-        const long long row_at = mine ? b * a.os[0] + t * a.os[1] + h * a.os[2] : -1;
+        const bool dead = !have || l == 0.f;  // (a row that sees no key: O may hold anything)
+        float chk = 0.f;                      // NaN once a value is not finite
         // through shared memory (over Q, which no product reads any more), so that
         // whole rows are written, not 16 bytes of 32 rows at a time
         constexpr int CR = HD / 8;  // 16-byte chunks of a row; chunk c of row q at c ^ (q & 7)
         unsigned char* stage = sq + g * TB + (warp & 3) * (32 * HD * 2);
 #pragma unroll
         for (int c = 0; c < HD; c += 32) {
-          float o[32];
+          float o[32] = {};
           if (have) {
             tmem_ld32(to + lane_at + c, o);
             ld_wait<32>(o);
@@ -529,11 +568,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t w[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const float u = have ? o[e + 2 * q] * inv : 0.f, v = have ? o[e + 2 * q + 1] * inv : 0.f;
-              // (a row that sees no key has l 0; its O may hold anything)
-              const float u0 = l == 0.f ? 0.f : u, v0 = l == 0.f ? 0.f : v;
-              fin = fin && isfinite(u0) && isfinite(v0);
-              w[q] = pack2<F16>(u0, v0);
+              const float u = o[e + 2 * q] * inv, v = o[e + 2 * q + 1] * inv;
+              chk = fmaf(u, 0.f, fmaf(v, 0.f, chk));
+              w[q] = dead ? 0u : pack2<F16>(u, v);
             }
             *reinterpret_cast<uint4*>(stage + lane * (HD * 2) + ((((c + e) / 8) ^ (lane & 7)) << 4)) =
                 make_uint4(w[0], w[1], w[2], w[3]);
@@ -547,17 +584,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint4 v = *reinterpret_cast<const uint4*>(stage + q * (HD * 2) + ((c ^ (q & 7)) << 4));
           if (at >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c * 8) = v;
         }
-        if (mine && a.lse)
-          a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
         // rows of different masks shared V's tiles: one that is not finite may
         // owe that to a key it does not see (0 * infinity)
-        unsigned bad = __ballot_sync(0xffffffffu, mine && !fin);
+        unsigned bad = __ballot_sync(0xffffffffu, mine && !dead && chk != 0.f);
         if (__any_sync(0xffffffffu, s_fail)) bad = 0;  // (the same for every lane: exact_row shuffles)
         if (bad) __syncwarp();  // the rows' first values, stored by other lanes, come before the new ones
         while (bad) {
           const int i = row0 + g * 128 + (warp & 3) * 32 + __ffs(bad) - 1;
           bad &= bad - 1;
-          exact_row<HD, F16>(a, b, i / rep, hk * rep + i % rep, n, ql, lane);
+          const int ti = sh.by_rep.quot(i);
+          exact_row<HD, F16>(a, b, ti, hk * rep + i - ti * rep, n, ql, lane);
         }
       } else {
         // to shared memory over the drained ring: rows of HD floats, 16-byte
@@ -610,7 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             acc.w += fk * v[k].w;
           }
         }
-        const int i = row0 + q, t = i / rep, h = hk * rep + i % rep;
+        const int i = row0 + q, t = sh.by_rep.quot(i), h = hk * rep + i - t * rep;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const bool fin = isfinite(acc.x * inv) && isfinite(acc.y * inv) && isfinite(acc.z * inv) && isfinite(acc.w * inv);
         uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2] + c * 4;
@@ -634,6 +670,26 @@ __global__ void __launch_bounds__(kThreads, 1)
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
   }
+}
+
+// The map of Q's rows (see RowsShape); false: not of a form that a box of 128
+// rows fits, and the threads load them.
+bool make_q_map(CUtensorMap* map, const AttnOpArgs& a, bool prefix) {
+  const int rep = a.Hq / a.Hkv;
+  if (a.q_f32 || 128 % rep) return false;
+  const int seqs = prefix ? 1 : a.B, rows = prefix ? a.B : a.Tq;
+  // (an axis of extent 1 takes any stride)
+  const long long st[3] = {a.Hq > 1 ? a.qs[2] : a.hd, rows > 1 ? (prefix ? a.qs[0] : a.qs[1]) : a.hd, seqs > 1 ? a.qs[0] : a.hd};
+  for (long long x : st)
+    if (x == 0 || x >= (1ll << 39)) return false;
+  const cuuint64_t dims[5] = {64, (cuuint64_t)a.Hq, (cuuint64_t)rows, (cuuint64_t)(a.hd / 64), (cuuint64_t)seqs};
+  const cuuint64_t strides[4] = {(cuuint64_t)st[0] * 2, (cuuint64_t)st[1] * 2, 128, (cuuint64_t)st[2] * 2};
+  const cuuint32_t box[5] = {64, (cuuint32_t)rep, (cuuint32_t)(128 / rep), (cuuint32_t)(a.hd / 64), 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return tensor_map_encoder()(map, a.f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5,
+                              const_cast<void*>(a.q), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int HD, bool F16, bool PREFIX>
@@ -709,7 +765,16 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, maps, a, split, tiles);
+  RowsShape sh;
+  CUtensorMap q_map = {};
+  sh.split = split;
+  sh.tiles = tiles;
+  sh.q_tma = make_q_map(&q_map, a, PREFIX);
+  sh.by_split = FastDiv(split);
+  sh.by_heads = FastDiv(a.Hkv);
+  sh.by_group = FastDiv(PREFIX ? a.Hkv : a.Hkv * a.B);
+  sh.by_rep = FastDiv(rep);
+  return cudaLaunchKernelEx(&cfg, kern, maps, q_map, a, sh);
 }
 
 template <bool PREFIX>

@@ -142,8 +142,10 @@ __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 // Scores whose bit is 0 become -infinity (selects on bits: as 128 conditions
-// they were branches, 6000 to 11000 clocks a masked tile).
+// they were branches, 6000 to 11000 clocks a masked tile).  A warp's rows have
+// few positions, so most groups of 32 keys are whole for all of them.
 __device__ __forceinline__ void keep_only(float* s, uint32_t bits) {
+  if (__all_sync(0xffffffffu, bits == 0xffffffffu)) return;
 #pragma unroll
   for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? s[e] : -INFINITY;
 }

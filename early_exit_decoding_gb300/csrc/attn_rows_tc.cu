@@ -142,10 +142,8 @@ __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.
 // Bits 0 .. n - 1.
 __device__ __forceinline__ uint32_t below(int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1; }
 // Scores whose bit is 0 become -infinity (selects on bits: as 128 conditions
-// they were branches, 6000 to 11000 clocks a masked tile).  A warp's rows have
-// few positions, so most groups of 32 keys are whole for all of them.
+// they were branches, 6000 to 11000 clocks a masked tile).
 __device__ __forceinline__ void keep_only(float* s, uint32_t bits) {
-  if (__all_sync(0xffffffffu, bits == 0xffffffffu)) return;
 #pragma unroll
   for (int e = 0; e < 32; ++e) s[e] = (bits >> e) & 1u ? s[e] : -INFINITY;
 }
@@ -422,6 +420,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // positions of the tile's first and last row that count
       const int pa = PREFIX ? 0 : max(n - ql + sh.by_rep.quot(row0 + g * 128), 0);
       const int pz = PREFIX ? 0 : n - ql + sh.by_rep.quot(row0 + min(nrow, g * 128 + 128) - 1);
+      // and of the warp's
+      const int wr = row0 + g * 128 + (warp & 3) * 32;
+      const int wa = PREFIX ? 0 : n - ql + sh.by_rep.quot(wr);
+      const int wz = PREFIX ? 0 : n - ql + sh.by_rep.quot(wr + 31);
       for (int j = 0; j < nt; ++j) {
         const int k0 = key0(j0 + j), cnt = count(j0 + j);
         if (!(go = wait_warp(&bar.s_full[g], j & 1))) break;
@@ -433,14 +435,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (PREFIX) {
           if (cnt < kKeys) {
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 32) keep_only(s + c, below(cnt - c));
+            for (int c = 0; c < kKeys; c += 32)
+              if (c + 32 > cnt) keep_only(s + c, below(cnt - c));
           }
         } else if (cnt < kKeys || k0 + kKeys - 1 > pa || (pz - k0 >= a.window && k0 + kKeys > a.sinks)) {
           // keys this row sees: below `end`, and from `beg` on or below `snk`
           const int end = min(cnt, p - k0 + 1), beg = p - a.window + 1 - k0, snk = a.sinks - k0;
 #pragma unroll
-          for (int c = 0; c < kKeys; c += 32)
-            keep_only(s + c, below(end - c) & (~below(beg - c) | below(snk - c)));
+          for (int c = 0; c < kKeys; c += 32) {
+            // (a warp's rows have few positions: most groups of 32 keys are whole for all)
+            const int k = k0 + c;
+            if (c + 32 > cnt || k + 31 > wa || (wz - k >= a.window && k + 31 >= a.sinks))
+              keep_only(s + c, below(end - c) & (~below(beg - c) | below(snk - c)));
+          }
         }
         float x[4];
 #pragma unroll
@@ -489,13 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         const float2 yy = add2(y[0], y[1]);
         l += yy.x + yy.y;
-        if (cnt < kKeys) {
-          // V rows behind the range may hold anything: 0 * NaN must not happen
+        // V rows behind the sequence or the sinks may hold anything: 0 * NaN must
+        // not happen (a prefix has none; a NaN in keys of the window that only
+        // other rows see is met at the end)
+        const int from = PREFIX ? kKeys : j0 + j < su ? cnt : n - k0;
+        if (from < kKeys) {
           const int iv = 2 * j + 1;
           if (!(go = wait_warp(&bar.full[iv % NST], (iv / NST) & 1))) break;
           unsigned char* sv = ring + (iv % NST) * TB;
-          for (int it = tid & 127; it < (kKeys - cnt) * (HD / 8); it += 128) {
-            const int kr = cnt + it / (HD / 8), ch = it % (HD / 8);
+          for (int it = tid & 127; it < (kKeys - from) * (HD / 8); it += 128) {
+            const int kr = from + it / (HD / 8), ch = it % (HD / 8);
             *reinterpret_cast<uint4*>(sv + (ch >> 3) * (kKeys * 128) + kr * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
           }
           fence_proxy_async_smem();

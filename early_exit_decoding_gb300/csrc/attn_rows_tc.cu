@@ -235,7 +235,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   const int su = (sink_end + kKeys - 1) / kKeys;
   const int all = su + (hi - lo + kKeys - 1) / kKeys;
-  const int j0 = (int)((long long)all * part / split), nt = (int)((long long)all * (part + 1) / split) - j0;
+  // (all < 2^24: at most 2^30 keys, in two ranges)
+  const int j0 = sh.by_split.quot(all * part), nt = sh.by_split.quot(all * (part + 1)) - j0;
   auto key0 = [&](int j) { return j < su ? j * kKeys : lo + (j - su) * kKeys; };
   auto count = [&](int j) { return min(kKeys, (j < su ? sink_end : hi) - key0(j)); };
   const int ngrp = nrow > 128 ? 2 : 1;

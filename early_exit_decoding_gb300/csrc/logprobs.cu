@@ -245,7 +245,7 @@ __device__ __forceinline__ void add(Part& p, float x, float mu) {
 }
 
 template <typename T, bool kTop>
-__global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __grid_constant__ LogprobArgs a, int split) {
+__global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __grid_constant__ LogprobArgs a, int log_split) {
   using E = Elem<T>;
   constexpr int VEC = E::kVec;
   extern __shared__ __align__(16) unsigned char ring_all[];
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
   __shared__ int s_n;
   __shared__ unsigned long long s_top[kTop ? 32 : 1];
 
-  const int row = blockIdx.x / split, part = blockIdx.x % split;
+  const int split = 1 << log_split, row = blockIdx.x >> log_split, part = blockIdx.x & (split - 1);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const T* x = static_cast<const T*>(a.x) + (long long)row * a.ld;
   const int V = a.V, k = a.top_k;
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
   // of warp 0.
   const int head = min(V, (int)((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
   const int nvec = (V - head) / VEC;
-  const int v0 = (int)((long long)nvec * part / split), v1 = (int)((long long)nvec * (part + 1) / split);
+  const int v0 = (int)((long long)nvec * part >> log_split), v1 = (int)((long long)nvec * (part + 1) >> log_split);
   const T* xv = x + head;
   const int ntile = (v1 - v0 + kLpTile - 1) / kLpTile;
   unsigned char* ring = ring_all + warp * kLpStages * kLpTile * 16;
@@ -534,8 +534,8 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
           if (tid + q * kLpThreads < split * k) s_all[tid + q * kLpThreads] = v[q];
         if (tid == 0) s_n = 0;
         __syncthreads();
-        const int each = 32 / split;  // (split is a power of two up to 16)
-        const int li = lane / each, le = lane % each;
+        const int each = 32 >> log_split;  // of each of the CTAs' lists
+        const int li = lane >> (5 - log_split), le = lane & (each - 1);
         const uint32_t least = kth_of_lanes(le < k ? (uint32_t)(s_all[li * k + le] >> 32) : 0u, k, lane);
 #pragma unroll
         for (int q = 0; q < 2; ++q)
@@ -581,10 +581,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
 // CTAs a row is split over: as many as give every SM two (a cluster's start and
 // join cost about 3 us: 64 rows of 128,256 fp32 logits took 15.9 us in 4 parts,
 // 17.4 in 8; 256 rows 24.6 in one, 45 in 2), not below one tile a warp.
+// A power of two; returns its logarithm.
 int pick_split(int rows, long long vecs, int sm_count) {
-  int s = 1;
-  while (s < kLpMaxSplit && (long long)rows * s <= sm_count && vecs > (long long)s * kLpWarps * kLpTile) s *= 2;
-  return s;
+  int l = 0;
+  while ((1 << l) < kLpMaxSplit && ((long long)rows << l) <= sm_count && vecs > (long long)kLpWarps * kLpTile << l) ++l;
+  return l;
 }
 
 template <typename T, bool kTop>
@@ -607,7 +608,8 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
       done[dev] = true;
     }
   }
-  const int split = pick_split(a.rows, ((long long)a.V + Elem<T>::kVec - 1) / Elem<T>::kVec, sms);
+  const int log_split = pick_split(a.rows, ((long long)a.V + Elem<T>::kVec - 1) / Elem<T>::kVec, sms);
+  const int split = 1 << log_split;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.rows * split);
   cfg.blockDim = dim3(kLpThreads);
@@ -620,7 +622,7 @@ cudaError_t launch(const LogprobArgs& a, cudaStream_t s) {
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, split);
+  return cudaLaunchKernelEx(&cfg, kern, a, log_split);
 }
 
 }  // namespace

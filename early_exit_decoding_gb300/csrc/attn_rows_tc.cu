@@ -19,13 +19,18 @@
 // thread the launch has, the control warps give most to them (216 + 216 + 72
 // = 3 x 168; with 168 they spilled, and a tile pair took 5900 clocks, not 3300).
 //
-// What bounds it: a row tile's chain, softmax (about 1500 clocks: 128 keys
-// loaded, compared, raised and packed by each thread) -> the 16 products of
-// its values and next scores (1290; 1035 if they ran alone) -> the hand-offs
-// between the warps (500), two of them interleaved: 3300 clocks a tile pair,
-// in which the tensor cores could do 6.3 products.  8192 queries, 32 heads, 8
-// KV heads, head_dim 128: 260.8 us, 0.49 of the measured bf16 rate, of them
-// about 50 us CTAs' starts and ends.
+// What bounds it (8192 queries, window 2048, 32 heads, 8 KV heads, head_dim
+// 128: 238 us, 0.54 of the measured bf16 rate; tensor pipe 45 % busy while a
+// CTA runs): a row tile's chain.  Softmax 1600 clocks (maxima 470, the vote on
+// rescaling 200, exponentials 820 of which the ex2 unit takes 512; a tile that
+// a mask cuts 700 more), then the 16 products of its values and next scores
+// (1345 from the first's issue to the last's arrival: 65 each behind 300), then
+// two hand-offs; the two tiles of a CTA interleave to 3500 clocks a pair of
+// tiles, in which the tensor cores could do 54 products and do 32.  The rest
+// is CTAs' starts (4800 clocks to the first scores, most of it Q's and the
+// first K's way from HBM) and ends (5000, and 1500 until the next one runs) of
+// 75000.  At head_dim 64 a product still takes 63 clocks (N = 64), so the rate
+// is half: 5 ragged prompts, window 500: 38 us.
 // The running maximum follows lazily: O and the sum are rescaled only when a
 // row's maximum grew by more than 2^8 since the last time (weights then stay
 // below 2^8, far inside both types; the sum is fp32), so most tiles touch O

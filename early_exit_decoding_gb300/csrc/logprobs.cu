@@ -20,6 +20,12 @@
 // logits reaches the threshold costs one comparison a thread and one vote.
 // The warps' lists are merged in order, then the CTAs'.
 //
+// What bounds it: HBM at many rows (4096 rows of 128,256 fp32 logits: 302 us,
+// 6.95 TB/s, 1.02 of a measured copy); at few rows the chain of a launch, the
+// copies' first arrival and the joins of warps and CTAs (one row 7.6 us, of
+// 0.5 MB), with top k above all the candidates' selection (64 rows: 10.1 us
+// without, 19.7 with 20 alternatives).
+//
 // A few rows are split over a thread-block cluster each (up to 16 CTAs); its
 // CTAs exchange sums and candidates through distributed shared memory, so
 // there is no workspace and no second launch.

@@ -17,9 +17,9 @@
 //   the rounding of the result.
 //
 // HBM bounds it: 16 keys bring 64 HD bytes and cost HD / 4 MMAs.  64 sequences,
-// window 4096, head_dim 128, 8 KV heads: 128 us, 6.35 TB/s, 0.94 of a measured
+// window 4096, head_dim 128, 8 KV heads: 127 us, 6.4 TB/s, 0.94 of a measured
 // copy.  A few sequences are bound by a launch's and a cluster's latency (one
-// of 1,024 keys: 7.7 us for 2 MB).
+// of 1,024 keys: 6.5 us for 2 MB).
 #include <mutex>
 
 #include "attn_ops.cuh"
@@ -410,9 +410,9 @@ __global__ void __launch_bounds__(kThreads, 3)
 
 // CTAs a row tile's keys are split over: as many as keep all of them within two
 // a SM, a unit for each warp.  More only queue clusters behind one another:
-// head_dim 128, window 2048, 8 KV heads: one sequence 27.9 us in 1 part, 13.7 in
-// 4, 11.1 in 8, 10.0 in 12, 11.3 in 16; 8 sequences 28.5, 16.8, 25.6, 25.4,
-// 43.1; 32 sequences 45 us in 1 part, 60 in 2.
+// head_dim 128, window 2048, 8 KV heads: one sequence 26.3 us in 1 part, 11.9 in
+// 4, 9.3 in 8, 8.1 in 12, 9.3 in 16; 8 sequences 27.1, 16.4, 24.4, 23.1, 37.0;
+// 32 sequences 43.8 us in 1 part, 54.8 in 4.
 int pick_split(long long tiles, int keys, int sm_count) {
   const int units = (keys + kUnit - 1) / kUnit;
   const long long s = min(2ll * sm_count / tiles, (long long)(units + kWarps - 1) / kWarps);

@@ -7,8 +7,9 @@
 // bulk copies (192 KB in flight a SM without a register held for them; plain
 // loads prefetched into registers spilled and gave 5.3 TB/s).  Every thread
 // keeps its own (m, s, t): a tile of 16 (fp32) or 32 (bf16, fp16) logits a
-// thread raises m by the tile's maximum first, s' = a s and t' = a (t + (m - m') s) with a = exp(m - m'), then adds
-// the tile's terms; threads, warps and the CTAs of a cluster join theirs by
+// thread raises m to the tile's maximum first, s' = a s and
+// t' = a (t + (m - m') s) with a = exp(m - m'), then adds the tile's terms;
+// threads, warps and the CTAs of a cluster join theirs by
 // the same rule in a fixed order, so results repeat bit for bit.
 //
 // Top k (k <= 32): every warp keeps the candidates above its threshold in a
@@ -585,8 +586,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpResident) k_logprobs(const __gr
 }
 
 // CTAs a row is split over: as many as give every SM two (a cluster's start and
-// join cost about 3 us: 64 rows of 128,256 fp32 logits took 15.9 us in 4 parts,
-// 17.4 in 8; 256 rows 24.6 in one, 45 in 2), not below one tile a warp.
+// join cost about 3 us: 16 rows of 128,256 fp32 logits take 16.9 us in one part,
+// 7.2 in 4, 5.7 in 8, 5.9 in 16; 64 rows 17.5, 10.1, 11.4, 14.0; 256 rows 24.0
+// in one, 41.8 in 2), not below one tile a warp.
 // A power of two; returns its logarithm.
 int pick_split(int rows, long long vecs, int sm_count) {
   int l = 0;

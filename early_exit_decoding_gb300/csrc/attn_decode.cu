@@ -9,7 +9,8 @@
 // barrier between warps.  The keys of a row tile are dealt out unit by unit
 // to the warps of a cluster of S CTAs; at the end the warps' states are joined
 // through shared memory, the CTAs' through distributed shared memory, in a
-// fixed order: no workspace, no atomics, one launch.
+// fixed order: no workspace, no atomics, one launch.  Behind a prefix its parts
+// are joined at the end too; with many sequences k_prefix_join does that.
 //
 //   S = q K^T (fp32), w = exp2(S - m) with the running maximum m of the unit's
 //   and all earlier keys, l += w in fp32 before w is rounded to the cache's
@@ -61,7 +62,7 @@ struct Tile {
 };
 // Divisors of a launch.
 struct DecodeShape {
-  int split, tiles, presplit;
+  int split, tiles, presplit, apart;
   FastDiv by_split, by_tiles, by_heads, by_rep;  // CTAs of a cluster, row tiles, KV heads, heads a KV head
 };
 
@@ -307,6 +308,20 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
       }
     }
+    if (sh.apart) {  // (one CTA a tile) to the workspace, as the prefix's parts lie there
+      const int i = t.row0 + r, pi = t.b * t.rep + i, rows = a.B * t.rep, pq = pi & 255;
+      const PrefixWs ws = prefix_ws(a.ws, pi >> 8, (rows + 255) / 256, rows, t.hk, a.Hkv, presplit, presplit + 1, HD);
+#pragma unroll
+      for (int i2 = 0; i2 < HD / 64; ++i2) {
+        const int d = 2 * lane + 64 * i2;
+        *reinterpret_cast<float2*>(ws.o + pq * HD + ((d >> 2) ^ (pq & (HD / 4 - 1))) * 4 + (d & 3)) = acc[i2];
+      }
+      if (lane == 0) {
+        ws.m[pq] = top;
+        ws.l[pq] = l;
+      }
+      continue;
+    }
     __syncwarp();
 #pragma unroll
     for (int i = 0; i < HD / 64; ++i)
@@ -315,6 +330,11 @@ __global__ void __launch_bounds__(kThreads, 3)
       c_m[r] = top;
       c_l[r] = l;
     }
+  }
+  if (sh.apart) {
+    // the join follows this kernel: it is not complete before the prefix's is
+    if (blockIdx.x == gridDim.x - 1) pdl_wait();
+    return;
   }
   if (split > 1)
     cluster_barrier();
@@ -408,6 +428,55 @@ __global__ void __launch_bounds__(kThreads, 3)
   if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
 }
 
+// A warp a row: the parts' maxima and sums a lane each, their outputs eight at a
+// time; as above.
+template <int HD, bool F16>
+__global__ void __launch_bounds__(256) k_prefix_join(const __grid_constant__ AttnOpArgs a, int parts, FastDiv by_rows, FastDiv by_rep) {
+  const int lane = threadIdx.x & 31, id = blockIdx.x * 8 + (threadIdx.x >> 5), rows = by_rows.d;
+  const int hk = by_rows.quot(id), pi = id - hk * rows;
+  if (hk >= a.Hkv) return;
+  const int b = by_rep.quot(pi), h = hk * by_rep.d + pi - b * by_rep.d, pq = pi & 255, ptiles = (rows + 255) / 256;
+  const PrefixWs ws = prefix_ws(a.ws, pi >> 8, ptiles, rows, hk, a.Hkv, 0, parts, HD);
+  const long long R = prefix_rows(ptiles, rows);
+  float pm = -INFINITY, pl = 0.f;
+  if (lane < parts) {
+    pm = ws.m[lane * 2 * R + pq];
+    pl = ws.l[lane * 2 * R + pq];
+  }
+  const float top = warp_max(pm), f = pm == -INFINITY ? 0.f : ex2(pm - top);
+  const float l = warp_sum(pm == -INFINITY ? pl : f * pl);
+  float2 acc[HD / 64];
+#pragma unroll
+  for (int i = 0; i < HD / 64; ++i) acc[i] = make_float2(0.f, 0.f);
+  for (int c0 = 0; c0 < parts; c0 += 8) {
+    float2 v[8][HD / 64];
+#pragma unroll
+    for (int c = 0; c < 8; ++c)
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i) {
+        const int d = 2 * lane + 64 * i;
+        v[c][i] = *reinterpret_cast<const float2*>(ws.o + min(c0 + c, parts - 1) * R * HD + pq * HD +
+                                                   ((d >> 2) ^ (pq & (HD / 4 - 1))) * 4 + (d & 3));
+      }
+#pragma unroll
+    for (int c = 0; c < 8; ++c) {
+      const float fc = __shfl_sync(0xffffffffu, f, (c0 + c) & 31);
+      if (c0 + c >= parts || fc == 0.f) continue;
+#pragma unroll
+      for (int i = 0; i < HD / 64; ++i) {
+        acc[i].x += fc * v[c][i].x;
+        acc[i].y += fc * v[c][i].y;
+      }
+    }
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < HD / 64; ++i)
+    *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + b * a.os[0] + h * a.os[2] + 2 * lane + 64 * i) =
+        pack2<F16>(acc[i].x * inv, acc[i].y * inv);
+  if (lane == 0 && a.lse) a.lse[(long long)b * a.Hq + h] = l == 0.f ? -INFINITY : (top + log2f(l)) * 0.6931471805599453f;
+}
+
 // CTAs a row tile's keys are split over: as many as keep all of them within two
 // a SM, a unit for each warp.  More only queue clusters behind one another:
 // head_dim 128, window 2048, 8 KV heads: one sequence 26.3 us in 1 part, 11.9 in
@@ -442,7 +511,8 @@ cudaError_t launch(const AttnOpArgs& a, bool pdl, cudaStream_t s) {
   const int tiles = (a.Tq * (a.Hq / a.Hkv) + kRows - 1) / kRows;
   const long long all = (long long)a.B * a.Hkv * tiles;
   const int presplit = a.P > 0 ? prefix_split(a.B, a.Hq / a.Hkv, a.Hkv, a.P) : 0;
-  const int split = pick_split(all, (int)min((long long)a.cap, (long long)a.window + a.Tq + a.sinks), sms);
+  const int apart = a.P > 0 && prefix_apart(a.B, a.Hq / a.Hkv, a.Hkv);
+  const int split = apart ? 1 : pick_split(all, (int)min((long long)a.cap, (long long)a.window + a.Tq + a.sinks), sms);
   if (all * split >= (1ll << 31)) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(all * split));
@@ -458,7 +528,7 @@ cudaError_t launch(const AttnOpArgs& a, bool pdl, cudaStream_t s) {
   attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = pdl ? 2 : 1;
-  const DecodeShape sh{split, tiles, presplit, FastDiv(split), FastDiv(tiles), FastDiv(a.Hkv), FastDiv(a.Hq / a.Hkv)};
+  const DecodeShape sh{split, tiles, presplit, apart, FastDiv(split), FastDiv(tiles), FastDiv(a.Hkv), FastDiv(a.Hq / a.Hkv)};
   return cudaLaunchKernelEx(&cfg, kern, maps, a, sh);
 }
 
@@ -488,6 +558,19 @@ bool make_kv_maps(KvMaps* m, const KeySrc& s, bool f16, int B, int Hkv, int hd, 
 }
 
 }  // namespace attn
+
+cudaError_t launch_prefix_join(const AttnOpArgs& a, cudaStream_t s) {
+  const int rep = a.Hq / a.Hkv, rows = a.B * rep, parts = prefix_split(a.B, rep, a.Hkv, a.P) + 1;
+  const unsigned grid = (unsigned)(((long long)rows * a.Hkv + 7) / 8);
+  const FastDiv by_rows(rows), by_rep(rep);
+  if (a.hd == 64)
+    a.f16 ? k_prefix_join<64, true><<<grid, 256, 0, s>>>(a, parts, by_rows, by_rep)
+          : k_prefix_join<64, false><<<grid, 256, 0, s>>>(a, parts, by_rows, by_rep);
+  else
+    a.f16 ? k_prefix_join<128, true><<<grid, 256, 0, s>>>(a, parts, by_rows, by_rep)
+          : k_prefix_join<128, false><<<grid, 256, 0, s>>>(a, parts, by_rows, by_rep);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_attn_decode(const AttnOpArgs& a, bool pdl, cudaStream_t s) {
   if (a.hd == 64) return a.f16 ? launch<64, true>(a, pdl, s) : launch<64, false>(a, pdl, s);

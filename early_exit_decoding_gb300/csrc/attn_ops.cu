@@ -32,13 +32,16 @@ cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s) {
 size_t shared_prefix_ws_bytes(int B, int Hq, int Hkv, int hd, int P) { return prefix_ws_bytes(B, Hq / Hkv, Hkv, hd, P); }
 
 // The prefix for all rows first, then each sequence's own keys; the second
-// kernel starts beside the first and takes the prefix's part at its end.
+// kernel starts beside the first and takes the prefix's part at its end, or
+// (many sequences) leaves its own part to a third that joins them.
 cudaError_t launch_shared_prefix_attention(const AttnOpArgs& a, cudaStream_t s) {
   if (a.P > 0) {
     const cudaError_t e = launch_attn_rows_tc(a, true, s);
     if (e != cudaSuccess) return e;
   }
-  return launch_attn_decode(a, a.P > 0, s);
+  const cudaError_t e = launch_attn_decode(a, a.P > 0, s);
+  if (e != cudaSuccess || a.P == 0 || !prefix_apart(a.B, a.Hq / a.Hkv, a.Hkv)) return e;
+  return launch_prefix_join(a, s);
 }
 
 }  // namespace river

@@ -200,7 +200,7 @@ struct PrefixWs {
   float *o, *m, *l;
 };
 __device__ __forceinline__ PrefixWs prefix_ws(void* ws, int tile, int tiles, int rows, int hk, int Hkv, int part, int split,
-                                              int hd) {
+                                              int hd) {  // split: parts of a tile and KV head, the own keys' too
   const long long R = prefix_rows(tiles, rows), e = ((long long)tile * Hkv + hk) * split + part;
   float* base = static_cast<float*>(ws);
   float* ml = base + (long long)tiles * Hkv * split * R * hd;
@@ -214,7 +214,13 @@ cudaError_t launch_attn_decode(const AttnOpArgs& a, bool pdl, cudaStream_t s);
 // Many query rows on the tensor cores (attn_rows_tc.cu): a prompt's window, or
 // (prefix) every sequence's rows against a.pre into a.ws.
 cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s);
-constexpr int kMaxPrefixSplit = 32;
+// Joins the prefix's parts and the own keys' part of every row (attn_decode.cu).
+cudaError_t launch_prefix_join(const AttnOpArgs& a, cudaStream_t s);
+constexpr int kMaxPrefixSplit = 31;  // and the own keys' part: one a lane
+// Whether the own keys' states go to the workspace too and a third launch joins
+// all: with more CTAs than the GPU holds at once, those that wait for the
+// prefix's products at their end would keep the others from starting.
+bool prefix_apart(int B, int rep, int Hkv);
 int prefix_split(int B, int rep, int Hkv, int P);
 size_t prefix_ws_bytes(int B, int rep, int Hkv, int hd, int P);
 

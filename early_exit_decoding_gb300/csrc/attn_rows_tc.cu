@@ -178,7 +178,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // A launch's shape: divisors, and whether Q comes by TMA (its map's axes: 64
 // dims, heads, query rows, 64-dim blocks, sequences; a box is a row tile).
 struct RowsShape {
-  int split, tiles, q_tma;
+  int split, tiles, q_tma, apart;
   FastDiv by_split, by_heads, by_group, by_rep;  // CTAs of a cluster, KV heads, KV heads x sequences, heads a KV head
 };
 
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           fence_proxy_async_smem();
           __syncwarp();
-          const PrefixWs ws = prefix_ws(a.ws, row0 / kRowsCta, tiles, a.B * rep, hk, a.Hkv, part, split, HD);
+          const PrefixWs ws = prefix_ws(a.ws, row0 / kRowsCta, tiles, a.B * rep, hk, a.Hkv, part, split + sh.apart, HD);
           if (lane == 0) {
             bulk_s2g(ws.o + (long long)q0 * HD, ring + q0 * HD * 4, rows * HD * 4);
             asm volatile("cp.async.bulk.commit_group;\ncp.async.bulk.wait_group 0;" ::: "memory");
@@ -788,6 +788,7 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   sh.split = split;
   sh.tiles = tiles;
   sh.q_tma = make_q_map(&q_map, a, PREFIX);
+  sh.apart = PREFIX && prefix_apart(a.B, rep, a.Hkv);
   sh.by_split = FastDiv(split);
   sh.by_heads = FastDiv(a.Hkv);
   sh.by_group = FastDiv(PREFIX ? a.Hkv : a.Hkv * a.B);
@@ -807,9 +808,23 @@ cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
 // measured): a CTA's start and end, its tiles of 128 keys (two row tiles, or
 // one), and the workspace traffic of a part.  152 SMs are planned for, so that
 // the workspace's size does not depend on the device.
+// CTAs of the prefix's products when the own keys' run beside them (two thirds
+// of the SMs: 256 sequences behind 32768 tokens, 32 heads, 8 KV heads, head_dim
+// 128, own keys up to 2000: 64 CTAs 249 us, 96 221, 128 255, 152 254; one after
+// the other, on all SMs, 274).
+constexpr int kApartCtas = 100;
+// More own-key CTAs than four an SM, of which three run at once (8 KV heads, head_dim 128, joined apart
+// against in place: 32 sequences behind 8192, up to 1024 of their own, 33.1 us
+// against 30.1, 64 45.4 against 46.3, 128 65.2 against 70.2; behind 1024, up to
+// 256, 14.5 against 12.2, 20.2 against 21.0, 29.0 against 29.6; called one by one
+// the third launch costs 2 us more).
+bool prefix_apart(int B, int rep, int Hkv) { return (long long)B * Hkv * ((rep + 15) / 16) > 4 * 152; }
+
 int prefix_split(int B, int rep, int Hkv, int P) {
   const long long rows = (long long)B * rep, tiles = (rows + kRowsCta - 1) / kRowsCta, items = tiles * Hkv;
   const long long nt = ((long long)P + kKeys - 1) / kKeys;
+  if (prefix_apart(B, rep, Hkv))  // the own keys run beside it on the other SMs
+    return (int)max(1ll, min(min(kApartCtas / items, nt), (long long)kMaxPrefixSplit));
   const double tile = rows > 128 ? 3400 : 2500;
   const double part = 0.5 * attn::prefix_rows((int)tiles, rows);
   int best = 1;
@@ -828,7 +843,7 @@ size_t prefix_ws_bytes(int B, int rep, int Hkv, int hd, int P) {
   const long long rows = (long long)B * rep;
   const int tiles = (int)((rows + kRowsCta - 1) / kRowsCta);
   const int split = P > 0 ? prefix_split(B, rep, Hkv, P) : 1;
-  return (size_t)tiles * Hkv * split * attn::prefix_rows(tiles, rows) * (hd + 2) * sizeof(float);
+  return (size_t)tiles * Hkv * (split + prefix_apart(B, rep, Hkv)) * attn::prefix_rows(tiles, rows) * (hd + 2) * sizeof(float);
 }
 
 cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s) {

@@ -526,8 +526,8 @@ RL_API rl_status rl_window_attention(const rl_attn_desc* a, const void* d_q, con
  *         overlap need one each
  * A sequence that sees no key gets 0 and lse -infinity; a kv_len outside
  * [0, kv_capacity] sets RL_DEVERR_CAPACITY and is clamped.  prefix_len 0 is
- * allowed (the prefix pointers are then not read).  Two launches (one without
- * a prefix), results repeat bit for bit.  Errors as rl_window_attention;
+ * allowed (the prefix pointers are then not read).  Two or three launches
+ * (one without a prefix), results repeat bit for bit.  Errors as rl_window_attention;
  * RL_ERR_INVALID_ARG also for a workspace too small. */
 RL_API rl_status rl_shared_prefix_workspace(const rl_attn_desc* a, int32_t prefix_len, uint64_t* bytes);
 RL_API rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const void* d_q,

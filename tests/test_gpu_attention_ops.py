@@ -332,6 +332,45 @@ def test_prefix_values(river, dtype, D, B, Hq, Hkv, P, cap):
     check_prefix(river.shared_prefix_attention(q, kp, vp, k, v, n), q, kp, vp, k, v, n)
 
 
+@pytest.mark.parametrize("B,Hq,Hkv,D,P,cap,dtype", [(160, 8, 4, 64, 300, 40, BF), (620, 3, 1, 128, 130, 17, FP), (80, 72, 4, 128, 513, 33, BF),
+                                                    (320, 8, 2, 128, 1, 300, BF), (640, 1, 1, 64, 2000, 5, FP)])
+def test_prefix_many_sequences(river, B, Hq, Hkv, D, P, cap, dtype):
+    """More own-key tiles than the GPU holds at once: a third launch joins."""
+    q, kp, vp, k, v = prefix_case(B, Hq, Hkv, D, P, cap, dtype, 171)
+    n = (torch.arange(B, device="cuda") * 7 % (cap + 1)).to(torch.int32)
+    got = river.shared_prefix_attention(q, kp, vp, k, v, n)
+    check_prefix(got, q, kp, vp, k, v, n)
+    again = river.shared_prefix_attention(q, kp, vp, k, v, n)
+    assert torch.equal(got["out"], again["out"]) and torch.equal(got["lse"], again["lse"])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        o = river.shared_prefix_attention(q, kp, vp, k, v, n)
+    for t in o.values():
+        t.zero_()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got["out"], o["out"]) and torch.equal(got["lse"], o["lse"])
+
+
+@pytest.mark.parametrize("Hq", [64, 128, 256])
+def test_many_heads_of_one_kv_head(river, Hq):
+    for T in (1, 5):
+        q, k, v = window_case(2, T, Hq, 1, 64, 300, BF, 181)
+        n = i32(300, 7)
+        check_window(river.window_attention(q, k, v, n, 90, 5), q, k, v, n, None, 90, 5)
+    c = prefix_case(3, Hq, 1, 64, 200, 20, BF, 183)
+    check_prefix(river.shared_prefix_attention(*c, i32(20, 0, 9)), *c, i32(20, 0, 9))
+
+
+def test_window_queries_shared_by_sequences_or_heads(river):
+    q, k, v = window_case(3, 40, 4, 2, 128, 200, BF, 185)
+    n = i32(200, 50, 3)
+    for x in (q[:1].expand(3, -1, -1, -1), q[:, :, :1].expand(-1, -1, 4, -1), q[:, :1].expand(-1, 40, -1, -1)):
+        check_window(river.window_attention(x, k, v, n, 60, 2), x, k, v, n, None, 60, 2)
+
+
 def test_prefix_alone_own_keys_alone_and_nothing(river):
     q, kp, vp, k, v = prefix_case(4, 8, 2, 64, 200, 50, BF, 101)
     zero = i32(0, 0, 0, 0)

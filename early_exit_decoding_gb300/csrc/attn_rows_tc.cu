@@ -755,7 +755,7 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   if (PREFIX) {
     split = prefix_split(a.B, rep, a.Hkv, a.P);
   } else {
-    // the count with the least time by this model (clocks, measured): rounds of
+    // the count with the least time by this model (clocks, measured): waves of
     // clusters, each a CTA's start and end, its tiles of 128 keys, a cluster's join
     const long long keys = min((long long)a.cap, (long long)a.window + min(a.Tq, kRowsCta / rep + 2) + a.sinks);
     const long long nt = (keys + kKeys - 1) / kKeys;

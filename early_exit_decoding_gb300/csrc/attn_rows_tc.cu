@@ -20,15 +20,15 @@
 // = 3 x 168; with 168 they spilled, and a tile pair took 5900 clocks, not 3300).
 //
 // What bounds it (8192 queries, window 2048, 32 heads, 8 KV heads, head_dim
-// 128: 238 us, 0.54 of the measured bf16 rate; tensor pipe 45 % busy while a
+// 128: 236 us, 0.55 of the measured bf16 rate; tensor pipe 45 % busy while a
 // CTA runs): a row tile's chain.  Softmax 1600 clocks (maxima 470, the vote on
 // rescaling 200, exponentials 820 of which the ex2 unit takes 512; a tile that
 // a mask cuts 700 more), then the 16 products of its values and next scores
 // (1345 from the first's issue to the last's arrival: 65 each behind 300), then
 // two hand-offs; the two tiles of a CTA interleave to 3500 clocks a pair of
 // tiles, in which the tensor cores could do 54 products and do 32.  The rest
-// is CTAs' starts (4800 clocks to the first scores, most of it Q's and the
-// first K's way from HBM) and ends (5000, and 1500 until the next one runs) of
+// is CTAs' starts (4000 clocks to the first scores, half of it the copies' way)
+// and ends (5000, and 1500 until the next one runs) of
 // 75000.  At head_dim 64 a product still takes 63 clocks (N = 64), so the rate
 // is half: 5 ragged prompts, window 500: 38 us.
 // The running maximum follows lazily: O and the sum are rescaled only when a
@@ -142,6 +142,12 @@ __device__ __forceinline__ void tma_load_q(void* dst, const CUtensorMap* map, in
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(0), "r"(head), "r"(row), "r"(seq)
       : "memory");
 }
+__device__ __forceinline__ void prefetch_q(const CUtensorMap* map, int head, int row, int seq) {
+  asm volatile("cp.async.bulk.prefetch.tensor.5d.L2.global.tile [%0, {%1, %2, %3, %1, %4}];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(0), "r"(head), "r"(row), "r"(seq)
+               : "memory");
+}
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Bits 0 .. n - 1.
@@ -179,6 +185,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 // dims, heads, query rows, 64-dim blocks, sequences; a box is a row tile).
 struct RowsShape {
   int split, tiles, q_tma, apart;
+  int ahead;  // clusters that run at once: the one this many on follows on these SMs
   FastDiv by_split, by_heads, by_group, by_rep;  // CTAs of a cluster, KV heads, KV heads x sequences, heads a KV head
 };
 
@@ -213,6 +220,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = sh.split, tiles = sh.tiles, rep = sh.by_rep.d;
   int id = sh.by_split.quot(blockIdx.x);
   const int part = blockIdx.x - id * split;
+  if (!PREFIX && tid == kThreads - 1 && part == 0 && sh.q_tma) {
+    // Q of the CTA that follows here into L2 (its first scores wait for Q: the
+    // 8192-token prompt 238 -> 236 us, the ragged ones 38.4 -> 37.6)
+    const int nid = id + sh.ahead, nback = sh.by_group.quot(nid), nrow0 = (tiles - 1 - nback) * kRowsCta;
+    if (nback < tiles) {
+      const int rest = nid - nback * sh.by_group.d, nb = sh.by_heads.quot(rest);
+      for (int g = 0; g < 2; ++g) {
+        const int t = sh.by_rep.quot(nrow0 + g * 128);
+        if (t < a.Tq) prefetch_q(&q_map, (rest - nb * sh.by_heads.d) * rep, t, nb);
+      }
+    }
+  }
   // later tiles of a prompt see more keys: first come, first served from the end
   const int back = sh.by_group.quot(id);
   const int row0 = (tiles - 1 - back) * kRowsCta;
@@ -770,7 +789,7 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
       }
     }
   }
-  if (ctas * split >= (1ll << 31)) return cudaErrorInvalidValue;
+  if (ctas * split >= (1ll << 31) - 4096) return cudaErrorInvalidValue;  // (a cluster some SMs ahead has a number too)
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(ctas * split));
   cfg.blockDim = dim3(kThreads);
@@ -788,6 +807,7 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   sh.split = split;
   sh.tiles = tiles;
   sh.q_tma = make_q_map(&q_map, a, PREFIX);
+  sh.ahead = PREFIX ? 0 : clusters[split];
   sh.apart = PREFIX && prefix_apart(a.B, rep, a.Hkv);
   sh.by_split = FastDiv(split);
   sh.by_heads = FastDiv(a.Hkv);

@@ -27,8 +27,8 @@
 // (1345 from the first's issue to the last's arrival: 65 each behind 300), then
 // two hand-offs; the two tiles of a CTA interleave to 3500 clocks a pair of
 // tiles, in which the tensor cores could do 54 products and do 32.  The rest
-// is CTAs' starts (4000 clocks to the first scores, half of it the copies' way)
-// and ends (5000, and 1500 until the next one runs) of
+// is CTAs' starts (4800 clocks to the first scores, half of it the copies' way,
+// before Q came from L2) and ends (5000, and 1500 until the next one runs) of
 // 75000.  At head_dim 64 a product still takes 63 clocks (N = 64), so the rate
 // is half: 5 ragged prompts, window 500: 38 us.
 // The running maximum follows lazily: O and the sum are rescaled only when a

@@ -599,6 +599,18 @@ def decode_step(model: Model, kv: KVCache, tokens, policy: Policy, out=None, str
     return o
 
 
+_TORCH = []
+
+
+def _torch():
+    """The module (imported with the first use; the statement in every call cost
+    the smallest calls 2 to 5 %)."""
+    if not _TORCH:
+        import torch
+        _TORCH.append(torch)
+    return _TORCH[0]
+
+
 def _refuse(msg, status=RL_ERR_INVALID_ARG):
     raise RiverError(status, msg)
 
@@ -606,7 +618,7 @@ def _refuse(msg, status=RL_ERR_INVALID_ARG):
 def _dtype_code(dtype):
     """RL_DT_* of a torch dtype; None for any other."""
     if not _DTYPES:
-        import torch
+        torch = _torch()
         _DTYPES.update({torch.float32: RL_DT_F32, torch.bfloat16: RL_DT_BF16, torch.float16: RL_DT_F16})
     return _DTYPES.get(dtype)
 
@@ -617,7 +629,7 @@ _DTYPES = {}
 def _operands(name, tensors):
     """The one CUDA device (index) of the tensors (None: absent), none of which
     may need a gradient (the operators have no backward pass)."""
-    import torch
+    torch = _torch()
     dev = tensors[0].get_device()
     grad = torch.is_grad_enabled()
     for t in tensors:
@@ -634,7 +646,7 @@ def _buffer(o, key, shape, like, dtype, stream, name):
     (taken on the stream that writes it)."""
     t = o.get(key)
     if t is None:
-        import torch
+        torch = _torch()
         if stream is None:
             t = torch.empty(shape, dtype=dtype, device=like.device)
         else:
@@ -651,7 +663,7 @@ def _buffer(o, key, shape, like, dtype, stream, name):
 def _run(dev, stream, fn, *args):
     """The library call ``fn(*args, stream)`` with device ``dev`` current;
     ``stream`` None: that device's current stream."""
-    import torch
+    torch = _torch()
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return _run(dev, stream, fn, *args)
@@ -662,7 +674,7 @@ def _run(dev, stream, fn, *args):
 
 
 def _int32(name, key, t, shape):
-    import torch
+    torch = _torch()
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         _refuse(f"{name}: {key} must be contiguous int32 {shape}")
 
@@ -678,7 +690,7 @@ def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None
     [R], ``logprob`` (tokens' shape), ``top_ids`` int32 and ``top_logprobs``
     [R][top_k]; buffers present in ``out`` are used.  ``err``: int32 [1] that
     collects RL_DEVERR_* bits.  See rl_token_logprobs."""
-    import torch
+    torch = _torch()
     name = "token_logprobs"
     dt = _dtype_code(logits.dtype)
     if logits.dim() != 2 or dt is None or logits.numel() == 0 or (logits.shape[1] > 1 and logits.stride(1) != 1):
@@ -693,7 +705,7 @@ def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None
         _int32(name, "tokens", tokens, (R,) if tokens.dim() == 1 else (R, n))
     if err is not None:
         _int32(name, "err", err, (1,))
-    o = {} if out is None else dict(out)
+    o = dict(out) if out else {}
     f32 = torch.float32
     lse = _buffer(o, "lse", (R,), logits, f32, stream, name).data_ptr()
     ent = _buffer(o, "entropy", (R,), logits, f32, stream, name).data_ptr()
@@ -767,14 +779,15 @@ def window_attention(q, k, v, kv_len, window, sinks=0, q_len=None, scale=None, o
     rows.  Returns a dict: ``out`` (q's shape, k's type) and ``lse`` fp32
     [B][T][Hq]; buffers present in ``out`` are used, their rows t >= q_len[b]
     left as they were.  See rl_window_attention."""
-    import torch
+    torch = _torch()
     name = "window_attention"
     dev = _operands(name, (q, k, v, kv_len, q_len, err))
     if q.dim() != 4:
         _refuse(f"{name}: q must be [B][T][Hq][hd]")
-    o = {} if out is None else dict(out)
+    o = dict(out) if out else {}
     res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
-    d = _plan(name, scale, (q, k, v, res), lambda: _attn_desc(name, q, k, v, res, scale))
+    # (a new result's layout follows q's shape)
+    d = _plan(name, scale, (q, k, v, res) if out else (q, k, v), lambda: _attn_desc(name, q, k, v, res, scale))
     B, T, Hq, _ = q.shape
     lse = _buffer(o, "lse", (B, T, Hq), q, torch.float32, stream, name)
     _int32(name, "kv_len", kv_len, (B,))
@@ -796,12 +809,12 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
     buffers present in ``out`` are used.  ``workspace``: a uint8 tensor of
     rl_shared_prefix_workspace bytes; None takes one from PyTorch's allocator
     for this call.  See rl_shared_prefix_attention."""
-    import torch
+    torch = _torch()
     name = "shared_prefix_attention"
     dev = _operands(name, (q, k_prefix, v_prefix, k, v, kv_len, workspace, err))
     if q.dim() != 3:
         _refuse(f"{name}: q must be [B][Hq][hd]")
-    o = {} if out is None else dict(out)
+    o = dict(out) if out else {}
     res = _buffer(o, "out", q.shape, q, k.dtype, stream, name)
 
     def make():
@@ -813,7 +826,7 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
         ps = (ctypes.c_int64 * 4)(*(t.stride(i) if t.shape[i] > 1 else 0 for t in (k_prefix, v_prefix) for i in (0, 1)))
         return d, ps, rl_shared_prefix_workspace(d, k_prefix.shape[1])
 
-    d, ps, need = _plan(name, scale, (q, k, v, res, k_prefix, v_prefix), make)
+    d, ps, need = _plan(name, scale, (q, k, v, k_prefix, v_prefix, res) if out else (q, k, v, k_prefix, v_prefix), make)
     B, Hq, _ = q.shape
     lse = _buffer(o, "lse", (B, Hq), q, torch.float32, stream, name)
     _int32(name, "kv_len", kv_len, (B,))

@@ -58,6 +58,12 @@ bool alloc_injected_failure() {
     if (e_ != cudaSuccess) return fail(RL_ERR_CUDA, "kernel launch: %s", cudaGetErrorString(e_)); \
   } while (0)
 
+#define RL_TRY(expr)                  \
+  do {                                \
+    rl_status s_ = (expr);            \
+    if (s_ != RL_OK) return s_;       \
+  } while (0)
+
 struct Linear {
   bf16* w = nullptr;        // [N][Kp]
   bf16* wt = nullptr;       // the same weights unit-tiled for the persistent step kernel
@@ -259,8 +265,9 @@ struct rl_kv {
   double prof_attn_keys = 0;     // keys the profiled step's attention reads per KV head
   std::vector<void*> allocs;
 
+  // Memory of the cache, not cleared: nothing is enqueued.
   template <typename T>
-  rl_status alloc(T** p, size_t n) {
+  rl_status alloc_raw(T** p, size_t n) {
     void* q = nullptr;
     if (n == 0) n = 1;
     if (alloc_injected_failure()) return fail(RL_ERR_OOM, "cudaMalloc(%zu bytes): injected failure", n * sizeof(T));
@@ -269,10 +276,16 @@ struct rl_kv {
       cudaGetLastError();
       return fail(RL_ERR_OOM, "cudaMalloc(%zu bytes): %s", n * sizeof(T), cudaGetErrorString(e));
     }
-    e = cudaMemset(q, 0, n * sizeof(T));
-    if (e != cudaSuccess) return fail(RL_ERR_CUDA, "cudaMemset: %s", cudaGetErrorString(e));
     allocs.push_back(q);
     *p = static_cast<T*>(q);
+    return RL_OK;
+  }
+  // Cleared on the null stream, which orders no other stream: whoever publishes
+  // the memory waits for that stream first.
+  template <typename T>
+  rl_status alloc(T** p, size_t n) {
+    RL_TRY(alloc_raw(p, n));
+    RL_CUDA(cudaMemset(*p, 0, (n == 0 ? 1 : n) * sizeof(T)));
     return RL_OK;
   }
   ~rl_kv() {
@@ -284,12 +297,6 @@ struct rl_kv {
 };
 
 namespace {
-
-#define RL_TRY(expr)                  \
-  do {                                \
-    rl_status s_ = (expr);            \
-    if (s_ != RL_OK) return s_;       \
-  } while (0)
 
 cudaStream_t as_stream(rl_stream_t s) { return static_cast<cudaStream_t>(s); }
 
@@ -1907,8 +1914,11 @@ rl_status rl_kv_share_prefix(rl_kv* kv, int32_t n) {
     for (int b = 1; b <= std::min(kv->maxB, kMaxBatch); ++b)
       need = std::max(need, shared_prefix_ws_bytes(b, m->Hq, m->Hkv, m->hd, n));
     if (need > kv->prefix_ws_bytes) {
+      // (a smaller one of before stays until the cache is freed; no clearing: every
+      // part that is read has been written by the same step, and a clearing would
+      // run on a stream that the steps' own does not wait for)
       char* p = nullptr;
-      RL_TRY(kv->alloc(&p, need));  // (a smaller one of before stays until the cache is freed)
+      RL_TRY(kv->alloc_raw(&p, need));
       kv->prefix_ws = p;
       kv->prefix_ws_bytes = need;
       kv->key = GraphKey();  // a captured step holds the old one's address
@@ -2275,6 +2285,7 @@ rl_status rl_kv_set_profiling(rl_kv* kv, int32_t enable) {
   }
   if (enable >= 2 && !kv->tl2)
     RL_TRY(kv->alloc(&kv->tl2, (size_t)kv->nph_cap * kv->m->sm_count * kTl2));
+  if (enable) RL_CUDA(cudaStreamSynchronize(nullptr));  // (the clearing)
   kv->profiling = enable != 0;
   kv->timeline = enable >= 2;
   return RL_OK;

@@ -256,8 +256,9 @@ RL_API rl_status rl_kv_set_window(rl_kv* kv, int32_t window, int32_t sinks);
  * slots, once for the whole batch, and each sequence's own slots from n on
  * (rl_shared_prefix_attention, on RL_PATH_GENERIC); each sequence writes its
  * own slots, so a prompt prefilled once with B = 1 serves them all.  n 0
- * switches it off, and so does the next rl_prefill.  Takes a workspace the
- * first time (waits for the device); make the call outside stream captures.
+ * switches it off, and so does the next rl_prefill.  Takes device memory for a
+ * workspace the first time (and for a prefix that needs more), enqueues
+ * nothing; make the call outside stream captures.
  * RL_ERR_STATE while a window is set; RL_ERR_INVALID_ARG for n outside [0, position];
  * RL_ERR_OOM (nothing changed). */
 RL_API rl_status rl_kv_share_prefix(rl_kv* kv, int32_t n);

@@ -196,6 +196,8 @@ extern "C" rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const voi
       return set_error(RL_ERR_UNSUPPORTED,
                        "rl_shared_prefix_attention: the prefix must start on 16-byte boundaries, strides whole "
                        "multiples of 16 bytes below 2^39 elements");
+    if (prefix_len > 1 && (prefix_stride[1] == 0 || prefix_stride[3] == 0))
+      return set_error(RL_ERR_UNSUPPORTED, "rl_shared_prefix_attention: the prefix's token strides must not be 0");
     o.pre.k = d_k_prefix;
     o.pre.v = d_v_prefix;
     o.pre.ks[1] = prefix_stride[0];

@@ -30,7 +30,7 @@ EXPORTS = (
     "rl_decode_step", "rl_decode_step_host", "rl_sync", "rl_decode_kernel_count",
     "rl_kv_set_profiling", "rl_kv_profile", "rl_kv_timeline", "rl_lm_head_static", "rl_kv_set_decode_path",
     "rl_kv_decode_path", "rl_save_exit_layers", "rl_load_exit_layers", "rl_exit_kv_cosine",
-    "rl_kv_set_wait_limit", "rl_debug_fail_allocations", "rl_model_offload_backbone",
+    "rl_kv_set_wait_limit", "rl_debug_fail_allocations", "rl_debug_limit_waits", "rl_model_offload_backbone",
     "rl_model_memory", "rl_token_logprobs", "rl_window_attention", "rl_shared_prefix_workspace",
     "rl_shared_prefix_attention", "rl_kv_set_window", "rl_kv_share_prefix", "rl_prefill_score",
 )
@@ -114,6 +114,7 @@ def _load():
         "rl_model_offload_backbone": (I, [P, I, P]),
         "rl_model_memory": (I, [P, ctypes.POINTER(ctypes.c_uint64), ctypes.POINTER(ctypes.c_uint64)]),
         "rl_debug_fail_allocations": (I, [ctypes.c_int64]),
+        "rl_debug_limit_waits": (I, [ctypes.c_int64]),
         "rl_load_exit_layers": (I, [P, ctypes.c_char_p, P]),
         "rl_kv_set_window": (I, [P, I, I]),
         "rl_kv_share_prefix": (I, [P, I]),
@@ -288,6 +289,11 @@ def rl_debug_fail_allocations(after):
     """Test hook: the next ``after`` library allocations succeed, later ones
     fail (RL_ERR_OOM); negative switches it off."""
     _check(_lib.rl_debug_fail_allocations(int(after)))
+
+
+def rl_debug_limit_waits(polls):
+    """The many-row attention kernel's waits give up after ``polls`` polls; negative switches it off."""
+    _check(_lib.rl_debug_limit_waits(int(polls)))
 
 
 def rl_kv_set_window(kv, window, sinks=0):

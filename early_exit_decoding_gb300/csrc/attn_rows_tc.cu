@@ -39,6 +39,7 @@
 // Keys are dealt out over a cluster of S CTAs when the row tiles alone do not
 // fill the GPU; its CTAs join their (maximum, sum, O) through distributed
 // shared memory in a fixed order.
+#include <atomic>
 #include <mutex>
 
 #include "attn_ops.cuh"
@@ -57,6 +58,8 @@ constexpr int kMaxSplit = 8;     // CTAs of a cluster (of 16, no more than 7 clu
 constexpr int kSpin = 1 << 20;   // polls of a wait before it gives up (one that fails takes 1.3 us)
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLazy = 8.f;     // log2 growth of a maximum that is let pass
+
+std::atomic<long long> g_wait_polls{-1};  // rl_debug_limit_waits (below 0: kSpin)
 
 template <int HD>
 constexpr int kTileBytes = kKeys * HD * 2;  // a Q, K or V tile: HD / 64 blocks of 128 rows x 128 bytes
@@ -186,6 +189,7 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 struct RowsShape {
   int split, tiles, q_tma, apart;
   int ahead;  // clusters that run at once: the one this many on follows on these SMs
+  int polls;  // of a wait before it gives up
   FastDiv by_split, by_heads, by_group, by_rep;  // CTAs of a cluster, KV heads, KV heads x sequences, heads a KV head
 };
 
@@ -206,6 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) Bars bar;
   __shared__ uint32_t s_tmem;
   __shared__ volatile int s_fail;
+  __shared__ int s_loaded;  // K and V tiles copied (set where the copying ends)
   __shared__ float s_m[kRowsCta], s_l[kRowsCta];  // a row's maximum (log2 units) and sum
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -338,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto wait = [&](uint64_t* w, uint32_t ph) {
     // (counted, not timed, and no more than this: a few instructions more here
     // cost the issuing warp's chain 8 % of a prompt's time)
-    for (int i = 0; i < kSpin; ++i) {
+    for (int i = 0; i < sh.polls; ++i) {
       if (mbar_try(w, ph)) return true;
       if ((i & 255) == 255 && s_fail) return false;
     }
@@ -354,13 +359,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == 8) {
     if (lane == 0) {
       int i = 1;
-      bool go = true;
       for (; i < 2 * nt; ++i) {
-        if (i >= NST && !(go = wait(&bar.empty[i % NST], ((i / NST) - 1) & 1))) break;
+        if (i >= NST && !wait(&bar.empty[i % NST], ((i / NST) - 1) & 1)) break;
         load(i);
       }
-      if (!go || s_fail)  // the copies in flight still land before anybody leaves
-        for (int q = max(0, i - NST); q < i; ++q) mbar_wait(&bar.full[q % NST], (q / NST) & 1, kSpin);
+      s_loaded = nt > 0 ? i : 0;
     }
     __syncwarp();
   } else if (warp == 9) {
@@ -702,7 +705,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   fence_before();
   __syncthreads();
-  if (tid == 0 && s_fail && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
+  if (tid == 0 && s_fail) {
+    // the copies in flight still land before anybody leaves (here: a wait may
+    // give up after the copying has ended)
+    for (int q = max(0, s_loaded - NST); q < s_loaded; ++q) mbar_wait(&bar.full[q % NST], (q / NST) & 1, kSpin);
+    if (a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
+  }
   if (warp == 9) {
     fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512) : "memory");
@@ -804,6 +812,8 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   cfg.numAttrs = 1;
   RowsShape sh;
   CUtensorMap q_map = {};
+  const long long polls = g_wait_polls.load();
+  sh.polls = polls < 0 ? kSpin : (int)min(polls, (long long)kSpin);
   sh.split = split;
   sh.tiles = tiles;
   sh.q_tma = make_q_map(&q_map, a, PREFIX);
@@ -871,3 +881,8 @@ cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s
 }
 
 }  // namespace river
+
+extern "C" rl_status rl_debug_limit_waits(int64_t polls) {
+  river::g_wait_polls.store(polls);
+  return RL_OK;
+}

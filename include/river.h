@@ -393,9 +393,20 @@ RL_API rl_status rl_kv_timeline(rl_kv* kv, rl_stream_t stream, int64_t cap, uint
  * the library succeed and every later one fails as if cudaMalloc had
  * (RL_ERR_OOM), until it is called with a negative value (the default: no
  * injection).  Process-wide; not thread-safe with respect to concurrent
- * allocating calls. */
+ * allocating calls.
+ *
+ * rl_debug_limit_waits: the waits of the many-row attention kernel (more than
+ * 16 query rows a KV head of rl_window_attention, the prefix of
+ * rl_shared_prefix_attention, and the model's paths over them) give up after
+ * `polls` polls from the next launch on (a captured one keeps its limit),
+ * until it is called with a negative value (the default: the kernel's own
+ * limit, about a second).  A wait that gives up sets RL_DEVERR_TIMEOUT, and a
+ * row that could not be computed gets NaN; the copies and tensor-core
+ * operations in flight are waited for with the kernel's own limit, and the
+ * context stays usable.  Process-wide. */
 RL_API rl_status rl_kv_set_wait_limit(rl_kv* kv, int64_t polls);
 RL_API rl_status rl_debug_fail_allocations(int64_t after);
+RL_API rl_status rl_debug_limit_waits(int64_t polls);
 
 /* Number of kernels one decode step launches for batch B (for launch
  * accounting); 0 on bad arguments. */

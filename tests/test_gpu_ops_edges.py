@@ -76,3 +76,53 @@ def test_share_prefix_beside_a_busy_default_stream(river, stream, tiny):
     want = run(False)[0]
     for got in run(True):
         assert torch.equal(got, want)
+
+
+def rnd(*shape, seed, dtype=torch.bfloat16):
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    return torch.randn(shape, device="cuda", generator=g).to(dtype)
+
+
+def given_up(river, call):
+    """``call(err)`` with waits that give up at once, between two ordinary
+    calls that must agree: the outputs of the second one's kind."""
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    want = call(err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    river.rl_debug_limit_waits(0)
+    try:
+        got = call(err)
+        torch.cuda.synchronize()
+    finally:
+        river.rl_debug_limit_waits(-1)
+    assert int(err) == river.RL_DEVERR_TIMEOUT
+    err.zero_()
+    again = call(err)
+    torch.cuda.synchronize()
+    assert int(err) == 0
+    for n in want:
+        assert torch.equal(want[n], again[n]), n
+    return got
+
+
+# (sequences, query rows, heads, KV heads, head_dim, keys, window): one key tile (every copy
+# is issued before any wait) and many; one CTA a row tile and a cluster
+WAITS = [(2, 40, 8, 2, 64, 100, 50), (2, 40, 8, 2, 128, 100, 100), (40, 300, 8, 4, 128, 1500, 900), (1, 40, 8, 1, 64, 4000, 4000)]
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,n,window", WAITS)
+def test_rows_whose_waits_give_up(river, B, T, Hq, Hkv, D, n, window):
+    q, k, v = rnd(B, T, Hq, D, seed=1), rnd(B, Hkv, n, D, seed=2), rnd(B, Hkv, n, D, seed=3)
+    kv_len = torch.full((B,), n, dtype=torch.int32, device="cuda")
+    given_up(river, lambda err: river.window_attention(q, k, v, kv_len, window, err=err))
+
+
+@pytest.mark.parametrize("B,prefix", [(3, 100), (40, 3000), (160, 700)])
+def test_prefix_whose_waits_give_up(river, B, prefix):
+    q, pk, pv = rnd(B, 8, 128, seed=1), rnd(4, prefix, 128, seed=2), rnd(4, prefix, 128, seed=3)
+    k, v = rnd(B, 4, 24, 128, seed=4), rnd(B, 4, 24, 128, seed=5)
+    kv_len = torch.arange(B, dtype=torch.int32, device="cuda") % 25
+    got = given_up(river, lambda err: river.shared_prefix_attention(q, pk, pv, k, v, kv_len, err=err))
+    assert torch.isnan(got["out"]).all() and torch.isnan(got["lse"]).all()

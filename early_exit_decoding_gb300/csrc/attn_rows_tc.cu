@@ -555,7 +555,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (g < ngrp && nt > 0) {
       // (the last tile's: the ring, which the other tile's products still read,
       // is written over below)
-      if (!go || !wait_warp(&bar.o_full[PREFIX || !direct ? ngrp - 1 : g], 0)) l = inv = NAN;
+      if (!go || !(go = wait_warp(&bar.o_full[PREFIX || !direct ? ngrp - 1 : g], 0))) {
+        l = inv = NAN;
+        if (row_at >= 0 && a.lse) {  // (stored above, of the keys there were)
+          const int t = sh.by_rep.quot(i_row);
+          a.lse[((long long)b * a.Tq + t) * a.Hq + hk * rep + i_row - t * rep] = NAN;
+        }
+      }
       fence_after();
     }
     auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
@@ -621,7 +627,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int q = lane / CR; q < 32; q += 32 / CR) {
           const long long at = __shfl_sync(0xffffffffu, row_at, q);
           const int c = lane % CR;
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + q * (HD * 2) + ((c ^ (q & 7)) << 4));
+          uint4 v = *reinterpret_cast<const uint4*>(stage + q * (HD * 2) + ((c ^ (q & 7)) << 4));
+          // (after a wait that gave up Q's copy may land on the staged rows)
+          if (!go) v = make_uint4(0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu, 0x7fff7fffu);
           if (at >= 0) *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at + c * 8) = v;
         }
         // rows of different masks shared V's tiles: one that is not finite may

@@ -1981,6 +1981,7 @@ rl_status enqueue_scores(rl_model* m, rl_kv* kv, const StepIO& io, const Work& w
   const int M = io.B * io.T;
   for (int r0 = 0; r0 < M; r0 += rows) {
     const int n = std::min(rows, M - r0);
+    if (alloc_injected_failure()) return fail(RL_ERR_OOM, "scores from row %d on: injected failure", r0);
     GemvArgs a = gemv_base(m, Linear(), W4_OFF, nullptr, 0);
     a.w = m->lm_head;
     a.N = m->V;
@@ -2073,15 +2074,18 @@ rl_status prefill_run(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B
     }
   }
   rl_status st = reset_sync_words(kv, s);
-  if (st == RL_OK) st = enqueue_pass(m, kv, io, w, s);
-  if (st == RL_OK && score) st = enqueue_scores(m, kv, io, w, *score, score_logits, (int)score_rows, s);
+  if (st == RL_OK) {
+    kv->prefix = 0;  // its slots are written over from here on
+    st = enqueue_pass(m, kv, io, w, s);
+  }
+  if (st == RL_OK) {  // the cache holds the prompt, whatever becomes of the scores
+    kv->host_pos = T;
+    kv->host_step = 0;
+    if (score) st = enqueue_scores(m, kv, io, w, *score, score_logits, (int)score_rows, s);
+  }
   if (score_logits) cudaFreeAsync(score_logits, s);
   cudaFreeAsync(base, s);
-  if (st != RL_OK) return st;
-  kv->host_pos = T;
-  kv->host_step = 0;
-  kv->prefix = 0;
-  return RL_OK;
+  return st;
 }
 
 }  // namespace

@@ -297,8 +297,9 @@ RL_API rl_status rl_prefill(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int
  *   d_entropy [B][T] fp32 (may be NULL): of the distribution after position t
  *   d_top_ids, d_top_logprobs [B][T][top_k] (NULL when top_k is 0; top_k <= 32):
  *             the most likely tokens after position t
- * Not on the pages: it compares what exits cost in likelihood (the perplexity
- * of a text under a policy). */
+ * An error after the prompt's own pass leaves the cache as rl_prefill does, the
+ * scores unwritten.  Not on the pages: it compares what exits cost in likelihood
+ * (the perplexity of a text under a policy). */
 RL_API rl_status rl_prefill_score(rl_model* m, rl_kv* kv, const int32_t* d_tokens, int32_t B, int32_t T,
                                   const rl_exit_policy* policy, float* d_logits, int32_t* d_next_token,
                                   int32_t* d_exit_layer, float* d_min_cos, float* d_logprob,
@@ -392,8 +393,8 @@ RL_API rl_status rl_kv_timeline(rl_kv* kv, rl_stream_t stream, int64_t cap, uint
  * rl_debug_fail_allocations: the next `after` device allocations made by
  * the library succeed and every later one fails as if cudaMalloc had
  * (RL_ERR_OOM), until it is called with a negative value (the default: no
- * injection).  Process-wide; not thread-safe with respect to concurrent
- * allocating calls.
+ * injection); every 512 rows that rl_prefill_score scores count as one more.
+ * Process-wide; not thread-safe with respect to concurrent allocating calls.
  *
  * rl_debug_limit_waits: the waits of the many-row attention kernel (more than
  * 16 query rows a KV head of rl_window_attention, the prefix of

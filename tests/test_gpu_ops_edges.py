@@ -127,3 +127,31 @@ def test_prefix_whose_waits_give_up(river, B, prefix):
     kv_len = torch.arange(B, dtype=torch.int32, device="cuda") % 25
     got = given_up(river, lambda err: river.shared_prefix_attention(q, pk, pv, k, v, kv_len, err=err))
     assert torch.isnan(got["out"]).all() and torch.isnan(got["lse"]).all()
+
+
+def test_scores_that_fail_leave_the_prompt(river, stream, tiny):
+    """A failure behind the prompt's own pass: position, slots and prefix are
+    those of a plain prefill, and decoding goes on from there."""
+    kv = tiny.kv_cache_alloc(3, 32)
+    pol = river.Policy.forced(torch.tensor([TINY.n_layers], dtype=torch.int32, device="cuda"))
+    first = torch.from_numpy(synth.gen_tokens(TINY.vocab, (1, 9), seed=1)).cuda()
+    toks = torch.from_numpy(synth.gen_tokens(TINY.vocab, (3, 5), seed=2)).cuda()
+    tok = torch.from_numpy(synth.gen_tokens(TINY.vocab, (3,), seed=3)).cuda()
+    with torch.cuda.stream(stream):
+        river.prefill(tiny, kv, toks, pol, stream=stream)
+        want = [river.decode_step(tiny, kv, tok, pol, stream=stream)["logits"] for _ in range(3)]
+        river.prefill(tiny, kv, first, pol, stream=stream)
+        kv.share_prefix()
+        river.rl_debug_fail_allocations(2)  # both workspaces are there, the scores are not
+        try:
+            with pytest.raises(river.RiverError) as e:
+                river.prefill_score(tiny, kv, toks, pol, stream=stream)
+        finally:
+            river.rl_debug_fail_allocations(-1)
+        assert e.value.status == river.RL_ERR_OOM and "injected" in str(e.value)
+        assert kv.position() == (5, 0)
+        got = [river.decode_step(tiny, kv, tok, pol, stream=stream)["logits"] for _ in range(3)]
+        kv.sync(stream)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        kv.set_position(0, 0, stream)  # no prefix any more

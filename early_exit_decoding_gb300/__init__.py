@@ -634,16 +634,18 @@ _DTYPES = {}
 
 def _operands(name, tensors):
     """The one CUDA device (index) of the tensors (None: absent), none of which
-    may need a gradient (the operators have no backward pass)."""
+    may need a gradient or carry a tangent (the operators have no derivatives)."""
     torch = _torch()
     dev = tensors[0].get_device()
-    grad = torch.is_grad_enabled()
+    grad, dual = torch.is_grad_enabled(), torch.autograd.forward_ad._current_level >= 0
     for t in tensors:
         if t is not None:
-            if t.get_device() != dev or dev < 0:
-                _refuse(f"{name}: every operand must be on one CUDA device (found {t.device})")
             if grad and t.requires_grad:
                 _refuse(f"{name}: an operand requires a gradient; the operator has no backward pass", RL_ERR_UNSUPPORTED)
+            if dual and torch.autograd.forward_ad.unpack_dual(t).tangent is not None:
+                _refuse(f"{name}: an operand carries a tangent; the operator has no forward-mode derivative", RL_ERR_UNSUPPORTED)
+            if t.get_device() != dev or dev < 0:
+                _refuse(f"{name}: every operand must be on one CUDA device (found {t.device})")
     return dev
 
 

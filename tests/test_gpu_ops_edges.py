@@ -5,6 +5,7 @@ import pytest
 
 import synth
 from tests.harness import build_pair
+from tests.test_ops_edges import derivatives_refused, forms
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -155,3 +156,8 @@ def test_scores_that_fail_leave_the_prompt(river, stream, tiny):
         for a, b in zip(got, want):
             assert torch.equal(a, b)
         kv.set_position(0, 0, stream)  # no prefix any more
+
+
+def test_operands_with_derivatives_are_refused(river):
+    for call, ops in forms(river, "cuda"):
+        derivatives_refused(river, call, ops, range(len(ops)), lambda given: given())

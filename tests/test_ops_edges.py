@@ -21,3 +21,47 @@ def test_prefix_token_stride_zero_is_refused(river, ps):
     """Rows 64 elements apart would be read behind a buffer of one row."""
     assert _shared(river, ps=ps) == river.RL_ERR_UNSUPPORTED
     assert "token strides" in river.rl_last_error()
+
+
+def derivatives_refused(river, call, ops, which, plain):
+    """Each operand of `which` in turn with a gradient, with a tangent, and
+    plain beside an open dual level (`plain(call)`: what holds then)."""
+    import torch.autograd.forward_ad as fw
+    for i in which:
+        x = ops[i]
+
+        def given(y):
+            return lambda: call(*ops[:i], y, *ops[i + 1:])
+
+        def refused(y):
+            with pytest.raises(river.RiverError) as e:
+                given(y)()
+            assert e.value.status == river.RL_ERR_UNSUPPORTED, e.value
+        refused(x.clone().requires_grad_())
+        with fw.dual_level():
+            refused(fw.make_dual(x, torch.ones_like(x)))
+            with torch.no_grad():  # (which does not stop forward mode)
+                refused(fw.make_dual(x, torch.ones_like(x)))
+            plain(given(x))
+
+
+def forms(river, device):
+    """The Python forms as functions of their floating-point operands."""
+    n = torch.ones(1, dtype=torch.int32, device=device)
+
+    def zeros(*shape):
+        return torch.zeros(shape, dtype=torch.bfloat16, device=device)
+    return [(river.token_logprobs, [zeros(2, 10)]),
+            (lambda q, k, v: river.window_attention(q, k, v, n, 4), [zeros(1, 1, 4, 64), zeros(1, 2, 8, 64), zeros(1, 2, 8, 64)]),
+            (lambda q, pk, pv, k, v: river.shared_prefix_attention(q, pk, pv, k, v, n),
+             [zeros(1, 4, 64), zeros(2, 8, 64), zeros(2, 8, 64), zeros(1, 2, 8, 64), zeros(1, 2, 8, 64)])]
+
+
+def test_operands_with_derivatives_are_refused(river):
+    """A tangent (forward mode) is no more dropped in silence than a gradient."""
+    def plain(call):
+        with pytest.raises(river.RiverError) as e:
+            call()
+        assert e.value.status == river.RL_ERR_INVALID_ARG  # (host tensors)
+    for call, ops in forms(river, "cpu"):
+        derivatives_refused(river, call, ops, [0], plain)

@@ -296,12 +296,21 @@ def rl_debug_limit_waits(polls):
     _check(_lib.rl_debug_limit_waits(int(polls)))
 
 
+_INT32_MAX = 2**31 - 1
+
+
+def _int32_of(n):
+    """n for a C int32 that a larger one may stand for (ctypes keeps the low 32
+    bits): what is beyond becomes the largest, what is negative -1."""
+    return max(-1, min(n, _INT32_MAX))
+
+
 def rl_kv_set_window(kv, window, sinks=0):
-    _check(_lib.rl_kv_set_window(kv, int(window), int(sinks)))
+    _check(_lib.rl_kv_set_window(kv, _int32_of(int(window)), _int32_of(int(sinks))))
 
 
 def rl_kv_share_prefix(kv, n):
-    _check(_lib.rl_kv_share_prefix(kv, int(n)))
+    _check(_lib.rl_kv_share_prefix(kv, _int32_of(int(n))))
 
 
 def rl_prefill_score(model, kv, d_tokens, B, T, policy, d_logits, d_next_token, d_exit_layer, d_min_cos,
@@ -360,7 +369,7 @@ def rl_token_logprobs(d_logits, dtype, rows, vocab, row_stride, d_tokens, n_tok,
 def rl_window_attention(desc, d_q, d_k, d_v, d_kv_len, d_q_len, window, sinks, d_out, d_lse,
                         d_err=None, stream=None):
     _check(_lib.rl_window_attention(ctypes.byref(desc), _ptr(d_q), _ptr(d_k), _ptr(d_v), _ptr(d_kv_len),
-                                    _ptr(d_q_len), window, sinks, _ptr(d_out), _ptr(d_lse), _ptr(d_err),
+                                    _ptr(d_q_len), _int32_of(window), _int32_of(sinks), _ptr(d_out), _ptr(d_lse), _ptr(d_err),
                                     _stream(stream)))
 
 
@@ -739,7 +748,6 @@ def _strides(d, t):
 
 
 _PLANS = {}
-_INT32_MAX = 2**31 - 1
 
 
 def _plan(name, scale, tensors, make):
@@ -804,7 +812,7 @@ def window_attention(q, k, v, kv_len, window, sinks=0, q_len=None, scale=None, o
     if err is not None:
         _int32(name, "err", err, (1,))
     _run(dev, stream, _lib.rl_window_attention, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), kv_len.data_ptr(),
-         _addr(q_len), min(window, _INT32_MAX), min(sinks, _INT32_MAX), res.data_ptr(), lse.data_ptr(), _addr(err))
+         _addr(q_len), _int32_of(window), _int32_of(sinks), res.data_ptr(), lse.data_ptr(), _addr(err))
     return o
 
 

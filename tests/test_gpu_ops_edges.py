@@ -161,3 +161,18 @@ def test_scores_that_fail_leave_the_prompt(river, stream, tiny):
 def test_operands_with_derivatives_are_refused(river):
     for call, ops in forms(river, "cuda"):
         derivatives_refused(river, call, ops, range(len(ops)), lambda given: given())
+
+
+def test_windows_beyond_32_bits(river):
+    q, k = rnd(1, 1, 4, 64, seed=1), rnd(1, 2, 40, 64, seed=2)
+    n = torch.full((1,), 40, dtype=torch.int32, device="cuda")
+    want = river.window_attention(q, k, k, n, 40)
+    for window in (2**31, 2**32 + 5):
+        got = river.window_attention(q, k, k, n, window, 0)
+        assert torch.equal(got["out"], want["out"])
+        got = river.window_attention(q, k, k, n, 3, window)
+        assert torch.equal(got["out"], want["out"])
+    for window, sinks in ((0, 0), (-2**31 - 1, 0), (-2**32 + 5, 0), (5, -2**32 + 1), (5, -1)):
+        with pytest.raises(river.RiverError) as e:
+            river.window_attention(q, k, k, n, window, sinks)
+        assert e.value.status == river.RL_ERR_INVALID_ARG

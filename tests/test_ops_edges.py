@@ -65,3 +65,38 @@ def test_operands_with_derivatives_are_refused(river):
         assert e.value.status == river.RL_ERR_INVALID_ARG  # (host tensors)
     for call, ops in forms(river, "cpu"):
         derivatives_refused(river, call, ops, [0], plain)
+
+
+class Recorder:
+    """Stands in for the library: every call's 32-bit arguments as C sees them."""
+
+    def __init__(self, lib):
+        self.lib, self.seen = lib, []
+
+    def __getattr__(self, name):
+        real = getattr(self.lib, name)
+
+        def call(*args):
+            self.seen.append([t(a).value if t is ctypes.c_int32 else None for t, a in zip(real.argtypes, args)])
+            return 0
+        return call
+
+
+def test_windows_and_prefixes_beyond_32_bits(river, monkeypatch):
+    """2^32 + 5 is no window of 5, and -2^31 - 1 none at all."""
+    rec = Recorder(river._lib)
+    monkeypatch.setattr(river, "_lib", rec)
+    kv = object.__new__(river.KVCache)
+    kv.handle = None
+    big = 2**31 - 1
+    for n, c in ((0, 0), (5, 5), (big, big), (2**32, big), (2**32 + 5, big), (-1, -1), (-2**31 - 1, -1), (-2**32 + 5, -1)):
+        kv.set_window(n, n)
+        assert rec.seen.pop()[1:] == [c, c]
+        kv.share_prefix(n)
+        assert rec.seen.pop()[1:] == [c]
+        river.rl_window_attention(_desc(river), None, None, None, None, None, n, n, None, None, stream=Stream)
+        assert rec.seen.pop()[6:8] == [c, c]
+
+
+class Stream:
+    cuda_stream = None

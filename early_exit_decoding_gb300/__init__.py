@@ -712,8 +712,10 @@ def token_logprobs(logits, tokens=None, top_k=0, out=None, err=None, stream=None
     dt = _dtype_code(logits.dtype)
     if logits.dim() != 2 or dt is None or logits.numel() == 0 or (logits.shape[1] > 1 and logits.stride(1) != 1):
         _refuse(f"{name}: logits must be fp32, bf16 or fp16 [R][V] with contiguous rows")
-    dev = _operands(name, (logits, tokens, err))
     R, V = logits.shape
+    if R > _INT32_MAX or V > _INT32_MAX:
+        _refuse(f"{name}: rows and vocabulary must be below 2^31", RL_ERR_UNSUPPORTED)
+    dev = _operands(name, (logits, tokens, err))
     if not 0 <= top_k <= min(32, V):
         _refuse(f"{name}: top_k {top_k} outside [0, {min(32, V)}]")
     n = 0
@@ -773,6 +775,8 @@ def _attn_desc(name, q, k, v, out, scale):
     B, Hq, hd = q.shape[0], q.shape[-2], q.shape[-1]
     T = q.shape[1] if q.dim() == 4 else 1
     _, Hkv, S, _ = k.shape
+    if max(*q.shape, *k.shape) > _INT32_MAX:
+        _refuse(f"{name}: sizes must be below 2^31", RL_ERR_UNSUPPORTED)
     qc, kc = _dtype_code(q.dtype), _dtype_code(k.dtype)
     if k.shape != v.shape or k.shape[0] != B or k.shape[3] != hd or v.dtype != k.dtype or out.dtype != k.dtype or \
             qc is None or kc is None:
@@ -839,6 +843,8 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
                 v_prefix.dtype != k.dtype or k_prefix.shape[0] != d.n_kv_heads or k_prefix.shape[2] != d.head_dim or \
                 k_prefix.stride(2) != 1 or v_prefix.stride(2) != 1:
             _refuse(f"{name}: k_prefix and v_prefix must be {k.dtype} [{d.n_kv_heads}][P][{d.head_dim}] with a contiguous last axis")
+        if k_prefix.shape[1] > _INT32_MAX:
+            _refuse(f"{name}: sizes must be below 2^31", RL_ERR_UNSUPPORTED)
         ps = (ctypes.c_int64 * 4)(*(t.stride(i) if t.shape[i] > 1 else 0 for t in (k_prefix, v_prefix) for i in (0, 1)))
         return d, ps, rl_shared_prefix_workspace(d, k_prefix.shape[1])
 

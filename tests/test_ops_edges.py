@@ -100,3 +100,23 @@ def test_windows_and_prefixes_beyond_32_bits(river, monkeypatch):
 
 class Stream:
     cuda_stream = None
+
+
+def test_sizes_beyond_32_bits_are_refused(river, monkeypatch):
+    """A size is never taken for its low 32 bits (2^32 + 2 rows for two)."""
+    n = 2**32 + 2
+
+    def refused(call, *args, **kw):
+        with pytest.raises(river.RiverError) as e:
+            call(*args, **kw)
+        assert e.value.status == river.RL_ERR_UNSUPPORTED, e.value
+    for shape in ((n, 1), (1, n)):  # (meta tensors: sizes without memory)
+        refused(river.token_logprobs, torch.empty(shape, dtype=torch.bfloat16, device="meta"))
+    q, k = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16), torch.zeros((1, 2, 8, 64), dtype=torch.bfloat16)
+    for bad in (k[:, :, :1].expand(1, 2, n, 64), k[:, :1].expand(1, n, 8, 64)):
+        refused(river._attn_desc, "x", q, bad, bad, q, None)
+    river._attn_desc("x", q, k, k, q, None)
+    # behind the check of devices, which these host tensors pass by
+    monkeypatch.setattr(river, "_operands", lambda name, tensors: 0)
+    refused(river.shared_prefix_attention, q[0], k[0, :, :1].expand(2, n, 64), k[0, :, :1].expand(2, n, 64), k, k,
+            torch.ones(1, dtype=torch.int32))

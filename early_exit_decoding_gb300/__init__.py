@@ -784,6 +784,8 @@ def _attn_desc(name, q, k, v, out, scale):
     if scale is not None and not scale > 0.0:
         _refuse(f"{name}: scale must be above 0")
     d = rl_attn_desc(kc, qc, B, T, Hq, Hkv, hd, S, 0.0 if scale is None else scale)
+    if scale is not None and d.scale == 0.0:  # (which would stand for the default)
+        _refuse(f"{name}: scale {scale} is 0 in fp32")
     _strides(d.q_stride, q)
     _strides(d.out_stride, out)
     _strides(d.k_stride, k)

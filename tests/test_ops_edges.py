@@ -120,3 +120,13 @@ def test_sizes_beyond_32_bits_are_refused(river, monkeypatch):
     monkeypatch.setattr(river, "_operands", lambda name, tensors: 0)
     refused(river.shared_prefix_attention, q[0], k[0, :, :1].expand(2, n, 64), k[0, :, :1].expand(2, n, 64), k, k,
             torch.ones(1, dtype=torch.int32))
+
+
+def test_a_scale_that_rounds_to_zero_is_not_the_default(river):
+    q, k = torch.zeros((1, 1, 4, 64), dtype=torch.bfloat16), torch.zeros((1, 2, 8, 64), dtype=torch.bfloat16)
+    for scale in (1e-50, 2.0**-150, 0.0, -1.0, float("nan")):
+        with pytest.raises(river.RiverError) as e:
+            river._attn_desc("x", q, k, k, q, scale)
+        assert e.value.status == river.RL_ERR_INVALID_ARG
+    assert river._attn_desc("x", q, k, k, q, None).scale == 0.0  # (0 asks for the default)
+    assert river._attn_desc("x", q, k, k, q, 2.0**-149).scale == 2.0**-149

@@ -565,23 +565,31 @@ class KVCache:
         rl_sync(self.model.handle, self.handle, stream)
 
 
-def _outputs(model, B, out):
-    import torch
+def _new(shape, dtype, device, stream):
+    """A tensor taken on the stream that writes it (None: the current one):
+    memory of another stream may still be in use there."""
+    torch = _torch()
+    if not isinstance(stream, torch.cuda.Stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _outputs(model, B, out, stream):
+    torch = _torch()
     S = model.shape
-    if out is None:
-        out = {}
-    o = dict(out)
-    o.setdefault("logits", torch.empty((B, S.vocab), dtype=torch.float32, device="cuda"))
-    o.setdefault("next_token", torch.empty((B,), dtype=torch.int32, device="cuda"))
-    o.setdefault("exit_layer", torch.empty((1,), dtype=torch.int32, device="cuda"))
-    o.setdefault("min_cos", torch.empty((S.n_layers,), dtype=torch.float32, device="cuda"))
+    o = dict(out) if out else {}
+    for key, shape, dtype in (("logits", (B, S.vocab), torch.float32), ("next_token", (B,), torch.int32),
+                              ("exit_layer", (1,), torch.int32), ("min_cos", (S.n_layers,), torch.float32)):
+        if key not in o:
+            o[key] = _new(shape, dtype, "cuda", stream)
     return o
 
 
 def prefill(model: Model, kv: KVCache, tokens, policy: Policy, out=None, stream=None):
     """tokens: CUDA int32 [B][T].  Returns a dict of output tensors."""
     B, T = tokens.shape
-    o = _outputs(model, B, out)
+    o = _outputs(model, B, out, stream)
     rl_prefill(model.handle, kv.handle, tokens, B, T, policy.c(), o["logits"], o["next_token"],
                o["exit_layer"], o["min_cos"], stream)
     return o
@@ -592,13 +600,14 @@ def prefill_score(model: Model, kv: KVCache, tokens, policy: Policy, top_k=0, ou
     the tokens before it, 0 for the first), ``entropy [B][T]`` and, for
     ``top_k`` > 0, ``top_ids`` and ``top_logprobs`` [B][T][top_k] of every
     position.  See rl_prefill_score."""
-    import torch
+    torch = _torch()
     B, T = tokens.shape
-    o = _outputs(model, B, out)
+    o = _outputs(model, B, out, stream)
     f32 = torch.float32
     for n, shape, dt in (("logprob", (B, T), f32), ("entropy", (B, T), f32)) + (
             (("top_ids", (B, T, top_k), torch.int32), ("top_logprobs", (B, T, top_k), f32)) if top_k > 0 else ()):
-        o.setdefault(n, torch.empty(shape, dtype=dt, device="cuda"))
+        if n not in o:
+            o[n] = _new(shape, dt, "cuda", stream)
     rl_prefill_score(model.handle, kv.handle, tokens, B, T, policy.c(), o["logits"], o["next_token"],
                      o["exit_layer"], o["min_cos"], o["logprob"], o["entropy"], top_k, o.get("top_ids"),
                      o.get("top_logprobs"), stream)
@@ -608,7 +617,7 @@ def prefill_score(model: Model, kv: KVCache, tokens, policy: Policy, top_k=0, ou
 def decode_step(model: Model, kv: KVCache, tokens, policy: Policy, out=None, stream=None):
     """tokens: CUDA int32 [B].  Returns a dict of output tensors."""
     B = tokens.shape[0]
-    o = _outputs(model, B, out)
+    o = _outputs(model, B, out, stream)
     rl_decode_step(model.handle, kv.handle, tokens, B, policy.c(), o["logits"], o["next_token"],
                    o["exit_layer"], o["min_cos"], stream)
     return o
@@ -663,13 +672,7 @@ def _buffer(o, key, shape, like, dtype, stream, name):
     (taken on the stream that writes it)."""
     t = o.get(key)
     if t is None:
-        torch = _torch()
-        if stream is None:
-            t = torch.empty(shape, dtype=dtype, device=like.device)
-        else:
-            with torch.cuda.stream(stream):
-                t = torch.empty(shape, dtype=dtype, device=like.device)
-        o[key] = t
+        t = o[key] = _new(shape, dtype, like.device, stream)
     elif t.shape != shape or t.dtype != dtype or t.get_device() != like.get_device() or \
             (key != "out" and not t.is_contiguous()):
         _refuse(f"{name}: out[{key!r}] must be {dtype} {tuple(shape)} on {like.device}"

@@ -176,3 +176,30 @@ def test_windows_beyond_32_bits(river):
         with pytest.raises(river.RiverError) as e:
             river.window_attention(q, k, k, n, window, sinks)
         assert e.value.status == river.RL_ERR_INVALID_ARG
+
+
+def test_outputs_are_taken_on_the_stream_that_writes_them(river, stream, tiny):
+    """Memory that was freed under work still queued on the current stream is
+    not written by another one."""
+    B, T, V, L = 3, 6, TINY.vocab, TINY.n_layers
+    pol = river.Policy.forced(torch.tensor([L], dtype=torch.int32, device="cuda"))
+    toks = torch.from_numpy(synth.gen_tokens(V, (B, T), seed=2)).cuda()
+    tok = torch.from_numpy(synth.gen_tokens(V, (B,), seed=3)).cuda()
+    kv = tiny.kv_cache_alloc(B, 32)
+    rows = torch.randn((B, V), device="cuda")
+    torch.cuda.synchronize()
+    calls = [lambda: river.prefill(tiny, kv, toks, pol, stream=stream),
+             lambda: river.decode_step(tiny, kv, tok, pol, stream=stream),
+             lambda: river.prefill_score(tiny, kv, toks, pol, top_k=3, stream=stream),
+             lambda: river.token_logprobs(rows, tok, top_k=3, stream=stream)]
+    want = [{n: t.clone() for n, t in call().items() if stream.synchronize() is None} for call in calls]
+    torch.cuda.synchronize()
+    sizes = {tuple(t.shape): t.dtype for w in want for t in w.values()}
+    torch.cuda._sleep(1_000_000_000)  # the current stream stays behind; what it frees is written late
+    late = [torch.empty(s, dtype=d, device="cuda").fill_(77) for s, d in sizes.items() for _ in range(4)]
+    del late
+    got = [call() for call in calls]
+    torch.cuda.synchronize()
+    for w, g in zip(want, got):
+        for n in w:
+            assert torch.equal(w[n], g[n]), n

@@ -599,15 +599,23 @@ def prefill_score(model: Model, kv: KVCache, tokens, policy: Policy, top_k=0, ou
     """prefill that also scores the prompt: ``logprob [B][T]`` (of token t after
     the tokens before it, 0 for the first), ``entropy [B][T]`` and, for
     ``top_k`` > 0, ``top_ids`` and ``top_logprobs`` [B][T][top_k] of every
-    position.  See rl_prefill_score."""
+    position.  ``tokens``: CUDA int32 [B][T], contiguous; buffers present in
+    ``out`` are used.  See rl_prefill_score."""
     torch = _torch()
+    name = "prefill_score"
+    if tokens.dim() != 2:
+        _refuse(f"{name}: tokens must be [B][T]")
     B, T = tokens.shape
-    o = _outputs(model, B, out, stream)
-    f32 = torch.float32
-    for n, shape, dt in (("logprob", (B, T), f32), ("entropy", (B, T), f32)) + (
-            (("top_ids", (B, T, top_k), torch.int32), ("top_logprobs", (B, T, top_k), f32)) if top_k > 0 else ()):
-        if n not in o:
-            o[n] = _new(shape, dt, "cuda", stream)
+    _int32(name, "tokens", tokens, (B, T))
+    _operands(name, (tokens,))
+    S, f32, i32 = model.shape, torch.float32, torch.int32
+    if not 0 <= top_k <= min(32, S.vocab):
+        _refuse(f"{name}: top_k {top_k} outside [0, {min(32, S.vocab)}]")
+    o = dict(out) if out else {}
+    for n, shape, dt in (("logits", (B, S.vocab), f32), ("next_token", (B,), i32), ("exit_layer", (1,), i32),
+                         ("min_cos", (S.n_layers,), f32), ("logprob", (B, T), f32), ("entropy", (B, T), f32)) + (
+            (("top_ids", (B, T, top_k), i32), ("top_logprobs", (B, T, top_k), f32)) if top_k else ()):
+        _buffer(o, n, shape, tokens, dt, stream, name)
     rl_prefill_score(model.handle, kv.handle, tokens, B, T, policy.c(), o["logits"], o["next_token"],
                      o["exit_layer"], o["min_cos"], o["logprob"], o["entropy"], top_k, o.get("top_ids"),
                      o.get("top_logprobs"), stream)

@@ -203,3 +203,26 @@ def test_outputs_are_taken_on_the_stream_that_writes_them(river, stream, tiny):
     for w, g in zip(want, got):
         for n in w:
             assert torch.equal(w[n], g[n]), n
+
+
+def test_prefill_score_refuses_buffers_that_do_not_fit(river, stream, tiny):
+    """A buffer of another shape, type or place is refused, not written past its end."""
+    B, T, k = 2, 6, 3
+    kv = tiny.kv_cache_alloc(B, 16)
+    pol = river.Policy.forced(torch.tensor([TINY.n_layers], dtype=torch.int32, device="cuda"))
+    toks = torch.from_numpy(synth.gen_tokens(TINY.vocab, (B, T), seed=2)).cuda()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        good = river.prefill_score(tiny, kv, toks, pol, top_k=k, stream=stream)
+        again = river.prefill_score(tiny, kv, toks, pol, top_k=k, out=good, stream=stream)
+        kv.sync(stream)
+    for n, t in good.items():
+        assert again[n] is t
+        wrong = [t[:1] if t.shape[0] > 1 else t[:0], t.cpu(), t.to(torch.float16), torch.stack([t, t], -1)[..., 0]]
+        for bad in (x for i, x in enumerate(wrong) if i < 3 or not x.is_contiguous()):
+            with pytest.raises(river.RiverError) as e:
+                river.prefill_score(tiny, kv, toks, pol, top_k=k, out={n: bad}, stream=stream)
+            assert e.value.status == river.RL_ERR_INVALID_ARG, n
+    with pytest.raises(river.RiverError) as e:
+        river.prefill_score(tiny, kv, toks, pol, top_k=k + 1, out=good, stream=stream)
+    assert e.value.status == river.RL_ERR_INVALID_ARG

@@ -130,3 +130,12 @@ def test_a_scale_that_rounds_to_zero_is_not_the_default(river):
         assert e.value.status == river.RL_ERR_INVALID_ARG
     assert river._attn_desc("x", q, k, k, q, None).scale == 0.0  # (0 asks for the default)
     assert river._attn_desc("x", q, k, k, q, 2.0**-149).scale == 2.0**-149
+
+
+def test_prefill_score_refuses_tokens_it_cannot_read(river):
+    """Before the library sees an address (no model is needed for that)."""
+    t = torch.zeros((2, 6), dtype=torch.int32)
+    for bad in (t[0], t.long(), t.t(), t[:, ::2], t):  # (the last: host memory)
+        with pytest.raises(river.RiverError) as e:
+            river.prefill_score(None, None, bad, None)
+        assert e.value.status == river.RL_ERR_INVALID_ARG

@@ -685,6 +685,8 @@ def _buffer(o, key, shape, like, dtype, stream, name):
             (key != "out" and not t.is_contiguous()):
         _refuse(f"{name}: out[{key!r}] must be {dtype} {tuple(shape)} on {like.device}"
                 + ("" if key == "out" else ", contiguous"))
+    elif t.requires_grad and _torch().is_grad_enabled():
+        _refuse(f"{name}: out[{key!r}] requires a gradient; the operator has no backward pass", RL_ERR_UNSUPPORTED)
     return t
 
 

@@ -226,3 +226,19 @@ def test_prefill_score_refuses_buffers_that_do_not_fit(river, stream, tiny):
     with pytest.raises(river.RiverError) as e:
         river.prefill_score(tiny, kv, toks, pol, top_k=k + 1, out=good, stream=stream)
     assert e.value.status == river.RL_ERR_INVALID_ARG
+
+
+def test_out_buffers_with_a_gradient_are_refused(river):
+    """A buffer that requires one would be written behind autograd's back."""
+    q, k = rnd(1, 1, 4, 64, seed=1), rnd(1, 2, 40, 64, seed=2)
+    n = torch.full((1,), 40, dtype=torch.int32, device="cuda")
+    x, pre = torch.randn((1, 9), device="cuda"), k[0]
+    for call in (lambda **kw: river.token_logprobs(x, **kw), lambda **kw: river.window_attention(q, k, k, n, 4, **kw),
+                 lambda **kw: river.shared_prefix_attention(q[0], pre, pre, k, k, n, **kw)):
+        for key, t in call().items():
+            bad = t.clone().requires_grad_()
+            with pytest.raises(river.RiverError) as e:
+                call(out={key: bad})
+            assert e.value.status == river.RL_ERR_UNSUPPORTED
+            with torch.no_grad():
+                assert call(out={key: bad})[key] is bad

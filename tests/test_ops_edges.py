@@ -139,3 +139,12 @@ def test_prefill_score_refuses_tokens_it_cannot_read(river):
         with pytest.raises(river.RiverError) as e:
             river.prefill_score(None, None, bad, None)
         assert e.value.status == river.RL_ERR_INVALID_ARG
+
+
+def test_a_buffer_that_requires_a_gradient_is_refused(river):
+    t = torch.zeros(3).requires_grad_()
+    with pytest.raises(river.RiverError) as e:
+        river._buffer({"lse": t}, "lse", (3,), t, torch.float32, None, "x")
+    assert e.value.status == river.RL_ERR_UNSUPPORTED
+    with torch.no_grad():
+        assert river._buffer({"lse": t}, "lse", (3,), t, torch.float32, None, "x") is t

@@ -20,7 +20,7 @@
 // HBM bounds it: 16 keys bring 64 HD bytes and cost HD / 4 MMAs.  64 sequences,
 // window 4096, head_dim 128, 8 KV heads: 127 us, 6.4 TB/s, 0.94 of a measured
 // copy.  A few sequences are bound by a launch's and a cluster's latency (one
-// of 1,024 keys: 6.5 us for 2 MB).
+// of 1,024 keys: 6.7 us for 2 MB).
 #include <mutex>
 
 #include "attn_ops.cuh"

@@ -20,7 +20,7 @@
 // = 3 x 168; with 168 they spilled, and a tile pair took 5900 clocks, not 3300).
 //
 // What bounds it (8192 queries, window 2048, 32 heads, 8 KV heads, head_dim
-// 128: 236 us, 0.55 of the measured bf16 rate; tensor pipe 45 % busy while a
+// 128: 230 us, 0.56 of the measured bf16 rate; tensor pipe 45 % busy while a
 // CTA runs): a row tile's chain.  Softmax 1600 clocks (maxima 470, the vote on
 // rescaling 200, exponentials 820 of which the ex2 unit takes 512; a tile that
 // a mask cuts 700 more), then the 16 products of its values and next scores
@@ -28,8 +28,8 @@
 // two hand-offs; the two tiles of a CTA interleave to 3500 clocks a pair of
 // tiles, in which the tensor cores could do 54 products and do 32.  The rest
 // is CTAs' starts (4800 clocks to the first scores, half of it the copies' way,
-// before Q came from L2) and ends (5000, and 1500 until the next one runs) of
-// 75000.  At head_dim 64 a product still takes 63 clocks (N = 64), so the rate
+// before Q came from L2) and ends (5800 from the last weights on, and 1500 until
+// the next one runs) of 75000.  At head_dim 64 a product still takes 63 clocks (N = 64), so the rate
 // is half: 5 ragged prompts, window 500: 38 us.
 // The running maximum follows lazily: O and the sum are rescaled only when a
 // row's maximum grew by more than 2^8 since the last time (weights then stay
@@ -846,16 +846,24 @@ cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
 // measured): a CTA's start and end, its tiles of 128 keys (two row tiles, or
 // one), and the workspace traffic of a part.  152 SMs are planned for, so that
 // the workspace's size does not depend on the device.
-// CTAs of the prefix's products when the own keys' run beside them (two thirds
-// of the SMs: 256 sequences behind 32768 tokens, 32 heads, 8 KV heads, head_dim
+// CTAs of the prefix's products, at most, when the own keys' run beside them
+// (256 sequences behind 32768 tokens, 32 heads, 8 KV heads, head_dim
 // 128, own keys up to 2000: 64 CTAs 249 us, 96 221, 128 255, 152 254; one after
-// the other, on all SMs, 274).
+// the other, on all SMs, 274).  Each (row tile, KV head) gets the whole number of
+// parts below that, so the CTAs there are vary: at these heads 96 for 80 to 256
+// sequences, 80 for 320, 64 for 512, 128 for 1024 (one part each).
 constexpr int kApartCtas = 100;
 // More own-key CTAs than four an SM, of which three run at once (8 KV heads, head_dim 128, joined apart
 // against in place: 32 sequences behind 8192, up to 1024 of their own, 33.1 us
 // against 30.1, 64 45.4 against 46.3, 128 65.2 against 70.2; behind 1024, up to
 // 256, 14.5 against 12.2, 20.2 against 21.0, 29.0 against 29.6; called one by one
-// the third launch costs 2 us more).
+// the third launch costs 2 us more).  It knows neither the prefix's length nor
+// the capacity.  With a long prefix and few own keys in place is faster, the
+// more the fewer CTAs the constant above leaves (behind 32768, up to 16 of their
+// own, apart against in place: 80 sequences 88 us against 70, 128 88 against 78,
+// 256 165 against 151, 512 463 against 290; up to 2000: 98 against 105, 127
+// against 151, 226 against 278, 473 against 520; behind 8192, up to 512: 36
+// against 39, 50 against 54, 83 against 90, 139 against 161).
 bool prefix_apart(int B, int rep, int Hkv) { return (long long)B * Hkv * ((rep + 15) / 16) > 4 * 152; }
 
 int prefix_split(int B, int rep, int Hkv, int P) {

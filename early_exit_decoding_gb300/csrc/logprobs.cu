@@ -25,7 +25,9 @@
 // 6.95 TB/s, 1.02 of a measured copy); at few rows the chain of a launch, the
 // copies' first arrival and the joins of warps and CTAs (one row 7.6 us, of
 // 0.5 MB), with top k above all the candidates' selection (64 rows: 10.1 us
-// without, 19.7 with 20 alternatives).
+// without, 19.7 with 20 alternatives).  16-bit rows bring twice the logits a
+// byte and every logit is unpacked, so instructions bind them before HBM (777
+// odd rows of 50,257 bf16 logits: 33 us, 17 of them issue slots, 2.4 TB/s).
 //
 // A few rows are split over a thread-block cluster each (up to 16 CTAs); its
 // CTAs exchange sums and candidates through distributed shared memory, so

@@ -245,18 +245,27 @@ RL_API rl_status rl_kv_set_trace(rl_kv* kv, float* d_hidden);
  * window 0 (the default) switches it off.  While no position is past the window
  * every path runs as without it; from then on decode steps run RL_PATH_GENERIC
  * with the attention of rl_window_attention (a forced other path makes
- * rl_decode_step return RL_ERR_UNSUPPORTED).  Not on the pages: long
- * generations at a bounded cost of attention.  RL_ERR_STATE while a prefix is
- * shared; RL_ERR_INVALID_ARG for a negative value. */
+ * rl_decode_step return RL_ERR_UNSUPPORTED).  Small batches give up
+ * RL_PATH_STEP for that, so a window makes their steps cheaper only from long
+ * contexts on (window 1000, 1B shape on a GB300: one sequence past some 9,000
+ * positions, four past 3,500; 32 from the window on).  Past the window queries
+ * and attention weights are rounded to bf16 once, where the attention of the
+ * other paths keeps both in two parts.  Not on the pages: long generations at
+ * a bounded cost of attention.  RL_ERR_STATE while a prefix is shared;
+ * RL_ERR_INVALID_ARG for a negative value. */
 RL_API rl_status rl_kv_set_window(rl_kv* kv, int32_t window, int32_t sinks);
 
 /* One prompt, many continuations: the first n positions of sequence 0 (n at
  * most the cache's position) become the first n positions of every sequence.
- * Later decode steps of any batch up to max_batch read them from sequence 0's
- * slots, once for the whole batch, and each sequence's own slots from n on
- * (rl_shared_prefix_attention, on RL_PATH_GENERIC); each sequence writes its
- * own slots, so a prompt prefilled once with B = 1 serves them all.  n 0
- * switches it off, and so does the next rl_prefill.  Takes device memory for a
+ * Later decode steps of any batch that rl_decode_step takes read them from
+ * sequence 0's slots, once for the whole batch, and each sequence's own slots
+ * from n on (rl_shared_prefix_attention, on RL_PATH_GENERIC, with
+ * rl_kv_set_window's roundings; cheaper than copies of the prompt from some
+ * 3,000 positions on for four sequences, from 1,000 for 32); each sequence
+ * writes its own slots, so a prompt prefilled once with B = 1 serves them all.
+ * n 0 switches it off, and so does the next rl_prefill; the sequences behind
+ * the first then have what their own slots hold, which a shared prompt never
+ * filled (the same for positions that a smaller n leaves out).  Takes device memory for a
  * workspace the first time (and for a prefix that needs more), enqueues
  * nothing; make the call outside stream captures.
  * RL_ERR_STATE while a window is set; RL_ERR_INVALID_ARG for n outside [0, position];
@@ -410,7 +419,7 @@ RL_API rl_status rl_debug_fail_allocations(int64_t after);
 RL_API rl_status rl_debug_limit_waits(int64_t polls);
 
 /* Number of kernels one decode step launches for batch B (for launch
- * accounting); 0 on bad arguments. */
+ * accounting; without a window or a shared prefix); 0 on bad arguments. */
 RL_API int32_t rl_decode_kernel_count(const rl_model* m, int32_t B);
 
 /* rl_lm_head_static: final RMSNorm + LM head + greedy argmax of B residual

@@ -12,6 +12,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libriver.so")
@@ -33,6 +34,7 @@ EXPORTS = (
     "rl_kv_set_wait_limit", "rl_debug_fail_allocations", "rl_debug_limit_waits", "rl_model_offload_backbone",
     "rl_model_memory", "rl_token_logprobs", "rl_window_attention", "rl_shared_prefix_workspace",
     "rl_shared_prefix_attention", "rl_kv_set_window", "rl_kv_share_prefix", "rl_prefill_score",
+    "rl_packed_attention", "rl_kv4_append", "rl_kv4_read", "rl_kv4_attention", "rl_sample",
 )
 RL_DT_F32, RL_DT_BF16, RL_DT_F16 = range(3)
 RL_PATH_AUTO, RL_PATH_STEP, RL_PATH_FUSED, RL_PATH_GENERIC = range(4)
@@ -66,6 +68,25 @@ class rl_attn_desc(ctypes.Structure):
         "kv_dtype", "q_dtype", "batch", "q_len", "n_q_heads", "n_kv_heads", "head_dim",
         "kv_capacity")] + [("scale", ctypes.c_float)] + [(n, ctypes.c_int64 * 3) for n in (
             "q_stride", "out_stride", "k_stride", "v_stride")]
+
+
+class rl_packed_desc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "dtype", "batch", "rows", "max_rows", "n_q_heads", "n_kv_heads", "head_dim")] + [
+        ("scale", ctypes.c_float)] + [(n, ctypes.c_int64 * 2) for n in (
+            "q_stride", "k_stride", "v_stride", "out_stride")]
+
+
+class rl_kv4(ctypes.Structure):
+    _fields_ = [("n_pages", ctypes.c_int32), ("page", ctypes.c_int32)] + [(n, ctypes.c_void_p) for n in (
+        "k_codes", "k_scale", "v_codes", "v_scale")] + [
+        ("code_stride", ctypes.c_int64 * 2), ("scale_stride", ctypes.c_int64 * 2), ("d_table", ctypes.c_void_p),
+        ("table_stride", ctypes.c_int64), ("table_width", ctypes.c_int32)]
+
+
+class rl_sampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_float), ("top_k", ctypes.c_int32), ("top_p", ctypes.c_float), ("min_p", ctypes.c_float)] + [
+        (n, ctypes.c_void_p) for n in ("d_temperature", "d_top_k", "d_top_p", "d_min_p")]
 
 
 class RiverError(RuntimeError):
@@ -125,6 +146,11 @@ def _load():
         "rl_shared_prefix_attention": (I, [ctypes.POINTER(rl_attn_desc), P, P, P, I,
                                            ctypes.POINTER(ctypes.c_int64), P, P, P, P, P, P,
                                            ctypes.c_uint64, P, P]),
+        "rl_packed_attention": (I, [ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, P, P]),
+        "rl_kv4_append": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, I, P, P, P]),
+        "rl_kv4_read": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P]),
+        "rl_kv4_attention": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, P]),
+        "rl_sample": (I, [P, I, I, I, ctypes.c_int64, P, ctypes.POINTER(rl_sampling), P, P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -387,6 +413,31 @@ def rl_shared_prefix_attention(desc, d_q, d_k_prefix, d_v_prefix, prefix_len, pr
                                            _ptr(d_v_prefix), prefix_len, st, _ptr(d_k), _ptr(d_v),
                                            _ptr(d_kv_len), _ptr(d_out), _ptr(d_lse), _ptr(d_ws), ws_bytes,
                                            _ptr(d_err), _stream(stream)))
+
+
+def rl_packed_attention(desc, d_q, d_k, d_v, d_start, d_out, d_lse, d_err=None, stream=None):
+    _check(_lib.rl_packed_attention(ctypes.byref(desc), _ptr(d_q), _ptr(d_k), _ptr(d_v), _ptr(d_start), _ptr(d_out),
+                                    _ptr(d_lse), _ptr(d_err), _stream(stream)))
+
+
+def rl_kv4_append(cache, desc, d_start, d_kv_len, d_q, d_k, d_v, d_rope, rope_len, d_out, d_err=None, stream=None):
+    _check(_lib.rl_kv4_append(ctypes.byref(cache), ctypes.byref(desc), _ptr(d_start), _ptr(d_kv_len), _ptr(d_q), _ptr(d_k),
+                              _ptr(d_v), _ptr(d_rope), _int32_of(rope_len), _ptr(d_out), _ptr(d_err), _stream(stream)))
+
+
+def rl_kv4_read(cache, desc, d_start, d_kv_len, d_k, d_v, d_err=None, stream=None):
+    _check(_lib.rl_kv4_read(ctypes.byref(cache), ctypes.byref(desc), _ptr(d_start), _ptr(d_kv_len), _ptr(d_k), _ptr(d_v),
+                            _ptr(d_err), _stream(stream)))
+
+
+def rl_kv4_attention(cache, desc, d_start, d_kv_len, d_q, d_out, d_lse, d_err=None, stream=None):
+    _check(_lib.rl_kv4_attention(ctypes.byref(cache), ctypes.byref(desc), _ptr(d_start), _ptr(d_kv_len), _ptr(d_q),
+                                 _ptr(d_out), _ptr(d_lse), _ptr(d_err), _stream(stream)))
+
+
+def rl_sample(d_logits, dtype, rows, vocab, row_stride, d_u, settings, d_token, d_logprob, d_err=None, stream=None):
+    _check(_lib.rl_sample(_ptr(d_logits), dtype, rows, vocab, row_stride, _ptr(d_u), ctypes.byref(settings), _ptr(d_token),
+                          _ptr(d_logprob), _ptr(d_err), _stream(stream)))
 
 
 # --------------------------------------------------------------- conveniences
@@ -879,6 +930,275 @@ def shared_prefix_attention(q, k_prefix, v_prefix, k, v, kv_len, scale=None, out
     return o
 
 
+class KV4Cache(NamedTuple):
+    """A paged cache held in 4 bits: ``k_codes``, ``v_codes`` uint8
+    [pages][Hkv][page][hd / 2], ``k_scale``, ``v_scale`` bf16 or fp16
+    [pages][Hkv][page][2] (step, minimum); views of a larger pool may have any
+    page stride.  The kv4 functions also take such four tensors in a plain
+    tuple.  See rl_kv4."""
+    k_codes: Any
+    k_scale: Any
+    v_codes: Any
+    v_scale: Any
+
+    @staticmethod
+    def alloc(n_pages, n_kv_heads, head_dim, page=64, dtype=None, device="cuda"):
+        """A cache of zeros (dtype None: bf16)."""
+        torch = _torch()
+        codes, scale = (n_pages, n_kv_heads, page, head_dim // 2), (n_pages, n_kv_heads, page, 2)
+        return KV4Cache(*(torch.zeros(s, dtype=t, device=device) for _ in "kv"
+                          for s, t in ((codes, torch.uint8), (scale, dtype or torch.bfloat16))))
+
+
+def rope_table(n, head_dim, theta, device="cuda"):
+    """(cos, sin) of positions 0 .. n - 1 for kv4_append: fp32 [n][head_dim / 2][2],
+    frequencies theta^(-2 i / head_dim) and angles in 64 bits."""
+    torch = _torch()
+    f = float(theta) ** (-2.0 * torch.arange(head_dim // 2, dtype=torch.float64, device=device) / head_dim)
+    a = torch.arange(n, dtype=torch.float64, device=device)[:, None] * f
+    return torch.stack([a.cos(), a.sin()], dim=-1).float()
+
+
+def _packed_desc(name, dtype, heads, batch, rows, max_rows, scale, **tensors):
+    """rl_packed_desc of packed tensors [rows][heads][hd] by their names (q, k, v, out; None: absent)."""
+    d = rl_packed_desc()
+    n_q, n_kv, hd = heads
+    code = _dtype_code(dtype)
+    if code is None:
+        _refuse(f"{name}: bf16 or fp16 operands are needed (found {dtype})")
+    if max(batch, rows, n_q, n_kv, hd) > _INT32_MAX:
+        _refuse(f"{name}: sizes must be below 2^31", RL_ERR_UNSUPPORTED)
+    if scale is not None and not scale > 0.0:
+        _refuse(f"{name}: scale must be above 0")
+    d.dtype, d.batch, d.rows, d.max_rows, d.n_q_heads, d.n_kv_heads, d.head_dim = code, batch, rows, _int32_of(max_rows), n_q, n_kv, hd
+    d.scale = 0.0 if scale is None else scale
+    if scale is not None and d.scale == 0.0:  # (which would stand for the default)
+        _refuse(f"{name}: scale {scale} is 0 in fp32")
+    for key, t in tensors.items():
+        if t is None:
+            continue
+        want = (rows, n_q if key in ("q", "out") else n_kv, hd)
+        if t.shape != want or t.dtype != dtype or t.stride(2) != 1:
+            _refuse(f"{name}: {key} must be {dtype} {want} with a contiguous last axis (found {t.dtype} {tuple(t.shape)})")
+        s = getattr(d, key + "_stride")
+        s[0] = t.stride(0) if rows > 1 else 0
+        s[1] = t.stride(1) if want[1] > 1 else 0
+    return d
+
+
+def _kv4_desc(name, cache, table, dtype):
+    """(rl_kv4 without its addresses, KV heads, head_dim) of a cache and a page table."""
+    kc, km, vc, vm = cache
+    torch = _torch()
+    if kc.dim() != 4 or kc.dtype != torch.uint8 or kc.shape != vc.shape or vc.dtype != torch.uint8 or kc.numel() == 0 or \
+            km.shape != (*kc.shape[:3], 2) or vm.shape != km.shape or km.dtype != vm.dtype or (dtype is not None and km.dtype != dtype):
+        _refuse(f"{name}: the cache must be uint8 [pages][Hkv][page][hd / 2] codes and {dtype or 'bf16 or fp16'} [pages][Hkv][page][2] scales, k's and v's alike")
+    n, heads, page, half = kc.shape
+    for t, w in ((kc, half), (vc, half), (km, 2), (vm, 2)):
+        if t.stride()[2:] != (w, 1) or (heads > 1 and t.stride(1) != page * w):
+            _refuse(f"{name}: the cache's pages must be contiguous")
+    if table.dim() != 2 or table.dtype != torch.int32 or table.numel() == 0 or (table.shape[1] > 1 and table.stride(1) != 1):
+        _refuse(f"{name}: table must be int32 [B][pages] with contiguous rows")
+    if max(n, heads, page, *table.shape) > _INT32_MAX:
+        _refuse(f"{name}: sizes must be below 2^31", RL_ERR_UNSUPPORTED)
+    c = rl_kv4(n, page)
+    c.code_stride[:] = [t.stride(0) if n > 1 else 0 for t in (kc, vc)]
+    c.scale_stride[:] = [t.stride(0) if n > 1 else 0 for t in (km, vm)]
+    c.table_stride, c.table_width = table.stride(0) if table.shape[0] > 1 else table.shape[1], table.shape[1]
+    return c, heads, 2 * half
+
+
+def _kv4_with(c, cache, table):
+    """A copy of the descriptor with this call's addresses."""
+    d = rl_kv4.from_buffer_copy(c)
+    d.k_codes, d.k_scale, d.v_codes, d.v_scale = (t.data_ptr() for t in cache)
+    d.d_table = table.data_ptr()
+    return d
+
+
+def _spans(name, start, kv_len, batch, rows, err):
+    if start is None:
+        if rows != batch:
+            _refuse(f"{name}: {rows} rows for {batch} sequences need start")
+    else:
+        _int32(name, "start", start, (batch + 1,))
+    if kv_len is not None:
+        _int32(name, "kv_len", kv_len, (batch,))
+    if err is not None:
+        _int32(name, "err", err, (1,))
+
+
+def packed_attention(q, k, v, start, max_rows=None, scale=None, out=None, err=None, stream=None):
+    """Causal attention of packed prompts: ``q [N][Hq][hd]``, ``k``, ``v``
+    [N][Hkv][hd] bf16 or fp16, sequence b the rows ``start[b]`` .. ``start[b + 1]``
+    (int32 [B + 1]).  ``max_rows``: no sequence has more (None: unknown; known,
+    it saves time).  Returns a dict: ``out`` (q's shape and type) and ``lse``
+    fp32 [N][Hq]; buffers present in ``out`` are used, their rows of no sequence
+    left as they were.  See rl_packed_attention."""
+    torch = _torch()
+    name = "packed_attention"
+    dev = _operands(name, (q, k, v, start, err))
+    if q.dim() != 3 or k.dim() != 3 or start.dim() != 1 or q.numel() == 0 or k.numel() == 0 or start.numel() < 2:
+        _refuse(f"{name}: q, k, v must be [N][heads][hd], not empty, start [B + 1]")
+    o = dict(out) if out else {}
+    res = _buffer(o, "out", q.shape, q, q.dtype, stream, name)
+    B, N = start.numel() - 1, q.shape[0]
+    d = _plan((name, B, max_rows), scale, (q, k, v, res) if out else (q, k, v), lambda: _packed_desc(
+        name, q.dtype, (q.shape[1], k.shape[1], q.shape[2]), B, N, max_rows or 0, scale, q=q, k=k, v=v, out=res))
+    lse = _buffer(o, "lse", (N, q.shape[1]), q, torch.float32, stream, name)
+    _spans(name, start, None, B, N, err)
+    _run(dev, stream, _lib.rl_packed_attention, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), start.data_ptr(), res.data_ptr(),
+         lse.data_ptr(), _addr(err))
+    return o
+
+
+def kv4_append(cache, table, kv_len, k, v, q=None, rope=None, start=None, out=None, err=None, stream=None):
+    """The sequences' new rows into a 4-bit cache, rotated on the way: ``k``,
+    ``v`` [N][Hkv][hd] of the scales' type, packed by ``start`` (int32 [B + 1];
+    None: one row each), the last of ``kv_len`` (int32 [B], the new ones
+    counted).  ``table``: int32 [B][pages]; ``rope``: rope_table's, for q and k
+    (None: no rotation).  Returns a dict, with ``q [N][Hq][hd]`` given ``q`` its
+    rotated rows; a buffer present in ``out`` is used (q itself may be).  See
+    rl_kv4_append."""
+    torch = _torch()
+    name = "kv4_append"
+    dev = _operands(name, (k, v, q, table, kv_len, rope, start, err, *cache))
+    if k.dim() != 3 or k.numel() == 0 or kv_len.dim() != 1 or kv_len.numel() == 0:
+        _refuse(f"{name}: k and v must be [N][Hkv][hd], not empty, kv_len [B]")
+    o = dict(out) if out else {}
+    B, N = kv_len.numel(), k.shape[0]
+    res = None
+    if q is not None:
+        if q.dim() != 3 or q.numel() == 0:
+            _refuse(f"{name}: q must be [N][Hq][hd], not empty")
+        res = o.get("q")
+        if res is None:
+            res = o["q"] = _new(q.shape, q.dtype, q.device, stream)
+        else:
+            _operands(name, (k, res))
+
+    def make():
+        c, heads, hd = _kv4_desc(name, cache, table, k.dtype)
+        d = _packed_desc(name, k.dtype, (q.shape[1] if q is not None else heads, heads, hd), B, N, 0, None, q=q, k=k, v=v, out=res)
+        return c, d
+
+    ts = (*cache, table, k, v) + (() if q is None else (q, res) if out else (q,))
+    c, d = _plan((name, B, q is None), None, ts, make)
+    if table.shape[0] != B:
+        _refuse(f"{name}: table must have a row for each of the {B} sequences")
+    _spans(name, start, kv_len, B, N, err)
+    n_rope = 0
+    if rope is not None:
+        if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[0] < 1 or rope.shape[1:] != (d.head_dim // 2, 2) or not rope.is_contiguous():
+            _refuse(f"{name}: rope must be contiguous fp32 [n][{d.head_dim // 2}][2]")
+        n_rope = min(rope.shape[0], _INT32_MAX)
+    _run(dev, stream, _lib.rl_kv4_append, _kv4_with(c, cache, table), d, _addr(start), kv_len.data_ptr(), _addr(q), k.data_ptr(),
+         v.data_ptr(), _addr(rope), n_rope, _addr(res), _addr(err))
+    return o
+
+
+def kv4_read(cache, table, kv_len, start=None, rows=None, out=None, err=None, stream=None):
+    """Rows of a 4-bit cache as values: of sequence b the last ``start[b + 1] -
+    start[b]`` of its ``kv_len[b]`` rows (``start`` None: the last one), packed;
+    ``rows``: how many there is room for (without ``start`` one a sequence).  Returns a
+    dict: ``k``, ``v`` [rows][Hkv][hd] of the scales' type; buffers present in
+    ``out`` are used, their rows of no sequence left as they were.  See rl_kv4_read."""
+    name = "kv4_read"
+    dev = _operands(name, (table, kv_len, start, err, *cache))
+    if kv_len.dim() != 1 or kv_len.numel() == 0:
+        _refuse(f"{name}: kv_len must be [B]")
+    B = kv_len.numel()
+    if rows is None and start is not None:
+        _refuse(f"{name}: start needs rows")
+    N = B if rows is None else int(rows)
+    if not 1 <= N <= _INT32_MAX:
+        _refuse(f"{name}: rows must be in [1, 2^31)")
+    c, heads, hd = _plan((name, None), None, (*cache, table), lambda: _kv4_desc(name, cache, table, None))
+    o = dict(out) if out else {}
+    for key in ("k", "v"):
+        if o.get(key) is None:
+            o[key] = _new((N, heads, hd), cache[1].dtype, table.device, stream)
+        else:
+            _operands(name, (table, o[key]))
+            if o[key].dim() != 3:
+                _refuse(f"{name}: out[{key!r}] must be [{N}][{heads}][{hd}]")
+    k, v = o["k"], o["v"]
+    d = _plan((name, B, N), None, (*cache[:2], k, v), lambda: _packed_desc(
+        name, cache[1].dtype, (heads, heads, hd), B, N, 0, None, k=k, v=v))
+    if table.shape[0] != B:
+        _refuse(f"{name}: table must have a row for each of the {B} sequences")
+    _spans(name, start, kv_len, B, N, err)
+    _run(dev, stream, _lib.rl_kv4_read, _kv4_with(c, cache, table), d, _addr(start), kv_len.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(err))
+    return o
+
+
+def kv4_attention(q, cache, table, kv_len, start=None, max_rows=None, scale=None, out=None, err=None, stream=None):
+    """Attention of single tokens and drafts over a 4-bit cache: ``q [N][Hq][hd]``
+    of the scales' type, packed by ``start`` (int32 [B + 1]; None: one row each),
+    the last rows of ``kv_len`` (int32 [B]).  ``max_rows``: no sequence has more
+    rows here (None: unknown; known, it saves time).  Returns a dict: ``out``
+    (q's shape and type) and ``lse`` fp32 [N][Hq]; buffers present in ``out``
+    are used, their rows of no sequence left as they were.  See rl_kv4_attention."""
+    torch = _torch()
+    name = "kv4_attention"
+    dev = _operands(name, (q, table, kv_len, start, err, *cache))
+    if q.dim() != 3 or q.numel() == 0 or kv_len.dim() != 1 or kv_len.numel() == 0:
+        _refuse(f"{name}: q must be [N][Hq][hd], not empty, kv_len [B]")
+    o = dict(out) if out else {}
+    res = _buffer(o, "out", q.shape, q, q.dtype, stream, name)
+    B, N = kv_len.numel(), q.shape[0]
+
+    def make():
+        c, heads, hd = _kv4_desc(name, cache, table, q.dtype)
+        return c, _packed_desc(name, q.dtype, (q.shape[1], heads, hd), B, N, max_rows or 0, scale, q=q, out=res)
+
+    c, d = _plan((name, B, max_rows), scale, (*cache, table, q, res) if out else (*cache, table, q), make)
+    lse = _buffer(o, "lse", (N, q.shape[1]), q, torch.float32, stream, name)
+    if table.shape[0] != B:
+        _refuse(f"{name}: table must have a row for each of the {B} sequences")
+    _spans(name, start, kv_len, B, N, err)
+    _run(dev, stream, _lib.rl_kv4_attention, _kv4_with(c, cache, table), d, _addr(start), kv_len.data_ptr(), q.data_ptr(),
+         res.data_ptr(), lse.data_ptr(), _addr(err))
+    return o
+
+
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, err=None, stream=None):
+    """Draws one token a row of ``logits [R][V]`` (as token_logprobs) with the
+    random numbers ``u`` (fp32 [R] in [0, 1)).  Each setting is a number or a
+    tensor [R] (fp32; top_k int32).  Returns a dict: ``token`` int32 [R] and
+    ``logprob`` fp32 [R], of the token among those kept; buffers present in
+    ``out`` are used.  See rl_sample."""
+    torch = _torch()
+    name = "sample"
+    dt = _dtype_code(logits.dtype)
+    if logits.dim() != 2 or dt is None or logits.numel() == 0 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        _refuse(f"{name}: logits must be fp32, bf16 or fp16 [R][V] with contiguous rows")
+    R, V = logits.shape
+    if R > _INT32_MAX or V > _INT32_MAX:
+        _refuse(f"{name}: rows and vocabulary must be below 2^31", RL_ERR_UNSUPPORTED)
+    s = rl_sampling()
+    given = []
+    for key, x in (("temperature", temperature), ("top_k", top_k), ("top_p", top_p), ("min_p", min_p)):
+        if isinstance(x, torch.Tensor):
+            if x.dtype != (torch.int32 if key == "top_k" else torch.float32) or x.shape != (R,) or not x.is_contiguous():
+                _refuse(f"{name}: {key} must be a number or contiguous {'int32' if key == 'top_k' else 'fp32'} ({R},)")
+            setattr(s, "d_" + key, x.data_ptr())
+            given.append(x)
+        else:
+            setattr(s, key, _int32_of(int(x)) if key == "top_k" else float(x))
+    dev = _operands(name, (logits, u, err, *given))
+    if u.dtype != torch.float32 or u.shape != (R,) or not u.is_contiguous():
+        _refuse(f"{name}: u must be contiguous fp32 ({R},)")
+    if err is not None:
+        _int32(name, "err", err, (1,))
+    o = dict(out) if out else {}
+    token = _buffer(o, "token", (R,), logits, torch.int32, stream, name)
+    lp = _buffer(o, "logprob", (R,), logits, torch.float32, stream, name)
+    _run(dev, stream, _lib.rl_sample, logits.data_ptr(), dt, R, V, logits.stride(0) if R > 1 else V, u.data_ptr(), s,
+         token.data_ptr(), lp.data_ptr(), _addr(err))
+    return o
+
+
 def quantize_exit_layers(model: Model, stream=None):
     model.quantize_exit_layers(stream)
 
@@ -889,4 +1209,5 @@ def kv_cache_alloc(model: Model, max_batch, max_seq):
 
 __all__ = [*EXPORTS, "Model", "KVCache", "Policy", "RiverError", "prefill", "decode_step",
            "quantize_exit_layers", "kv_cache_alloc", "prefill_score", "token_logprobs", "window_attention",
-           "shared_prefix_attention", "rl_attn_desc", "LIB_PATH"]
+           "shared_prefix_attention", "rl_attn_desc", "packed_attention", "kv4_append", "kv4_read", "kv4_attention",
+           "sample", "KV4Cache", "rope_table", "rl_packed_desc", "rl_kv4", "rl_sampling", "LIB_PATH"]

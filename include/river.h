@@ -559,6 +559,141 @@ RL_API rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const void* d
                                             void* d_out, float* d_lse, void* d_ws, uint64_t ws_bytes,
                                             int32_t* d_err, rl_stream_t stream);
 
+/* Rows of several sequences packed side by side: sequence b has the rows
+ * d_start[b] .. d_start[b + 1] - 1 of q, k, v and out (d_start [batch + 1] int32,
+ * device, not decreasing; NULL, where a call allows it: row b alone).  Strides
+ * are in elements; the innermost (head_dim) axis is contiguous.  Requirements:
+ * head_dim 64 or 128, n_q_heads a multiple of n_kv_heads, 16-byte starts,
+ * strides whole multiples of 16 bytes (RL_ERR_UNSUPPORTED otherwise); what is
+ * written has its rows and heads apart (RL_ERR_INVALID_ARG otherwise).  Rows in
+ * front of d_start[0] and from d_start[batch] on are left as they were.  An
+ * entry of d_start outside [0, rows], or below the one before, sets
+ * RL_DEVERR_CAPACITY and is moved there. */
+typedef struct {
+  int32_t dtype;       /* of q, k, v and out: RL_DT_BF16 or RL_DT_F16 */
+  int32_t batch, rows; /* sequences; rows laid out */
+  int32_t max_rows;    /* at most that many rows of a sequence count (0: rows) */
+  int32_t n_q_heads, n_kv_heads, head_dim;
+  float scale;         /* of q.k; 0 means 1 / sqrt(head_dim) */
+  int64_t q_stride[2]; /* row, head */
+  int64_t k_stride[2];
+  int64_t v_stride[2];
+  int64_t out_stride[2];
+} rl_packed_desc;
+
+/* rl_packed_attention: causal attention of whole prompts of different lengths,
+ * packed: row t of a sequence sees that sequence's rows 0 .. t.  out and lse
+ * ([rows][n_q_heads] fp32, may be NULL) as rl_window_attention, with its
+ * roundings; keys a row does not see have no part in its result, whatever they
+ * hold.  A sequence of more than max_rows rows sets RL_DEVERR_CAPACITY and has
+ * its first max_rows rows computed, the others are left as they were.  rows is
+ * at most 2^27, batch 2^20.  One launch, no workspace, results repeat bit for
+ * bit. */
+RL_API rl_status rl_packed_attention(const rl_packed_desc* p, const void* d_q, const void* d_k,
+                                     const void* d_v, const int32_t* d_start, void* d_out, float* d_lse,
+                                     int32_t* d_err, rl_stream_t stream);
+
+/* A paged key/value cache held in 4 bits.  A page holds `page` token rows of
+ * every KV head; a row's head_dim values are one group with a step s and a
+ * minimum m (of the call's dtype) and a code c in 0 .. 15 for each value, which
+ * stands for m + s c; the code of dim d is the nibble at bits 4 (d % 8) of the
+ * row's 32-bit word d / 8 (the packing of the exit layers).
+ *   k_codes, v_codes  [n_pages][n_kv_heads][page][head_dim / 2] bytes, 16-byte
+ *                     aligned, pages code_stride (k, v) bytes apart (multiples of 16)
+ *   k_scale, v_scale  [n_pages][n_kv_heads][page][2] (s, m), 16-byte aligned,
+ *                     pages scale_stride (k, v) elements apart (multiples of 8)
+ *   d_table           [batch][table_width] int32: page i of sequence b holds its
+ *                     positions i page .. (i + 1) page - 1; rows table_stride entries apart
+ * Entries past a sequence's length are not used; one outside [0, n_pages) that
+ * is used sets RL_DEVERR_CAPACITY, and page 0 is read instead (nothing written). */
+typedef struct {
+  int32_t n_pages, page; /* pages laid out; token rows of a page: 16, 32, 64, 128 or 256 */
+  void *k_codes, *k_scale, *v_codes, *v_scale;
+  int64_t code_stride[2], scale_stride[2];
+  const int32_t* d_table;
+  int64_t table_stride;
+  int32_t table_width;
+} rl_kv4;
+
+/* rl_kv4_append: the sequences' new rows into their pages, with the position
+ * rotation on the way.  Sequence b holds d_kv_len[b] rows with the new ones, its
+ * n = d_start[b + 1] - d_start[b] rows here the last of them: row t stands at
+ * position d_kv_len[b] - n + t.  q (may be NULL) and k are rotated as the
+ * model's layers do (dims i and i + head_dim / 2 a pair) by d_rope
+ * [rope_len][head_dim / 2] (cos, sin) fp32, 16-byte aligned, rounded once (NULL:
+ * taken as they are); out receives q (out may be q itself, with its strides).
+ * k and v are then stored with
+ *   m = the row's smallest value,  s = (largest - m) / 15 rounded to dtype (0 below 2^-100),
+ *   c = (x - m) / s rounded to the nearest, ties to even, at most 15  (0 where s is 0),
+ * all in IEEE fp32.  A row with a NaN or infinity (or, in bf16, whose largest minus
+ * smallest value is infinite) reads back as NaN.  A position outside the
+ * sequence's pages or the rotation's table sets RL_DEVERR_CAPACITY; nothing of
+ * that row is written.  Rows that two sequences' tables put in one place must
+ * not be appended at once.  max_rows is not used.  d_start NULL: one row each
+ * (rows == batch). */
+RL_API rl_status rl_kv4_append(const rl_kv4* c, const rl_packed_desc* p, const int32_t* d_start,
+                               const int32_t* d_kv_len, const void* d_q, const void* d_k, const void* d_v,
+                               const float* d_rope, int32_t rope_len, void* d_out, int32_t* d_err,
+                               rl_stream_t stream);
+
+/* rl_kv4_read: what the cache holds for rows, as values: the last
+ * d_start[b + 1] - d_start[b] of sequence b's d_kv_len[b] rows, to k and v
+ * (k_stride, v_stride), m + s c in fp32 rounded once to dtype.  A prompt's
+ * attention over these sees what later steps will see.  Positions outside the
+ * sequence's pages set RL_DEVERR_CAPACITY, their rows are left as they were. */
+RL_API rl_status rl_kv4_read(const rl_kv4* c, const rl_packed_desc* p, const int32_t* d_start,
+                             const int32_t* d_kv_len, void* d_k, void* d_v, int32_t* d_err, rl_stream_t stream);
+
+/* rl_kv4_attention: single tokens and drafts over the cache: row t of sequence
+ * b's n rows stands at position d_kv_len[b] - n + t and sees the positions up
+ * to its own; out and lse ([rows][n_q_heads] fp32, may be NULL) as
+ * rl_window_attention.  A row that sees no key gets 0 and lse -infinity.  A
+ * length outside [0, table_width * page] sets RL_DEVERR_CAPACITY and is
+ * clamped; rows past max_rows of a sequence set it and are left as they were.
+ * Positions from d_kv_len[b] on have no part in any result, whatever their
+ * pages hold.  Sums and statistics are fp32.  One launch, no workspace, results
+ * repeat bit for bit.  d_start NULL: one row each (rows == batch). */
+RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, const int32_t* d_start,
+                                  const int32_t* d_kv_len, const void* d_q, void* d_out, float* d_lse,
+                                  int32_t* d_err, rl_stream_t stream);
+
+/* rl_sample: one token a row of logits, from a given random number.  With
+ * w_i = exp((x_i - max x) / temperature) the ids are ordered by logit, largest
+ * first, equal ones by the lower id, and kept while
+ *   rank < top_k                          (top_k 0: all),
+ *   the weights in front < top_p S        (S: the sum of what top_k keeps; 1: all),
+ *   w_i >= min_p;
+ * the first id is always kept.  The token is the first kept id, in the order
+ * of ids, at which the kept weights' running sum exceeds u times their sum.
+ * Temperature 0 is the largest logit (the lower id of equal ones).
+ *   d_logits  [rows][vocab] as rl_token_logprobs; vocab at most 2^19
+ *   d_u       [rows] fp32 in [0, 1) (what is outside is taken for the nearest there, NaN for 0)
+ *   settings  of all rows, or (a pointer that is not NULL) one a row
+ *   d_token   [rows] int32
+ *   d_logprob [rows] fp32, may be NULL: ln of the token's share of the kept weights
+ *   d_err     [1] int32, may be NULL: RL_DEVERR_* bits are ORed into it
+ * Weights are whole multiples of 2^-44 (their exponentials are good to
+ * 2^-38), sums are exact, so results repeat bit for bit and do not depend on
+ * how a row is split.  Logits of -infinity are never drawn.  A row with a NaN or
+ * +infinity gives the id rl_token_logprobs would put first and logprob NaN, a
+ * row of -infinity alone id 0 and NaN; settings of d_ arrays: a temperature
+ * not above 0 (or NaN) is 0, a top_k below 1 or from vocab on keeps all, a top_p
+ * or min_p that is NaN keeps all.  One launch, no workspace.
+ * RL_ERR_INVALID_ARG for a missing buffer, a size below 1, row_stride < vocab,
+ * a temperature, top_k, top_p or min_p that is negative or not finite, an
+ * unknown dtype or misaligned logits; RL_ERR_UNSUPPORTED for a larger vocab. */
+typedef struct {
+  float temperature;
+  int32_t top_k;
+  float top_p, min_p;
+  const float* d_temperature; /* [rows], may be NULL: temperature for all; so the others */
+  const int32_t* d_top_k;
+  const float *d_top_p, *d_min_p;
+} rl_sampling;
+RL_API rl_status rl_sample(const void* d_logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
+                           const float* d_u, const rl_sampling* settings, int32_t* d_token, float* d_logprob,
+                           int32_t* d_err, rl_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -91,11 +91,11 @@ struct RowAcc {
       m = mn;
     }
   }
-  // Every key that query row t of sequence b, of n rows and ql queries, sees.
-  __device__ __forceinline__ void window(const AttnOpArgs& a, int b, int t, int hk, int n, int ql, int lane) {
+  // Every key that query row t of sequence b, of n rows and ql queries, sees (its first key at `base`).
+  __device__ __forceinline__ void window(const AttnOpArgs& a, int b, int t, int hk, int n, int ql, int lane, int base) {
     const int p = n - ql + t, lo = max(0, p - a.window + 1);
-    keys(a.kv, b, hk, 0, min(min(a.sinks, lo), p + 1), a.scale, lane);
-    keys(a.kv, b, hk, lo, p + 1, a.scale, lane);
+    keys(a.kv, b, hk, base, base + min(min(a.sinks, lo), p + 1), a.scale, lane);
+    keys(a.kv, b, hk, base + lo, base + p + 1, a.scale, lane);
   }
   __device__ __forceinline__ void store(const AttnOpArgs& a, int b, int t, int h, int lane) {
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -110,11 +110,11 @@ struct RowAcc {
 };
 
 template <int HD, bool F16>
-__device__ __noinline__ void exact_row(const AttnOpArgs& a, int b, int t, int h, int n, int ql, int lane) {
+__device__ __noinline__ void exact_row(const AttnOpArgs& a, int b, int t, int h, int n, int ql, int lane, int base = 0) {
   RowAcc<HD, F16> r;
-  r.load_q(a, b, t, h, lane);
-  r.window(a, b, t, h / (a.Hq / a.Hkv), n, ql, lane);
-  r.store(a, b, t, h, lane);
+  r.load_q(a, b, base + t, h, lane);
+  r.window(a, b, t, h / (a.Hq / a.Hkv), n, ql, lane, base);
+  r.store(a, b, base + t, h, lane);
 }
 
 // Division of n < 2^31 by a fixed d >= 1 as a multiplication and a shift (a
@@ -211,8 +211,8 @@ __device__ __forceinline__ PrefixWs prefix_ws(void* ws, int tile, int tiles, int
 
 // Few query rows against long key ranges (attn_decode.cu).
 cudaError_t launch_attn_decode(const AttnOpArgs& a, bool pdl, cudaStream_t s);
-// Many query rows on the tensor cores (attn_rows_tc.cu): a prompt's window, or
-// (prefix) every sequence's rows against a.pre into a.ws.
+// Many query rows on the tensor cores (attn_rows_tc.cu): a prompt's window,
+// packed prompts (a.start), or (prefix) every sequence's rows against a.pre into a.ws.
 cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s);
 // Joins the prefix's parts and the own keys' part of every row (attn_decode.cu).
 cudaError_t launch_prefix_join(const AttnOpArgs& a, cudaStream_t s);

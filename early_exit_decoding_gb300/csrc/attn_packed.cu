@@ -1,55 +1,37 @@
-// Causal attention of packed prompts (rl_packed_attention).
-//
-// Simplest form: a warp a row and query head, one key at a time.
-#include <float.h>
-#include <math.h>
+// Causal attention of packed prompts (rl_packed_attention): the rows of
+// attn_rows_tc.cu, whose CTAs find their sequence and row tile themselves.
+#include <string.h>
 
 #include "kv4.cuh"
 
 namespace river {
 
-namespace {
-
-using namespace dev;
-using namespace attn;
-
-template <int HD, bool F16>
-__global__ void __launch_bounds__(256) k_packed(const __grid_constant__ PackedArgs a) {
-  const int lane = threadIdx.x & 31;
-  check_start(a);
-  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
-  const int r = (int)(w / a.Hq), h = (int)(w - (long long)r * a.Hq);
-  if (r >= a.N) return;
-  const int b = seq_of_row(a, r, lane);
-  if (b < 0) return;
-  const Span sp = seq_span(a, b, h == 0 && lane == 0);
-  if (r - sp.first >= sp.n) return;
-  AttnOpArgs o = {};
-  o.q = a.q;
-  o.out = a.out;
-  o.lse = a.lse;
-  o.Tq = a.N;
-  o.Hq = a.Hq;
-  for (int i = 0; i < 2; ++i) {
-    o.qs[i + 1] = a.qs[i];
-    o.os[i + 1] = a.os[i];
-  }
-  const KeySrc s{a.k, a.v, {0, a.ks[1], a.ks[0]}, {0, a.vs[1], a.vs[0]}};
-  RowAcc<HD, F16> acc;
-  acc.load_q(o, 0, r, h, lane);
-  acc.keys(s, 0, h / (a.Hq / a.Hkv), sp.first, r + 1, a.scale, lane);
-  acc.store(o, 0, r, h, lane);
-}
-
-}  // namespace
-
 cudaError_t launch_packed_attention(const PackedArgs& p, cudaStream_t s) {
-  const unsigned grid = (unsigned)(((long long)p.N * p.Hq + 7) / 8);
-  if (p.hd == 64)
-    p.f16 ? k_packed<64, true><<<grid, 256, 0, s>>>(p) : k_packed<64, false><<<grid, 256, 0, s>>>(p);
-  else
-    p.f16 ? k_packed<128, true><<<grid, 256, 0, s>>>(p) : k_packed<128, false><<<grid, 256, 0, s>>>(p);
-  return cudaGetLastError();
+  AttnOpArgs o;
+  memset(&o, 0, sizeof(o));
+  o.q = p.q;
+  o.out = p.out;
+  o.lse = p.lse;
+  o.kv.k = p.k;
+  o.kv.v = p.v;
+  for (int i = 0; i < 2; ++i) {
+    o.qs[1 + i] = p.qs[i];
+    o.os[1 + i] = p.os[i];
+    o.kv.ks[2 - i] = p.ks[i];
+    o.kv.vs[2 - i] = p.vs[i];
+  }
+  o.f16 = p.f16;
+  o.B = p.B;
+  o.Tq = p.max_rows;
+  o.cap = p.N;
+  o.Hq = p.Hq;
+  o.Hkv = p.Hkv;
+  o.hd = p.hd;
+  o.window = 1 << 30;  // (every key)
+  o.scale = p.scale;
+  o.start = p.start;
+  o.err = p.err;
+  return launch_attn_rows_tc(o, false, s);
 }
 
 }  // namespace river

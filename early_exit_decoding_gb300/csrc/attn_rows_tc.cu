@@ -197,11 +197,65 @@ struct Bars {
   uint64_t s_full[2], p_full[2], o_full[2], full[8], empty[8], drain;
 };
 
-template <int HD, bool F16, bool PREFIX>
+enum { kWindow = 0, kPrefix = 1, kPacked = 2 };  // what the rows are
+
+// The row tile that comes `rank`-th when packed sequences' tiles are taken from
+// the last of the longest on (a later tile of a prompt sees more keys): its
+// sequence and number in it; false: there are no more.  The tiles numbered L or
+// more are f(L) = sum_b max(0, n_b - L), so the number is the L with
+// f(L + 1) <= rank < f(L).  The same for every lane of every warp.
+struct PackedTile {
+  int first, n, number;  // the sequence's first row and its rows
+};
+__device__ __forceinline__ bool packed_tile(const AttnOpArgs& a, int rep, int rank, int lane, PackedTile* t) {
+  auto span = [&](int b, int* first) {
+    if (b >= a.B) return 0;
+    const int s0 = __ldg(a.start + b), s1 = __ldg(a.start + b + 1);
+    *first = max(0, min(s0, a.cap));
+    return min(max(0, min(s1, a.cap) - *first), a.Tq);
+  };
+  auto tiles_of = [&](int b) {
+    int first;
+    return (int)(((long long)span(b, &first) * rep + kRowsCta - 1) / kRowsCta);
+  };
+  const int own = tiles_of(lane);
+  auto above = [&](int L) {  // f(L)
+    int n = max(0, own - L);
+    for (int b = 32 + lane; b < a.B; b += 32) n += max(0, tiles_of(b) - L);
+    return (int)__reduce_add_sync(0xffffffffu, n);
+  };
+  int most = own;
+  for (int b = 32 + lane; b < a.B; b += 32) most = max(most, tiles_of(b));
+  int lo = 0, hi = __reduce_max_sync(0xffffffffu, most);
+  if (rank >= above(0)) return false;
+  while (hi - lo > 1) {  // f(lo) > rank >= f(hi)
+    const int mid = (lo + hi) >> 1;
+    if (above(mid) > rank)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  rank -= above(hi);
+  t->number = lo;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const unsigned has = __ballot_sync(0xffffffffu, (b0 ? tiles_of(b0 + lane) : own) > lo);
+    const int n = __popc(has);
+    if (rank < n) {
+      const unsigned it = __ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == rank);
+      t->n = span(b0 + __ffs(it) - 1, &t->first);
+      return true;
+    }
+    rank -= n;
+  }
+  return false;  // (not reached)
+}
+
+template <int HD, bool F16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_rows_tc(const __grid_constant__ KvMaps maps, const __grid_constant__ CUtensorMap q_map,
                    const __grid_constant__ AttnOpArgs a, const __grid_constant__ RowsShape sh) {
   constexpr int NST = kStages<HD>, TB = kTileBytes<HD>;
+  constexpr bool PREFIX = MODE == kPrefix, PACKED = MODE == kPacked;
   extern __shared__ unsigned char smem_dyn[];
   unsigned char* smem =
       reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(smem_dyn) + 1023) & ~(uintptr_t)1023);
@@ -225,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int split = sh.split, tiles = sh.tiles, rep = sh.by_rep.d;
   int id = sh.by_split.quot(blockIdx.x);
   const int part = blockIdx.x - id * split;
-  if (!PREFIX && tid == kThreads - 1 && part == 0 && sh.q_tma) {
+  if (MODE == kWindow && tid == kThreads - 1 && part == 0 && sh.q_tma) {
     // Q of the CTA that follows here into L2 (its first scores wait for Q: the
     // 8192-token prompt 238 -> 236 us, the ragged ones 38.4 -> 37.6)
     const int nid = id + sh.ahead, nback = sh.by_group.quot(nid), nrow0 = (tiles - 1 - nback) * kRowsCta;
@@ -239,14 +293,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // later tiles of a prompt see more keys: first come, first served from the end
   const int back = sh.by_group.quot(id);
-  const int row0 = (tiles - 1 - back) * kRowsCta;
+  int row0 = (tiles - 1 - back) * kRowsCta;
   id -= back * sh.by_group.d;
-  const int b = sh.by_heads.quot(id), hk = id - b * sh.by_heads.d;  // (b is 0 for a prefix)
-  int n, ql, nrow, p0 = 0, lo = 0, hi, sink_end = 0;
+  const int b = sh.by_heads.quot(id), hk = id - b * sh.by_heads.d;  // (b is 0 for a prefix and packed rows)
+  int n, ql, nrow, p0 = 0, lo = 0, hi, sink_end = 0, base = 0;      // base: the sequence's first row and key
   if constexpr (PREFIX) {
     n = hi = a.P;
     ql = a.B;
     nrow = min(kRowsCta, a.B * rep - row0);
+  } else if constexpr (PACKED) {
+    if (a.err && blockIdx.x == 0)
+      for (int i = tid; i <= a.B; i += kThreads) {
+        const int s0 = i > 0 ? __ldg(a.start + i - 1) : 0, s1 = __ldg(a.start + i);
+        if (s1 < s0 || s1 > a.cap || (i > 0 && s1 - max(s0, 0) > a.Tq)) atomicOr(a.err, RL_DEVERR_CAPACITY);
+      }
+    PackedTile t;
+    if (!packed_tile(a, rep, back, lane, &t)) return;  // (its whole cluster)
+    base = t.first;
+    n = ql = t.n;
+    row0 = t.number * kRowsCta;
+    nrow = min(kRowsCta, n * rep - row0);
+    p0 = sh.by_rep.quot(row0);
+    hi = sh.by_rep.quot(row0 + nrow - 1) + 1;
   } else {
     const bool report = part == 0 && tid == 0 && hk == 0 && row0 == 0;
     const Lens len = seq_lens(a, b, report);
@@ -271,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int ngrp = nrow > 128 ? 2 : 1;
 
   auto load = [&](int i) {  // K (i even) or V tile i / 2 into its stage
-    const int st = i % NST, j = key0(j0 + (i >> 1));
+    const int st = i % NST, j = base + key0(j0 + (i >> 1));
     mbar_expect_tx(&bar.full[st], i == 0 && sh.q_tma ? (1 + ngrp) * TB : TB);
     if (i & 1)
       tma_load_5d(ring + st * TB, &maps.v, j, hk * maps.vh, b * maps.vb, &bar.full[st]);
@@ -297,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (sh.q_tma)
           for (int g = 0; g < ngrp; ++g) {
             const int t = sh.by_rep.quot(row0 + g * 128);
-            tma_load_q(sq + g * TB, &q_map, hk * rep, t, b, &bar.full[0]);
+            tma_load_q(sq + g * TB, &q_map, hk * rep, base + t, b, &bar.full[0]);
           }
       }
     }
@@ -311,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int g = warp / 4, r = tid & 127;
     auto at = [&](int e) {  // 16-byte chunk e * 128 + r of the tile: its place in q
       const int it = e * 128 + r, i = row0 + min(g * 128 + it / (HD / 8), nrow - 1), t = sh.by_rep.quot(i);
-      return (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)t * a.qs[1]) +
+      return (PREFIX ? (long long)t * a.qs[0] : (long long)b * a.qs[0] + (long long)(base + t) * a.qs[1]) +
              (long long)(hk * rep + i - t * rep) * a.qs[2] + it % (HD / 8) * 8;
     };
     auto put = [&](int e, uint4 v) {
@@ -466,6 +534,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < kKeys; c += 32)
               if (c + 32 > cnt) keep_only(s + c, below(cnt - c));
           }
+        } else if (PACKED) {
+          if (cnt < kKeys || k0 + kKeys - 1 > pa) {  // keys this row sees: below `end`
+            const int end = min(cnt, p - k0 + 1);
+#pragma unroll
+            for (int c = 0; c < kKeys; c += 32)
+              if (c + 32 > cnt || k0 + c + 31 > wa) keep_only(s + c, below(end - c));
+          }
         } else if (cnt < kKeys || k0 + kKeys - 1 > pa || (pz - k0 >= a.window && k0 + kKeys > a.sinks)) {
           // keys this row sees: below `end`, and from `beg` on or below `snk`
           const int end = min(cnt, p - k0 + 1), beg = p - a.window + 1 - k0, snk = a.sinks - k0;
@@ -548,9 +623,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     float inv = 0.f;
     if (!PREFIX && direct && mine) {  // (while the last products run)
       const int t = sh.by_rep.quot(i_row), h = hk * rep + i_row - t * rep;
-      row_at = b * a.os[0] + t * a.os[1] + h * a.os[2];
+      row_at = b * a.os[0] + (base + t) * a.os[1] + h * a.os[2];
       inv = l == 0.f ? 0.f : 1.f / l;
-      if (a.lse) a.lse[((long long)b * a.Tq + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
+      if (a.lse) a.lse[((long long)b * a.Tq + base + t) * a.Hq + h] = l == 0.f ? -INFINITY : (m * sc + log2f(l)) * 0.6931471805599453f;
     }
     if (g < ngrp && nt > 0) {
       // (the last tile's: the ring, which the other tile's products still read,
@@ -559,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         l = inv = NAN;
         if (row_at >= 0 && a.lse) {  // (stored above, of the keys there were)
           const int t = sh.by_rep.quot(i_row);
-          a.lse[((long long)b * a.Tq + t) * a.Hq + hk * rep + i_row - t * rep] = NAN;
+          a.lse[((long long)b * a.Tq + base + t) * a.Hq + hk * rep + i_row - t * rep] = NAN;
         }
       }
       fence_after();
@@ -641,7 +716,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int i = row0 + g * 128 + (warp & 3) * 32 + __ffs(bad) - 1;
           bad &= bad - 1;
           const int ti = sh.by_rep.quot(i);
-          exact_row<HD, F16>(a, b, ti, hk * rep + i - ti * rep, n, ql, lane);
+          exact_row<HD, F16>(a, b, ti, hk * rep + i - ti * rep, n, ql, lane, base);
         }
       } else {
         // to shared memory over the drained ring: rows of HD floats, 16-byte
@@ -697,15 +772,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int i = row0 + q, t = sh.by_rep.quot(i), h = hk * rep + i - t * rep;
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const bool fin = isfinite(acc.x * inv) && isfinite(acc.y * inv) && isfinite(acc.z * inv) && isfinite(acc.w * inv);
-        uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + t * a.os[1] + h * a.os[2] + c * 4;
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + b * a.os[0] + (base + t) * a.os[1] + h * a.os[2] + c * 4;
         if (lane < CH)
           *reinterpret_cast<uint2*>(dst) =
               make_uint2(pack2<F16>(acc.x * inv, acc.y * inv), pack2<F16>(acc.z * inv, acc.w * inv));
         if (lane == 0 && a.lse)
-          a.lse[((long long)b * a.Tq + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+          a.lse[((long long)b * a.Tq + base + t) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
         if (__any_sync(0xffffffffu, !fin) && !__any_sync(0xffffffffu, s_fail)) {
           __syncwarp();  // (its stores come after those above)
-          exact_row<HD, F16>(a, b, t, h, n, ql, lane);
+          exact_row<HD, F16>(a, b, t, h, n, ql, lane, base);
         }
       }
       cluster_barrier();  // nobody leaves while its shared memory may still be read
@@ -727,10 +802,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // The map of Q's rows (see RowsShape); false: not of a form that a box of 128
 // rows fits, and the threads load them.
-bool make_q_map(CUtensorMap* map, const AttnOpArgs& a, bool prefix) {
+bool make_q_map(CUtensorMap* map, const AttnOpArgs& a, int mode) {
   const int rep = a.Hq / a.Hkv;
   if (a.q_f32 || 128 % rep) return false;
-  const int seqs = prefix ? 1 : a.B, rows = prefix ? a.B : a.Tq;
+  const bool prefix = mode == kPrefix;
+  const int seqs = mode == kWindow ? a.B : 1, rows = prefix ? a.B : mode == kPacked ? a.cap : a.Tq;
   // (an axis of extent 1 takes any stride)
   const long long st[3] = {a.Hq > 1 ? a.qs[2] : a.hd, rows > 1 ? (prefix ? a.qs[0] : a.qs[1]) : a.hd, seqs > 1 ? a.qs[0] : a.hd};
   for (long long x : st)
@@ -745,13 +821,14 @@ bool make_q_map(CUtensorMap* map, const AttnOpArgs& a, bool prefix) {
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int HD, bool F16, bool PREFIX>
+template <int HD, bool F16, int MODE>
 cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sm_count(dev, &sms);
   if (e != cudaSuccess) return e;
-  auto kern = k_attn_rows_tc<HD, F16, PREFIX>;
+  constexpr bool PREFIX = MODE == kPrefix, PACKED = MODE == kPacked;
+  auto kern = k_attn_rows_tc<HD, F16, MODE>;
   const int* clusters = nullptr;  // that fit the GPU at once, by their CTAs (fixed once set)
   {
     static std::mutex mu;
@@ -780,19 +857,23 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   }
   KvMaps maps;
   const bool got = PREFIX ? make_kv_maps(&maps, a.pre, a.f16 != 0, 1, a.Hkv, HD, a.P, kKeys)
-                          : make_kv_maps(&maps, a.kv, a.f16 != 0, a.B, a.Hkv, HD, a.cap, kKeys);
+                          : make_kv_maps(&maps, a.kv, a.f16 != 0, PACKED ? 1 : a.B, a.Hkv, HD, a.cap, kKeys);
   if (!got) return cudaErrorInvalidValue;
   const int rep = a.Hq / a.Hkv;
   const long long rows = (long long)(PREFIX ? a.B : a.Tq) * rep;
-  const int tiles = (int)((rows + kRowsCta - 1) / kRowsCta);
-  const long long ctas = (long long)tiles * a.Hkv * (PREFIX ? 1 : a.B);
+  // (packed: no more than this many; the lengths are on the device)
+  const long long each = (rows + kRowsCta - 1) / kRowsCta;
+  const long long bound = PACKED ? min(each * a.B, (long long)a.cap * rep / kRowsCta + a.B) : each;
+  if (bound >= 1ll << 31) return cudaErrorInvalidValue;
+  const int tiles = (int)bound;
+  const long long ctas = (long long)tiles * a.Hkv * (MODE == kWindow ? a.B : 1);
   int split = 1;
   if (PREFIX) {
     split = prefix_split(a.B, rep, a.Hkv, a.P);
   } else {
     // the count with the least time by this model (clocks, measured): waves of
     // clusters, each a CTA's start and end, its tiles of 128 keys, a cluster's join
-    const long long keys = min((long long)a.cap, (long long)a.window + min(a.Tq, kRowsCta / rep + 2) + a.sinks);
+    const long long keys = PACKED ? a.Tq : min((long long)a.cap, (long long)a.window + min(a.Tq, kRowsCta / rep + 2) + a.sinks);
     const long long nt = (keys + kKeys - 1) / kKeys;
     double least = 0;
     for (int c = 1; c <= kMaxSplit && c <= nt; ++c) {
@@ -824,20 +905,20 @@ cudaError_t launch(const AttnOpArgs& a, cudaStream_t s) {
   sh.polls = polls < 0 ? kSpin : (int)min(polls, (long long)kSpin);
   sh.split = split;
   sh.tiles = tiles;
-  sh.q_tma = make_q_map(&q_map, a, PREFIX);
-  sh.ahead = PREFIX ? 0 : clusters[split];
+  sh.q_tma = make_q_map(&q_map, a, MODE);
+  sh.ahead = MODE == kWindow ? clusters[split] : 0;
   sh.apart = PREFIX && prefix_apart(a.B, rep, a.Hkv);
   sh.by_split = FastDiv(split);
   sh.by_heads = FastDiv(a.Hkv);
-  sh.by_group = FastDiv(PREFIX ? a.Hkv : a.Hkv * a.B);
+  sh.by_group = FastDiv(MODE == kWindow ? a.Hkv * a.B : a.Hkv);
   sh.by_rep = FastDiv(rep);
   return cudaLaunchKernelEx(&cfg, kern, maps, q_map, a, sh);
 }
 
-template <bool PREFIX>
+template <int MODE>
 cudaError_t launch_any(const AttnOpArgs& a, cudaStream_t s) {
-  if (a.hd == 64) return a.f16 ? launch<64, true, PREFIX>(a, s) : launch<64, false, PREFIX>(a, s);
-  return a.f16 ? launch<128, true, PREFIX>(a, s) : launch<128, false, PREFIX>(a, s);
+  if (a.hd == 64) return a.f16 ? launch<64, true, MODE>(a, s) : launch<64, false, MODE>(a, s);
+  return a.f16 ? launch<128, true, MODE>(a, s) : launch<128, false, MODE>(a, s);
 }
 
 }  // namespace
@@ -893,7 +974,8 @@ size_t prefix_ws_bytes(int B, int rep, int Hkv, int hd, int P) {
 }
 
 cudaError_t launch_attn_rows_tc(const AttnOpArgs& a, bool prefix, cudaStream_t s) {
-  return prefix ? launch_any<true>(a, s) : launch_any<false>(a, s);
+  if (a.start) return launch_any<kPacked>(a, s);
+  return prefix ? launch_any<kPrefix>(a, s) : launch_any<kWindow>(a, s);
 }
 
 }  // namespace river

@@ -499,6 +499,9 @@ struct AttnOpArgs {
   KeySrc pre;
   int P;
   void* ws;                 // shared-prefix partials
+  // packed rows: sequence b has the rows start[b] .. start[b + 1] - 1 (of which at
+  // most Tq count) of the `cap` laid out, in q, k, v and out (strides [1], [2]; B sequences)
+  const int* start;
 };
 cudaError_t launch_window_attention(const AttnOpArgs& a, cudaStream_t s);
 size_t shared_prefix_ws_bytes(int B, int Hq, int Hkv, int hd, int P);

@@ -132,6 +132,59 @@ struct FastDiv {
   __device__ __forceinline__ int quot(int n) const { return (int)((__umulhi(m, (uint32_t)n) + (uint32_t)n) >> l); }
 };
 
+// The tile of `rows` rows that comes `rank`-th when packed sequences' tiles (of
+// their rows x rep; at most `most` rows of a sequence count, of the N laid out)
+// are taken from the last of the longest on, since a later tile of a prompt sees
+// more keys; false: there are no more.  The tiles numbered L or more are
+// f(L) = sum_b max(0, n_b - L), so the number is the L with
+// f(L + 1) <= rank < f(L).  The same for every lane.
+struct RowTile {
+  int seq, first, n, number;  // the sequence, its first row and rows; which of its tiles
+};
+__device__ __forceinline__ bool row_tile(const int* start, int B, int N, int most, int rep, int rows, int rank, int lane, RowTile* t) {
+  auto span = [&](int b, int* first) {
+    if (b >= B) return 0;
+    const int s0 = __ldg(start + b), s1 = __ldg(start + b + 1);
+    *first = max(0, min(s0, N));
+    return min(max(0, min(s1, N) - *first), most);
+  };
+  auto tiles_of = [&](int b) {
+    int first;
+    return (int)(((long long)span(b, &first) * rep + rows - 1) / rows);
+  };
+  const int own = tiles_of(lane);
+  auto above = [&](int L) {  // f(L)
+    int n = max(0, own - L);
+    for (int b = 32 + lane; b < B; b += 32) n += max(0, tiles_of(b) - L);
+    return (int)__reduce_add_sync(0xffffffffu, n);
+  };
+  int top = own;
+  for (int b = 32 + lane; b < B; b += 32) top = max(top, tiles_of(b));
+  int lo = 0, hi = __reduce_max_sync(0xffffffffu, top);
+  if (rank >= above(0)) return false;
+  while (hi - lo > 1) {  // f(lo) > rank >= f(hi)
+    const int mid = (lo + hi) >> 1;
+    if (above(mid) > rank)
+      lo = mid;
+    else
+      hi = mid;
+  }
+  rank -= above(hi);
+  t->number = lo;
+  for (int b0 = 0; b0 < B; b0 += 32) {
+    const unsigned has = __ballot_sync(0xffffffffu, (b0 ? tiles_of(b0 + lane) : own) > lo);
+    const int n = __popc(has);
+    if (rank < n) {
+      const unsigned it = __ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == rank);
+      t->seq = b0 + __ffs(it) - 1;
+      t->n = span(t->seq, &t->first);
+      return true;
+    }
+    rank -= n;
+  }
+  return false;  // (not reached)
+}
+
 // Tensor maps of one K and one V source: five axes (64 dims, token rows,
 // 64-dim blocks, KV heads, sequences), so one copy brings `rows` token rows of
 // all dims as HD / 64 blocks of rows x 128 bytes, 128-byte swizzle; rows past

@@ -199,57 +199,6 @@ struct Bars {
 
 enum { kWindow = 0, kPrefix = 1, kPacked = 2 };  // what the rows are
 
-// The row tile that comes `rank`-th when packed sequences' tiles are taken from
-// the last of the longest on (a later tile of a prompt sees more keys): its
-// sequence and number in it; false: there are no more.  The tiles numbered L or
-// more are f(L) = sum_b max(0, n_b - L), so the number is the L with
-// f(L + 1) <= rank < f(L).  The same for every lane of every warp.
-struct PackedTile {
-  int first, n, number;  // the sequence's first row and its rows
-};
-__device__ __forceinline__ bool packed_tile(const AttnOpArgs& a, int rep, int rank, int lane, PackedTile* t) {
-  auto span = [&](int b, int* first) {
-    if (b >= a.B) return 0;
-    const int s0 = __ldg(a.start + b), s1 = __ldg(a.start + b + 1);
-    *first = max(0, min(s0, a.cap));
-    return min(max(0, min(s1, a.cap) - *first), a.Tq);
-  };
-  auto tiles_of = [&](int b) {
-    int first;
-    return (int)(((long long)span(b, &first) * rep + kRowsCta - 1) / kRowsCta);
-  };
-  const int own = tiles_of(lane);
-  auto above = [&](int L) {  // f(L)
-    int n = max(0, own - L);
-    for (int b = 32 + lane; b < a.B; b += 32) n += max(0, tiles_of(b) - L);
-    return (int)__reduce_add_sync(0xffffffffu, n);
-  };
-  int most = own;
-  for (int b = 32 + lane; b < a.B; b += 32) most = max(most, tiles_of(b));
-  int lo = 0, hi = __reduce_max_sync(0xffffffffu, most);
-  if (rank >= above(0)) return false;
-  while (hi - lo > 1) {  // f(lo) > rank >= f(hi)
-    const int mid = (lo + hi) >> 1;
-    if (above(mid) > rank)
-      lo = mid;
-    else
-      hi = mid;
-  }
-  rank -= above(hi);
-  t->number = lo;
-  for (int b0 = 0; b0 < a.B; b0 += 32) {
-    const unsigned has = __ballot_sync(0xffffffffu, (b0 ? tiles_of(b0 + lane) : own) > lo);
-    const int n = __popc(has);
-    if (rank < n) {
-      const unsigned it = __ballot_sync(0xffffffffu, (has >> lane & 1) && __popc(has & ((1u << lane) - 1)) == rank);
-      t->n = span(b0 + __ffs(it) - 1, &t->first);
-      return true;
-    }
-    rank -= n;
-  }
-  return false;  // (not reached)
-}
-
 template <int HD, bool F16, int MODE>
 __global__ void __launch_bounds__(kThreads, 1)
     k_attn_rows_tc(const __grid_constant__ KvMaps maps, const __grid_constant__ CUtensorMap q_map,
@@ -307,8 +256,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s0 = i > 0 ? __ldg(a.start + i - 1) : 0, s1 = __ldg(a.start + i);
         if (s1 < s0 || s1 > a.cap || (i > 0 && s1 - max(s0, 0) > a.Tq)) atomicOr(a.err, RL_DEVERR_CAPACITY);
       }
-    PackedTile t;
-    if (!packed_tile(a, rep, back, lane, &t)) return;  // (its whole cluster)
+    RowTile t;
+    if (!row_tile(a.start, a.B, a.cap, a.Tq, rep, kRowsCta, back, lane, &t)) return;  // (its whole cluster)
     base = t.first;
     n = ql = t.n;
     row0 = t.number * kRowsCta;

@@ -34,7 +34,8 @@ EXPORTS = (
     "rl_kv_set_wait_limit", "rl_debug_fail_allocations", "rl_debug_limit_waits", "rl_model_offload_backbone",
     "rl_model_memory", "rl_token_logprobs", "rl_window_attention", "rl_shared_prefix_workspace",
     "rl_shared_prefix_attention", "rl_kv_set_window", "rl_kv_share_prefix", "rl_prefill_score",
-    "rl_packed_attention", "rl_kv4_append", "rl_kv4_read", "rl_kv4_attention", "rl_sample",
+    "rl_packed_attention", "rl_kv4_append", "rl_kv4_read", "rl_kv4_attention_workspace", "rl_kv4_attention",
+    "rl_sample",
 )
 RL_DT_F32, RL_DT_BF16, RL_DT_F16 = range(3)
 RL_PATH_AUTO, RL_PATH_STEP, RL_PATH_FUSED, RL_PATH_GENERIC = range(4)
@@ -149,7 +150,8 @@ def _load():
         "rl_packed_attention": (I, [ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, P, P]),
         "rl_kv4_append": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, I, P, P, P]),
         "rl_kv4_read": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P]),
-        "rl_kv4_attention": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, P]),
+        "rl_kv4_attention_workspace": (I, [ctypes.POINTER(rl_packed_desc), ctypes.POINTER(ctypes.c_uint64)]),
+        "rl_kv4_attention": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, ctypes.c_uint64, P, P]),
         "rl_sample": (I, [P, I, I, I, ctypes.c_int64, P, ctypes.POINTER(rl_sampling), P, P, P, P]),
     }
     for name, (res, args) in sig.items():
@@ -430,9 +432,16 @@ def rl_kv4_read(cache, desc, d_start, d_kv_len, d_k, d_v, d_err=None, stream=Non
                             _ptr(d_err), _stream(stream)))
 
 
-def rl_kv4_attention(cache, desc, d_start, d_kv_len, d_q, d_out, d_lse, d_err=None, stream=None):
+def rl_kv4_attention_workspace(desc):
+    """Workspace bytes of rl_kv4_attention."""
+    n = ctypes.c_uint64()
+    _check(_lib.rl_kv4_attention_workspace(ctypes.byref(desc), ctypes.byref(n)))
+    return n.value
+
+
+def rl_kv4_attention(cache, desc, d_start, d_kv_len, d_q, d_out, d_lse, d_ws, ws_bytes, d_err=None, stream=None):
     _check(_lib.rl_kv4_attention(ctypes.byref(cache), ctypes.byref(desc), _ptr(d_start), _ptr(d_kv_len), _ptr(d_q),
-                                 _ptr(d_out), _ptr(d_lse), _ptr(d_err), _stream(stream)))
+                                 _ptr(d_out), _ptr(d_lse), _ptr(d_ws), ws_bytes, _ptr(d_err), _stream(stream)))
 
 
 def rl_sample(d_logits, dtype, rows, vocab, row_stride, d_u, settings, d_token, d_logprob, d_err=None, stream=None):
@@ -1132,16 +1141,18 @@ def kv4_read(cache, table, kv_len, start=None, rows=None, out=None, err=None, st
     return o
 
 
-def kv4_attention(q, cache, table, kv_len, start=None, max_rows=None, scale=None, out=None, err=None, stream=None):
+def kv4_attention(q, cache, table, kv_len, start=None, max_rows=None, scale=None, out=None, workspace=None, err=None, stream=None):
     """Attention of single tokens and drafts over a 4-bit cache: ``q [N][Hq][hd]``
     of the scales' type, packed by ``start`` (int32 [B + 1]; None: one row each),
     the last rows of ``kv_len`` (int32 [B]).  ``max_rows``: no sequence has more
     rows here (None: unknown; known, it saves time).  Returns a dict: ``out``
     (q's shape and type) and ``lse`` fp32 [N][Hq]; buffers present in ``out``
-    are used, their rows of no sequence left as they were.  See rl_kv4_attention."""
+    are used, their rows of no sequence left as they were.  ``workspace``: a
+    uint8 tensor of rl_kv4_attention_workspace bytes; None takes one from
+    PyTorch's allocator for this call.  See rl_kv4_attention."""
     torch = _torch()
     name = "kv4_attention"
-    dev = _operands(name, (q, table, kv_len, start, err, *cache))
+    dev = _operands(name, (q, table, kv_len, start, workspace, err, *cache))
     if q.dim() != 3 or q.numel() == 0 or kv_len.dim() != 1 or kv_len.numel() == 0:
         _refuse(f"{name}: q must be [N][Hq][hd], not empty, kv_len [B]")
     o = dict(out) if out else {}
@@ -1150,15 +1161,20 @@ def kv4_attention(q, cache, table, kv_len, start=None, max_rows=None, scale=None
 
     def make():
         c, heads, hd = _kv4_desc(name, cache, table, q.dtype)
-        return c, _packed_desc(name, q.dtype, (q.shape[1], heads, hd), B, N, max_rows or 0, scale, q=q, out=res)
+        d = _packed_desc(name, q.dtype, (q.shape[1], heads, hd), B, N, max_rows or 0, scale, q=q, out=res)
+        return c, d, rl_kv4_attention_workspace(d)
 
-    c, d = _plan((name, B, max_rows), scale, (*cache, table, q, res) if out else (*cache, table, q), make)
+    c, d, need = _plan((name, B, max_rows), scale, (*cache, table, q, res) if out else (*cache, table, q), make)
     lse = _buffer(o, "lse", (N, q.shape[1]), q, torch.float32, stream, name)
     if table.shape[0] != B:
         _refuse(f"{name}: table must have a row for each of the {B} sequences")
     _spans(name, start, kv_len, B, N, err)
+    if workspace is None:
+        workspace = _new((need,), torch.uint8, q.device, stream)
+    elif not workspace.is_contiguous():
+        _refuse(f"{name}: workspace must be contiguous")
     _run(dev, stream, _lib.rl_kv4_attention, _kv4_with(c, cache, table), d, _addr(start), kv_len.data_ptr(), q.data_ptr(),
-         res.data_ptr(), lse.data_ptr(), _addr(err))
+         res.data_ptr(), lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(), _addr(err))
     return o
 
 

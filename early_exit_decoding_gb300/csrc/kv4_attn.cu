@@ -22,14 +22,17 @@
 // of eights beside the codes).  Scores, sums and statistics are fp32.  Maxima
 // follow lazily: everything is rescaled only when one grew by more than 2^8.
 //
-// Each warp runs its own ring: 32 keys a stage, copied by 4 or 8 bulk copies
-// (codes and scales of k and v; a page's rows of a head are contiguous).  Keys
-// are dealt out unit by unit to the warps of a cluster of S CTAs and the states
-// joined at the end, as in attn_decode.cu: no workspace, one launch.
+// Work is counted in units of 32 keys of a row tile and KV head, over the whole
+// batch, and each CTA takes an equal, contiguous share of it, however ragged the
+// contexts are: the end of one sequence, whole ones, the start of another.  A
+// tile whose keys fall to one CTA is finished there; the others' states (sums of
+// weighted values, maximum, sum of weights) go to the workspace, at most two a
+// CTA, and a second kernel joins them in a fixed order.  Within a share the
+// warps take the units in turn, each with a ring of its own filled by
+// asynchronous copies.
 #include <float.h>
 #include <math.h>
 
-#include <stdlib.h>
 #include <mutex>
 
 #include "kv4.cuh"
@@ -43,110 +46,176 @@ using namespace attn;
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kUnit = 32;      // keys a warp takes at a time
-constexpr int kMaxSplit = 16;  // CTAs of a cluster
-constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
+constexpr int kUnit = 32;       // keys a warp takes at a time
+constexpr int kStages = 3;      // units of a warp's ring
+constexpr int kLeast = 4;       // units a CTA takes at least
+constexpr int kMaxCtas = 608;   // four on each of 152 SMs; the workspace holds that many CTAs' parts
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLazy = 8.f;   // log2 growth of a maximum that is let pass
+constexpr float kMost = 256.f;  // a weight, or weight times step, that is let pass (1 where it was the largest)
 
 template <int HD>
 constexpr int kStageBytes = kUnit * HD + 2 * kUnit * 4;  // codes of k and v, scales of k and v
 template <int HD>
-constexpr int kStages = HD == 128 ? 4 : 8;
-template <int HD>
-constexpr int kSmem = kWarps * kStages<HD> * kStageBytes<HD>;
+constexpr int kSmem = kWarps * kStages * kStageBytes<HD>;
+template <int NT>
+constexpr int kResident = NT == 1 ? 4 : 2;  // CTAs of an SM (registers)
 
 struct Kv4Shape {
-  int split, tiles;  // CTAs of a cluster; row tiles of a sequence (without start)
-  FastDiv by_split, by_heads, by_rep, by_tiles;
+  FastDiv by_heads, by_rep;
 };
+
+// The workspace: of every CTA two parts (its first tile's and its last's), each
+// R rows of HD sums, R maxima (log2 units) and R sums of weights; then a word
+// pair for every row and query head: the first CTA that holds a part of it; how
+// many more do (<< 6), which of that CTA's two it is (<< 5; the others' first)
+// and the row's place in its tile.
+struct Kv4Ws {
+  float* part;
+  int2* where;
+};
+template <int HD, int R>
+constexpr int kPartFloats = R * (HD + 2);
 
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   uint32_t d;
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
+
+// Row tiles and units of a tile of sequence b (0 behind the last sequence).
+struct Load {
+  int tiles, units;
+};
+__device__ __forceinline__ Load seq_load(const PackedArgs& a, int cap, int rep, int rows, int b) {
+  if (b >= a.B) return Load{0, 0};
+  const int n = max(0, min(__ldg(a.kv_len + b), cap));
+  return Load{(int)(((long long)seq_span(a, b, false).n * rep + rows - 1) / rows), (n + kUnit - 1) / kUnit};
 }
-__device__ __forceinline__ float pivot(float m) { return m == -INFINITY ? 0.f : m; }
+
+__device__ __forceinline__ void cp_wait_stages() { asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory"); }
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 
 template <int HD, bool F16, int NT>
-__global__ void __launch_bounds__(kThreads, 3)
-    k_kv4_attn(const __grid_constant__ PackedArgs a, const __grid_constant__ Kv4Args c, const __grid_constant__ Kv4Shape sh) {
-  constexpr int NST = kStages<HD>, SB = kStageBytes<HD>, R = 8 * NT, KW = HD / 32;  // KW: words of k's codes a lane takes
+__global__ void __launch_bounds__(kThreads, kResident<NT>)
+    k_kv4_attn(const __grid_constant__ PackedArgs a, const __grid_constant__ Kv4Args c, const __grid_constant__ Kv4Shape sh, Kv4Ws ws) {
+  constexpr int NST = kStages, SB = kStageBytes<HD>, R = 8 * NT, KW = HD / 32;  // KW: words of k's codes a lane takes
   constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
   extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ __align__(8) uint64_t full[kWarps][NST];
   __shared__ float s_m[kWarps][R], s_l[kWarps][R];
-  __shared__ float c_m[R], c_l[R];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   check_start(a);
-  const int id = sh.by_split.quot(blockIdx.x), part = blockIdx.x - id * sh.split;
-  const int tile = sh.by_heads.quot(id), hk = id - tile * sh.by_heads.d, rep = sh.by_rep.d;
-  int b, row0;
-  if (a.start) {
-    RowTile rt;
-    if (!row_tile(a.start, a.B, a.N, a.max_rows, rep, R, tile, lane, &rt)) return;  // (its whole cluster)
-    b = rt.seq;
-    row0 = rt.number * R;
-  } else {
-    b = sh.by_tiles.quot(tile);
-    row0 = (tile - b * sh.tiles) * R;
+  const int rep = sh.by_rep.d, cap = c.width << c.page_log, in_page = (1 << c.page_log) - 1;
+  if (blockIdx.x == 0 && a.err)
+    for (int b = tid; b < a.B; b += kThreads) {
+      const int len = __ldg(a.kv_len + b);
+      seq_span(a, b, true);
+      if (len < 0 || len > cap) atomicOr(a.err, RL_DEVERR_CAPACITY);
+    }
+  // the batch's units, and this CTA's share of them
+  long long all = 0;
+  for (int b0 = 0; b0 < a.B; b0 += 32) {
+    const Load x = seq_load(a, cap, rep, R, b0 + lane);
+    all += (long long)x.tiles * x.units;
   }
-  const bool report = part == 0 && hk == 0 && row0 == 0 && tid == 0;
-  const Span sp = seq_span(a, b, report);
-  const int cap = c.width << c.page_log, len = __ldg(a.kv_len + b);
-  if (report && a.err && (len < 0 || len > cap)) atomicOr(a.err, RL_DEVERR_CAPACITY);
-  const int old = max(0, min(len, cap)) - sp.all;  // position of the sequence's first row here
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
+  all *= a.Hkv;
+  const long long ctas = max(1ll, min((long long)gridDim.x, (all + kLeast - 1) / kLeast));
+  long long at = all * blockIdx.x / ctas;
+  const long long stop_at = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : 0;
+  if (at >= stop_at) return;
+  // the sequence, tile and head, and unit it starts with
+  int b = 0, item = 0, u0 = 0;
+  Load ld;
+  {
+    long long before = 0;
+    for (int b0 = 0; b0 < a.B; b0 += 32) {
+      const Load x = seq_load(a, cap, rep, R, b0 + lane);
+      const long long mine = (long long)x.tiles * x.units * a.Hkv;
+      long long sum = mine;  // of this lane's sequence and those in front
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, sum, d);
+        if (lane >= d) sum += y;
+      }
+      const unsigned it = __ballot_sync(0xffffffffu, before + sum > at);
+      if (it) {
+        const int who = __ffs(it) - 1;
+        b = b0 + who;
+        ld.tiles = __shfl_sync(0xffffffffu, x.tiles, who);
+        ld.units = __shfl_sync(0xffffffffu, x.units, who);
+        const long long rest = at - before - __shfl_sync(0xffffffffu, sum - mine, who);
+        item = (int)(rest / ld.units);
+        u0 = (int)(rest - (long long)item * ld.units);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
+    }
+  }
+  unsigned char* const ring = smem + warp * NST * SB;
+  for (bool head_part = true;; head_part = false) {
+  const int u1 = (int)min((long long)ld.units, u0 + (stop_at - at));
+  const int tile = sh.by_heads.quot(item), hk = item - tile * sh.by_heads.d, row0 = tile * R;
+  const Span sp = seq_span(a, b, false);
+  const int old = max(0, min(__ldg(a.kv_len + b), cap)) - sp.all;  // position of the sequence's first row here
   const int nrow = min(R, sp.n * rep - row0);
-  if (nrow <= 0) return;
   // keys that every row sees, and that any row sees
   const int every = old + sh.by_rep.quot(row0) + 1, any = max(0, old + sh.by_rep.quot(row0 + nrow - 1) + 1);
-  const int units = (any + kUnit - 1) / kUnit, W = sh.split * kWarps, first = part * kWarps + warp;
+  const int units = min(u1, (any + kUnit - 1) / kUnit);
 
-  unsigned char* ring = smem + warp * NST * SB;
-  if (lane == 0) {
-    for (int i = 0; i < NST; ++i) mbar_init(&full[warp][i], 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-  }
-  __syncwarp();
-  // lanes 0-7 copy: 16 keys (lane / 4) of k's codes, k's scales, v's codes, v's
-  // scales (lane % 4); where a page holds a whole unit lanes 0-3 all of it
-  const int sub = (lane >> 2) & 1, what = lane & 3;
-  auto page_of = [&](int u) {  // page of this lane's keys of unit u
-    const int j = u * kUnit + sub * 16;
-    return lane < 8 && j < any ? max(0, page_at(a, c, b, j >> c.page_log)) : 0;
-  };
-  auto issue = [&](int u, int st, int page) {
-    unsigned char* dst = ring + st * SB;
-    const int nsub = any - u * kUnit > 16 ? 2 : 1;
-    const bool whole = nsub == 2 && c.page_log >= 5;
-    if (lane == 0) mbar_expect_tx(&full[warp][st], nsub * (16 * HD + 128));
-    __syncwarp();
-    if (lane < (whole ? 4 : 4 * nsub)) {
-      const long long at = page_row(c, hk, (u * kUnit + sub * 16) & ((1 << c.page_log) - 1));
-      const int n = whole ? kUnit : 16;
-      const unsigned char* src;
-      if (what == 0)
-        src = c.kc + page * c.kc_step + at * (HD / 2);
-      else if (what == 1)
-        src = reinterpret_cast<const unsigned char*>(c.km + page * c.km_step + at);
-      else if (what == 2)
-        src = c.vc + page * c.vc_step + at * (HD / 2);
-      else
-        src = reinterpret_cast<const unsigned char*>(c.vm + page * c.vm_step + at);
-      const int row = what & 1 ? 4 : HD / 2;
-      // stage: k's codes, v's codes, k's scales, v's scales
-      dst += (what == 0 ? 0 : what == 2 ? kUnit * HD / 2 : what == 1 ? kUnit * HD : kUnit * HD + kUnit * 4) + sub * 16 * row;
-      bulk_g2s(dst, src, n * row, &full[warp][st]);
+  // this lane's 16-byte pieces of a unit: of k's and v's codes every 512 bytes,
+  // and (lanes 0-15) one of the scales
+  const long long head0 = page_row(c, hk, 0);
+  const unsigned char *const kc0 = c.kc + head0 * (HD / 2) + lane * 16, *const vc0 = c.vc + head0 * (HD / 2) + lane * 16;
+  const bool v_scales = lane & 8;
+  const unsigned char* const sc0 = reinterpret_cast<const unsigned char*>((v_scales ? c.vm : c.km) + head0) + (lane & 3) * 16;
+  const long long sc_step = 4 * (v_scales ? c.vm_step : c.km_step);
+  const uint32_t dst0 = smem_u32(ring) + lane * 16, dst_sc = smem_u32(ring) + kUnit * HD + (lane & 15) * 16;
+  auto pages_of = [&](int u) {  // of a unit's first and last 16 keys (-1: nobody sees them)
+    const int j = u * kUnit, *row = c.table + (long long)b * c.table_step;
+    int2 p = make_int2(-1, -1);
+    if (u < units) {
+      p.x = __ldg(row + (j >> c.page_log));
+      if (j + 16 < any) p.y = __ldg(row + ((j + 16) >> c.page_log));
+      // (out of the cache: reported, page 0 is read)
+      if ((unsigned)p.x >= (unsigned)c.n_pages || (j + 16 < any && (unsigned)p.y >= (unsigned)c.n_pages)) {
+        if (a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
+        if ((unsigned)p.x >= (unsigned)c.n_pages) p.x = 0;
+        if (j + 16 < any && (unsigned)p.y >= (unsigned)c.n_pages) p.y = 0;
+      }
     }
+    return p;
+  };
+  auto copy = [&](uint32_t dst, const unsigned char* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  };
+  auto issue = [&](int u, int st, int2 p) {
+    if (p.x >= 0) {
+      constexpr int NI = HD / 64;  // pieces of 16 keys
+      const int r0 = (u * kUnit) & in_page, r1 = (u * kUnit + 16) & in_page;
+      const uint32_t d = dst0 + st * SB;
+      const unsigned char *k0 = kc0 + p.x * c.kc_step + r0 * (HD / 2), *v0 = vc0 + p.x * c.vc_step + r0 * (HD / 2);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) copy(d + i * 512, k0 + i * 512);
+#pragma unroll
+      for (int i = 0; i < NI; ++i) copy(d + kUnit * HD / 2 + i * 512, v0 + i * 512);
+      if (p.y >= 0) {
+        k0 = kc0 + p.y * c.kc_step + r1 * (HD / 2);
+        v0 = vc0 + p.y * c.vc_step + r1 * (HD / 2);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) copy(d + (NI + i) * 512, k0 + i * 512);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) copy(d + kUnit * HD / 2 + (NI + i) * 512, v0 + i * 512);
+      }
+      const int ps = lane & 4 ? p.y : p.x;
+      if (lane < 16 && ps >= 0) copy(dst_sc + st * SB, sc0 + ps * sc_step + (lane & 4 ? r1 : r0) * 4);
+    }
+    cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < NST; ++i)
-    if (first + i * W < units) issue(first + i * W, i, page_of(first + i * W));
+  for (int i = 0; i < NST - 1; ++i) issue(u0 + warp + i * kWarps, i, pages_of(u0 + warp + i * kWarps));
+  int2 next = pages_of(u0 + warp + (NST - 1) * kWarps);
 
   // B operands of q: this lane has row g of each tile, dims 32 t (16 t) and on
   uint32_t qb[NT][2 * KW][2];
@@ -198,6 +267,7 @@ __global__ void __launch_bounds__(kThreads, 3)
 
   float o[NT][HD / 16][4], o8[NT][4];  // sums over codes: dims (rows) g and g + 8 of a tile, query rows 2 t, 2 t + 1
   float m[NT][2], M[NT][2], l[NT][2], z[NT][2];
+  float base[NT][2], rel[NT][2];  // what scores are taken from, pivot(m); 2^(m - M): takes a weight times a step below 2^8
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -206,55 +276,53 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       m[nt][r] = M[nt][r] = -INFINITY;
-      l[nt][r] = z[nt][r] = 0.f;
+      l[nt][r] = z[nt][r] = base[nt][r] = rel[nt][r] = 0.f;
     }
   }
   // Key of a tile's row g: neighbours swapped in every second pair, so that the
   // loads of k (rows g, lanes t) and of v (rows 2 t, 2 t + 1, lanes g) both
   // spread over the banks.
   const int kg = g ^ ((g >> 1) & 1), ka = (2 * t) ^ (t & 1), kb = ka ^ 1;
-  int st = 0, ph = 0, stop = units;
-  bool ok = true;
-  int next = first + NST * W < units ? page_of(first + NST * W) : 0;  // page of the unit to be copied next
-  // After a wait that gave up nothing is copied or computed any more; the
-  // copies already in flight are still waited for (`stop`).
-  for (int u = first; u < stop; u += W) {
-    const bool got = mbar_wait_lazy(&full[warp][st], ph, kWaitNs);
-    if (!__all_sync(0xffffffffu, got) && ok) {
-      ok = false;
-      stop = min(units, u + NST * W);
-      if (lane == 0 && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
-    }
-    if (ok) {
+  bool force = true;  // a row has no maximum yet
+  int st = 0, st_in = NST - 1;
+  for (int u = u0 + warp; u < units; u += kWarps) {
+    cp_wait_stages();
+    __syncwarp();  // everybody's copies have landed, and everybody is done with the stage before
+    issue(u + (NST - 1) * kWarps, st_in, next);
+    next = pages_of(u + NST * kWarps);
+    st_in = st;
+    {
       const unsigned char* sk = ring + st * SB;
       const unsigned char* sv = sk + kUnit * HD / 2;
       const uint32_t* sm = reinterpret_cast<const uint32_t*>(sk + kUnit * HD);
       const int j0 = u * kUnit;
       const bool cut = j0 + kUnit > every;
-      float s[2][NT][4], tv[2][NT][4], vm8[2][2];  // scores; plus log2 of v's step; v's m + 8 s of keys g, g + 8
+      // scores from `base` on, weights, weights times v's steps; of keys g, g + 8:
+      // v's step and m + 8 s
+      float s[2][NT][4], w[2][NT][4], ws_[2][NT][4], vs[2][2], vm8[2][2];
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        uint32_t w[2][KW];
+        uint32_t x[2][KW];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const unsigned char* src = sk + (q * 16 + h * 8 + kg) * (HD / 2) + t * (HD / 8);
           if constexpr (HD == 128) {
-            const uint4 x = *reinterpret_cast<const uint4*>(src);
-            w[h][0] = x.x;
-            w[h][1] = x.y;
-            w[h][2] = x.z;
-            w[h][3] = x.w;
+            const uint4 v = *reinterpret_cast<const uint4*>(src);
+            x[h][0] = v.x;
+            x[h][1] = v.y;
+            x[h][2] = v.z;
+            x[h][3] = v.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(src);
-            w[h][0] = x.x;
-            w[h][1] = x.y;
+            const uint2 v = *reinterpret_cast<const uint2*>(src);
+            x[h][0] = v.x;
+            x[h][1] = v.y;
           }
         }
         float acc[NT][4] = {};
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
-          const uint32_t x0 = w[0][i] >> 8, x1 = w[1][i] >> 8;
-          const uint32_t lo[4] = {w[0][i] & kLow, w[1][i] & kLow, w[0][i] & kHigh, w[1][i] & kHigh};
+          const uint32_t x0 = x[0][i] >> 8, x1 = x[1][i] >> 8;
+          const uint32_t lo[4] = {x[0][i] & kLow, x[1][i] & kLow, x[0][i] & kHigh, x[1][i] & kHigh};
           const uint32_t hi[4] = {x0 & kLow, x1 & kLow, x0 & kHigh, x1 & kHigh};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -266,55 +334,75 @@ __global__ void __launch_bounds__(kThreads, 3)
         for (int h = 0; h < 2; ++h) {
           const int key = q * 16 + h * 8 + kg;
           const float2 km = unpack2<F16>(sm[key]), vm = unpack2<F16>(sm[kUnit + key]);
-          const float lv = lg2(vm.x);
+          vs[q][h] = vm.x;
           vm8[q][h] = fmaf(8.f, vm.x, vm.y);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-              const float x = fmaf(acc[nt][2 * h + r] * mul[nt][r], km.x, km.y * qsum[nt][r]);
-              s[q][nt][2 * h + r] = x;
-              tv[q][nt][2 * h + r] = x + lv;
-            }
+            for (int r = 0; r < 2; ++r)
+              s[q][nt][2 * h + r] = fmaf(acc[nt][2 * h + r] * mul[nt][r], km.x, fmaf(km.y, qsum[nt][r], -base[nt][r]));
         }
       }
       if (cut) {
+        asm volatile("");  // (a branch: as selects it cost every unit 16 of them)
 #pragma unroll
         for (int q = 0; q < 2; ++q)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (j0 + q * 16 + (e >> 1) * 8 + kg >= end[nt][e & 1]) s[q][nt][e] = tv[q][nt][e] = -INFINITY;
+              if (j0 + q * 16 + (e >> 1) * 8 + kg >= end[nt][e & 1]) s[q][nt][e] = -INFINITY;
       }
-      float x[NT][2], y[NT][2];
-      bool up = false;
+      float most = 0.f;
+      auto weigh = [&] {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          x[nt][r] = fmaxf(fmaxf(s[0][nt][r], s[0][nt][2 + r]), fmaxf(s[1][nt][r], s[1][nt][2 + r]));
-          y[nt][r] = fmaxf(fmaxf(tv[0][nt][r], tv[0][nt][2 + r]), fmaxf(tv[1][nt][r], tv[1][nt][2 + r]));
-          up = up || x[nt][r] > m[nt][r] + kLazy || y[nt][r] > M[nt][r] + kLazy;
-        }
-      if (__any_sync(0xffffffffu, up)) {
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              w[q][nt][e] = ex2(s[q][nt][e]);
+              ws_[q][nt][e] = w[q][nt][e] * rel[nt][e & 1] * vs[q][e >> 1];  // (in this order nothing overflows that the result holds)
+              most = fmaxf(most, fmaxf(w[q][nt][e], ws_[q][nt][e]));
+            }
+      };
+      weigh();
+      if (__any_sync(0xffffffffu, most > kMost) || force) {
+        // (seldom) new maxima of the rows, of weights and of weights times steps
+        force = false;
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float fo[2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
+            float x = -INFINITY, y = -INFINITY;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                x = fmaxf(x, s[q][nt][2 * h + r]);
+                y = fmaxf(y, s[q][nt][2 * h + r] + log2f(fabsf(vs[q][h])));
+              }
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
-              x[nt][r] = fmaxf(x[nt][r], __shfl_xor_sync(0xffffffffu, x[nt][r], d));
-              y[nt][r] = fmaxf(y[nt][r], __shfl_xor_sync(0xffffffffu, y[nt][r], d));
+              x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, d));
+              y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
             }
-            const float mn = fmaxf(m[nt][r], x[nt][r]), Mn = fmaxf(M[nt][r], y[nt][r]);
-            const float f = ex2(m[nt][r] - pivot(mn));
-            fo[r] = ex2(M[nt][r] - pivot(Mn));
-            m[nt][r] = mn;
-            M[nt][r] = Mn;
+            const float mn = fmaxf(m[nt][r], x + base[nt][r]), to = mn == -INFINITY ? 0.f : mn, f = ex2(m[nt][r] - to);
+            float Mn = fmaxf(M[nt][r], y + base[nt][r]);
+            if (Mn != -INFINITY) Mn = fmaxf(Mn, to - 100.f);  // (2^-100 of the largest weight: as good as nothing)
+            fo[r] = M[nt][r] == -INFINITY ? 0.f : ex2(M[nt][r] - Mn);
             l[nt][r] *= f;
             z[nt][r] *= f;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+              for (int h = 0; h < 2; ++h) s[q][nt][2 * h + r] += base[nt][r] - to;
+            m[nt][r] = mn;
+            M[nt][r] = Mn;
+            base[nt][r] = to;
+            rel[nt][r] = Mn == -INFINITY ? 0.f : ex2(to - Mn);
+            force = force || mn == -INFINITY;
           }
 #pragma unroll
           for (int i = 0; i < HD / 16; ++i)
@@ -323,23 +411,38 @@ __global__ void __launch_bounds__(kThreads, 3)
 #pragma unroll
           for (int e = 0; e < 4; ++e) o8[nt][e] *= fo[e & 1];
         }
+        force = __any_sync(0xffffffffu, force);
+        weigh();
+      }
+      if (cut) {  // a key that a row does not see may hold anything
+        asm volatile("");
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const bool see = j0 + q * 16 + (e >> 1) * 8 + kg < end[nt][e & 1];
+              if (see) z[nt][e & 1] = fmaf(w[q][nt][e], vm8[q][e >> 1], z[nt][e & 1]);
+              if (!see) ws_[q][nt][e] = 0.f;
+            }
+      } else {
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) z[nt][e & 1] = fmaf(w[q][nt][e], vm8[q][e >> 1], z[nt][e & 1]);
       }
       uint32_t p[2][NT][2];  // B operands: weights times steps
 #pragma unroll
       for (int q = 0; q < 2; ++q)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          float e[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float w = ex2(s[q][nt][i] - pivot(m[nt][i & 1]));
-            l[nt][i & 1] += w;
-            // (a key that a row does not see may hold anything)
-            z[nt][i & 1] = fmaf(w, cut && s[q][nt][i] == -INFINITY ? 0.f : vm8[q][i >> 1], z[nt][i & 1]);
-            e[i] = ex2(tv[q][nt][i] - pivot(M[nt][i & 1]));
-          }
-          p[q][nt][0] = transposed(pack2<true>(e[0], e[1]));
-          p[q][nt][1] = transposed(pack2<true>(e[2], e[3]));
+          for (int e = 0; e < 4; ++e) l[nt][e & 1] += w[q][nt][e];
+          p[q][nt][0] = transposed(pack2<true>(ws_[q][nt][0], ws_[q][nt][1]));
+          p[q][nt][1] = transposed(pack2<true>(ws_[q][nt][2], ws_[q][nt][3]));
         }
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
@@ -373,15 +476,7 @@ __global__ void __launch_bounds__(kThreads, 3)
           mma_f16(o8[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, p[q][nt][0], p[q][nt][1]);
       }
     }
-    __syncwarp();
-    if (ok && u + NST * W < units) {
-      issue(u + NST * W, st, next);
-      if (u + (NST + 1) * W < units) next = page_of(u + (NST + 1) * W);
-    }
-    if (++st == NST) {
-      st = 0;
-      ph ^= 1;
-    }
+    if (++st == NST) st = 0;
   }
 
   // The warps' states meet in shared memory (each in its own ring, drained):
@@ -397,8 +492,7 @@ __global__ void __launch_bounds__(kThreads, 3)
         l[nt][r] += __shfl_xor_sync(0xffffffffu, l[nt][r], d);
         z[nt][r] += __shfl_xor_sync(0xffffffffu, z[nt][r], d);
       }
-      if (!ok) l[nt][r] = NAN;  // a copy did not arrive (reported): no result
-      const float f = M[nt][r] == -INFINITY ? 0.f : ex2(M[nt][r] - m[nt][r] + 20.f);
+      const float f = rel[nt][r] == 0.f ? 0.f : 1048576.f / rel[nt][r];  // 2^20 2^(M - m)
       const int row = nt * 8 + 2 * t + r;
 #pragma unroll
       for (int i = 0; i < HD / 16; ++i) {
@@ -411,8 +505,10 @@ __global__ void __launch_bounds__(kThreads, 3)
       }
     }
   __syncthreads();
-  // the CTA's state per row, in warp 0's ring: one row a warp, lane has dims 2 lane + 64 i
-  auto weight = [](float x, float top) { return x == -INFINITY ? 0.f : ex2(x - top); };
+  // The tile's rows, one a warp, lane with dims 2 lane + 64 i: finished here if
+  // all of its units were, else a part.
+  const bool whole = u0 == 0 && u1 == ld.units;
+  float* const part = ws.part + ((long long)blockIdx.x * 2 + !head_part) * kPartFloats<HD, R>;
   for (int r = warp; r < nrow; r += kWarps) {
     float top = -INFINITY, sum = 0.f;
     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
@@ -421,8 +517,8 @@ __global__ void __launch_bounds__(kThreads, 3)
     for (int i = 0; i < HD / 64; ++i) acc[i] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = weight(s_m[w][r], top);
-      // a state without keys has sum 0 (NaN only after a failed wait, or of NaN scores: kept)
+      const float f = s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - top);
+      // a state without keys has sum 0 (NaN of NaN scores: kept)
       sum += s_m[w][r] == -INFINITY ? s_l[w][r] : f * s_l[w][r];
       const float* src = reinterpret_cast<const float*>(smem + w * NST * SB) + r * HD + 2 * lane;
       if (f != 0.f) {
@@ -434,63 +530,136 @@ __global__ void __launch_bounds__(kThreads, 3)
         }
       }
     }
-    __syncwarp();
+    const int i = row0 + r, tq = sh.by_rep.quot(i);
+    const long long n = sp.first + tq, h = hk * rep + i - tq * rep;
+    if (whole) {
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      uint16_t* o = static_cast<uint16_t*>(a.out) + n * a.os[0] + h * a.os[1] + 2 * lane;
 #pragma unroll
-    for (int i = 0; i < HD / 64; ++i) *reinterpret_cast<float2*>(reinterpret_cast<float*>(smem) + r * HD + 2 * lane + 64 * i) = acc[i];
-    if (lane == 0) {
-      c_m[r] = top;
-      c_l[r] = sum;
+      for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<uint32_t*>(o + 64 * e) = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
+      if (lane == 0 && a.lse) a.lse[n * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    } else {
+#pragma unroll
+      for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<float2*>(part + r * HD + 2 * lane + 64 * e) = acc[e];
+      if (lane == 0) {
+        part[R * HD + r] = top;
+        part[R * HD + R + r] = sum;
+      }
+    }
+    if (u0 == 0 && lane == 0) {  // (the CTA of unit x is that of the largest i with i all / ctas <= x)
+      const long long last = at + ld.units - 1;
+      const int end_cta = whole ? blockIdx.x : (int)(((last + 1) * ctas - 1) / all);
+      ws.where[n * a.Hq + h] = make_int2(blockIdx.x, (end_cta - (int)blockIdx.x) << 6 | !head_part << 5 | r);
     }
   }
-  if (sh.split > 1)
-    cluster_barrier();
-  else
-    __syncthreads();
-  for (int r = part * kWarps + warp; r < nrow; r += W) {
-    const int i = row0 + r, tq = sh.by_rep.quot(i), h = hk * rep + i - tq * rep;
-    float cm = -INFINITY, cl = 0.f;
-    if (lane < sh.split) {
-      cm = cluster_ld(cluster_addr(&c_m[r], lane));
-      cl = cluster_ld(cluster_addr(&c_l[r], lane));
+  at += u1 - u0;
+  if (at >= stop_at) break;
+  // the next tile: of this sequence, or of the next with any
+  u0 = 0;
+  if (++item == ld.tiles * a.Hkv) {
+    item = 0;
+    do ld = seq_load(a, cap, rep, R, ++b);
+    while (ld.tiles == 0 || ld.units == 0);
+  }
+  __syncthreads();  // (the rings are free)
+  }
+}
+
+// A CTA a row and query head: its parts, a warp every fourth; rows without a key.
+template <int HD, bool F16, int R>
+__global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ PackedArgs a, Kv4Ws ws, FastDiv by_heads) {
+  __shared__ float s_m[4], s_l[4], s_o[4][HD];
+  const int n = by_heads.quot(blockIdx.x), h = blockIdx.x - n * a.Hq;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int b = seq_of_row(a, n, lane);
+  pdl_wait();  // (everybody: what follows on the stream may take the first kernel as complete, too)
+  if (b < 0) return;
+  const Span sp = seq_span(a, b, false);
+  if (n - sp.first >= sp.n) return;
+  uint16_t* out = static_cast<uint16_t*>(a.out) + n * a.os[0] + h * a.os[1] + 2 * lane;
+  if (__ldg(a.kv_len + b) <= 0) {
+    if (warp == 0) {
+#pragma unroll
+      for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<uint32_t*>(out + 64 * e) = 0u;
+      if (lane == 0 && a.lse) a.lse[(long long)n * a.Hq + h] = -INFINITY;
     }
-    const float top = warp_max(cm), f = weight(cm, top), sum = warp_sum(cm == -INFINITY ? cl : f * cl);
-    float2 acc[HD / 64];
+    return;
+  }
+  const int2 where = ws.where[(long long)n * a.Hq + h];
+  const int parts = (where.y >> 6) + 1, r = where.y & 31;
+  if (parts == 1) return;
+  auto at = [&](int i) { return ws.part + ((long long)(where.x + i) * 2 + (i == 0 ? where.y >> 5 & 1 : 0)) * kPartFloats<HD, R>; };
+  float top = -INFINITY, sum = 0.f;
+  float2 acc[HD / 64];
 #pragma unroll
-    for (int i2 = 0; i2 < HD / 64; ++i2) acc[i2] = make_float2(0.f, 0.f);
-    const uint32_t own = smem_u32(reinterpret_cast<float*>(smem) + r * HD + 2 * lane);
-    for (int c0 = 0; c0 < sh.split; c0 += 4) {  // four CTAs' loads in flight together
-      float2 v[4][HD / 64];
+  for (int e = 0; e < HD / 64; ++e) acc[e] = make_float2(0.f, 0.f);
+  for (int i0 = warp; i0 < parts; i0 += 16) {  // four parts' loads in flight together
+    float m[4], l[4];
+    float2 v[4][HD / 64];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const uint32_t src = cluster_map(own, min(c0 + q, sh.split - 1));
+    for (int q = 0; q < 4; ++q) {
+      const int i = min(i0 + 4 * q, parts - 1);
+      const float* p = at(i);
+      m[q] = i0 + 4 * q < parts ? p[R * HD + r] : -INFINITY;
+      l[q] = i0 + 4 * q < parts ? p[R * HD + R + r] : 0.f;
 #pragma unroll
-        for (int i2 = 0; i2 < HD / 64; ++i2) v[q][i2] = cluster_ld2(src + 256 * i2);
-      }
+      for (int e = 0; e < HD / 64; ++e) v[q][e] = *reinterpret_cast<const float2*>(p + r * HD + 2 * lane + 64 * e);
+    }
+    const float mx = fmaxf(fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])), top);
+    const float f0 = top == -INFINITY ? 0.f : ex2(top - mx);
+    sum *= top == -INFINITY ? 1.f : f0;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const float fq = __shfl_sync(0xffffffffu, f, (c0 + q) & 31);
-        if (c0 + q >= sh.split || fq == 0.f) continue;
+    for (int e = 0; e < HD / 64; ++e) {
+      acc[e].x *= f0;
+      acc[e].y *= f0;
+    }
+    top = mx;
 #pragma unroll
-        for (int i2 = 0; i2 < HD / 64; ++i2) {
-          acc[i2].x += fq * v[q][i2].x;
-          acc[i2].y += fq * v[q][i2].y;
+    for (int q = 0; q < 4; ++q) {
+      const float f = m[q] == -INFINITY ? 0.f : ex2(m[q] - top);
+      sum += m[q] == -INFINITY ? l[q] : f * l[q];
+      if (f != 0.f) {
+#pragma unroll
+        for (int e = 0; e < HD / 64; ++e) {
+          acc[e].x += f * v[q][e].x;
+          acc[e].y += f * v[q][e].y;
         }
       }
     }
-    // (sum NaN: of a visible key's NaN, or a failed wait)
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    const long long at = (long long)(sp.first + tq) * a.os[0] + (long long)h * a.os[1] + 2 * lane;
-#pragma unroll
-    for (int i2 = 0; i2 < HD / 64; ++i2)
-      *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at + 64 * i2) = pack2<F16>(acc[i2].x * inv, acc[i2].y * inv);
-    if (lane == 0 && a.lse)
-      a.lse[(long long)(sp.first + tq) * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
   }
-  if (sh.split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
+#pragma unroll
+  for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<float2*>(&s_o[warp][2 * lane + 64 * e]) = acc[e];
+  if (lane == 0) {
+    s_m[warp] = top;
+    s_l[warp] = sum;
+  }
+  __syncthreads();
+  if (warp != 0) return;
+  top = fmaxf(fmaxf(s_m[0], s_m[1]), fmaxf(s_m[2], s_m[3]));
+  sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < HD / 64; ++e) acc[e] = make_float2(0.f, 0.f);
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    const float f = s_m[w] == -INFINITY ? 0.f : ex2(s_m[w] - top);
+    sum += s_m[w] == -INFINITY ? s_l[w] : f * s_l[w];
+    if (f != 0.f) {
+#pragma unroll
+      for (int e = 0; e < HD / 64; ++e) {
+        const float2 v = *reinterpret_cast<const float2*>(&s_o[w][2 * lane + 64 * e]);
+        acc[e].x += f * v.x;
+        acc[e].y += f * v.y;
+      }
+    }
+  }
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+  for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<uint32_t*>(out + 64 * e) = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
+  if (lane == 0 && a.lse) a.lse[(long long)n * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 template <int HD, bool F16, int NT>
-cudaError_t launch(const PackedArgs& p, const Kv4Args& c, cudaStream_t s) {
+cudaError_t launch(const PackedArgs& p, const Kv4Args& c, void* d_ws, cudaStream_t s) {
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = device_sm_count(dev, &sms);
@@ -502,53 +671,70 @@ cudaError_t launch(const PackedArgs& p, const Kv4Args& c, cudaStream_t s) {
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
       e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<HD>);
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
   }
-  const int rep = p.Hq / p.Hkv, most = p.start ? p.max_rows : 1;
-  const long long each = ((long long)most * rep + 8 * NT - 1) / (8 * NT);
-  const long long tiles = p.start ? min(each * p.B, (long long)p.N * rep / (8 * NT) + p.B) : each * p.B;
-  const long long items = tiles * p.Hkv;
+  Kv4Ws ws;
+  ws.where = static_cast<int2*>(d_ws);
+  ws.part = static_cast<float*>(d_ws) + 2ll * p.N * p.Hq;
+  // no more CTAs than units there can be
   const long long units = (((long long)c.width << c.page_log) + kUnit - 1) / kUnit;
-  int split = (int)max(1ll, min(min(4ll * 3 * sms / items, (units + kWarps - 1) / kWarps), (long long)kMaxSplit));
-  if (const char* x = getenv("RL_SPLIT")) split = atoi(x);
-  if (each >= 1ll << 31 || items * split >= 1ll << 31) return cudaErrorInvalidValue;
+  const long long tiles = ((long long)(p.start ? min((long long)p.max_rows * p.B, (long long)p.N) : p.B) * (p.Hq / p.Hkv) + 8 * NT - 1) / (8 * NT) + p.B;
+  const int grid = (int)min((long long)min(kMaxCtas / NT, kResident<NT> * sms), (tiles * p.Hkv * units + kLeast - 1) / kLeast);
+  kern<<<grid, kThreads, kSmem<HD>, s>>>(p, c, Kv4Shape{FastDiv(p.Hkv), FastDiv(p.Hq / p.Hkv)}, ws);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(items * split));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem<HD>;
+  cfg.gridDim = dim3((unsigned)p.N * p.Hq);
+  cfg.blockDim = dim3(128);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = split;
-  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  const Kv4Shape sh{split, (int)each, FastDiv(split), FastDiv(p.Hkv), FastDiv(rep), FastDiv((int)each)};
-  return cudaLaunchKernelEx(&cfg, kern, p, c, sh);
+  return cudaLaunchKernelEx(&cfg, k_kv4_join<HD, F16, 8 * NT>, p, ws, FastDiv(p.Hq));
 }
 
+// One tile of 8 rows, or two to an operand of codes: with more than 8 rows of a
+// KV head a sequence (that share its keys) the second saves reading them again.
+int row_tiles(const PackedArgs& p) { return (long long)(p.start ? p.max_rows : 1) * (p.Hq / p.Hkv) <= 8 ? 1 : 2; }
+
 template <int HD, bool F16>
-cudaError_t launch_rows(const PackedArgs& p, const Kv4Args& c, cudaStream_t s) {
-  const long long rows = (long long)(p.start ? p.max_rows : 1) * (p.Hq / p.Hkv);
-  return rows <= 8 ? launch<HD, F16, 1>(p, c, s) : launch<HD, F16, 2>(p, c, s);
+cudaError_t launch_rows(const PackedArgs& p, const Kv4Args& c, void* ws, cudaStream_t s) {
+  return row_tiles(p) == 1 ? launch<HD, F16, 1>(p, c, ws, s) : launch<HD, F16, 2>(p, c, ws, s);
 }
 
 }  // namespace
 
-cudaError_t launch_kv4_attention(const PackedArgs& p, const Kv4Args& c, cudaStream_t s) {
-  if (p.hd == 64) return p.f16 ? launch_rows<64, true>(p, c, s) : launch_rows<64, false>(p, c, s);
-  return p.f16 ? launch_rows<128, true>(p, c, s) : launch_rows<128, false>(p, c, s);
+size_t kv4_attention_ws_bytes(const PackedArgs& p) {
+  // (half the CTAs with tiles of twice the rows: the same)
+  return 8ull * p.N * p.Hq + 2ull * kMaxCtas * 8 * (p.hd + 2) * sizeof(float);
+}
+
+cudaError_t launch_kv4_attention(const PackedArgs& p, const Kv4Args& c, void* ws, cudaStream_t s) {
+  if (p.hd == 64) return p.f16 ? launch_rows<64, true>(p, c, ws, s) : launch_rows<64, false>(p, c, ws, s);
+  return p.f16 ? launch_rows<128, true>(p, c, ws, s) : launch_rows<128, false>(p, c, ws, s);
 }
 
 }  // namespace river
 
 using namespace river;
 
+extern "C" rl_status rl_kv4_attention_workspace(const rl_packed_desc* p, uint64_t* bytes) {
+  const char* who = "rl_kv4_attention_workspace";
+  PackedArgs a;
+  const rl_status st = check_packed(who, p, kUsesQ, kUsesOut, &a);
+  if (st != RL_OK) return st;
+  if (!bytes) return op_error(who, RL_ERR_INVALID_ARG, "bytes is NULL");
+  *bytes = kv4_attention_ws_bytes(a);
+  return RL_OK;
+}
+
 extern "C" rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, const int32_t* d_start, const int32_t* d_kv_len,
-                                      const void* d_q, void* d_out, float* d_lse, int32_t* d_err, rl_stream_t stream) {
+                                      const void* d_q, void* d_out, float* d_lse, void* d_ws, uint64_t ws_bytes, int32_t* d_err,
+                                      rl_stream_t stream) {
   const char* who = "rl_kv4_attention";
   PackedArgs a;
   Kv4Args k;
@@ -557,14 +743,16 @@ extern "C" rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, 
   if (st != RL_OK) return st;
   if (!d_kv_len || !d_q || !d_out || d_out == d_q) return op_error(who, RL_ERR_INVALID_ARG, "NULL argument, or out in q's place");
   if (!d_start && p->rows != p->batch) return op_error(who, RL_ERR_INVALID_ARG, "rows must be batch without d_start");
-  if (!op_aligned16(d_q) || !op_aligned16(d_out)) return op_error(who, RL_ERR_UNSUPPORTED, "q and out must start on 16-byte boundaries");
+  if (!op_aligned16(d_q) || !op_aligned16(d_out) || !op_aligned16(d_ws))
+    return op_error(who, RL_ERR_UNSUPPORTED, "q, out and the workspace must start on 16-byte boundaries");
+  if (!d_ws || ws_bytes < kv4_attention_ws_bytes(a)) return op_error(who, RL_ERR_INVALID_ARG, "workspace NULL or too small");
   a.q = d_q;
   a.out = d_out;
   a.lse = d_lse;
   a.start = d_start;
   a.kv_len = d_kv_len;
   a.err = d_err;
-  const cudaError_t e = launch_kv4_attention(a, k, static_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_kv4_attention(a, k, d_ws, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error(RL_ERR_CUDA, cudaGetErrorString(e));
   return RL_OK;
 }

@@ -651,11 +651,18 @@ RL_API rl_status rl_kv4_read(const rl_kv4* c, const rl_packed_desc* p, const int
  * length outside [0, table_width * page] sets RL_DEVERR_CAPACITY and is
  * clamped; rows past max_rows of a sequence set it and are left as they were.
  * Positions from d_kv_len[b] on have no part in any result, whatever their
- * pages hold.  Sums and statistics are fp32.  One launch, no workspace, results
- * repeat bit for bit.  d_start NULL: one row each (rows == batch). */
+ * pages hold.  Scores, sums and statistics are fp32; q is scaled by a power
+ * of two a row and rounded to fp16 (exact but for what is 2^-37 below the row's
+ * largest), weights times v's steps are rounded to fp16.  Two launches, results
+ * repeat bit for bit.  d_start NULL: one row each (rows == batch).
+ *   d_ws  workspace of rl_kv4_attention_workspace bytes (16-byte aligned), in use
+ *         until the call's work on the stream is done: calls that may overlap
+ *         need one each
+ * RL_ERR_INVALID_ARG also for a workspace too small. */
+RL_API rl_status rl_kv4_attention_workspace(const rl_packed_desc* p, uint64_t* bytes);
 RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, const int32_t* d_start,
                                   const int32_t* d_kv_len, const void* d_q, void* d_out, float* d_lse,
-                                  int32_t* d_err, rl_stream_t stream);
+                                  void* d_ws, uint64_t ws_bytes, int32_t* d_err, rl_stream_t stream);
 
 /* rl_sample: one token a row of logits, from a given random number.  With
  * w_i = exp((x_i - max x) / temperature) the ids are ordered by logit, largest

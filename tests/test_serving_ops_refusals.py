@@ -37,7 +37,7 @@ def _cache(river, **kw):
 
 def _call(river, name, **kw):
     a = dict(q=A + 20480, k=A + 24576, v=A + 28672, out=A + 32768, start=A + 36864, kv_len=A + 40960, rope=A + 45056, rope_len=9, ro=A + 49152,
-             cache=True, desc=True)
+             cache=True, desc=True, ws=A + 53248, ws_bytes=1 << 40)
     a.update({k: v for k, v in kw.items() if k in a})
     d, c = _packed(river, **kw), _cache(river, **kw)
     pd, pc = (ctypes.byref(d) if a["desc"] else None), (ctypes.byref(c) if a["cache"] else None)
@@ -48,7 +48,8 @@ def _call(river, name, **kw):
                                         P(a["out"]), None, None)
     if name == "read":
         return river._lib.rl_kv4_read(pc, pd, P(a["start"]), P(a["kv_len"]), P(a["k"]), P(a["v"]), None, None)
-    return river._lib.rl_kv4_attention(pc, pd, P(a["start"]), P(a["kv_len"]), P(a["q"]), P(a["out"]), None, None, None)
+    return river._lib.rl_kv4_attention(pc, pd, P(a["start"]), P(a["kv_len"]), P(a["q"]), P(a["out"]), None,
+                                       P(a["ws"]), a["ws_bytes"], None, None)
 
 
 ALL = ("packed", "append", "read", "attention")
@@ -92,6 +93,7 @@ def test_cache(river, name, kw, status):
     ("read", dict(k=None), "INVALID_ARG"), ("read", dict(v=A + 24576), "INVALID_ARG"), ("read", dict(k_stride=(64, 64)), "INVALID_ARG"),
     ("read", dict(v=A + 4), "UNSUPPORTED"),
     ("attention", dict(q=None), "INVALID_ARG"), ("attention", dict(out=None), "INVALID_ARG"), ("attention", dict(out=A + 20480), "INVALID_ARG"),
+    ("attention", dict(ws=None), "INVALID_ARG"), ("attention", dict(ws_bytes=1000), "INVALID_ARG"), ("attention", dict(ws=A + 8), "UNSUPPORTED"),
     ("attention", dict(q=A + 8), "UNSUPPORTED"), ("attention", dict(out_stride=(0, 64)), "INVALID_ARG")])
 def test_operands(river, name, kw, status):
     assert _call(river, name, **kw) == getattr(river, "RL_ERR_" + status), river.rl_last_error()

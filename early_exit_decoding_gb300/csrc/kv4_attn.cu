@@ -49,6 +49,9 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;       // keys a warp takes at a time
 constexpr int kStages = 3;      // units of a warp's ring
 constexpr int kLeast = 4;       // units a CTA takes at least
+// Units that a tile's start and end are worth in sharing out (64 sequences of 130
+// to 8191 positions: 99 us with 0, 84 with 4, 81 with 8, 77 with 12, 78 with 20).
+constexpr int kStart = 12;
 constexpr int kMaxCtas = 608;   // four on each of 152 SMs; the workspace holds that many CTAs' parts
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMost = 256.f;  // a weight, or weight times step, that is let pass (1 where it was the largest)
@@ -82,7 +85,9 @@ __device__ __forceinline__ uint32_t transposed(uint32_t a) {
   return d;
 }
 
-// Row tiles and units of a tile of sequence b (0 behind the last sequence).
+// Row tiles of sequence b and the units of each (0 behind the last sequence).
+// In sharing out a tile counts kStart more, in front: what its start and end
+// take (short contexts else keep their CTAs longest).
 struct Load {
   int tiles, units;
 };
@@ -116,12 +121,12 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   long long all = 0;
   for (int b0 = 0; b0 < a.B; b0 += 32) {
     const Load x = seq_load(a, cap, rep, R, b0 + lane);
-    all += (long long)x.tiles * x.units;
+    all += x.units ? (long long)x.tiles * (x.units + kStart) : 0;
   }
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
   all *= a.Hkv;
-  const long long ctas = max(1ll, min((long long)gridDim.x, (all + kLeast - 1) / kLeast));
+  const long long ctas = max(1ll, min((long long)gridDim.x, all / (kStart + kLeast)));
   long long at = all * blockIdx.x / ctas;
   const long long stop_at = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : 0;
   if (at >= stop_at) return;
@@ -132,7 +137,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
     long long before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
       const Load x = seq_load(a, cap, rep, R, b0 + lane);
-      const long long mine = (long long)x.tiles * x.units * a.Hkv;
+      const long long mine = x.units ? (long long)x.tiles * (x.units + kStart) * a.Hkv : 0;
       long long sum = mine;  // of this lane's sequence and those in front
 #pragma unroll
       for (int d = 1; d < 32; d <<= 1) {
@@ -146,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
         ld.tiles = __shfl_sync(0xffffffffu, x.tiles, who);
         ld.units = __shfl_sync(0xffffffffu, x.units, who);
         const long long rest = at - before - __shfl_sync(0xffffffffu, sum - mine, who);
-        item = (int)(rest / ld.units);
-        u0 = (int)(rest - (long long)item * ld.units);
+        item = (int)(rest / (ld.units + kStart));
+        u0 = (int)(rest - (long long)item * (ld.units + kStart)) - kStart;
         break;
       }
       before += __shfl_sync(0xffffffffu, sum, 31);
@@ -156,6 +161,9 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   unsigned char* const ring = smem + warp * NST * SB;
   for (bool head_part = true;; head_part = false) {
   const int u1 = (int)min((long long)ld.units, u0 + (stop_at - at));
+  if (u1 <= 0) break;  // (the share ends before the tile's first unit)
+  at -= min(u0, 0);
+  u0 = max(u0, 0);
   const int tile = sh.by_heads.quot(item), hk = item - tile * sh.by_heads.d, row0 = tile * R;
   const Span sp = seq_span(a, b, false);
   const int old = max(0, min(__ldg(a.kv_len + b), cap)) - sp.all;  // position of the sequence's first row here
@@ -166,23 +174,21 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
 
   // this lane's 16-byte pieces of a unit: of k's and v's codes every 512 bytes,
   // and (lanes 0-15) one of the scales
-  const long long head0 = page_row(c, hk, 0);
-  const unsigned char *const kc0 = c.kc + head0 * (HD / 2) + lane * 16, *const vc0 = c.vc + head0 * (HD / 2) + lane * 16;
+  const int head0 = hk << c.page_log;  // the head's first row in a page
   const bool v_scales = lane & 8;
   const unsigned char* const sc0 = reinterpret_cast<const unsigned char*>((v_scales ? c.vm : c.km) + head0) + (lane & 3) * 16;
   const long long sc_step = 4 * (v_scales ? c.vm_step : c.km_step);
-  const uint32_t dst0 = smem_u32(ring) + lane * 16, dst_sc = smem_u32(ring) + kUnit * HD + (lane & 15) * 16;
-  auto pages_of = [&](int u) {  // of a unit's first and last 16 keys (-1: nobody sees them)
+  const uint32_t dst0 = smem_u32(ring) + lane * 16;
+  auto pages_of = [&](int u) {  // of a unit's first and last 16 keys (that nobody may see: then the first's)
     const int j = u * kUnit, *row = c.table + (long long)b * c.table_step;
-    int2 p = make_int2(-1, -1);
+    int2 p = make_int2(0, 0);
     if (u < units) {
       p.x = __ldg(row + (j >> c.page_log));
-      if (j + 16 < any) p.y = __ldg(row + ((j + 16) >> c.page_log));
-      // (out of the cache: reported, page 0 is read)
-      if ((unsigned)p.x >= (unsigned)c.n_pages || (j + 16 < any && (unsigned)p.y >= (unsigned)c.n_pages)) {
+      p.y = __ldg(row + ((j + (j + 16 < any ? 16 : 0)) >> c.page_log));
+      if (max((unsigned)p.x, (unsigned)p.y) >= (unsigned)c.n_pages) {  // out of the cache: reported, page 0 is read
         if (a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
         if ((unsigned)p.x >= (unsigned)c.n_pages) p.x = 0;
-        if (j + 16 < any && (unsigned)p.y >= (unsigned)c.n_pages) p.y = 0;
+        if ((unsigned)p.y >= (unsigned)c.n_pages) p.y = 0;
       }
     }
     return p;
@@ -191,25 +197,21 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   };
   auto issue = [&](int u, int st, int2 p) {
-    if (p.x >= 0) {
+    if (u < units) {
       constexpr int NI = HD / 64;  // pieces of 16 keys
       const int r0 = (u * kUnit) & in_page, r1 = (u * kUnit + 16) & in_page;
+      const int o0 = (head0 + r0) * (HD / 2) + lane * 16, o1 = (head0 + r1) * (HD / 2) + lane * 16;
       const uint32_t d = dst0 + st * SB;
-      const unsigned char *k0 = kc0 + p.x * c.kc_step + r0 * (HD / 2), *v0 = vc0 + p.x * c.vc_step + r0 * (HD / 2);
+      const unsigned char *k0 = c.kc + p.x * c.kc_step + o0, *k1 = c.kc + p.y * c.kc_step + o1;
+      const unsigned char *v0 = c.vc + p.x * c.vc_step + o0, *v1 = c.vc + p.y * c.vc_step + o1;
 #pragma unroll
-      for (int i = 0; i < NI; ++i) copy(d + i * 512, k0 + i * 512);
-#pragma unroll
-      for (int i = 0; i < NI; ++i) copy(d + kUnit * HD / 2 + i * 512, v0 + i * 512);
-      if (p.y >= 0) {
-        k0 = kc0 + p.y * c.kc_step + r1 * (HD / 2);
-        v0 = vc0 + p.y * c.vc_step + r1 * (HD / 2);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) copy(d + (NI + i) * 512, k0 + i * 512);
-#pragma unroll
-        for (int i = 0; i < NI; ++i) copy(d + kUnit * HD / 2 + (NI + i) * 512, v0 + i * 512);
+      for (int i = 0; i < NI; ++i) {
+        copy(d + i * 512, k0 + i * 512);
+        copy(d + (NI + i) * 512, k1 + i * 512);
+        copy(d + kUnit * HD / 2 + i * 512, v0 + i * 512);
+        copy(d + kUnit * HD / 2 + (NI + i) * 512, v1 + i * 512);
       }
-      const int ps = lane & 4 ? p.y : p.x;
-      if (lane < 16 && ps >= 0) copy(dst_sc + st * SB, sc0 + ps * sc_step + (lane & 4 ? r1 : r0) * 4);
+      if (lane < 16) copy(d + kUnit * HD, sc0 + (lane & 4 ? p.y : p.x) * sc_step + (lane & 4 ? r1 : r0) * 4);
     }
     cp_commit();
   };
@@ -220,7 +222,6 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   // B operands of q: this lane has row g of each tile, dims 32 t (16 t) and on
   uint32_t qb[NT][2 * KW][2];
   float mul[NT][2], qsum[NT][2];  // of the rows 2 t and 2 t + 1: scores are acc mul s + qsum m
-  int end[NT][2];                 // and the keys they see
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
     const int i = row0 + nt * 8 + g, tq = sh.by_rep.quot(i);
@@ -261,12 +262,12 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
     for (int r = 0; r < 2; ++r) {
       mul[nt][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
       qsum[nt][r] = __shfl_sync(0xffffffffu, sum * sc, (2 * t + r) * 4);
-      end[nt][r] = old + sh.by_rep.quot(row0 + nt * 8 + 2 * t + r) + 1;
     }
   }
 
+  auto end_of = [&](int nt, int r) { return old + sh.by_rep.quot(row0 + nt * 8 + 2 * t + r) + 1; };  // keys a row sees
   float o[NT][HD / 16][4], o8[NT][4];  // sums over codes: dims (rows) g and g + 8 of a tile, query rows 2 t, 2 t + 1
-  float m[NT][2], M[NT][2], l[NT][2], z[NT][2];
+  float m[NT][2], l[NT][2], z[NT][2];
   float base[NT][2], rel[NT][2];  // what scores are taken from, pivot(m); 2^(m - M): takes a weight times a step below 2^8
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
@@ -275,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
     o8[nt][0] = o8[nt][1] = o8[nt][2] = o8[nt][3] = 0.f;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      m[nt][r] = M[nt][r] = -INFINITY;
+      m[nt][r] = -INFINITY;
       l[nt][r] = z[nt][r] = base[nt][r] = rel[nt][r] = 0.f;
     }
   }
@@ -351,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-              if (j0 + q * 16 + (e >> 1) * 8 + kg >= end[nt][e & 1]) s[q][nt][e] = -INFINITY;
+              if (j0 + q * 16 + (e >> 1) * 8 + kg >= end_of(nt, e & 1)) s[q][nt][e] = -INFINITY;
       }
       float most = 0.f;
       auto weigh = [&] {
@@ -389,9 +390,10 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
               y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, d));
             }
             const float mn = fmaxf(m[nt][r], x + base[nt][r]), to = mn == -INFINITY ? 0.f : mn, f = ex2(m[nt][r] - to);
-            float Mn = fmaxf(M[nt][r], y + base[nt][r]);
+            const float M = rel[nt][r] == 0.f ? -INFINITY : base[nt][r] - log2f(rel[nt][r]);
+            float Mn = fmaxf(M, y + base[nt][r]);
             if (Mn != -INFINITY) Mn = fmaxf(Mn, to - 100.f);  // (2^-100 of the largest weight: as good as nothing)
-            fo[r] = M[nt][r] == -INFINITY ? 0.f : ex2(M[nt][r] - Mn);
+            fo[r] = M == -INFINITY ? 0.f : ex2(M - Mn);
             l[nt][r] *= f;
             z[nt][r] *= f;
 #pragma unroll
@@ -399,7 +401,6 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
 #pragma unroll
               for (int h = 0; h < 2; ++h) s[q][nt][2 * h + r] += base[nt][r] - to;
             m[nt][r] = mn;
-            M[nt][r] = Mn;
             base[nt][r] = to;
             rel[nt][r] = Mn == -INFINITY ? 0.f : ex2(to - Mn);
             force = force || mn == -INFINITY;
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const bool see = j0 + q * 16 + (e >> 1) * 8 + kg < end[nt][e & 1];
+              const bool see = j0 + q * 16 + (e >> 1) * 8 + kg < end_of(nt, e & 1);
               if (see) z[nt][e & 1] = fmaf(w[q][nt][e], vm8[q][e >> 1], z[nt][e & 1]);
               if (!see) ws_[q][nt][e] = 0.f;
             }
@@ -555,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   at += u1 - u0;
   if (at >= stop_at) break;
   // the next tile: of this sequence, or of the next with any
-  u0 = 0;
+  u0 = -kStart;
   if (++item == ld.tiles * a.Hkv) {
     item = 0;
     do ld = seq_load(a, cap, rep, R, ++b);

@@ -4,20 +4,30 @@
 // The ids ordered by (logit, lower id) are kept up to some last one, so what the
 // three filters keep is a key: ids whose 64-bit key (ordered logit, then the
 // lower id) is at least `cut`.  top-k's cut is the k-th largest key, top-p's the
-// key at which the weights' running sum reaches top_p of their total, both
-// found a digit of the key at a time (a histogram of the ids that agree in the
-// digits before: counts, or weights); min-p's is a logit.  The token is then
-// found among the ids of at least `cut` by running sums in the order of ids.
+// key at which the weights' running sum reaches top_p of their total; min-p's is
+// a logit.  The token is then found among the ids of at least `cut` by running
+// sums in the order of ids.
 //
 // A weight is a 64-bit whole number, exp((x - max) / T) 2^44 rounded: sums are
 // exact whatever their order, and with exponentials good to 2^-38 a token
 // differs from that of exact weights only where u is that near a border (fp32
 // sums: 1 in 50 rows of 128,256 logits with a long tail).
 //
-// Simplest form: one CTA a row, which reads the row once a step.
+// A row is read once: a cluster of CTAs holds it in shared memory, each a part
+// whose warps have contiguous segments.  A cut is found a digit of 9 bits at a
+// time from a histogram of the ids that agree in the digits before (counts, or
+// weights in three limbs of 17 bits that a part's sums do not overflow); the
+// digits are those of -log2 of the weight first, in fixed point (even bins where
+// weights matter), then of the logit's bits and of the id, until no more than
+// kList ids are left, which are ordered one against another.  A small top-k
+// needs no histogram of the row: bins of the threads' largest logits give a
+// bound that at least k ids reach and few others, and one CTA finishes with
+// those alone.
 #include <float.h>
 #include <math.h>
 #include <stdio.h>
+
+#include <mutex>
 
 #include "dev_common.cuh"
 #include "internal.h"
@@ -40,8 +50,12 @@ namespace {
 using namespace dev;
 using u64 = unsigned long long;
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kMaxSplit = 16;    // CTAs of a row's cluster
+constexpr int kBins = kThreads;  // of a digit (9 bits), one a thread
+constexpr int kList = 128;       // ids that are ordered one against another
+constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
 
 __device__ __forceinline__ uint32_t order_bits(float x) {
   const uint32_t u = x != x ? 0x7fffffffu : __float_as_uint(x + 0.f);
@@ -88,172 +102,493 @@ __device__ __forceinline__ u64 warp_sum64(u64 v) {
   for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
 }
-
-template <typename T>
-__device__ __forceinline__ float load_at(const void* x, long long i);
-template <>
-__device__ __forceinline__ float load_at<float>(const void* x, long long i) {
-  return __ldg(static_cast<const float*>(x) + i);
-}
-template <>
-__device__ __forceinline__ float load_at<bf16>(const void* x, long long i) {
-  return __bfloat162float(static_cast<const bf16*>(x)[i]);
-}
-template <>
-__device__ __forceinline__ float load_at<__half>(const void* x, long long i) {
-  return __half2float(static_cast<const __half*>(x)[i]);
+__device__ __forceinline__ u64 warp_scan64(u64 v, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += t;
+  }
+  return v;
 }
 
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ u64 remote64(const u64* p, int rank) {
+  u64 v;
+  asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t remote32(const uint32_t* p, int rank) {
+  uint32_t v;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(remote(p, rank)) : "memory");
+  return v;
+}
+
+struct List {
+  uint32_t n;
+  u64 key[kList];
+};
 struct Shared {
-  u64 red[kWarps];
-  u64 hist[2048];
-  u64 before;
-  int bin;
+  uint64_t full;            // the row's copies
   u64 table[64];
+  uint32_t hist[2][4][kBins];  // by a digit's parity: counts, weights' limbs
+  List list[2];             // this part's ids that are ordered one against another: for top-k, for top-p
+  u64 key[kList], wt[kList];   // the cluster's, and their weights
+  int n_key;
+  u64 red[kWarps], sums[kWarps];
+  u64 best, mass;           // this part's
+  u64 before;               // in front of the digit's bin
+  u64 cut;
+  uint32_t count;           // ids of the bin
+  int bin;
 };
 
-__device__ u64 block_sum(Shared& s, u64 v) {
-  v = warp_sum64(v);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 t = 0;
-  for (int i = 0; i < kWarps; ++i) t += s.red[i];
-  return t;
+// The place of an id in the order: (~fixed-point -log2 of its weight, ordered
+// logit, ~id), as digits of 9 bits from the largest down.
+struct Place {
+  uint32_t q, o, i;
+};
+constexpr int kLevels = 11;
+__device__ __forceinline__ uint32_t field_of(const Place& p, int level) { return level < 4 ? p.q : level < 8 ? p.o : p.i; }
+__device__ __forceinline__ int shift_of(int level) {  // of the field: 23, 14, 5, 0 (20 bits of ~id: 11, 2, 0)
+  const int l = level & 3;
+  return level < 8 ? (l == 0 ? 23 : l == 1 ? 14 : l == 2 ? 5 : 0) : (l == 0 ? 11 : l == 1 ? 2 : 0);
 }
-__device__ u64 block_max(Shared& s, u64 v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v = max(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) s.red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  u64 t = 0;
-  for (int i = 0; i < kWarps; ++i) t = max(t, s.red[i]);
-  return t;
-}
+__device__ __forceinline__ int bits_of(int level) { return level < 8 ? ((level & 3) == 3 ? 5 : 9) : level == 10 ? 2 : 9; }
 
-// The largest key at which the running sum of `value` (keys from the largest
-// down, those of at least `least`) reaches `goal`.
-template <typename T, typename Value>
-__device__ u64 find_cut(Shared& s, const void* x, long long at, int V, u64 least, u64 goal, Value value) {
-  u64 prefix = 0;
-  int shift = 64;
-  u64 before = 0;
-  while (shift > 0) {
-    const int bits = shift >= 11 ? 11 : shift, next = shift - bits;
-    for (int i = threadIdx.x; i < 2048; i += kThreads) s.hist[i] = 0;
-    __syncthreads();
-    for (int i = threadIdx.x; i < V; i += kThreads) {
-      const float f = load_at<T>(x, at + i);
-      const u64 k = key_of(f, i);
-      if (k < least || (shift < 64 && (k >> shift) != (prefix >> shift))) continue;
-      const u64 v = value(f);
-      if (v) atomicAdd(&s.hist[(k >> next) & ((1 << bits) - 1)], v);
+template <typename T>
+struct Row {
+  const SampleArgs& a;
+  Shared& s;
+  const T* x;          // this part's logits, in shared memory
+  int first, n;        // their ids
+  int i0, i1;          // this warp's segment of them
+  int split, part, tid, lane, warp;
+  float m;
+  Weight w;
+
+  __device__ __forceinline__ float at(int i) const { return to_float(x[i]); }
+  __device__ __forceinline__ Place place(float v, int i) const {
+    const float y = (m - v) * w.ch;
+    const uint32_t p = y >= 0.f ? __float2uint_rz(y * 67108864.f) : 0xffffffffu;  // 2^26; saturates (NaN: 0 times infinity)
+    return Place{~p, order_bits(v), 0xfffffu - (uint32_t)(first + i)};
+  }
+  __device__ __forceinline__ u64 key(float v, int i) const { return key_of(v, first + i); }
+
+  __device__ __forceinline__ void barrier() const {
+    if (split > 1)
+      cluster_barrier();
+    else
+      __syncthreads();
+  }
+  // Lists of all parts into s.key (a barrier after they were filled).
+  __device__ void collect(const List& l) {
+    int at = 0;
+    for (int r = 0; r < split; ++r) {
+      const int k = min((int)remote32(&l.n, r), kList - at);
+      if (tid < k) s.key[at + tid] = remote64(&l.key[tid], r);
+      at += k;
     }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      u64 run = before;
-      int b = (1 << bits) - 1;
-      while (b > 0 && run + s.hist[b] < goal) run += s.hist[b--];
-      s.bin = b;
-      s.before = run;
-    }
-    __syncthreads();
-    before = s.before;
-    prefix |= (u64)s.bin << next;
-    shift = next;
+    if (tid == 0) s.n_key = at;
     __syncthreads();
   }
-  return prefix;
+  __device__ __forceinline__ void push(List& l, u64 k) {
+    const uint32_t at = atomicAdd(&l.n, 1u);
+    if (at < kList) l.key[at] = k;
+  }
+
+  // The largest key at which the running sum (keys of at least `least`, from the
+  // largest down) of counts, or weights (MASS), reaches the goal; goal_of(total)
+  // gives it from the sum of all.
+  template <bool MASS, typename Goal>
+  __device__ u64 find_cut(u64 least, Goal goal_of) {
+    Place want{0, 0, 0}, mask{0, 0, 0};
+    u64 before = 0, goal = 0;
+    List& list = s.list[MASS];
+    for (int level = 0; level < kLevels; ++level) {
+      const int shift = shift_of(level), bits = bits_of(level);
+      uint32_t(*h)[kBins] = s.hist[level & 1];
+#pragma unroll
+      for (int j = 0; j < (MASS ? 4 : 1); ++j) h[j][tid] = 0;
+      __syncthreads();
+      for (int i = i0 + lane; i < i1; i += 32) {
+        const float v = at(i);
+        if (key(v, i) < least) continue;
+        const Place p = place(v, i);
+        if (((p.q ^ want.q) & mask.q) | ((p.o ^ want.o) & mask.o) | ((p.i ^ want.i) & mask.i)) continue;
+        const uint32_t bin = (field_of(p, level) >> shift) & ((1u << bits) - 1);
+        if constexpr (MASS) {
+          const u64 k = w(v);
+          if (k == 0) continue;
+          atomicAdd(&h[0][bin], 1u);
+          atomicAdd(&h[1][bin], (uint32_t)k & 0x1ffffu);
+          if (k >> 17) atomicAdd(&h[2][bin], (uint32_t)(k >> 17) & 0x1ffffu);
+          if (k >> 34) atomicAdd(&h[3][bin], (uint32_t)(k >> 34));
+        } else {
+          atomicAdd(&h[0][bin], 1u);
+        }
+      }
+      barrier();
+      const int bin = kBins - 1 - tid;
+      u64 sum = 0;
+      uint32_t count = 0;
+      for (int r = 0; r < split; ++r) {
+        const uint32_t k = remote32(&h[0][bin], r);
+        count += k;
+        if constexpr (MASS)
+          sum += remote32(&h[1][bin], r) + ((u64)remote32(&h[2][bin], r) << 17) + ((u64)remote32(&h[3][bin], r) << 34);
+        else
+          sum += k;
+      }
+      // the bin that reaches the goal
+      const u64 inc = warp_scan64(sum, lane);
+      if (lane == 31) s.red[warp] = inc;
+      __syncthreads();
+      u64 front = before, total = before;
+      for (int k = 0; k < kWarps; ++k) {
+        if (k < warp) front += s.red[k];
+        total += s.red[k];
+      }
+      if (level == 0) goal = goal_of(total);
+      if (front + inc - sum < goal && goal <= front + inc) {
+        s.bin = bin;
+        s.before = front + inc - sum;
+        s.count = count;
+      }
+      __syncthreads();
+      before = s.before;
+      const uint32_t digit = (uint32_t)s.bin << shift, dm = ((1u << bits) - 1) << shift;
+      if (level < 4) {
+        want.q |= digit;
+        mask.q |= dm;
+      } else if (level < 8) {
+        want.o |= digit;
+        mask.o |= dm;
+      } else {
+        want.i |= digit;
+        mask.i |= dm;
+      }
+      if (s.count <= kList) break;
+    }
+    // the ids left, one against another
+    for (int i = i0 + lane; i < i1; i += 32) {
+      const float v = at(i);
+      const u64 k = key(v, i);
+      if (k < least) continue;
+      const Place p = place(v, i);
+      if (!(((p.q ^ want.q) & mask.q) | ((p.o ^ want.o) & mask.o) | ((p.i ^ want.i) & mask.i))) {
+        if (!MASS || w(v)) push(list, k);
+      }
+    }
+    barrier();
+    collect(list);
+    const int n = s.n_key;
+    u64 k = 0, v = 0;
+    if (tid < n) {
+      k = s.key[tid];
+      v = MASS ? w(value_of((uint32_t)(k >> 32))) : 1;
+      s.wt[tid] = v;
+    }
+    __syncthreads();
+    if (tid < n) {
+      u64 front = before;
+      for (int j = 0; j < n; ++j)
+        if (s.key[j] > k) front += s.wt[j];
+      if (front < goal && goal <= front + v) s.cut = k;
+    }
+    __syncthreads();
+    return s.cut;
+  }
+};
+
+// floor(u S) and top_p S rounded up, of u and top_p in [0, 1).
+__device__ __forceinline__ u64 share(float u, u64 S) { return __umul64hi((u64)((double)u * 18446744073709551616.0), S); }
+__device__ __forceinline__ u64 share_up(float p, u64 S) {
+  const u64 f = (u64)(fmax((double)p, 0.0) * 18446744073709551616.0);
+  return max(1ull, __umul64hi(f, S) + (f * S != 0));
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) k_sample(const __grid_constant__ SampleArgs a, const __grid_constant__ Pow2Table pow2) {
+__global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a, const __grid_constant__ Pow2Table pow2, int split) {
+  extern __shared__ __align__(16) unsigned char smem_row[];
   __shared__ Shared s;
-  const int row = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
-  const long long at = (long long)row * a.ld;
-  if (tid < 64) s.table[tid] = pow2.t[tid];
-  u64 best = 0;
-  for (int i = tid; i < V; i += kThreads) best = max(best, key_of(load_at<T>(a.x, at + i), i));
-  best = block_max(s, best);
-  const float m = value_of((uint32_t)(best >> 32));
-  const float temp = a.set.d_temperature ? a.set.d_temperature[row] : a.set.temperature;
-  const int first = (int)(0xffffffffu - (uint32_t)best);
-  if (!(fabsf(m) < INFINITY) || !(temp > 0.f)) {
-    if (tid == 0) {
-      a.token[row] = first;
-      if (a.logprob) a.logprob[row] = fabsf(m) < INFINITY ? 0.f : NAN;
-    }
-    return;
+  const int row = blockIdx.x / split, part = blockIdx.x - row * split;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
+
+  // This part's ids, to shared memory at the address modulo 16 that they have:
+  // whole 16 bytes by bulk copies, the edges by threads.
+  const int v0 = (int)((long long)V * part / split), v1 = (int)((long long)V * (part + 1) / split);
+  const T* src = static_cast<const T*>(a.x) + (long long)row * a.ld + v0;
+  const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15), n = v1 - v0;
+  T* const dst = reinterpret_cast<T*>(smem_row + off);
+  const int head = min(n, off ? (int)((16 - off) / sizeof(T)) : 0);
+  const int whole = (int)((n - head) * sizeof(T) / 16) * 16;  // bytes
+  if (tid == 0) {
+    mbar_init(&s.full, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    mbar_expect_tx(&s.full, whole);
+    for (int b = 0; b < whole; b += 16384)
+      bulk_g2s(smem_row + off + head * sizeof(T) + b, reinterpret_cast<const unsigned char*>(src + head) + b, min(16384, whole - b), &s.full);
   }
+  const int tail = head + whole / (int)sizeof(T);
+  if (tid < head) dst[tid] = src[tid];
+  if (tid >= 32 && tail + tid - 32 < n) dst[tail + tid - 32] = src[tail + tid - 32];
+  if (tid < 64) s.table[tid] = pow2.t[tid];
+  if (tid < 2) s.list[tid].n = 0;
+  const float temp = a.set.d_temperature ? a.set.d_temperature[row] : a.set.temperature;
   const int k = a.set.d_top_k ? a.set.d_top_k[row] : a.set.top_k;
   const float tp = a.set.d_top_p ? a.set.d_top_p[row] : a.set.top_p, mp = a.set.d_min_p ? a.set.d_min_p[row] : a.set.min_p;
-  const double c = fmin(1.4426950408889634 / (double)temp, 1e38);  // (finite in fp32)
-  Weight w{m, (float)c, (float)(c - (double)(float)c), s.table};
-  u64 cut = 0;
-  if (k >= 1 && k < V) cut = find_cut<T>(s, a.x, at, V, 0, (u64)k, [](float) -> u64 { return 1; });
-  if (tp < 1.f) {
-    u64 sum = 0;
-    for (int i = tid; i < V; i += kThreads) {
-      const float f = load_at<T>(a.x, at + i);
-      if (key_of(f, i) >= cut) sum += w(f);
+  const float u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604644775390625e-8f);
+  __syncthreads();
+  const bool got = __syncthreads_and(mbar_wait_lazy(&s.full, 0, kWaitNs)) != 0;
+  if (!got && tid == 0 && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
+
+  const int seg = (n + kWarps - 1) / kWarps;
+  Row<T> r{a, s, dst, v0, n, min(n, warp * seg), min(n, (warp + 1) * seg), split, part, tid, lane, warp, 0.f, Weight{}};
+  // the largest logit (the lowest id of equal ones)
+  uint32_t top = 0;
+  int top_i = 0;
+  for (int i = r.i0 + lane; i < r.i1; i += 32) {
+    const uint32_t o = order_bits(r.at(i));
+    if (o > top) {
+      top = o;
+      top_i = i;
     }
-    sum = block_sum(s, sum);
-    // top_p S, rounded up
-    const u64 p64 = (u64)(fmax((double)tp, 0.0) * 18446744073709551616.0);
-    const u64 goal = max(1ull, __umul64hi(p64, sum) + (p64 * sum != 0));
-    cut = max(cut, find_cut<T>(s, a.x, at, V, cut, goal, w));
   }
+  u64 best = top ? ((u64)top << 32) | (0xffffffffu - (uint32_t)(v0 + top_i)) : 0;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
+  if (lane == 0) s.red[warp] = best;
+  __syncthreads();
+  for (int j = 0; j < kWarps; ++j) best = max(best, s.red[j]);
+  if (split > 1) {
+    if (tid == 0) s.best = best;
+    cluster_barrier();
+    for (int j = 0; j < split; ++j) best = max(best, remote64(&s.best, j));
+  }
+  const float m = value_of((uint32_t)(best >> 32));
+  if (!got || !(fabsf(m) < INFINITY) || !(temp > 0.f)) {
+    if (part == 0 && tid == 0) {
+      a.token[row] = (int)(0xffffffffu - (uint32_t)best);
+      if (a.logprob) a.logprob[row] = got && fabsf(m) < INFINITY ? 0.f : NAN;
+    }
+    if (split > 1) cluster_barrier();
+    return;
+  }
+  const double c = fmin(1.4426950408889634 / (double)temp, 1e38);  // (finite in fp32)
+  r.m = m;
+  r.w = Weight{m, (float)c, (float)(c - (double)(float)c), s.table};
+  float least = -INFINITY;  // min-p's
   if (mp > 0.f) {
     const double b = (double)m + (double)temp * log((double)mp);
-    float f = (float)b;
-    if ((double)f < b) f = nextafterf(f, INFINITY);
-    cut = max(cut, (u64)order_bits(f) << 32);
+    least = (float)b;
+    if ((double)least < b) least = nextafterf(least, INFINITY);
   }
+  const bool has_k = k >= 1 && k < V;
+
+  if (has_k && k <= kList / 2) {
+    // Few ids: a bin of -log2 of the weight such that k threads' largest logits
+    // reach it; the ids that do are no fewer.
+    uint32_t* h = s.hist[0][0];
+    h[tid] = 0;
+    __syncthreads();
+    const Place mine = r.place(value_of(top), 0);
+    if (top) atomicAdd(&h[mine.q >> 23], 1u);
+    r.barrier();
+    const int bin = kBins - 1 - tid;
+    uint32_t count = 0;
+    for (int j = 0; j < split; ++j) count += remote32(&h[bin], j);
+    const u64 inc = warp_scan64(count, lane);
+    __syncthreads();
+    if (lane == 31) s.red[warp] = inc;
+    if (tid == 0) s.bin = 0;  // (fewer than k threads have one: all ids)
+    __syncthreads();
+    u64 front = 0;
+    for (int j = 0; j < warp; ++j) front += s.red[j];
+    if (front + inc - count < (u64)k && (u64)k <= front + inc) s.bin = bin;
+    __syncthreads();
+    const uint32_t from = (uint32_t)s.bin;
+    if (top && mine.q >> 23 >= from)
+      for (int i = r.i0 + lane; i < r.i1; i += 32) {
+        const float v = r.at(i);
+        if (r.place(v, i).q >> 23 >= from) r.push(s.list[0], r.key(v, i));
+      }
+    r.barrier();
+    uint32_t all = 0;
+    for (int j = 0; j < split; ++j) all += remote32(&s.list[0].n, j);
+    if (all <= kList) {
+      if (part == 0) {
+        r.collect(s.list[0]);
+        const int cnt = s.n_key;
+        u64 key = 0, v = 0;
+        float x = 0.f;
+        int rank = 0;
+        if (tid < cnt) {
+          key = s.key[tid];
+          x = value_of((uint32_t)(key >> 32));
+          for (int j = 0; j < cnt; ++j) rank += s.key[j] > key;
+          v = rank < k ? r.w(x) : 0;
+          s.wt[tid] = v;
+        }
+        __syncthreads();
+        bool keep = tid < cnt && rank < k && (rank == 0 || x >= least);
+        u64 sum = 0, front_w = 0;
+        if (tid < cnt) {
+          for (int j = 0; j < cnt; ++j) {
+            sum += s.wt[j];
+            if (s.key[j] > key) front_w += s.wt[j];
+          }
+          if (tp < 1.f && rank > 0) keep = keep && front_w < share_up(tp, sum);
+        }
+        __syncthreads();
+        if (tid < cnt) s.wt[tid] = keep ? v : 0;
+        __syncthreads();
+        if (tid < cnt) {
+          const uint32_t id = (uint32_t)key;  // (~id)
+          u64 total = 0, upto = 0;
+          for (int j = 0; j < cnt; ++j) {
+            total += s.wt[j];
+            if ((uint32_t)s.key[j] > id) upto += s.wt[j];
+          }
+          const u64 goal = share(u, total);
+          if (keep && upto <= goal && goal < upto + v) {
+            a.token[row] = (int)(0xffffffffu - id);
+            if (a.logprob) a.logprob[row] = logf((float)v / (float)total);
+          }
+        }
+      }
+      if (split > 1) cluster_barrier();
+      return;
+    }
+    r.barrier();
+    if (tid == 0) s.list[0].n = 0;
+    __syncthreads();
+  }
+
+  u64 cut = 0;
+  if (has_k) cut = r.template find_cut<false>(0, [&](u64) { return (u64)k; });
+  if (tp < 1.f) cut = max(cut, r.template find_cut<true>(cut, [&](u64 S) { return share_up(tp, S); }));
+  if (mp > 0.f) cut = max(cut, (u64)order_bits(least) << 32);
   cut = min(cut, best);
-  // the weights of each warp's share, of the warps in front, and of all
-  const int per = (V + kWarps - 1) / kWarps, i0 = min(V, warp * per), i1 = min(V, i0 + per);
+  // the weights of each warp's segment, of those in front, and of all
   u64 sum = 0;
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const float f = load_at<T>(a.x, at + i);
-    if (key_of(f, i) >= cut) sum += w(f);
+  for (int i = r.i0 + lane; i < r.i1; i += 32) {
+    const float v = r.at(i);
+    if (r.key(v, i) >= cut) sum += r.w(v);
   }
   sum = warp_sum64(sum);
+  if (lane == 0) s.sums[warp] = sum;
   __syncthreads();
-  if (lane == 0) s.red[warp] = sum;
-  __syncthreads();
-  u64 all = 0, before = 0;
-  for (int i = 0; i < kWarps; ++i) {
-    if (i < warp) before += s.red[i];
-    all += s.red[i];
-  }
-  const float u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604644775390625e-8f);
-  const u64 goal = __umul64hi((u64)((double)u * 18446744073709551616.0), all);
-  if (before <= goal && goal < before + sum) {
-    u64 run = before;
-    for (int i = i0; i < i1; i += 32) {
-      u64 v = 0;
-      if (i + lane < i1) {
-        const float f = load_at<T>(a.x, at + i + lane);
-        if (key_of(f, i + lane) >= cut) v = w(f);
-      }
-      u64 inc = v;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const u64 t = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += t;
-      }
-      const unsigned hit = __ballot_sync(0xffffffffu, run + inc > goal);
-      if (hit) {
-        if (lane == __ffs(hit) - 1) {
-          a.token[row] = i + lane;
-          if (a.logprob) a.logprob[row] = logf((float)v / (float)all);
-        }
-        break;
-      }
-      run += __shfl_sync(0xffffffffu, inc, 31);
+  u64 here = 0;
+  for (int j = 0; j < kWarps; ++j) here += s.sums[j];
+  u64 front = 0, all = here;
+  if (split > 1) {
+    if (tid == 0) s.mass = here;
+    cluster_barrier();
+    all = 0;
+    for (int j = 0; j < split; ++j) {
+      const u64 x = remote64(&s.mass, j);
+      if (j < part) front += x;
+      all += x;
     }
   }
+  const u64 goal = share(u, all);
+  if (front <= goal && goal < front + here) {
+    // the segment it is in, then the sixteenth of that, then the id
+    int ow = 0;
+    while (front + s.sums[ow] <= goal) front += s.sums[ow++];
+    const int s0 = min(n, ow * seg), s1 = min(n, s0 + seg), sub = (s1 - s0 + kWarps - 1) / kWarps;
+    auto range = [&](int j, int* b, int* e) {
+      *b = min(s1, s0 + j * sub);
+      *e = min(s1, *b + sub);
+    };
+    int b, e;
+    range(warp, &b, &e);
+    sum = 0;
+    for (int i = b + lane; i < e; i += 32) {
+      const float v = r.at(i);
+      if (r.key(v, i) >= cut) sum += r.w(v);
+    }
+    sum = warp_sum64(sum);
+    if (lane == 0) s.red[warp] = sum;
+    __syncthreads();
+    int os = 0;
+    while (front + s.red[os] <= goal) front += s.red[os++];
+    if (warp == 0) {
+      range(os, &b, &e);
+      for (int i = b; i < e; i += 32) {
+        u64 x = 0;
+        if (i + lane < e) {
+          const float v = r.at(i + lane);
+          if (r.key(v, i + lane) >= cut) x = r.w(v);
+        }
+        const u64 inc = warp_scan64(x, lane);
+        const unsigned hit = __ballot_sync(0xffffffffu, front + inc > goal);
+        if (hit) {
+          if (lane == __ffs(hit) - 1) {
+            a.token[row] = v0 + i + lane;
+            if (a.logprob) a.logprob[row] = logf((float)x / (float)all);
+          }
+          break;
+        }
+        front += __shfl_sync(0xffffffffu, inc, 31);
+      }
+    }
+  }
+  if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
+}
+
+// CTAs a row is split over: as many as bring a part to 64 KB (so that two or
+// three of them share an SM), more where the rows alone do not fill the GPU.
+int pick_split(int rows, int V, int size, int sms) {
+  int s = 1;
+  while (s < kMaxSplit && ((long long)V * size > 65536ll * s || ((long long)rows * s * 2 <= sms && V > 4096 * s))) s *= 2;
+  return s;
+}
+
+template <typename T>
+cudaError_t launch(const SampleArgs& a, const Pow2Table& table, cudaStream_t st) {
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = device_sm_count(dev, &sms);
+  if (e != cudaSuccess) return e;
+  auto kern = k_sample<T>;
+  constexpr int kMost = (1 << 19) / kMaxSplit * 4 + 64;
+  {
+    static std::mutex mu;
+    static bool done[kOpDevices] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+      if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+  }
+  const int split = pick_split(a.rows, a.V, sizeof(T), sms);
+  if ((long long)a.rows * split >= 1ll << 31) return cudaErrorInvalidValue;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)a.rows * split);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (a.V / split + 1) * sizeof(T) + 32;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = split;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a, table, split);
 }
 
 }  // namespace
@@ -264,13 +599,9 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
     for (int j = 0; j < 64; ++j) t.t[j] = (u64)llrint(exp2(44.0 - j / 64.0));
     return t;
   }();
-  if (a.dtype == RL_DT_F32)
-    k_sample<float><<<a.rows, kThreads, 0, s>>>(a, table);
-  else if (a.dtype == RL_DT_BF16)
-    k_sample<bf16><<<a.rows, kThreads, 0, s>>>(a, table);
-  else
-    k_sample<__half><<<a.rows, kThreads, 0, s>>>(a, table);
-  return cudaGetLastError();
+  if (a.dtype == RL_DT_F32) return launch<float>(a, table, s);
+  if (a.dtype == RL_DT_BF16) return launch<bf16>(a, table, s);
+  return launch<__half>(a, table, s);
 }
 
 }  // namespace river

@@ -28,6 +28,7 @@
 #include <stdio.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "dev_common.cuh"
 #include "internal.h"
@@ -89,10 +90,10 @@ struct Weight {
     const float lh = 0.693147182464599609375f, ll = -1.904654323148236017e-9f;  // ln 2 in two parts
     const float ah = r * lh, al = fmaf(e, lh, fmaf(r, ll, fmaf(r, lh, -ah)));
     const float v = fmaf(-ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al);  // 1 - 2^-r = ah + v
-    const long long w = (long long)__float2int_rn(ah * 274877906944.f) + __float2int_rn(v * 274877906944.f);  // 2^38
+    const int w = __float2int_rn(ah * 274877906944.f) + __float2int_rn(v * 274877906944.f);  // 2^38 (below 2^31)
     const u64 t = table[k & 63];
     const int n = k >> 6;
-    const u64 f = t - (u64)(((long long)(t >> 13) * w) >> 25);
+    const u64 f = t - (u64)(((long long)(int)(t >> 14) * w) >> 24);
     return (f + ((1ull << n) >> 1)) >> n;
   }
 };
@@ -111,9 +112,15 @@ __device__ __forceinline__ u64 warp_scan64(u64 v, int lane) {
   return v;
 }
 
-__device__ __forceinline__ float to_float(float x) { return x; }
-__device__ __forceinline__ float to_float(bf16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
+template <typename T>
+__device__ __forceinline__ T of_float(float x) {
+  if constexpr (sizeof(T) == 4)
+    return x;
+  else if constexpr (std::is_same<T, bf16>::value)
+    return __float2bfloat16(x);
+  else
+    return __float2half(x);
+}
 
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -166,25 +173,69 @@ __device__ __forceinline__ int shift_of(int level) {  // of the field: 23, 14, 5
 }
 __device__ __forceinline__ int bits_of(int level) { return level < 8 ? ((level & 3) == 3 ? 5 : 9) : level == 10 ? 2 : 9; }
 
+// A key that parts ids: those of a larger logit, or of its own and no higher id.
+struct Cut {
+  float v;
+  uint32_t id;
+  __device__ __forceinline__ bool takes(float x, int i) const { return x > v || (x == v && (uint32_t)i <= id); }
+};
+__device__ __forceinline__ Cut cut_of(u64 key) {  // 0: takes every id
+  return Cut{key ? value_of((uint32_t)(key >> 32)) : -INFINITY, 0xffffffffu - (uint32_t)key};
+}
+
+// 16 bytes of logits.
+template <typename T>
+struct Vec {
+  static constexpr int kN = 16 / sizeof(T);
+  float v[kN];
+  __device__ __forceinline__ explicit Vec(const uint4& x) {
+#pragma unroll
+    for (int e = 0; e < kN; ++e) {
+      if constexpr (sizeof(T) == 4) {
+        v[e] = __uint_as_float(u4get(x, e));
+      } else {
+        const uint32_t h = u4get(x, e >> 1);
+        if constexpr (std::is_same<T, bf16>::value)
+          v[e] = __uint_as_float(e & 1 ? h & 0xffff0000u : h << 16);
+        else
+          v[e] = __half2float(__ushort_as_half((unsigned short)(e & 1 ? h >> 16 : h & 0xffffu)));
+      }
+    }
+  }
+};
+
 template <typename T>
 struct Row {
-  const SampleArgs& a;
+  static constexpr int VE = Vec<T>::kN;
   Shared& s;
-  const T* x;          // this part's logits, in shared memory
-  int first, n;        // their ids
-  int i0, i1;          // this warp's segment of them
-  int split, part, tid, lane, warp;
+  const uint4* x;      // this part's logits, in shared memory: whole vectors, -infinity in front of and behind them
+  int first, id0, id1;  // id of the first vector's first element; this part's ids
+  int i0, i1;          // this warp's segment (vectors)
+  int split, tid, lane, warp;
   float m;
   Weight w;
 
-  __device__ __forceinline__ float at(int i) const { return to_float(x[i]); }
-  __device__ __forceinline__ Place place(float v, int i) const {
-    const float y = (m - v) * w.ch;
-    const uint32_t p = y >= 0.f ? __float2uint_rz(y * 67108864.f) : 0xffffffffu;  // 2^26; saturates (NaN: 0 times infinity)
-    return Place{~p, order_bits(v), 0xfffffu - (uint32_t)(first + i)};
+  __device__ __forceinline__ int id(int vec, int e) const { return first + vec * VE + e; }
+  // f(logit, id) of every element of vectors b .. e - 1, the lanes' in turn
+  template <typename F>
+  __device__ __forceinline__ void each(int b, int e, F f) const {
+    for (int i = b + lane; i < e; i += 32) {
+      const Vec<T> v(x[i]);
+#pragma unroll
+      for (int k = 0; k < VE; ++k) f(v.v[k], id(i, k));
+    }
   }
-  __device__ __forceinline__ u64 key(float v, int i) const { return key_of(v, first + i); }
-
+  __device__ __forceinline__ u64 mass(int b, int e, const Cut& cut) const {  // of this lane's
+    u64 sum = 0;
+    each(b, e, [&](float v, int i) {
+      if (cut.takes(v, i)) sum += w(v);
+    });
+    return sum;
+  }
+  __device__ __forceinline__ uint32_t place_q(float v) const {
+    const float y = (m - v) * w.ch;
+    return y >= 0.f ? ~__float2uint_rz(y * 67108864.f) : 0u;  // 2^26; saturates (NaN: 0 times infinity)
+  }
   __device__ __forceinline__ void barrier() const {
     if (split > 1)
       cluster_barrier();
@@ -207,29 +258,38 @@ struct Row {
     if (at < kList) l.key[at] = k;
   }
 
-  // The largest key at which the running sum (keys of at least `least`, from the
-  // largest down) of counts, or weights (MASS), reaches the goal; goal_of(total)
-  // gives it from the sum of all.
+  // The largest key at which the running sum (ids that `least` takes, from the
+  // largest key down) of counts, or weights (MASS), reaches the goal;
+  // goal_of(total) gives it from the sum of all.
   template <bool MASS, typename Goal>
-  __device__ u64 find_cut(u64 least, Goal goal_of) {
+  __device__ u64 find_cut(const Cut least, Goal goal_of) {
     Place want{0, 0, 0}, mask{0, 0, 0};
     u64 before = 0, goal = 0;
     List& list = s.list[MASS];
-    for (int level = 0; level < kLevels; ++level) {
+    // whether an id agrees in the digits so far, and its place (what of it is needed)
+    auto agrees = [&](float v, int i, int level, Place* p) {
+      if (!least.takes(v, i) || (!MASS && (i < id0 || i >= id1))) return false;
+      p->q = place_q(v);
+      if ((p->q ^ want.q) & mask.q) return false;
+      if (level < 4) return true;
+      p->o = order_bits(v);
+      p->i = 0xfffffu - (uint32_t)i;
+      return !(((p->o ^ want.o) & mask.o) | ((p->i ^ want.i) & mask.i));
+    };
+    int level = 0;
+    for (;; ++level) {
       const int shift = shift_of(level), bits = bits_of(level);
       uint32_t(*h)[kBins] = s.hist[level & 1];
 #pragma unroll
       for (int j = 0; j < (MASS ? 4 : 1); ++j) h[j][tid] = 0;
       __syncthreads();
-      for (int i = i0 + lane; i < i1; i += 32) {
-        const float v = at(i);
-        if (key(v, i) < least) continue;
-        const Place p = place(v, i);
-        if (((p.q ^ want.q) & mask.q) | ((p.o ^ want.o) & mask.o) | ((p.i ^ want.i) & mask.i)) continue;
+      each(i0, i1, [&](float v, int i) {
+        Place p;
+        if (!agrees(v, i, level, &p)) return;
         const uint32_t bin = (field_of(p, level) >> shift) & ((1u << bits) - 1);
         if constexpr (MASS) {
           const u64 k = w(v);
-          if (k == 0) continue;
+          if (k == 0) return;
           atomicAdd(&h[0][bin], 1u);
           atomicAdd(&h[1][bin], (uint32_t)k & 0x1ffffu);
           if (k >> 17) atomicAdd(&h[2][bin], (uint32_t)(k >> 17) & 0x1ffffu);
@@ -237,7 +297,7 @@ struct Row {
         } else {
           atomicAdd(&h[0][bin], 1u);
         }
-      }
+      });
       barrier();
       const int bin = kBins - 1 - tid;
       u64 sum = 0;
@@ -268,28 +328,17 @@ struct Row {
       __syncthreads();
       before = s.before;
       const uint32_t digit = (uint32_t)s.bin << shift, dm = ((1u << bits) - 1) << shift;
-      if (level < 4) {
-        want.q |= digit;
-        mask.q |= dm;
-      } else if (level < 8) {
-        want.o |= digit;
-        mask.o |= dm;
-      } else {
-        want.i |= digit;
-        mask.i |= dm;
-      }
-      if (s.count <= kList) break;
+      uint32_t& wf = level < 4 ? want.q : level < 8 ? want.o : want.i;
+      uint32_t& mf = level < 4 ? mask.q : level < 8 ? mask.o : mask.i;
+      wf |= digit;
+      mf |= dm;
+      if (s.count <= kList || level == kLevels - 1) break;  // (a bin of the last digit is one id)
     }
     // the ids left, one against another
-    for (int i = i0 + lane; i < i1; i += 32) {
-      const float v = at(i);
-      const u64 k = key(v, i);
-      if (k < least) continue;
-      const Place p = place(v, i);
-      if (!(((p.q ^ want.q) & mask.q) | ((p.o ^ want.o) & mask.o) | ((p.i ^ want.i) & mask.i))) {
-        if (!MASS || w(v)) push(list, k);
-      }
-    }
+    each(i0, i1, [&](float v, int i) {
+      Place p;
+      if (agrees(v, i, level, &p) && (!MASS || w(v))) push(list, key_of(v, i));
+    });
     barrier();
     collect(list);
     const int n = s.n_key;
@@ -327,22 +376,26 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
 
   // This part's ids, to shared memory at the address modulo 16 that they have:
   // whole 16 bytes by bulk copies, the edges by threads.
+  constexpr int VE = Vec<T>::kN;
   const int v0 = (int)((long long)V * part / split), v1 = (int)((long long)V * (part + 1) / split);
   const T* src = static_cast<const T*>(a.x) + (long long)row * a.ld + v0;
-  const int off = (int)(reinterpret_cast<uintptr_t>(src) & 15), n = v1 - v0;
-  T* const dst = reinterpret_cast<T*>(smem_row + off);
-  const int head = min(n, off ? (int)((16 - off) / sizeof(T)) : 0);
-  const int whole = (int)((n - head) * sizeof(T) / 16) * 16;  // bytes
+  const int off = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T)), n = v1 - v0;  // (elements)
+  const int nvec = (off + n + VE - 1) / VE;
+  T* const dst = reinterpret_cast<T*>(smem_row) + off;
+  const int head = min(n, off ? VE - off : 0), whole = (n - head) / VE * VE, tail = head + whole;
   if (tid == 0) {
     mbar_init(&s.full, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    mbar_expect_tx(&s.full, whole);
-    for (int b = 0; b < whole; b += 16384)
-      bulk_g2s(smem_row + off + head * sizeof(T) + b, reinterpret_cast<const unsigned char*>(src + head) + b, min(16384, whole - b), &s.full);
+    mbar_expect_tx(&s.full, whole * sizeof(T));
+    for (int b = 0; b < whole; b += 8192)
+      bulk_g2s(dst + head + b, src + head + b, min(8192, whole - b) * sizeof(T), &s.full);
   }
-  const int tail = head + whole / (int)sizeof(T);
   if (tid < head) dst[tid] = src[tid];
   if (tid >= 32 && tail + tid - 32 < n) dst[tail + tid - 32] = src[tail + tid - 32];
+  // (what fills the first and the last vector has weight 0, and never comes before an id of the row but in a row of -infinity alone)
+  const T none = of_float<T>(-INFINITY);
+  if (tid >= 64 && tid - 64 < off) dst[64 - tid - 1] = none;
+  if (tid >= 96 && off + n + tid - 96 < nvec * VE) dst[n + tid - 96] = none;
   if (tid < 64) s.table[tid] = pow2.t[tid];
   if (tid < 2) s.list[tid].n = 0;
   const float temp = a.set.d_temperature ? a.set.d_temperature[row] : a.set.temperature;
@@ -353,19 +406,20 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const bool got = __syncthreads_and(mbar_wait_lazy(&s.full, 0, kWaitNs)) != 0;
   if (!got && tid == 0 && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
 
-  const int seg = (n + kWarps - 1) / kWarps;
-  Row<T> r{a, s, dst, v0, n, min(n, warp * seg), min(n, (warp + 1) * seg), split, part, tid, lane, warp, 0.f, Weight{}};
+  const int seg = (nvec + kWarps - 1) / kWarps;
+  Row<T> r{s, reinterpret_cast<const uint4*>(smem_row), v0 - off, v0, v1, min(nvec, warp * seg), min(nvec, (warp + 1) * seg), split, tid, lane, warp,
+           0.f, Weight{}};
   // the largest logit (the lowest id of equal ones)
   uint32_t top = 0;
   int top_i = 0;
-  for (int i = r.i0 + lane; i < r.i1; i += 32) {
-    const uint32_t o = order_bits(r.at(i));
+  r.each(r.i0, r.i1, [&](float v, int i) {
+    const uint32_t o = order_bits(v);
     if (o > top) {
       top = o;
       top_i = i;
     }
-  }
-  u64 best = top ? ((u64)top << 32) | (0xffffffffu - (uint32_t)(v0 + top_i)) : 0;
+  });
+  u64 best = top ? ((u64)top << 32) | (0xffffffffu - (uint32_t)top_i) : 0;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) best = max(best, __shfl_xor_sync(0xffffffffu, best, o));
   if (lane == 0) s.red[warp] = best;
@@ -379,7 +433,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const float m = value_of((uint32_t)(best >> 32));
   if (!got || !(fabsf(m) < INFINITY) || !(temp > 0.f)) {
     if (part == 0 && tid == 0) {
-      a.token[row] = (int)(0xffffffffu - (uint32_t)best);
+      a.token[row] = m == -INFINITY ? 0 : (int)(0xffffffffu - (uint32_t)best);
       if (a.logprob) a.logprob[row] = got && fabsf(m) < INFINITY ? 0.f : NAN;
     }
     if (split > 1) cluster_barrier();
@@ -402,8 +456,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     uint32_t* h = s.hist[0][0];
     h[tid] = 0;
     __syncthreads();
-    const Place mine = r.place(value_of(top), 0);
-    if (top) atomicAdd(&h[mine.q >> 23], 1u);
+    const uint32_t mine = r.place_q(value_of(top)) >> 23;
+    if (top) atomicAdd(&h[mine], 1u);
     r.barrier();
     const int bin = kBins - 1 - tid;
     uint32_t count = 0;
@@ -418,11 +472,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if (front + inc - count < (u64)k && (u64)k <= front + inc) s.bin = bin;
     __syncthreads();
     const uint32_t from = (uint32_t)s.bin;
-    if (top && mine.q >> 23 >= from)
-      for (int i = r.i0 + lane; i < r.i1; i += 32) {
-        const float v = r.at(i);
-        if (r.place(v, i).q >> 23 >= from) r.push(s.list[0], r.key(v, i));
-      }
+    if (top && mine >= from)
+      r.each(r.i0, r.i1, [&](float v, int i) {
+        if (r.place_q(v) >> 23 >= from) r.push(s.list[0], key_of(v, i));
+      });
     r.barrier();
     uint32_t all = 0;
     for (int j = 0; j < split; ++j) all += remote32(&s.list[0].n, j);
@@ -476,17 +529,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   }
 
   u64 cut = 0;
-  if (has_k) cut = r.template find_cut<false>(0, [&](u64) { return (u64)k; });
-  if (tp < 1.f) cut = max(cut, r.template find_cut<true>(cut, [&](u64 S) { return share_up(tp, S); }));
+  if (has_k) cut = r.template find_cut<false>(cut_of(0), [&](u64) { return (u64)k; });
+  if (tp < 1.f) cut = max(cut, r.template find_cut<true>(cut_of(cut), [&](u64 S) { return share_up(tp, S); }));
   if (mp > 0.f) cut = max(cut, (u64)order_bits(least) << 32);
   cut = min(cut, best);
   // the weights of each warp's segment, of those in front, and of all
-  u64 sum = 0;
-  for (int i = r.i0 + lane; i < r.i1; i += 32) {
-    const float v = r.at(i);
-    if (r.key(v, i) >= cut) sum += r.w(v);
-  }
-  sum = warp_sum64(sum);
+  const Cut keep = cut_of(cut);
+  u64 sum = warp_sum64(r.mass(r.i0, r.i1, keep));
   if (lane == 0) s.sums[warp] = sum;
   __syncthreads();
   u64 here = 0;
@@ -507,19 +556,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     // the segment it is in, then the sixteenth of that, then the id
     int ow = 0;
     while (front + s.sums[ow] <= goal) front += s.sums[ow++];
-    const int s0 = min(n, ow * seg), s1 = min(n, s0 + seg), sub = (s1 - s0 + kWarps - 1) / kWarps;
+    const int s0 = min(nvec, ow * seg), s1 = min(nvec, s0 + seg), sub = (s1 - s0 + kWarps - 1) / kWarps;
     auto range = [&](int j, int* b, int* e) {
       *b = min(s1, s0 + j * sub);
       *e = min(s1, *b + sub);
     };
     int b, e;
     range(warp, &b, &e);
-    sum = 0;
-    for (int i = b + lane; i < e; i += 32) {
-      const float v = r.at(i);
-      if (r.key(v, i) >= cut) sum += r.w(v);
-    }
-    sum = warp_sum64(sum);
+    sum = warp_sum64(r.mass(b, e, keep));
     if (lane == 0) s.red[warp] = sum;
     __syncthreads();
     int os = 0;
@@ -527,17 +571,27 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if (warp == 0) {
       range(os, &b, &e);
       for (int i = b; i < e; i += 32) {
-        u64 x = 0;
+        u64 w[VE] = {}, x = 0;
         if (i + lane < e) {
-          const float v = r.at(i + lane);
-          if (r.key(v, i + lane) >= cut) x = r.w(v);
+          const Vec<T> v(r.x[i + lane]);
+#pragma unroll
+          for (int j = 0; j < VE; ++j) x += w[j] = keep.takes(v.v[j], r.id(i + lane, j)) ? r.w(v.v[j]) : 0;
         }
         const u64 inc = warp_scan64(x, lane);
         const unsigned hit = __ballot_sync(0xffffffffu, front + inc > goal);
         if (hit) {
           if (lane == __ffs(hit) - 1) {
-            a.token[row] = v0 + i + lane;
-            if (a.logprob) a.logprob[row] = logf((float)x / (float)all);
+            u64 at = front + inc - x;
+            bool done = false;
+#pragma unroll
+            for (int j = 0; j < VE; ++j) {
+              at += w[j];
+              if (!done && at > goal) {
+                done = true;
+                a.token[row] = r.id(i + lane, j);
+                if (a.logprob) a.logprob[row] = logf((float)w[j] / (float)all);
+              }
+            }
           }
           break;
         }

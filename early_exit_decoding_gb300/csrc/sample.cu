@@ -67,7 +67,7 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 }
 __device__ __forceinline__ u64 key_of(float x, int id) { return ((u64)order_bits(x) << 32) | (0xffffffffu - (uint32_t)id); }
 
-// 2^(-j / 64) 2^44, j < 64.
+// 2^(-j / 64) 2^45, j < 64.
 struct Pow2Table {
   u64 t[64];
 };
@@ -75,7 +75,7 @@ struct Pow2Table {
 // exp((x - m) / T) 2^44, rounded: 2^-y with y = (m - x) c, c = log2(e) / T.
 struct Weight {
   float m, ch, cl;  // c = ch + cl
-  const u64* table;
+  uint32_t table;   // Pow2Table in shared memory
   __device__ __forceinline__ u64 operator()(float x) const {
     // y = p + e: the difference and the product exact in two parts each
     const float d = m - x, b = d - m, dl = (m - (d - b)) - (x + b);
@@ -85,16 +85,18 @@ struct Weight {
     // y = k / 64 + r, |r| <= 1 / 128
     const float big = 196608.f;  // 1.5 2^17: its sums are whole multiples of 1 / 64
     const float s = p + big, r = p - (s - big);
-    const int k = (int)(__float_as_uint(s) - __float_as_uint(big));
+    const uint32_t k = __float_as_uint(s) - __float_as_uint(big);
     // 2^-r = 1 - a + a^2 / 2 - a^3 / 6 + a^4 / 24 (the next term is below 2^-44), a = ln 2 (r + e) = ah + al
     const float lh = 0.693147182464599609375f, ll = -1.904654323148236017e-9f;  // ln 2 in two parts
     const float ah = r * lh, al = fmaf(e, lh, fmaf(r, ll, fmaf(r, lh, -ah)));
     const float v = fmaf(-ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al);  // 1 - 2^-r = ah + v
-    const int w = __float2int_rn(ah * 274877906944.f) + __float2int_rn(v * 274877906944.f);  // 2^38 (below 2^31)
-    const u64 t = table[k & 63];
-    const int n = k >> 6;
-    const u64 f = t - (u64)(((long long)(int)(t >> 14) * w) >> 24);
-    return (f + ((1ull << n) >> 1)) >> n;
+    // times 2^38, to whole numbers (v's is below 2^22: by a sum with 1.5 2^23)
+    const float unit = 274877906944.f, round = 12582912.f;
+    const int w = __float2int_rn(ah * unit) + ((int)__float_as_uint(fmaf(v, unit, round)) - (int)__float_as_uint(round));
+    u64 t;
+    asm("ld.shared.u64 %0, [%1];" : "=l"(t) : "r"(table + (k & 63) * 8));
+    const u64 f = t - (u64)(((long long)(int)(t >> 15) * w) >> 23);
+    return ((f >> (k >> 6)) + 1) >> 1;
   }
 };
 
@@ -153,7 +155,7 @@ struct Shared {
   u64 key[kList], wt[kList];   // the cluster's, and their weights
   int n_key;
   u64 red[kWarps], sums[kWarps];
-  u64 best, mass;           // this part's
+  u64 best, mass;           // this part's largest key, and weights kept
   u64 before;               // in front of the digit's bin
   u64 cut;
   uint32_t count;           // ids of the bin
@@ -260,7 +262,8 @@ struct Row {
 
   // The largest key at which the running sum (ids that `least` takes, from the
   // largest key down) of counts, or weights (MASS), reaches the goal;
-  // goal_of(total) gives it from the sum of all.
+  // goal_of(total) gives it from the sum of all.  With MASS s.mass is then this
+  // part's sum of the weights from the cut on.
   template <bool MASS, typename Goal>
   __device__ u64 find_cut(const Cut least, Goal goal_of) {
     Place want{0, 0, 0}, mask{0, 0, 0};
@@ -327,6 +330,10 @@ struct Row {
       }
       __syncthreads();
       before = s.before;
+      if constexpr (MASS) {  // this part's weights in the bins in front
+        const u64 own = warp_sum64(bin > s.bin ? h[1][bin] + ((u64)h[2][bin] << 17) + ((u64)h[3][bin] << 34) : 0);
+        if (lane == 0 && own) atomicAdd(&s.mass, own);
+      }
       const uint32_t digit = (uint32_t)s.bin << shift, dm = ((1u << bits) - 1) << shift;
       uint32_t& wf = level < 4 ? want.q : level < 8 ? want.o : want.i;
       uint32_t& mf = level < 4 ? mask.q : level < 8 ? mask.o : mask.i;
@@ -356,6 +363,10 @@ struct Row {
       if (front < goal && goal <= front + v) s.cut = k;
     }
     __syncthreads();
+    if (MASS && tid < (int)list.n) {
+      const u64 mine = list.key[tid];
+      if (mine >= s.cut) atomicAdd(&s.mass, w(value_of((uint32_t)(mine >> 32))));
+    }
     return s.cut;
   }
 };
@@ -398,6 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   if (tid >= 96 && off + n + tid - 96 < nvec * VE) dst[n + tid - 96] = none;
   if (tid < 64) s.table[tid] = pow2.t[tid];
   if (tid < 2) s.list[tid].n = 0;
+  if (tid == 0) s.mass = 0;
   const float temp = a.set.d_temperature ? a.set.d_temperature[row] : a.set.temperature;
   const int k = a.set.d_top_k ? a.set.d_top_k[row] : a.set.top_k;
   const float tp = a.set.d_top_p ? a.set.d_top_p[row] : a.set.top_p, mp = a.set.d_min_p ? a.set.d_min_p[row] : a.set.min_p;
@@ -441,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   }
   const double c = fmin(1.4426950408889634 / (double)temp, 1e38);  // (finite in fp32)
   r.m = m;
-  r.w = Weight{m, (float)c, (float)(c - (double)(float)c), s.table};
+  r.w = Weight{m, (float)c, (float)(c - (double)(float)c), smem_u32(s.table)};
   float least = -INFINITY;  // min-p's
   if (mp > 0.f) {
     const double b = (double)m + (double)temp * log((double)mp);
@@ -530,29 +542,43 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
 
   u64 cut = 0;
   if (has_k) cut = r.template find_cut<false>(cut_of(0), [&](u64) { return (u64)k; });
-  if (tp < 1.f) cut = max(cut, r.template find_cut<true>(cut_of(cut), [&](u64 S) { return share_up(tp, S); }));
-  if (mp > 0.f) cut = max(cut, (u64)order_bits(least) << 32);
+  bool known = false;  // s.mass holds the weights kept
+  if (tp < 1.f) {
+    cut = r.template find_cut<true>(cut_of(cut), [&](u64 S) { return share_up(tp, S); });
+    known = true;
+  }
+  if (mp > 0.f && ((u64)order_bits(least) << 32) > cut) {
+    cut = (u64)order_bits(least) << 32;
+    known = false;
+  }
   cut = min(cut, best);
-  // the weights of each warp's segment, of those in front, and of all
   const Cut keep = cut_of(cut);
-  u64 sum = warp_sum64(r.mass(r.i0, r.i1, keep));
-  if (lane == 0) s.sums[warp] = sum;
-  __syncthreads();
-  u64 here = 0;
-  for (int j = 0; j < kWarps; ++j) here += s.sums[j];
-  u64 front = 0, all = here;
-  if (split > 1) {
-    if (tid == 0) s.mass = here;
-    cluster_barrier();
-    all = 0;
-    for (int j = 0; j < split; ++j) {
-      const u64 x = remote64(&s.mass, j);
-      if (j < part) front += x;
-      all += x;
+  // the weights of each warp's segment
+  auto segments = [&] {
+    const u64 sum = warp_sum64(r.mass(r.i0, r.i1, keep));
+    if (lane == 0) s.sums[warp] = sum;
+    __syncthreads();
+  };
+  if (!known) {
+    segments();
+    if (tid == 0) {
+      u64 sum = 0;
+      for (int j = 0; j < kWarps; ++j) sum += s.sums[j];
+      s.mass = sum;
     }
   }
+  // and of each part: in front of this one's, this one's, all
+  r.barrier();
+  u64 front = 0, all = 0;
+  for (int j = 0; j < split; ++j) {
+    const u64 x = remote64(&s.mass, j);
+    if (j < part) front += x;
+    all += x;
+  }
+  const u64 here = s.mass;
   const u64 goal = share(u, all);
   if (front <= goal && goal < front + here) {
+    if (known) segments();
     // the segment it is in, then the sixteenth of that, then the id
     int ow = 0;
     while (front + s.sums[ow] <= goal) front += s.sums[ow++];
@@ -563,7 +589,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     };
     int b, e;
     range(warp, &b, &e);
-    sum = warp_sum64(r.mass(b, e, keep));
+    const u64 sum = warp_sum64(r.mass(b, e, keep));
     if (lane == 0) s.red[warp] = sum;
     __syncthreads();
     int os = 0;
@@ -650,7 +676,7 @@ cudaError_t launch(const SampleArgs& a, const Pow2Table& table, cudaStream_t st)
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
   static const Pow2Table table = [] {
     Pow2Table t;
-    for (int j = 0; j < 64; ++j) t.t[j] = (u64)llrint(exp2(44.0 - j / 64.0));
+    for (int j = 0; j < 64; ++j) t.t[j] = (u64)llrint(exp2(45.0 - j / 64.0));
     return t;
   }();
   if (a.dtype == RL_DT_F32) return launch<float>(a, table, s);

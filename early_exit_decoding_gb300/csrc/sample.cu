@@ -56,6 +56,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSplit = 16;    // CTAs of a row's cluster
 constexpr int kBins = kThreads;  // of a digit (9 bits), one a thread
 constexpr int kList = 128;       // ids that are ordered one against another
+constexpr int kGather = 1024;    // ids of a digit's bin that are brought together before the next 
 constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
 
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -154,26 +155,37 @@ struct Shared {
   List list[2];             // this part's ids that are ordered one against another: for top-k, for top-p
   u64 key[kList], wt[kList];   // the cluster's, and their weights
   int n_key;
+  uint32_t n_few;
+  u64 few[kGather];
   u64 red[kWarps], sums[kWarps];
   u64 best, mass;           // this part's largest key, and weights kept
+  u64 group[2][kWarps];     // by a digit's parity: this part's sums of 32 bins
+  u64 of_bin[kMaxSplit][32];       // the parts' sums and ids in the bins of a group
+  uint32_t in_bin[kMaxSplit][32];
   u64 before;               // in front of the digit's bin
+  float lo, hi;             // the logits whose digits so far are the cut's
   u64 cut;
   uint32_t count;           // ids of the bin
   int bin;
+  float ch, cl, least;      // log2(e) / T in two parts; min-p's logit
+  double span;              // T ln min_p
 };
 
-// The place of an id in the order: (~fixed-point -log2 of its weight, ordered
-// logit, ~id), as digits of 9 bits from the largest down.
+// An id's place in the order as digits of 9 bits from the largest down: of q, the
+// complement of -log2 of its weight in fixed point (levels 0-3), of o, the ordered
+// logit (4-7), and of i, the complement of the id (8-10).
 struct Place {
   uint32_t q, o, i;
 };
 constexpr int kLevels = 11;
-__device__ __forceinline__ uint32_t field_of(const Place& p, int level) { return level < 4 ? p.q : level < 8 ? p.o : p.i; }
 __device__ __forceinline__ int shift_of(int level) {  // of the field: 23, 14, 5, 0 (20 bits of ~id: 11, 2, 0)
   const int l = level & 3;
   return level < 8 ? (l == 0 ? 23 : l == 1 ? 14 : l == 2 ? 5 : 0) : (l == 0 ? 11 : l == 1 ? 2 : 0);
 }
 __device__ __forceinline__ int bits_of(int level) { return level < 8 ? ((level & 3) == 3 ? 5 : 9) : level == 10 ? 2 : 9; }
+
+// Whether sums of `front` and then `more` pass from below a goal (of 1 at least) to it.
+__device__ __forceinline__ bool reaches(u64 goal, u64 front, u64 more) { return goal - 1 - front < more; }
 
 // A key that parts ids: those of a larger logit, or of its own and no higher id.
 struct Cut {
@@ -246,13 +258,18 @@ struct Row {
   }
   // Lists of all parts into s.key (a barrier after they were filled).
   __device__ void collect(const List& l) {
-    int at = 0;
-    for (int r = 0; r < split; ++r) {
-      const int k = min((int)remote32(&l.n, r), kList - at);
-      if (tid < k) s.key[at + tid] = remote64(&l.key[tid], r);
-      at += k;
+    // (a warp a part; where its ids go from the parts' counts)
+    const int n = lane < split ? (int)min(remote32(&l.n, lane), (uint32_t)kList) : 0;
+    int end = n;
+#pragma unroll
+    for (int o = 1; o < kMaxSplit; o <<= 1) {
+      const int t = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += t;
     }
-    if (tid == 0) s.n_key = at;
+    static_assert(kWarps >= kMaxSplit, "a warp a part");
+    const int mine = __shfl_sync(0xffffffffu, n, warp), at = __shfl_sync(0xffffffffu, end, warp) - mine;
+    for (int i = lane; i < mine && at + i < kList; i += 32) s.key[at + i] = remote64(&l.key[i], warp);
+    if (warp == 0 && lane == kMaxSplit - 1) s.n_key = min(end, kList);
     __syncthreads();
   }
   __device__ __forceinline__ void push(List& l, u64 k) {
@@ -269,15 +286,13 @@ struct Row {
     Place want{0, 0, 0}, mask{0, 0, 0};
     u64 before = 0, goal = 0;
     List& list = s.list[MASS];
-    // whether an id agrees in the digits so far, and its place (what of it is needed)
-    auto agrees = [&](float v, int i, int level, Place* p) {
-      if (!least.takes(v, i) || (!MASS && (i < id0 || i >= id1))) return false;
-      p->q = place_q(v);
-      if ((p->q ^ want.q) & mask.q) return false;
-      if (level < 4) return true;
-      p->o = order_bits(v);
-      p->i = 0xfffffu - (uint32_t)i;
-      return !(((p->o ^ want.o) & mask.o) | ((p->i ^ want.i) & mask.i));
+    // the ids that agree in the digits so far have a logit in [lo, hi]
+    float lo = least.v, hi = INFINITY;
+    auto agrees = [&](float v, int i, int level) {
+      if (!(v >= lo && v <= hi) || !least.takes(v, i)) return false;
+      // (what fills the vectors is nobody's; weights of 0 would only crowd the others)
+      if (MASS ? !((m - v) * w.ch < 46.f) : i < id0 || i >= id1) return false;
+      return level < 5 || !(((order_bits(v) ^ want.o) & mask.o) | (((0xfffffu - (uint32_t)i) ^ want.i) & mask.i));
     };
     int level = 0;
     for (;; ++level) {
@@ -285,14 +300,13 @@ struct Row {
       uint32_t(*h)[kBins] = s.hist[level & 1];
 #pragma unroll
       for (int j = 0; j < (MASS ? 4 : 1); ++j) h[j][tid] = 0;
+      if (tid == 0) s.n_few = 0;
       __syncthreads();
-      each(i0, i1, [&](float v, int i) {
-        Place p;
-        if (!agrees(v, i, level, &p)) return;
-        const uint32_t bin = (field_of(p, level) >> shift) & ((1u << bits) - 1);
+      auto add = [&](float v, int i) {
+        const uint32_t field = level < 4 ? place_q(v) : level < 8 ? order_bits(v) : 0xfffffu - (uint32_t)i;
+        const uint32_t bin = (field >> shift) & ((1u << bits) - 1);
         if constexpr (MASS) {
           const u64 k = w(v);
-          if (k == 0) return;
           atomicAdd(&h[0][bin], 1u);
           atomicAdd(&h[1][bin], (uint32_t)k & 0x1ffffu);
           if (k >> 17) atomicAdd(&h[2][bin], (uint32_t)(k >> 17) & 0x1ffffu);
@@ -300,39 +314,91 @@ struct Row {
         } else {
           atomicAdd(&h[0][bin], 1u);
         }
-      });
-      barrier();
-      const int bin = kBins - 1 - tid;
-      u64 sum = 0;
-      uint32_t count = 0;
-      for (int r = 0; r < split; ++r) {
-        const uint32_t k = remote32(&h[0][bin], r);
-        count += k;
-        if constexpr (MASS)
-          sum += remote32(&h[1][bin], r) + ((u64)remote32(&h[2][bin], r) << 17) + ((u64)remote32(&h[3][bin], r) << 34);
-        else
-          sum += k;
+      };
+      if (MASS && level == 0 && least.v == -INFINITY) {  // (every id)
+        each(i0, i1, [&](float v, int i) {
+          if ((m - v) * w.ch < 46.f) add(v, i);
+        });
+      } else if (level == 0 || s.count > kGather) {
+        each(i0, i1, [&](float v, int i) {
+          if (agrees(v, i, level)) add(v, i);
+        });
+      } else {
+        // few ids, brought together first (a weight takes a warp the same time for one lane's)
+        each(i0, i1, [&](float v, int i) {
+          if (agrees(v, i, level)) s.few[atomicAdd(&s.n_few, 1u)] = key_of(v, i);  // (no more than were counted)
+        });
+        __syncthreads();
+        for (int i = tid; i < (int)s.n_few; i += kThreads) {
+          const Cut c = cut_of(s.few[i]);
+          add(c.v, (int)c.id);
+        }
       }
-      // the bin that reaches the goal
-      const u64 inc = warp_scan64(sum, lane);
-      if (lane == 31) s.red[warp] = inc;
       __syncthreads();
-      u64 front = before, total = before;
-      for (int k = 0; k < kWarps; ++k) {
-        if (k < warp) front += s.red[k];
-        total += s.red[k];
+      // The bin that reaches the goal: of the groups of 32 bins first, then of
+      // its group's (all bins of all parts took 6000 clocks: 64 KB a CTA from others').
+      const int mine = kBins - 1 - tid;  // (the largest first)
+      const u64 own = MASS ? h[1][mine] + ((u64)h[2][mine] << 17) + ((u64)h[3][mine] << 34) : h[0][mine];
+      const u64 own32 = warp_sum64(own);
+      if (lane == 0) s.group[level & 1][warp] = own32;
+      barrier();
+      {
+        const u64 x = warp_sum64(lane < split ? remote64(&s.group[level & 1][warp], lane) : 0);
+        if (lane == 0) s.red[warp] = x;
       }
-      if (level == 0) goal = goal_of(total);
-      if (front + inc - sum < goal && goal <= front + inc) {
-        s.bin = bin;
-        s.before = front + inc - sum;
-        s.count = count;
+      __syncthreads();
+      const u64 of_group = lane < kWarps ? s.red[lane] : 0, upto = before + warp_scan64(of_group, lane);
+      if (level == 0) goal = goal_of(__shfl_sync(0xffffffffu, upto, 31));
+      const unsigned reach = __ballot_sync(0xffffffffu, upto >= goal);
+      const int g = min(reach ? __ffs(reach) - 1 : 31, kWarps - 1);
+      const int bin = kBins - 1 - (g * 32 + lane);
+      if (warp < split) {  // (a warp a part)
+        s.of_bin[warp][lane] = MASS ? remote32(&h[1][bin], warp) + ((u64)remote32(&h[2][bin], warp) << 17) + ((u64)remote32(&h[3][bin], warp) << 34) : 0;
+        s.in_bin[warp][lane] = remote32(&h[0][bin], warp);
+      }
+      __syncthreads();
+      if (warp == 0) {
+        const u64 front = __shfl_sync(0xffffffffu, upto - of_group, g);
+        u64 sum = 0;
+        uint32_t count = 0;
+        for (int r = 0; r < split; ++r) {
+          sum += s.of_bin[r][lane];
+          count += s.in_bin[r][lane];
+        }
+        if (!MASS) sum = count;
+        const u64 inc = front + warp_scan64(sum, lane);
+        const unsigned it = __ballot_sync(0xffffffffu, reaches(goal, inc - sum, sum));
+        const int who = it ? __ffs(it) - 1 : 31;
+        if (lane == who) {
+          s.bin = bin;
+          s.before = inc - sum;
+          s.count = count;
+        }
+        if (level < 4) {
+          // the logits of that bin, by a search 16 ways at once on each side
+          const uint32_t digits = want.q | (uint32_t)__shfl_sync(0xffffffffu, bin, who) << shift, dm = mask.q | ((1u << bits) - 1) << shift;
+          uint32_t at = 0;  // ordered logits: the largest with a place below, or (upper lanes) not above
+          for (int step = 28; step >= 0; step -= 4) {
+            const uint32_t x = at + ((uint32_t)(lane & 15) << step);
+            const uint32_t q = place_q(fminf(value_of(x), m)) & dm;
+            const bool less = lane < 16 ? q < digits : q <= digits;
+            const bool nan = x < 0x007fffffu, up = x > 0xff800000u;  // (NaN's patterns: below and above all logits)
+            const unsigned yes = __ballot_sync(0xffffffffu, (lane & 15) == 0 || nan || (!up && less));
+            at += (uint32_t)(31 - __clz((lane < 16 ? yes : yes >> 16) & 0xffffu)) << step;
+          }
+          if (lane == 0) s.lo = value_of(max(at, 0x007ffffeu) + 1);
+          if (lane == 16) s.hi = value_of(min(max(at, 0x007fffffu), 0xff800000u));
+        }
       }
       __syncthreads();
       before = s.before;
+      if (level < 4) {
+        lo = fmaxf(s.lo, least.v);
+        hi = s.hi;
+      }
       if constexpr (MASS) {  // this part's weights in the bins in front
-        const u64 own = warp_sum64(bin > s.bin ? h[1][bin] + ((u64)h[2][bin] << 17) + ((u64)h[3][bin] << 34) : 0);
-        if (lane == 0 && own) atomicAdd(&s.mass, own);
+        const u64 mass = warp_sum64(mine > s.bin ? own : 0);
+        if (lane == 0 && mass) atomicAdd(&s.mass, mass);
       }
       const uint32_t digit = (uint32_t)s.bin << shift, dm = ((1u << bits) - 1) << shift;
       uint32_t& wf = level < 4 ? want.q : level < 8 ? want.o : want.i;
@@ -343,8 +409,7 @@ struct Row {
     }
     // the ids left, one against another
     each(i0, i1, [&](float v, int i) {
-      Place p;
-      if (agrees(v, i, level, &p) && (!MASS || w(v))) push(list, key_of(v, i));
+      if (agrees(v, i, kLevels)) push(list, key_of(v, i));
     });
     barrier();
     collect(list);
@@ -360,7 +425,7 @@ struct Row {
       u64 front = before;
       for (int j = 0; j < n; ++j)
         if (s.key[j] > k) front += s.wt[j];
-      if (front < goal && goal <= front + v) s.cut = k;
+      if (reaches(goal, front, v)) s.cut = k;
     }
     __syncthreads();
     if (MASS && tid < (int)list.n) {
@@ -371,10 +436,17 @@ struct Row {
   }
 };
 
-// floor(u S) and top_p S rounded up, of u and top_p in [0, 1).
-__device__ __forceinline__ u64 share(float u, u64 S) { return __umul64hi((u64)((double)u * 18446744073709551616.0), S); }
+// u 2^64 of u in [0, 1), what is below 1 dropped.
+__device__ __forceinline__ u64 fixed64(float u) {
+  const uint32_t b = __float_as_uint(u);
+  const int e = (int)(b >> 23) - 86;
+  const u64 f = (b & 0x7fffffu) | 0x800000u;
+  return e >= 0 ? f << e : e > -24 ? f >> -e : 0;
+}
+// floor(u S), and top_p S rounded up (1 at least).
+__device__ __forceinline__ u64 share(float u, u64 S) { return __umul64hi(fixed64(u), S); }
 __device__ __forceinline__ u64 share_up(float p, u64 S) {
-  const u64 f = (u64)(fmax((double)p, 0.0) * 18446744073709551616.0);
+  const u64 f = p > 0.f ? fixed64(p) : 0;
   return max(1ull, __umul64hi(f, S) + (f * S != 0));
 }
 
@@ -414,6 +486,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const int k = a.set.d_top_k ? a.set.d_top_k[row] : a.set.top_k;
   const float tp = a.set.d_top_p ? a.set.d_top_p[row] : a.set.top_p, mp = a.set.d_min_p ? a.set.d_min_p[row] : a.set.min_p;
   const float u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604644775390625e-8f);
+  // (one thread, while the row is on its way: in 64 bits, which all threads at
+  // once would wait for)
+  if (tid == kThreads - 1) {
+    const double c = fmin(1.4426950408889634 / (double)temp, 1e38);  // (finite in fp32)
+    s.ch = (float)c;
+    s.cl = (float)(c - (double)(float)c);
+    s.span = mp > 0.f ? (double)temp * log((double)mp) : 0.0;
+  }
   __syncthreads();
   const bool got = __syncthreads_and(mbar_wait_lazy(&s.full, 0, kWaitNs)) != 0;
   if (!got && tid == 0 && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
@@ -440,7 +520,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   if (split > 1) {
     if (tid == 0) s.best = best;
     cluster_barrier();
-    for (int j = 0; j < split; ++j) best = max(best, remote64(&s.best, j));
+    u64 x = lane < split ? remote64(&s.best, lane) : 0;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) x = max(x, __shfl_xor_sync(0xffffffffu, x, o));
+    best = x;
   }
   const float m = value_of((uint32_t)(best >> 32));
   if (!got || !(fabsf(m) < INFINITY) || !(temp > 0.f)) {
@@ -451,15 +534,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     if (split > 1) cluster_barrier();
     return;
   }
-  const double c = fmin(1.4426950408889634 / (double)temp, 1e38);  // (finite in fp32)
   r.m = m;
-  r.w = Weight{m, (float)c, (float)(c - (double)(float)c), smem_u32(s.table)};
-  float least = -INFINITY;  // min-p's
+  r.w = Weight{m, s.ch, s.cl, smem_u32(s.table)};
   if (mp > 0.f) {
-    const double b = (double)m + (double)temp * log((double)mp);
-    least = (float)b;
-    if ((double)least < b) least = nextafterf(least, INFINITY);
+    if (tid == 0) {
+      const double b = (double)m + s.span;
+      const float f = (float)b;
+      s.least = (double)f < b ? nextafterf(f, INFINITY) : f;
+    }
+    __syncthreads();
   }
+  const float least = mp > 0.f ? s.least : -INFINITY;
   const bool has_k = k >= 1 && k < V;
 
   if (has_k && k <= kList / 2) {
@@ -473,7 +558,13 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     r.barrier();
     const int bin = kBins - 1 - tid;
     uint32_t count = 0;
-    for (int j = 0; j < split; ++j) count += remote32(&h[bin], j);
+    for (int j0 = 0; j0 < split; j0 += 8) {  // eight parts' loads in flight together
+      uint32_t x[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = j0 + j < split ? remote32(&h[bin], j0 + j) : 0u;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) count += x[j];
+    }
     const u64 inc = warp_scan64(count, lane);
     __syncthreads();
     if (lane == 31) s.red[warp] = inc;
@@ -481,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     __syncthreads();
     u64 front = 0;
     for (int j = 0; j < warp; ++j) front += s.red[j];
-    if (front + inc - count < (u64)k && (u64)k <= front + inc) s.bin = bin;
+    if (reaches((u64)k, front + inc - count, count)) s.bin = bin;
     __syncthreads();
     const uint32_t from = (uint32_t)s.bin;
     if (top && mine >= from)
@@ -489,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
         if (r.place_q(v) >> 23 >= from) r.push(s.list[0], key_of(v, i));
       });
     r.barrier();
-    uint32_t all = 0;
-    for (int j = 0; j < split; ++j) all += remote32(&s.list[0].n, j);
+    const uint32_t all = __reduce_add_sync(0xffffffffu, lane < split ? remote32(&s.list[0].n, lane) : 0u);
     if (all <= kList) {
       if (part == 0) {
         r.collect(s.list[0]);
@@ -569,12 +659,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   }
   // and of each part: in front of this one's, this one's, all
   r.barrier();
-  u64 front = 0, all = 0;
-  for (int j = 0; j < split; ++j) {
-    const u64 x = remote64(&s.mass, j);
-    if (j < part) front += x;
-    all += x;
-  }
+  const u64 of_part = lane < split ? remote64(&s.mass, lane) : 0;
+  u64 front = warp_sum64(lane < part ? of_part : 0);
+  const u64 all = warp_sum64(of_part);
   const u64 here = s.mass;
   const u64 goal = share(u, all);
   if (front <= goal && goal < front + here) {
@@ -608,16 +695,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
         if (hit) {
           if (lane == __ffs(hit) - 1) {
             u64 at = front + inc - x;
-            bool done = false;
+            int pick = 0;  // elements whose sums do not exceed the goal
 #pragma unroll
             for (int j = 0; j < VE; ++j) {
               at += w[j];
-              if (!done && at > goal) {
-                done = true;
-                a.token[row] = r.id(i + lane, j);
-                if (a.logprob) a.logprob[row] = logf((float)w[j] / (float)all);
-              }
+              pick += at <= goal;
             }
+            u64 weight = w[0];
+#pragma unroll
+            for (int j = 1; j < VE; ++j) weight = j == pick ? w[j] : weight;
+            a.token[row] = r.id(i + lane, pick);
+            if (a.logprob) a.logprob[row] = logf((float)weight / (float)all);
           }
           break;
         }

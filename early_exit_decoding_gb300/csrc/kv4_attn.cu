@@ -47,12 +47,12 @@ using namespace attn;
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kUnit = 32;       // keys a warp takes at a time
-constexpr int kStages = 3;      // units of a warp's ring
+constexpr int kStages = 4;      // units of a warp's ring
 constexpr int kLeast = 4;       // units a CTA takes at least
 // Units that a tile's start and end are worth in sharing out (64 sequences of 130
 // to 8191 positions: 99 us with 0, 84 with 4, 81 with 8, 77 with 12, 78 with 20).
 constexpr int kStart = 12;
-constexpr int kMaxCtas = 608;   // four on each of 152 SMs; the workspace holds that many CTAs' parts
+constexpr int kSms = 152;       // the workspace holds the parts of as many SMs' CTAs
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMost = 256.f;  // a weight, or weight times step, that is let pass (1 where it was the largest)
 
@@ -61,7 +61,7 @@ constexpr int kStageBytes = kUnit * HD + 2 * kUnit * 4;  // codes of k and v, sc
 template <int HD>
 constexpr int kSmem = kWarps * kStages * kStageBytes<HD>;
 template <int NT>
-constexpr int kResident = NT == 1 ? 4 : 2;  // CTAs of an SM (registers)
+constexpr int kResident = NT == 1 ? 3 : 2;  // CTAs of an SM (registers)
 
 struct Kv4Shape {
   FastDiv by_heads, by_rep;
@@ -127,9 +127,15 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
   all *= a.Hkv;
   const long long ctas = max(1ll, min((long long)gridDim.x, all / (kStart + kLeast)));
-  long long at = all * blockIdx.x / ctas;
-  const long long stop_at = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : 0;
+  const long long at = all * blockIdx.x / ctas, stop_at = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : 0;
   if (at >= stop_at) return;
+  __shared__ long long s_all, s_ctas, s_stop;  // (needed at a tile's end only)
+  if (tid == 0) {
+    s_all = all;
+    s_ctas = ctas;
+    s_stop = stop_at;
+  }
+  int left = (int)min(stop_at - at, 0x7fffffffll);  // units of the share to come
   // the sequence, tile and head, and unit it starts with
   int b = 0, item = 0, u0 = 0;
   Load ld;
@@ -160,9 +166,9 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   }
   unsigned char* const ring = smem + warp * NST * SB;
   for (bool head_part = true;; head_part = false) {
-  const int u1 = (int)min((long long)ld.units, u0 + (stop_at - at));
+  const int u1 = min(ld.units, u0 + left);
   if (u1 <= 0) break;  // (the share ends before the tile's first unit)
-  at -= min(u0, 0);
+  left += min(u0, 0);
   u0 = max(u0, 0);
   const int tile = sh.by_heads.quot(item), hk = item - tile * sh.by_heads.d, row0 = tile * R;
   const Span sp = seq_span(a, b, false);
@@ -177,33 +183,33 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   const int head0 = hk << c.page_log;  // the head's first row in a page
   const bool v_scales = lane & 8;
   const unsigned char* const sc0 = reinterpret_cast<const unsigned char*>((v_scales ? c.vm : c.km) + head0) + (lane & 3) * 16;
-  const long long sc_step = 4 * (v_scales ? c.vm_step : c.km_step);
+  const unsigned sc_step = 4u * (unsigned)(v_scales ? c.vm_step : c.km_step), kc_step = (unsigned)c.kc_step, vc_step = (unsigned)c.vc_step;
   const uint32_t dst0 = smem_u32(ring) + lane * 16;
-  auto pages_of = [&](int u) {  // of a unit's first and last 16 keys (that nobody may see: then the first's)
-    const int j = u * kUnit, *row = c.table + (long long)b * c.table_step;
-    int2 p = make_int2(0, 0);
-    if (u < units) {
-      p.x = __ldg(row + (j >> c.page_log));
-      p.y = __ldg(row + ((j + (j + 16 < any ? 16 : 0)) >> c.page_log));
-      if (max((unsigned)p.x, (unsigned)p.y) >= (unsigned)c.n_pages) {  // out of the cache: reported, page 0 is read
-        if (a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
-        if ((unsigned)p.x >= (unsigned)c.n_pages) p.x = 0;
-        if ((unsigned)p.y >= (unsigned)c.n_pages) p.y = 0;
-      }
+  // Pages: lane i has that of the (i % 2)-th 16 keys of this warp's unit number
+  // k0 + i / 2 (of keys that nobody sees: some page of the sequence).
+  int pages = 0;
+  auto look_up = [&](int k0) {
+    const int j = max(0, min((u0 + warp + (k0 + (lane >> 1)) * kWarps) * kUnit + (lane & 1) * 16, any - 1));
+    pages = __ldg(c.table + (long long)b * c.table_step + (j >> c.page_log));
+    if ((unsigned)pages >= (unsigned)c.n_pages) {  // out of the cache: reported, page 0 is read
+      if (a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
+      pages = 0;
     }
-    return p;
   };
   auto copy = [&](uint32_t dst, const unsigned char* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
   };
-  auto issue = [&](int u, int st, int2 p) {
+  auto issue = [&](int k, int st) {  // this warp's k-th unit
+    if ((k & 15) == 0) look_up(k);
+    const int u = u0 + warp + k * kWarps;
+    const unsigned px = __shfl_sync(0xffffffffu, pages, 2 * k & 31), py = __shfl_sync(0xffffffffu, pages, (2 * k & 31) | 1);
     if (u < units) {
       constexpr int NI = HD / 64;  // pieces of 16 keys
       const int r0 = (u * kUnit) & in_page, r1 = (u * kUnit + 16) & in_page;
       const int o0 = (head0 + r0) * (HD / 2) + lane * 16, o1 = (head0 + r1) * (HD / 2) + lane * 16;
       const uint32_t d = dst0 + st * SB;
-      const unsigned char *k0 = c.kc + p.x * c.kc_step + o0, *k1 = c.kc + p.y * c.kc_step + o1;
-      const unsigned char *v0 = c.vc + p.x * c.vc_step + o0, *v1 = c.vc + p.y * c.vc_step + o1;
+      const unsigned char *k0 = c.kc + (size_t)px * kc_step + o0, *k1 = c.kc + (size_t)py * kc_step + o1;
+      const unsigned char *v0 = c.vc + (size_t)px * vc_step + o0, *v1 = c.vc + (size_t)py * vc_step + o1;
 #pragma unroll
       for (int i = 0; i < NI; ++i) {
         copy(d + i * 512, k0 + i * 512);
@@ -211,13 +217,12 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
         copy(d + kUnit * HD / 2 + i * 512, v0 + i * 512);
         copy(d + kUnit * HD / 2 + (NI + i) * 512, v1 + i * 512);
       }
-      if (lane < 16) copy(d + kUnit * HD, sc0 + (lane & 4 ? p.y : p.x) * sc_step + (lane & 4 ? r1 : r0) * 4);
+      if (lane < 16) copy(d + kUnit * HD, sc0 + (size_t)(lane & 4 ? py : px) * sc_step + (lane & 4 ? r1 : r0) * 4);
     }
     cp_commit();
   };
 #pragma unroll
-  for (int i = 0; i < NST - 1; ++i) issue(u0 + warp + i * kWarps, i, pages_of(u0 + warp + i * kWarps));
-  int2 next = pages_of(u0 + warp + (NST - 1) * kWarps);
+  for (int i = 0; i < NST - 1; ++i) issue(i, i);
 
   // B operands of q: this lane has row g of each tile, dims 32 t (16 t) and on
   uint32_t qb[NT][2 * KW][2];
@@ -286,11 +291,10 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   const int kg = g ^ ((g >> 1) & 1), ka = (2 * t) ^ (t & 1), kb = ka ^ 1;
   bool force = true;  // a row has no maximum yet
   int st = 0, st_in = NST - 1;
-  for (int u = u0 + warp; u < units; u += kWarps) {
+  for (int k = NST - 1, u = u0 + warp; u < units; u += kWarps, ++k) {
     cp_wait_stages();
     __syncwarp();  // everybody's copies have landed, and everybody is done with the stage before
-    issue(u + (NST - 1) * kWarps, st_in, next);
-    next = pages_of(u + NST * kWarps);
+    issue(k, st_in);
     st_in = st;
     {
       const unsigned char* sk = ring + st * SB;
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
             x[h][1] = v.y;
           }
         }
-        float acc[NT][4] = {};
+        float acc[NT][4] = {}, acc2[NT][4] = {};  // (two chains of products)
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
           const uint32_t x0 = x[0][i] >> 8, x1 = x[1][i] >> 8;
@@ -328,9 +332,13 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma_f16(acc[nt], lo[0], lo[1], lo[2], lo[3], qb[nt][2 * i][0], qb[nt][2 * i][1]);
-            mma_f16(acc[nt], hi[0], hi[1], hi[2], hi[3], qb[nt][2 * i + 1][0], qb[nt][2 * i + 1][1]);
+            mma_f16(acc2[nt], hi[0], hi[1], hi[2], hi[3], qb[nt][2 * i + 1][0], qb[nt][2 * i + 1][1]);
           }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][e] += acc2[nt][e];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int key = q * 16 + h * 8 + kg;
@@ -548,13 +556,12 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
       }
     }
     if (u0 == 0 && lane == 0) {  // (the CTA of unit x is that of the largest i with i all / ctas <= x)
-      const long long last = at + ld.units - 1;
-      const int end_cta = whole ? blockIdx.x : (int)(((last + 1) * ctas - 1) / all);
+      const int end_cta = whole ? blockIdx.x : (int)(((s_stop - left + ld.units) * s_ctas - 1) / s_all);
       ws.where[n * a.Hq + h] = make_int2(blockIdx.x, (end_cta - (int)blockIdx.x) << 6 | !head_part << 5 | r);
     }
   }
-  at += u1 - u0;
-  if (at >= stop_at) break;
+  left -= u1 - u0;
+  if (left <= 0) break;
   // the next tile: of this sequence, or of the next with any
   u0 = -kStart;
   if (++item == ld.tiles * a.Hkv) {
@@ -682,7 +689,7 @@ cudaError_t launch(const PackedArgs& p, const Kv4Args& c, void* d_ws, cudaStream
   // no more CTAs than units there can be
   const long long units = (((long long)c.width << c.page_log) + kUnit - 1) / kUnit;
   const long long tiles = ((long long)(p.start ? min((long long)p.max_rows * p.B, (long long)p.N) : p.B) * (p.Hq / p.Hkv) + 8 * NT - 1) / (8 * NT) + p.B;
-  const int grid = (int)min((long long)min(kMaxCtas / NT, kResident<NT> * sms), (tiles * p.Hkv * units + kLeast - 1) / kLeast);
+  const int grid = (int)min((long long)kResident<NT> * min(sms, kSms), (tiles * p.Hkv * units + kLeast - 1) / kLeast);
   kern<<<grid, kThreads, kSmem<HD>, s>>>(p, c, Kv4Shape{FastDiv(p.Hkv), FastDiv(p.Hq / p.Hkv)}, ws);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -710,8 +717,8 @@ cudaError_t launch_rows(const PackedArgs& p, const Kv4Args& c, void* ws, cudaStr
 }  // namespace
 
 size_t kv4_attention_ws_bytes(const PackedArgs& p) {
-  // (half the CTAs with tiles of twice the rows: the same)
-  return 8ull * p.N * p.Hq + 2ull * kMaxCtas * 8 * (p.hd + 2) * sizeof(float);
+  static_assert(kResident<1> * 8 <= kResident<2> * 16, "the larger of the two forms");
+  return 8ull * p.N * p.Hq + 2ull * kSms * kResident<2> * 16 * (p.hd + 2) * sizeof(float);
 }
 
 cudaError_t launch_kv4_attention(const PackedArgs& p, const Kv4Args& c, void* ws, cudaStream_t s) {

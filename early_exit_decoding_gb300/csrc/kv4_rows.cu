@@ -264,8 +264,8 @@ rl_status check_kv4(const char* who, const rl_kv4* c, const PackedArgs& p, Kv4Ar
   if (p.B > 1 && (c->table_stride < c->table_width || c->table_stride >= 1ll << 40))
     return op_error(who, RL_ERR_INVALID_ARG, "table_stride must be at least table_width, below 2^40");
   for (int i = 0; i < 2 && c->n_pages > 1; ++i) {
-    if (c->code_stride[i] % 16 || c->scale_stride[i] % 8 || c->code_stride[i] >= 1ll << 40 || c->scale_stride[i] >= 1ll << 40)
-      return op_error(who, RL_ERR_UNSUPPORTED, "page strides must be whole multiples of 16 bytes, below 2^40");
+    if (c->code_stride[i] % 16 || c->scale_stride[i] % 8 || c->code_stride[i] >= 1ll << 31 || c->scale_stride[i] >= 1ll << 30)
+      return op_error(who, RL_ERR_UNSUPPORTED, "page strides must be whole multiples of 16 bytes, below 2^31 bytes");
     if (c->code_stride[i] < rows * (p.hd / 2) || c->scale_stride[i] < rows * 2)
       return op_error(who, RL_ERR_INVALID_ARG, "pages overlap");
   }
@@ -275,10 +275,11 @@ rl_status check_kv4(const char* who, const rl_kv4* c, const PackedArgs& p, Kv4Ar
   o->vc = static_cast<unsigned char*>(c->v_codes);
   o->km = static_cast<uint32_t*>(c->k_scale);
   o->vm = static_cast<uint32_t*>(c->v_scale);
-  o->kc_step = c->code_stride[0];
-  o->vc_step = c->code_stride[1];
-  o->km_step = c->scale_stride[0] / 2;
-  o->vm_step = c->scale_stride[1] / 2;
+  const bool many = c->n_pages > 1;  // (of one page no stride matters)
+  o->kc_step = many ? c->code_stride[0] : 0;
+  o->vc_step = many ? c->code_stride[1] : 0;
+  o->km_step = many ? c->scale_stride[0] / 2 : 0;
+  o->vm_step = many ? c->scale_stride[1] / 2 : 0;
   o->table = c->d_table;
   o->table_step = p.B > 1 ? c->table_stride : 0;
   o->width = c->table_width;

@@ -599,9 +599,9 @@ RL_API rl_status rl_packed_attention(const rl_packed_desc* p, const void* d_q, c
  * stands for m + s c; the code of dim d is the nibble at bits 4 (d % 8) of the
  * row's 32-bit word d / 8 (the packing of the exit layers).
  *   k_codes, v_codes  [n_pages][n_kv_heads][page][head_dim / 2] bytes, 16-byte
- *                     aligned, pages code_stride (k, v) bytes apart (multiples of 16)
+ *                     aligned, pages code_stride (k, v) bytes apart (multiples of 16, below 2^31)
  *   k_scale, v_scale  [n_pages][n_kv_heads][page][2] (s, m), 16-byte aligned,
- *                     pages scale_stride (k, v) elements apart (multiples of 8)
+ *                     pages scale_stride (k, v) elements apart (multiples of 8, below 2^30)
  *   d_table           [batch][table_width] int32: page i of sequence b holds its
  *                     positions i page .. (i + 1) page - 1; rows table_stride entries apart
  * Entries past a sequence's length are not used; one outside [0, n_pages) that

@@ -13,10 +13,12 @@
 // differs from that of exact weights only where u is that near a border (fp32
 // sums: 1 in 50 rows of 128,256 logits with a long tail).
 //
-// A row is read once: a cluster of CTAs holds it in shared memory, each a part
-// whose warps have contiguous segments.  A cut is found a digit of 9 bits at a
-// time from a histogram of the ids that agree in the digits before (counts, or
-// weights in three limbs of 17 bits that a part's sums do not overflow); the
+// A cluster of CTAs takes a row, each a part whose warps have contiguous
+// segments, and reads it from HBM once and then from L2 (held in shared memory
+// no more than half of 64 rows of 128,256 fit the SMs at once: 91 us).  A cut is
+// found a digit of 9 bits at a time from a histogram of the ids that agree in
+// the digits before (counts, or weights in three limbs of 16 bits, whose sums
+// over a part of at most 65,536 ids stay in 32); the
 // digits are those of -log2 of the weight first, in fixed point (even bins where
 // weights matter), then of the logit's bits and of the id, until no more than
 // kList ids are left, which are ordered one against another.  A small top-k
@@ -56,8 +58,8 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSplit = 16;    // CTAs of a row's cluster
 constexpr int kBins = kThreads;  // of a digit (9 bits), one a thread
 constexpr int kList = 128;       // ids that are ordered one against another
-constexpr int kGather = 1024;    // ids of a digit's bin that are brought together before the next 
-constexpr unsigned long long kWaitNs = 2000000000ull;  // a wait gives up after two seconds
+constexpr int kGather = 1024;    // a part's ids of a digit's bin that are brought together before the next 
+constexpr int kMostIds = 65536;  // of a part
 
 __device__ __forceinline__ uint32_t order_bits(float x) {
   const uint32_t u = x != x ? 0x7fffffffu : __float_as_uint(x + 0.f);
@@ -115,16 +117,6 @@ __device__ __forceinline__ u64 warp_scan64(u64 v, int lane) {
   return v;
 }
 
-template <typename T>
-__device__ __forceinline__ T of_float(float x) {
-  if constexpr (sizeof(T) == 4)
-    return x;
-  else if constexpr (std::is_same<T, bf16>::value)
-    return __float2bfloat16(x);
-  else
-    return __float2half(x);
-}
-
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
@@ -149,7 +141,6 @@ struct List {
   u64 key[kList];
 };
 struct Shared {
-  uint64_t full;            // the row's copies
   u64 table[64];
   uint32_t hist[2][4][kBins];  // by a digit's parity: counts, weights' limbs
   List list[2];             // this part's ids that are ordered one against another: for top-k, for top-p
@@ -165,7 +156,7 @@ struct Shared {
   u64 before;               // in front of the digit's bin
   float lo, hi;             // the logits whose digits so far are the cut's
   u64 cut;
-  uint32_t count;           // ids of the bin
+  uint32_t count, own;      // ids of the bin, and this part's
   int bin;
   float ch, cl, least;      // log2(e) / T in two parts; min-p's logit
   double span;              // T ln min_p
@@ -222,7 +213,8 @@ template <typename T>
 struct Row {
   static constexpr int VE = Vec<T>::kN;
   Shared& s;
-  const uint4* x;      // this part's logits, in shared memory: whole vectors, -infinity in front of and behind them
+  const T* x;          // this part's logits from the 16-byte boundary in front of them on
+  int off, end;        // where they start and end (elements)
   int first, id0, id1;  // id of the first vector's first element; this part's ids
   int i0, i1;          // this warp's segment (vectors)
   int split, tid, lane, warp;
@@ -230,18 +222,47 @@ struct Row {
   Weight w;
 
   __device__ __forceinline__ int id(int vec, int e) const { return first + vec * VE + e; }
-  // f(logit, id) of every element of vectors b .. e - 1, the lanes' in turn
-  template <typename F>
-  __device__ __forceinline__ void each(int b, int e, F f) const {
-    for (int i = b + lane; i < e; i += 32) {
-      const Vec<T> v(x[i]);
+  // Vector i; what is not of this part is -infinity (and not read).
+  __device__ __forceinline__ uint4 load(int i) const {
+    if (i * VE >= off && (i + 1) * VE <= end) return __ldg(reinterpret_cast<const uint4*>(x) + i);
+    return edge(i);
+  }
+  __device__ __noinline__ uint4 edge(int i) const {
+    constexpr uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, bf16>::value ? 0xff80u : 0xfc00u;
+    uint32_t w[4] = {};
 #pragma unroll
-      for (int k = 0; k < VE; ++k) f(v.v[k], id(i, k));
+    for (int k = 0; k < VE; ++k) {
+      const int at = i * VE + k;
+      uint32_t v = none;
+      if (at >= off && at < end) v = sizeof(T) == 4 ? reinterpret_cast<const uint32_t*>(x)[at] : reinterpret_cast<const uint16_t*>(x)[at];
+      w[k * 4 / VE] |= v << (sizeof(T) == 4 ? 0 : k % 2 * 16);
+    }
+    return make_uint4(w[0], w[1], w[2], w[3]);
+  }
+  // f(logit, id) of every element of vectors b .. e - 1, the lanes' in turn, the
+  // next U vectors on their way meanwhile
+  template <int U, typename F>
+  __device__ __forceinline__ void each(int b, int e, F f) const {
+    uint4 next[U];
+    const uint32_t none = sizeof(T) == 4 ? 0xff800000u : std::is_same<T, bf16>::value ? 0xff80ff80u : 0xfc00fc00u;
+#pragma unroll
+    for (int q = 0; q < U; ++q) next[q] = b + lane + 32 * q < e ? load(b + lane + 32 * q) : make_uint4(none, none, none, none);
+    for (int i = b + lane; i < e; i += 32 * U) {
+#pragma unroll
+      for (int q = 0; q < U; ++q) {
+        const Vec<T> v(next[q]);
+        const int j = i + 32 * q;
+        if (j + 32 * U < e) next[q] = load(j + 32 * U);
+        if (j < e) {
+#pragma unroll
+          for (int k = 0; k < VE; ++k) f(v.v[k], id(j, k));
+        }
+      }
     }
   }
   __device__ __forceinline__ u64 mass(int b, int e, const Cut& cut) const {  // of this lane's
     u64 sum = 0;
-    each(b, e, [&](float v, int i) {
+    each<1>(b, e, [&](float v, int i) {
       if (cut.takes(v, i)) sum += w(v);
     });
     return sum;
@@ -308,24 +329,24 @@ struct Row {
         if constexpr (MASS) {
           const u64 k = w(v);
           atomicAdd(&h[0][bin], 1u);
-          atomicAdd(&h[1][bin], (uint32_t)k & 0x1ffffu);
-          if (k >> 17) atomicAdd(&h[2][bin], (uint32_t)(k >> 17) & 0x1ffffu);
-          if (k >> 34) atomicAdd(&h[3][bin], (uint32_t)(k >> 34));
+          atomicAdd(&h[1][bin], (uint32_t)k & 0xffffu);
+          if (k >> 16) atomicAdd(&h[2][bin], (uint32_t)(k >> 16) & 0xffffu);
+          if (k >> 32) atomicAdd(&h[3][bin], (uint32_t)(k >> 32));
         } else {
           atomicAdd(&h[0][bin], 1u);
         }
       };
       if (MASS && level == 0 && least.v == -INFINITY) {  // (every id)
-        each(i0, i1, [&](float v, int i) {
+        each<1>(i0, i1, [&](float v, int i) {
           if ((m - v) * w.ch < 46.f) add(v, i);
         });
-      } else if (level == 0 || s.count > kGather) {
-        each(i0, i1, [&](float v, int i) {
+      } else if (level == 0 || s.own > kGather) {
+        each<1>(i0, i1, [&](float v, int i) {
           if (agrees(v, i, level)) add(v, i);
         });
       } else {
         // few ids, brought together first (a weight takes a warp the same time for one lane's)
-        each(i0, i1, [&](float v, int i) {
+        each<4>(i0, i1, [&](float v, int i) {
           if (agrees(v, i, level)) s.few[atomicAdd(&s.n_few, 1u)] = key_of(v, i);  // (no more than were counted)
         });
         __syncthreads();
@@ -338,7 +359,7 @@ struct Row {
       // The bin that reaches the goal: of the groups of 32 bins first, then of
       // its group's (all bins of all parts took 6000 clocks: 64 KB a CTA from others').
       const int mine = kBins - 1 - tid;  // (the largest first)
-      const u64 own = MASS ? h[1][mine] + ((u64)h[2][mine] << 17) + ((u64)h[3][mine] << 34) : h[0][mine];
+      const u64 own = MASS ? h[1][mine] + ((u64)h[2][mine] << 16) + ((u64)h[3][mine] << 32) : h[0][mine];
       const u64 own32 = warp_sum64(own);
       if (lane == 0) s.group[level & 1][warp] = own32;
       barrier();
@@ -353,7 +374,7 @@ struct Row {
       const int g = min(reach ? __ffs(reach) - 1 : 31, kWarps - 1);
       const int bin = kBins - 1 - (g * 32 + lane);
       if (warp < split) {  // (a warp a part)
-        s.of_bin[warp][lane] = MASS ? remote32(&h[1][bin], warp) + ((u64)remote32(&h[2][bin], warp) << 17) + ((u64)remote32(&h[3][bin], warp) << 34) : 0;
+        s.of_bin[warp][lane] = MASS ? remote32(&h[1][bin], warp) + ((u64)remote32(&h[2][bin], warp) << 16) + ((u64)remote32(&h[3][bin], warp) << 32) : 0;
         s.in_bin[warp][lane] = remote32(&h[0][bin], warp);
       }
       __syncthreads();
@@ -373,6 +394,7 @@ struct Row {
           s.bin = bin;
           s.before = inc - sum;
           s.count = count;
+          s.own = h[0][bin];
         }
         if (level < 4) {
           // the logits of that bin, by a search 16 ways at once on each side
@@ -408,7 +430,7 @@ struct Row {
       if (s.count <= kList || level == kLevels - 1) break;  // (a bin of the last digit is one id)
     }
     // the ids left, one against another
-    each(i0, i1, [&](float v, int i) {
+    each<4>(i0, i1, [&](float v, int i) {
       if (agrees(v, i, kLevels)) push(list, key_of(v, i));
     });
     barrier();
@@ -452,33 +474,16 @@ __device__ __forceinline__ u64 share_up(float p, u64 S) {
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a, const __grid_constant__ Pow2Table pow2, int split) {
-  extern __shared__ __align__(16) unsigned char smem_row[];
   __shared__ Shared s;
   const int row = blockIdx.x / split, part = blockIdx.x - row * split;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
 
-  // This part's ids, to shared memory at the address modulo 16 that they have:
-  // whole 16 bytes by bulk copies, the edges by threads.
+  // this part's ids, in whole vectors of 16 bytes
   constexpr int VE = Vec<T>::kN;
-  const int v0 = (int)((long long)V * part / split), v1 = (int)((long long)V * (part + 1) / split);
+  const int v0 = (int)((long long)V * part / split), v1 = (int)((long long)V * (part + 1) / split), n = v1 - v0;
   const T* src = static_cast<const T*>(a.x) + (long long)row * a.ld + v0;
-  const int off = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T)), n = v1 - v0;  // (elements)
+  const int off = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));  // (elements)
   const int nvec = (off + n + VE - 1) / VE;
-  T* const dst = reinterpret_cast<T*>(smem_row) + off;
-  const int head = min(n, off ? VE - off : 0), whole = (n - head) / VE * VE, tail = head + whole;
-  if (tid == 0) {
-    mbar_init(&s.full, 1);
-    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    mbar_expect_tx(&s.full, whole * sizeof(T));
-    for (int b = 0; b < whole; b += 8192)
-      bulk_g2s(dst + head + b, src + head + b, min(8192, whole - b) * sizeof(T), &s.full);
-  }
-  if (tid < head) dst[tid] = src[tid];
-  if (tid >= 32 && tail + tid - 32 < n) dst[tail + tid - 32] = src[tail + tid - 32];
-  // (what fills the first and the last vector has weight 0, and never comes before an id of the row but in a row of -infinity alone)
-  const T none = of_float<T>(-INFINITY);
-  if (tid >= 64 && tid - 64 < off) dst[64 - tid - 1] = none;
-  if (tid >= 96 && off + n + tid - 96 < nvec * VE) dst[n + tid - 96] = none;
   if (tid < 64) s.table[tid] = pow2.t[tid];
   if (tid < 2) s.list[tid].n = 0;
   if (tid == 0) s.mass = 0;
@@ -486,8 +491,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const int k = a.set.d_top_k ? a.set.d_top_k[row] : a.set.top_k;
   const float tp = a.set.d_top_p ? a.set.d_top_p[row] : a.set.top_p, mp = a.set.d_min_p ? a.set.d_min_p[row] : a.set.min_p;
   const float u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604644775390625e-8f);
-  // (one thread, while the row is on its way: in 64 bits, which all threads at
-  // once would wait for)
+  // (one thread, in 64 bits, which all threads at once would wait for)
   if (tid == kThreads - 1) {
     const double c = fmin(1.4426950408889634 / (double)temp, 1e38);  // (finite in fp32)
     s.ch = (float)c;
@@ -495,16 +499,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     s.span = mp > 0.f ? (double)temp * log((double)mp) : 0.0;
   }
   __syncthreads();
-  const bool got = __syncthreads_and(mbar_wait_lazy(&s.full, 0, kWaitNs)) != 0;
-  if (!got && tid == 0 && a.err) atomicOr(a.err, RL_DEVERR_TIMEOUT);
 
   const int seg = (nvec + kWarps - 1) / kWarps;
-  Row<T> r{s, reinterpret_cast<const uint4*>(smem_row), v0 - off, v0, v1, min(nvec, warp * seg), min(nvec, (warp + 1) * seg), split, tid, lane, warp,
+  Row<T> r{s, src - off, off, off + n, v0 - off, v0, v1, min(nvec, warp * seg), min(nvec, (warp + 1) * seg), split, tid, lane, warp,
            0.f, Weight{}};
   // the largest logit (the lowest id of equal ones)
   uint32_t top = 0;
   int top_i = 0;
-  r.each(r.i0, r.i1, [&](float v, int i) {
+  r.template each<4>(r.i0, r.i1, [&](float v, int i) {
     const uint32_t o = order_bits(v);
     if (o > top) {
       top = o;
@@ -526,10 +528,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     best = x;
   }
   const float m = value_of((uint32_t)(best >> 32));
-  if (!got || !(fabsf(m) < INFINITY) || !(temp > 0.f)) {
+  if (!(fabsf(m) < INFINITY) || !(temp > 0.f)) {
     if (part == 0 && tid == 0) {
       a.token[row] = m == -INFINITY ? 0 : (int)(0xffffffffu - (uint32_t)best);
-      if (a.logprob) a.logprob[row] = got && fabsf(m) < INFINITY ? 0.f : NAN;
+      if (a.logprob) a.logprob[row] = fabsf(m) < INFINITY ? 0.f : NAN;
     }
     if (split > 1) cluster_barrier();
     return;
@@ -576,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     __syncthreads();
     const uint32_t from = (uint32_t)s.bin;
     if (top && mine >= from)
-      r.each(r.i0, r.i1, [&](float v, int i) {
+      r.template each<4>(r.i0, r.i1, [&](float v, int i) {
         if (r.place_q(v) >> 23 >= from) r.push(s.list[0], key_of(v, i));
       });
     r.barrier();
@@ -660,16 +662,47 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   // and of each part: in front of this one's, this one's, all
   r.barrier();
   const u64 of_part = lane < split ? remote64(&s.mass, lane) : 0;
-  u64 front = warp_sum64(lane < part ? of_part : 0);
   const u64 all = warp_sum64(of_part);
-  const u64 here = s.mass;
   const u64 goal = share(u, all);
-  if (front <= goal && goal < front + here) {
-    if (known) segments();
+  // The part it is in; with its segments' sums at hand that part's CTA finds the
+  // id, else all take a share of it first (one alone took 35,000 clocks).
+  u64 upto = of_part;
+#pragma unroll
+  for (int o = 1; o < kMaxSplit; o <<= 1) {
+    const u64 t = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += t;
+  }
+  const int owner = __ffs(__ballot_sync(0xffffffffu, lane < split && upto > goal)) - 1;
+  u64 front = __shfl_sync(0xffffffffu, upto - of_part, owner);
+  const int o0 = (int)((long long)V * owner / split), o1 = (int)((long long)V * (owner + 1) / split);
+  const T* osrc = static_cast<const T*>(a.x) + (long long)row * a.ld + o0;
+  const int ooff = (int)((reinterpret_cast<uintptr_t>(osrc) & 15) / sizeof(T)), ovec = (ooff + o1 - o0 + VE - 1) / VE;
+  r.x = osrc - ooff;
+  r.off = ooff;
+  r.end = ooff + o1 - o0;
+  r.first = o0 - ooff;
+  int base = 0, width = kWarps * ((ovec + kWarps - 1) / kWarps);  // this CTA's vectors of it
+  bool mine = part == owner;
+  if (known) {
+    const int each = (ovec + split * kWarps - 1) / (split * kWarps);  // a warp's
+    base = part * kWarps * each;
+    width = kWarps * each;
+    const u64 sum = warp_sum64(r.mass(min(ovec, base + warp * each), min(ovec, base + (warp + 1) * each), keep));
+    if (lane == 0) s.sums[warp] = sum;
+    __syncthreads();
+    const u64 total = warp_sum64(lane < kWarps ? s.sums[lane] : 0);
+    if (tid == 0) s.best = total;  // (its last use is long past)
+    r.barrier();
+    const u64 x = lane < split ? remote64(&s.best, lane) : 0;
+    front += warp_sum64(lane < part ? x : 0);
+    mine = front <= goal && goal < front + total;
+  }
+  if (mine) {
     // the segment it is in, then the sixteenth of that, then the id
+    const int step = width / kWarps;
     int ow = 0;
     while (front + s.sums[ow] <= goal) front += s.sums[ow++];
-    const int s0 = min(nvec, ow * seg), s1 = min(nvec, s0 + seg), sub = (s1 - s0 + kWarps - 1) / kWarps;
+    const int s0 = min(ovec, base + ow * step), s1 = min(ovec, s0 + step), sub = (s1 - s0 + kWarps - 1) / kWarps;
     auto range = [&](int j, int* b, int* e) {
       *b = min(s1, s0 + j * sub);
       *e = min(s1, *b + sub);
@@ -686,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
       for (int i = b; i < e; i += 32) {
         u64 w[VE] = {}, x = 0;
         if (i + lane < e) {
-          const Vec<T> v(r.x[i + lane]);
+          const Vec<T> v(r.load(i + lane));
 #pragma unroll
           for (int j = 0; j < VE; ++j) x += w[j] = keep.takes(v.v[j], r.id(i + lane, j)) ? r.w(v.v[j]) : 0;
         }
@@ -716,11 +749,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
 }
 
-// CTAs a row is split over: as many as bring a part to 64 KB (so that two or
-// three of them share an SM), more where the rows alone do not fill the GPU.
-int pick_split(int rows, int V, int size, int sms) {
+// CTAs a row is split over: as many as its parts' sums need, and more while all
+// rows' are at work at once (two an SM) and have 4096 ids at least.
+int pick_split(int rows, int V, int sms) {
   int s = 1;
-  while (s < kMaxSplit && ((long long)V * size > 65536ll * s || ((long long)rows * s * 2 <= sms && V > 4096 * s))) s *= 2;
+  while (s < kMaxSplit && (V > kMostIds * s || ((long long)rows * s <= sms && V > 4096 * s))) s *= 2;
   return s;
 }
 
@@ -731,24 +764,21 @@ cudaError_t launch(const SampleArgs& a, const Pow2Table& table, cudaStream_t st)
   if (e == cudaSuccess) e = device_sm_count(dev, &sms);
   if (e != cudaSuccess) return e;
   auto kern = k_sample<T>;
-  constexpr int kMost = (1 << 19) / kMaxSplit * 4 + 64;
   {
     static std::mutex mu;
     static bool done[kOpDevices] = {};
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
-      e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
-      if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      e = cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
       if (e != cudaSuccess) return e;
       done[dev] = true;
     }
   }
-  const int split = pick_split(a.rows, a.V, sizeof(T), sms);
+  const int split = pick_split(a.rows, a.V, sms);
   if ((long long)a.rows * split >= 1ll << 31) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.rows * split);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (a.V / split + 1) * sizeof(T) + 32;
   cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -152,7 +152,7 @@ def _load():
         "rl_kv4_read": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P]),
         "rl_kv4_attention_workspace": (I, [ctypes.POINTER(rl_packed_desc), ctypes.POINTER(ctypes.c_uint64)]),
         "rl_kv4_attention": (I, [ctypes.POINTER(rl_kv4), ctypes.POINTER(rl_packed_desc), P, P, P, P, P, P, ctypes.c_uint64, P, P]),
-        "rl_sample": (I, [P, I, I, I, ctypes.c_int64, P, ctypes.POINTER(rl_sampling), P, P, P, P]),
+        "rl_sample": (I, [P, I, I, I, ctypes.c_int64, P, ctypes.POINTER(rl_sampling), P, P, P]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -444,9 +444,9 @@ def rl_kv4_attention(cache, desc, d_start, d_kv_len, d_q, d_out, d_lse, d_ws, ws
                                  _ptr(d_out), _ptr(d_lse), _ptr(d_ws), ws_bytes, _ptr(d_err), _stream(stream)))
 
 
-def rl_sample(d_logits, dtype, rows, vocab, row_stride, d_u, settings, d_token, d_logprob, d_err=None, stream=None):
+def rl_sample(d_logits, dtype, rows, vocab, row_stride, d_u, settings, d_token, d_logprob, stream=None):
     _check(_lib.rl_sample(_ptr(d_logits), dtype, rows, vocab, row_stride, _ptr(d_u), ctypes.byref(settings), _ptr(d_token),
-                          _ptr(d_logprob), _ptr(d_err), _stream(stream)))
+                          _ptr(d_logprob), _stream(stream)))
 
 
 # --------------------------------------------------------------- conveniences
@@ -1178,7 +1178,7 @@ def kv4_attention(q, cache, table, kv_len, start=None, max_rows=None, scale=None
     return o
 
 
-def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, err=None, stream=None):
+def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, stream=None):
     """Draws one token a row of ``logits [R][V]`` (as token_logprobs) with the
     random numbers ``u`` (fp32 [R] in [0, 1)).  Each setting is a number or a
     tensor [R] (fp32; top_k int32).  Returns a dict: ``token`` int32 [R] and
@@ -1202,16 +1202,14 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
             given.append(x)
         else:
             setattr(s, key, _int32_of(int(x)) if key == "top_k" else float(x))
-    dev = _operands(name, (logits, u, err, *given))
+    dev = _operands(name, (logits, u, *given))
     if u.dtype != torch.float32 or u.shape != (R,) or not u.is_contiguous():
         _refuse(f"{name}: u must be contiguous fp32 ({R},)")
-    if err is not None:
-        _int32(name, "err", err, (1,))
     o = dict(out) if out else {}
     token = _buffer(o, "token", (R,), logits, torch.int32, stream, name)
     lp = _buffer(o, "logprob", (R,), logits, torch.float32, stream, name)
     _run(dev, stream, _lib.rl_sample, logits.data_ptr(), dt, R, V, logits.stride(0) if R > 1 else V, u.data_ptr(), s,
-         token.data_ptr(), lp.data_ptr(), _addr(err))
+         token.data_ptr(), lp.data_ptr())
     return o
 
 

@@ -1,5 +1,11 @@
 // Causal attention of packed prompts (rl_packed_attention): the rows of
-// attn_rows_tc.cu, whose CTAs find their sequence and row tile themselves.
+// attn_rows_tc.cu, whose CTAs find their sequence and row tile themselves
+// (row_tile: longest first, so the last CTAs to start have the fewest keys).
+//
+// Tensor cores bound it as they do one prompt: two prompts of 8192 and 5001
+// tokens, 32 heads, 8 KV heads, head_dim 128: 600 us, 1.26 PFLOP/s, 0.65 of the
+// measured bf16 rate; 12 of 37 to 2999: 325 us, 0.49, as a CTA's start and end
+// weigh more on fewer key tiles.  17 of 1 to 97 tokens: 16 us, one tile's chain.
 #include <string.h>
 
 #include "kv4.cuh"

@@ -1,6 +1,6 @@
 // Many query rows against one key range on the 5th-generation tensor cores:
-// prompts under a sliding window, and the rows of all sequences against a
-// shared prefix.
+// prompts under a sliding window, packed prompts, and the rows of all sequences
+// against a shared prefix.
 //
 // A CTA takes 256 query rows (query position x the heads that share a KV
 // head; for a prefix, sequence x those heads) as two M = 128 tiles and walks

@@ -564,9 +564,9 @@ RL_API rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const void* d
  * device, not decreasing; NULL, where a call allows it: row b alone).  Strides
  * are in elements; the innermost (head_dim) axis is contiguous.  Requirements:
  * head_dim 64 or 128, n_q_heads a multiple of n_kv_heads, 16-byte starts,
- * strides whole multiples of 16 bytes (RL_ERR_UNSUPPORTED otherwise); what is
- * written has its rows and heads apart (RL_ERR_INVALID_ARG otherwise).  Rows in
- * front of d_start[0] and from d_start[batch] on are left as they were.  An
+ * strides whole multiples of 16 bytes, batch at most 2^16, rows 2^27,
+ * n_kv_heads 2^10 (RL_ERR_UNSUPPORTED otherwise); what is written has its rows
+ * and heads apart (RL_ERR_INVALID_ARG otherwise).  Rows in front of d_start[0] and from d_start[batch] on are left as they were.  An
  * entry of d_start outside [0, rows], or below the one before, sets
  * RL_DEVERR_CAPACITY and is moved there. */
 typedef struct {
@@ -586,9 +586,8 @@ typedef struct {
  * ([rows][n_q_heads] fp32, may be NULL) as rl_window_attention, with its
  * roundings; keys a row does not see have no part in its result, whatever they
  * hold.  A sequence of more than max_rows rows sets RL_DEVERR_CAPACITY and has
- * its first max_rows rows computed, the others are left as they were.  rows is
- * at most 2^27, batch 2^20.  One launch, no workspace, results repeat bit for
- * bit. */
+ * its first max_rows rows computed, the others are left as they were.  One
+ * launch, no workspace, results repeat bit for bit. */
 RL_API rl_status rl_packed_attention(const rl_packed_desc* p, const void* d_q, const void* d_k,
                                      const void* d_v, const int32_t* d_start, void* d_out, float* d_lse,
                                      int32_t* d_err, rl_stream_t stream);
@@ -678,7 +677,6 @@ RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, cons
  *   settings  of all rows, or (a pointer that is not NULL) one a row
  *   d_token   [rows] int32
  *   d_logprob [rows] fp32, may be NULL: ln of the token's share of the kept weights
- *   d_err     [1] int32, may be NULL: RL_DEVERR_* bits are ORed into it
  * Weights are whole multiples of 2^-44 (their exponentials are good to
  * 2^-38), sums are exact, so results repeat bit for bit and do not depend on
  * how a row is split.  Logits of -infinity are never drawn.  A row with a NaN or
@@ -699,7 +697,7 @@ typedef struct {
 } rl_sampling;
 RL_API rl_status rl_sample(const void* d_logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
                            const float* d_u, const rl_sampling* settings, int32_t* d_token, float* d_logprob,
-                           int32_t* d_err, rl_stream_t stream);
+                           rl_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -56,7 +56,7 @@ ALL = ("packed", "append", "read", "attention")
 DESC = [(dict(desc=False), "INVALID_ARG"), (dict(dtype=0), "UNSUPPORTED"), (dict(dtype=3), "UNSUPPORTED"), (dict(batch=0), "INVALID_ARG"),
         (dict(rows=0), "INVALID_ARG"), (dict(max_rows=-1), "INVALID_ARG"), (dict(n_q_heads=0), "INVALID_ARG"), (dict(n_kv_heads=0), "INVALID_ARG"),
         (dict(n_kv_heads=3), "UNSUPPORTED"), (dict(head_dim=96), "UNSUPPORTED"), (dict(scale=-1.0), "INVALID_ARG"),
-        (dict(scale=float("nan")), "INVALID_ARG"), (dict(batch=(1 << 20) + 1), "UNSUPPORTED"), (dict(rows=(1 << 27) + 1), "UNSUPPORTED"),
+        (dict(scale=float("nan")), "INVALID_ARG"), (dict(batch=(1 << 16) + 1), "UNSUPPORTED"), (dict(n_kv_heads=2048, n_q_heads=2048), "UNSUPPORTED"), (dict(rows=(1 << 27) + 1), "UNSUPPORTED"),
         (dict(rows=1 << 27, n_q_heads=32), "UNSUPPORTED")]
 
 
@@ -104,7 +104,7 @@ def _sample(river, **kw):
     a.update({k: v for k, v in kw.items() if k in a})
     s = river.rl_sampling(kw.get("temperature", 1.0), kw.get("top_k", 0), kw.get("top_p", 1.0), kw.get("min_p", 0.0))
     return river._lib.rl_sample(P(a["logits"]), a["dtype"], a["rows"], a["vocab"], a["stride"], P(a["u"]), ctypes.byref(s) if a["set"] else None,
-                                P(a["token"]), None, None, None)
+                                P(a["token"]), None, None)
 
 
 @pytest.mark.parametrize("kw,status", [

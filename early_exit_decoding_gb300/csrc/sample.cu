@@ -29,9 +29,9 @@
 // What bounds it: instructions, some 75 a logit where weights are summed (the
 // exponential's 45, the histogram's 20), and the chain of a digit: histogram,
 // barrier, the groups' and the bins' sums from the other parts.  64 rows of
-// 128,256 fp32 logits cut at 0.9 of their mass: 73 us (the row's first reading
+// 128,256 fp32 logits cut at 0.9 of their mass: 71 us (the row's first reading
 // 7, the histogram 16, the next digit 11, the id 5, the rest between them); 500
-// rows of 50,257 bf16 logits, each with settings of its own: 134 us; one row
+// rows of 50,257 bf16 logits, each with settings of its own: 118 us; one row
 // with top-k 50 and top-p 0.95: 14 us.
 #include <float.h>
 #include <math.h>
@@ -65,6 +65,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMaxSplit = 16;    // CTAs of a row's cluster
 constexpr int kBins = kThreads;  // of a digit (9 bits), one a thread
 constexpr int kList = 128;       // ids that are ordered one against another
+constexpr int kFew = 96;         // top-k that needs no histogram of the row
 constexpr int kGather = 1024;    // a part's ids of a digit's bin that are brought together before the next 
 constexpr int kMostIds = 65536;  // of a part
 
@@ -305,6 +306,55 @@ struct Row {
     if (at < kList) l.key[at] = k;
   }
 
+  // s.bin: the bin, from the largest down, at which the cluster's running sum over
+  // the histograms h reaches the goal from `before` on (bin 0 if none does); what
+  // is in front of it, its ids, and this part's.  Of the groups of 32 bins first,
+  // then of its group's (all bins of all parts took 6000 clocks: 64 KB a CTA from
+  // others').  *own: this part's sum in bin kBins - 1 - tid.  Warp 0 has the
+  // results (the others after a barrier).
+  template <bool MASS, typename Goal>
+  __device__ __forceinline__ void reach_bin(const uint32_t (*h)[kBins], int parity, u64 before, bool first_digit, u64* goal, Goal goal_of,
+                                            u64* own) {
+    const int mine = kBins - 1 - tid;  // (the largest first)
+    *own = MASS ? h[1][mine] + ((u64)h[2][mine] << 16) + ((u64)h[3][mine] << 32) : h[0][mine];
+    const u64 own32 = warp_sum64(*own);
+    if (lane == 0) s.group[parity][warp] = own32;
+    barrier();
+    {
+      const u64 x = warp_sum64(lane < split ? remote64(&s.group[parity][warp], lane) : 0);
+      if (lane == 0) s.red[warp] = x;
+    }
+    __syncthreads();
+    const u64 of_group = lane < kWarps ? s.red[lane] : 0, upto = before + warp_scan64(of_group, lane);
+    if (first_digit) *goal = goal_of(__shfl_sync(0xffffffffu, upto, 31));
+    const unsigned reach = __ballot_sync(0xffffffffu, upto >= *goal);
+    const int g = min(reach ? __ffs(reach) - 1 : 31, kWarps - 1);
+    const int bin = kBins - 1 - (g * 32 + lane);
+    if (warp < split) {  // (a warp a part)
+      s.of_bin[warp][lane] = MASS ? remote32(&h[1][bin], warp) + ((u64)remote32(&h[2][bin], warp) << 16) + ((u64)remote32(&h[3][bin], warp) << 32) : 0;
+      s.in_bin[warp][lane] = remote32(&h[0][bin], warp);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      const u64 front = __shfl_sync(0xffffffffu, upto - of_group, g);
+      u64 sum = 0;
+      uint32_t count = 0;
+      for (int r = 0; r < split; ++r) {
+        sum += s.of_bin[r][lane];
+        count += s.in_bin[r][lane];
+      }
+      if (!MASS) sum = count;
+      const u64 inc = front + warp_scan64(sum, lane);
+      const unsigned it = __ballot_sync(0xffffffffu, reaches(*goal, inc - sum, sum));
+      if (lane == (it ? __ffs(it) - 1 : 31)) {
+        s.bin = bin;
+        s.before = inc - sum;
+        s.count = count;
+        s.own = h[0][bin];
+      }
+    }
+  }
+
   // The largest key at which the running sum (ids that `least` takes, from the
   // largest key down) of counts, or weights (MASS), reaches the goal;
   // goal_of(total) gives it from the sum of all.  With MASS s.mass is then this
@@ -353,7 +403,7 @@ struct Row {
         });
       } else {
         // few ids, brought together first (a weight takes a warp the same time for one lane's)
-        each<4>(i0, i1, [&](float v, int i) {
+        each<2>(i0, i1, [&](float v, int i) {
           if (agrees(v, i, level)) s.few[atomicAdd(&s.n_few, 1u)] = key_of(v, i);  // (no more than were counted)
         });
         __syncthreads();
@@ -363,49 +413,13 @@ struct Row {
         }
       }
       __syncthreads();
-      // The bin that reaches the goal: of the groups of 32 bins first, then of
-      // its group's (all bins of all parts took 6000 clocks: 64 KB a CTA from others').
-      const int mine = kBins - 1 - tid;  // (the largest first)
-      const u64 own = MASS ? h[1][mine] + ((u64)h[2][mine] << 16) + ((u64)h[3][mine] << 32) : h[0][mine];
-      const u64 own32 = warp_sum64(own);
-      if (lane == 0) s.group[level & 1][warp] = own32;
-      barrier();
-      {
-        const u64 x = warp_sum64(lane < split ? remote64(&s.group[level & 1][warp], lane) : 0);
-        if (lane == 0) s.red[warp] = x;
-      }
-      __syncthreads();
-      const u64 of_group = lane < kWarps ? s.red[lane] : 0, upto = before + warp_scan64(of_group, lane);
-      if (level == 0) goal = goal_of(__shfl_sync(0xffffffffu, upto, 31));
-      const unsigned reach = __ballot_sync(0xffffffffu, upto >= goal);
-      const int g = min(reach ? __ffs(reach) - 1 : 31, kWarps - 1);
-      const int bin = kBins - 1 - (g * 32 + lane);
-      if (warp < split) {  // (a warp a part)
-        s.of_bin[warp][lane] = MASS ? remote32(&h[1][bin], warp) + ((u64)remote32(&h[2][bin], warp) << 16) + ((u64)remote32(&h[3][bin], warp) << 32) : 0;
-        s.in_bin[warp][lane] = remote32(&h[0][bin], warp);
-      }
-      __syncthreads();
+      u64 own;
+      reach_bin<MASS>(h, level & 1, before, level == 0, &goal, goal_of, &own);
       if (warp == 0) {
-        const u64 front = __shfl_sync(0xffffffffu, upto - of_group, g);
-        u64 sum = 0;
-        uint32_t count = 0;
-        for (int r = 0; r < split; ++r) {
-          sum += s.of_bin[r][lane];
-          count += s.in_bin[r][lane];
-        }
-        if (!MASS) sum = count;
-        const u64 inc = front + warp_scan64(sum, lane);
-        const unsigned it = __ballot_sync(0xffffffffu, reaches(goal, inc - sum, sum));
-        const int who = it ? __ffs(it) - 1 : 31;
-        if (lane == who) {
-          s.bin = bin;
-          s.before = inc - sum;
-          s.count = count;
-          s.own = h[0][bin];
-        }
+        __syncwarp();
         if (level < 4) {
           // the logits of that bin, by a search 16 ways at once on each side
-          const uint32_t digits = want.q | (uint32_t)__shfl_sync(0xffffffffu, bin, who) << shift, dm = mask.q | ((1u << bits) - 1) << shift;
+          const uint32_t digits = want.q | (uint32_t)s.bin << shift, dm = mask.q | ((1u << bits) - 1) << shift;
           uint32_t at = 0;  // ordered logits: the largest with a place below, or (upper lanes) not above
           for (int step = 28; step >= 0; step -= 4) {
             const uint32_t x = at + ((uint32_t)(lane & 15) << step);
@@ -426,7 +440,7 @@ struct Row {
         hi = s.hi;
       }
       if constexpr (MASS) {  // this part's weights in the bins in front
-        const u64 mass = warp_sum64(mine > s.bin ? own : 0);
+        const u64 mass = warp_sum64(kBins - 1 - tid > s.bin ? own : 0);
         if (lane == 0 && mass) atomicAdd(&s.mass, mass);
       }
       const uint32_t digit = (uint32_t)s.bin << shift, dm = ((1u << bits) - 1) << shift;
@@ -437,7 +451,7 @@ struct Row {
       if (s.count <= kList || level == kLevels - 1) break;  // (a bin of the last digit is one id)
     }
     // the ids left, one against another
-    each<4>(i0, i1, [&](float v, int i) {
+    each<2>(i0, i1, [&](float v, int i) {
       if (agrees(v, i, kLevels)) push(list, key_of(v, i));
     });
     barrier();
@@ -556,7 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const float least = mp > 0.f ? s.least : -INFINITY;
   const bool has_k = k >= 1 && k < V;
 
-  if (has_k && k <= kList / 2) {
+  if (has_k && k <= kFew) {
     // Few ids: a bin of -log2 of the weight such that k threads' largest logits
     // reach it; the ids that do are no fewer.
     uint32_t* h = s.hist[0][0];
@@ -564,28 +578,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
     __syncthreads();
     const uint32_t mine = r.place_q(value_of(top)) >> 23;
     if (top) atomicAdd(&h[mine], 1u);
-    r.barrier();
-    const int bin = kBins - 1 - tid;
-    uint32_t count = 0;
-    for (int j0 = 0; j0 < split; j0 += 8) {  // eight parts' loads in flight together
-      uint32_t x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = j0 + j < split ? remote32(&h[bin], j0 + j) : 0u;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) count += x[j];
-    }
-    const u64 inc = warp_scan64(count, lane);
-    __syncthreads();
-    if (lane == 31) s.red[warp] = inc;
-    if (tid == 0) s.bin = 0;  // (fewer than k threads have one: all ids)
-    __syncthreads();
-    u64 front = 0;
-    for (int j = 0; j < warp; ++j) front += s.red[j];
-    if (reaches((u64)k, front + inc - count, count)) s.bin = bin;
+    u64 goal = k, own;
+    r.template reach_bin<false>(s.hist[0], 0, 0, false, &goal, [](u64 x) { return x; }, &own);
     __syncthreads();
     const uint32_t from = (uint32_t)s.bin;
     if (top && mine >= from)
-      r.template each<4>(r.i0, r.i1, [&](float v, int i) {
+      r.template each<2>(r.i0, r.i1, [&](float v, int i) {
         if (r.place_q(v) >> 23 >= from) r.push(s.list[0], key_of(v, i));
       });
     r.barrier();
@@ -757,7 +755,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
 }
 
 // CTAs a row is split over: as many as its parts' sums need, and more while all
-// rows' are at work at once (two an SM) and have 4096 ids at least.
+// rows' are at work at once (two an SM) and have 4096 ids at least (64 rows of
+// 128,256 cut by mass: 71 us in 4 parts, 91 in 8, 167 in 16; one row: 14.4 us in
+// 16; 500 rows of 50,257: 118 us whole, 125 in halves).
 int pick_split(int rows, int V, int sms) {
   int s = 1;
   while (s < kMaxSplit && (V > kMostIds * s || ((long long)rows * s <= sms && V > 4096 * s))) s *= 2;

@@ -153,9 +153,9 @@ __device__ __forceinline__ bool row_tile(const int* start, int B, int N, int mos
     return (int)(((long long)span(b, &first) * rep + rows - 1) / rows);
   };
   const int own = tiles_of(lane);
-  auto above = [&](int L) {  // f(L)
-    int n = max(0, own - L);
-    for (int b = 32 + lane; b < B; b += 32) n += max(0, tiles_of(b) - L);
+  auto above = [&](int L) {  // f(L); at most 2^30, which only starts that overlap pass
+    int n = min(max(0, own - L), 1 << 25);
+    for (int b = 32 + lane; b < B; b += 32) n = min(n + max(0, tiles_of(b) - L), 1 << 25);
     return (int)__reduce_add_sync(0xffffffffu, n);
   };
   int top = own;

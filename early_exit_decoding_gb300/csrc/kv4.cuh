@@ -87,6 +87,7 @@ __device__ __forceinline__ long long page_row(const Kv4Args& c, int hk, int row)
 cudaError_t launch_kv4_append(const PackedArgs& p, const Kv4Args& c, const float2* rope, int rope_len, cudaStream_t s);
 cudaError_t launch_kv4_read(const PackedArgs& p, const Kv4Args& c, void* k, void* v, cudaStream_t s);
 size_t kv4_attention_ws_bytes(const PackedArgs& p);
+bool kv4_attention_fits(const PackedArgs& p, const Kv4Args& c);
 cudaError_t launch_kv4_attention(const PackedArgs& p, const Kv4Args& c, void* ws, cudaStream_t s);
 cudaError_t launch_packed_attention(const PackedArgs& p, cudaStream_t s);
 

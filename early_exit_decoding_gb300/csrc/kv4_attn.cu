@@ -61,6 +61,7 @@ constexpr int kLeast = 4;       // units a CTA takes at least
 // to 8191 positions: 99 us with 0, 84 with 4, 81 with 8, 77 with 12, 78 with 20).
 constexpr int kStart = 12;
 constexpr int kSms = 152;       // the workspace holds the parts of as many SMs' CTAs
+constexpr long long kMostUnits = 1ll << 38;  // of a call: below 2^31 a CTA of a full grid
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kMost = 256.f;  // a weight, or weight times step, that is let pass (1 where it was the largest)
 
@@ -73,6 +74,7 @@ constexpr int kResident = NT == 1 ? 3 : 2;  // CTAs of an SM (four of 128 regist
 
 struct Kv4Shape {
   FastDiv by_heads, by_rep;
+  long long most;  // units of sequences that do not overlap (kMostUnits at most)
 };
 
 // The workspace: of every CTA two parts (its first tile's and its last's), each
@@ -134,6 +136,10 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) all += __shfl_xor_sync(0xffffffffu, all, d);
   all *= a.Hkv;
+  if (all > sh.most) {  // (sequences overlap: not computed)
+    if (tid == 0 && a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
+    return;
+  }
   const long long ctas = max(1ll, min((long long)gridDim.x, all / (kStart + kLeast)));
   const long long at = all * blockIdx.x / ctas, stop_at = blockIdx.x < ctas ? all * (blockIdx.x + 1) / ctas : 0;
   if (at >= stop_at) return;
@@ -143,7 +149,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
     s_ctas = ctas;
     s_stop = stop_at;
   }
-  int left = (int)min(stop_at - at, 0x7fffffffll);  // units of the share to come
+  int left = (int)(stop_at - at);  // units of the share to come
   // the sequence, tile and head, and unit it starts with
   int b = 0, item = 0, u0 = 0;
   Load ld;
@@ -174,137 +180,136 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   }
   unsigned char* const ring = smem + warp * NST * SB;
   for (bool head_part = true;; head_part = false) {
-  const int u1 = min(ld.units, u0 + left);
-  if (u1 <= 0) break;  // (the share ends before the tile's first unit)
-  left += min(u0, 0);
-  u0 = max(u0, 0);
-  const int tile = sh.by_heads.quot(item), hk = item - tile * sh.by_heads.d, row0 = tile * R;
-  const Span sp = seq_span(a, b, false);
-  const int old = max(0, min(__ldg(a.kv_len + b), cap)) - sp.all;  // position of the sequence's first row here
-  const int nrow = min(R, sp.n * rep - row0);
-  // keys that every row sees, and that any row sees
-  const int every = old + sh.by_rep.quot(row0) + 1, any = max(0, old + sh.by_rep.quot(row0 + nrow - 1) + 1);
-  const int units = min(u1, (any + kUnit - 1) / kUnit);
+    const int u1 = min(ld.units, u0 + left);
+    if (u1 <= 0) break;  // (the share ends before the tile's first unit)
+    left += min(u0, 0);
+    u0 = max(u0, 0);
+    const int tile = sh.by_heads.quot(item), hk = item - tile * sh.by_heads.d, row0 = tile * R;
+    const Span sp = seq_span(a, b, false);
+    const int old = max(0, min(__ldg(a.kv_len + b), cap)) - sp.all;  // position of the sequence's first row here
+    const int nrow = min(R, sp.n * rep - row0);
+    // keys that every row sees, and that any row sees
+    const int every = old + sh.by_rep.quot(row0) + 1, any = max(0, old + sh.by_rep.quot(row0 + nrow - 1) + 1);
+    const int units = min(u1, (any + kUnit - 1) / kUnit);
 
-  // this lane's 16-byte pieces of a unit: of k's and v's codes every 512 bytes,
-  // and (lanes 0-15) one of the scales
-  const int head0 = hk << c.page_log;  // the head's first row in a page
-  const bool v_scales = lane & 8;
-  const unsigned char* const sc0 = reinterpret_cast<const unsigned char*>((v_scales ? c.vm : c.km) + head0) + (lane & 3) * 16;
-  const unsigned sc_step = 4u * (unsigned)(v_scales ? c.vm_step : c.km_step), kc_step = (unsigned)c.kc_step, vc_step = (unsigned)c.vc_step;
-  const uint32_t dst0 = smem_u32(ring) + lane * 16;
-  // Pages: lane i has that of the (i % 2)-th 16 keys of this warp's unit number
-  // k0 + i / 2 (of keys that nobody sees: some page of the sequence).
-  int pages = 0;
-  auto look_up = [&](int k0) {
-    const int j = max(0, min((u0 + warp + (k0 + (lane >> 1)) * kWarps) * kUnit + (lane & 1) * 16, any - 1));
-    pages = __ldg(c.table + (long long)b * c.table_step + (j >> c.page_log));
-    if ((unsigned)pages >= (unsigned)c.n_pages) {  // out of the cache: reported, page 0 is read
-      if (a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
-      pages = 0;
-    }
-  };
-  auto copy = [&](uint32_t dst, const unsigned char* src) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  };
-  auto issue = [&](int k, int st) {  // this warp's k-th unit
-    if ((k & 15) == 0) look_up(k);
-    const int u = u0 + warp + k * kWarps;
-    const unsigned px = __shfl_sync(0xffffffffu, pages, 2 * k & 31), py = __shfl_sync(0xffffffffu, pages, (2 * k & 31) | 1);
-    if (u < units) {
-      constexpr int NI = HD / 64;  // pieces of 16 keys
-      const int r0 = (u * kUnit) & in_page, r1 = (u * kUnit + 16) & in_page;
-      const int o0 = (head0 + r0) * (HD / 2) + lane * 16, o1 = (head0 + r1) * (HD / 2) + lane * 16;
-      const uint32_t d = dst0 + st * SB;
-      const unsigned char *k0 = c.kc + (size_t)px * kc_step + o0, *k1 = c.kc + (size_t)py * kc_step + o1;
-      const unsigned char *v0 = c.vc + (size_t)px * vc_step + o0, *v1 = c.vc + (size_t)py * vc_step + o1;
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        copy(d + i * 512, k0 + i * 512);
-        copy(d + (NI + i) * 512, k1 + i * 512);
-        copy(d + kUnit * HD / 2 + i * 512, v0 + i * 512);
-        copy(d + kUnit * HD / 2 + (NI + i) * 512, v1 + i * 512);
+    // this lane's 16-byte pieces of a unit: of k's and v's codes every 512 bytes,
+    // and (lanes 0-15) one of the scales
+    const int head0 = hk << c.page_log;  // the head's first row in a page
+    const bool v_scales = lane & 8;
+    const unsigned char* const sc0 = reinterpret_cast<const unsigned char*>((v_scales ? c.vm : c.km) + head0) + (lane & 3) * 16;
+    const unsigned sc_step = 4u * (unsigned)(v_scales ? c.vm_step : c.km_step), kc_step = (unsigned)c.kc_step, vc_step = (unsigned)c.vc_step;
+    const uint32_t dst0 = smem_u32(ring) + lane * 16;
+    // Pages: lane i has that of the (i % 2)-th 16 keys of this warp's unit number
+    // k0 + i / 2 (of keys that nobody sees: some page of the sequence).
+    int pages = 0;
+    auto look_up = [&](int k0) {
+      const int j = max(0, min((u0 + warp + (k0 + (lane >> 1)) * kWarps) * kUnit + (lane & 1) * 16, any - 1));
+      pages = __ldg(c.table + (long long)b * c.table_step + (j >> c.page_log));
+      if ((unsigned)pages >= (unsigned)c.n_pages) {  // out of the cache: reported, page 0 is read
+        if (a.err) atomicOr(a.err, RL_DEVERR_CAPACITY);
+        pages = 0;
       }
-      if (lane < 16) copy(d + kUnit * HD, sc0 + (size_t)(lane & 4 ? py : px) * sc_step + (lane & 4 ? r1 : r0) * 4);
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int i = 0; i < NST - 1; ++i) issue(i, i);
+    };
+    auto copy = [&](uint32_t dst, const unsigned char* src) {
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+    };
+    auto issue = [&](int k, int st) {  // this warp's k-th unit
+      if ((k & 15) == 0) look_up(k);
+      const int u = u0 + warp + k * kWarps;
+      const unsigned px = __shfl_sync(0xffffffffu, pages, 2 * k & 31), py = __shfl_sync(0xffffffffu, pages, (2 * k & 31) | 1);
+      if (u < units) {
+        constexpr int NI = HD / 64;  // pieces of 16 keys
+        const int r0 = (u * kUnit) & in_page, r1 = (u * kUnit + 16) & in_page;
+        const int o0 = (head0 + r0) * (HD / 2) + lane * 16, o1 = (head0 + r1) * (HD / 2) + lane * 16;
+        const uint32_t d = dst0 + st * SB;
+        const unsigned char *k0 = c.kc + (size_t)px * kc_step + o0, *k1 = c.kc + (size_t)py * kc_step + o1;
+        const unsigned char *v0 = c.vc + (size_t)px * vc_step + o0, *v1 = c.vc + (size_t)py * vc_step + o1;
+  #pragma unroll
+        for (int i = 0; i < NI; ++i) {
+          copy(d + i * 512, k0 + i * 512);
+          copy(d + (NI + i) * 512, k1 + i * 512);
+          copy(d + kUnit * HD / 2 + i * 512, v0 + i * 512);
+          copy(d + kUnit * HD / 2 + (NI + i) * 512, v1 + i * 512);
+        }
+        if (lane < 16) copy(d + kUnit * HD, sc0 + (size_t)(lane & 4 ? py : px) * sc_step + (lane & 4 ? r1 : r0) * 4);
+      }
+      cp_commit();
+    };
+  #pragma unroll
+    for (int i = 0; i < NST - 1; ++i) issue(i, i);
 
-  // B operands of q: this lane has row g of each tile, dims 32 t (16 t) and on
-  uint32_t qb[NT][2 * KW][2];
-  float mul[NT][2], qsum[NT][2];  // of the rows 2 t and 2 t + 1: scores are acc mul s + qsum m
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int i = row0 + nt * 8 + g, tq = sh.by_rep.quot(i);
-    float2 f[4 * KW];
-    float big = 0.f, sum = 0.f;
-    const bool live = nt * 8 + g < nrow;
-    const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long long)(sp.first + (live ? tq : 0)) * a.qs[0] +
-                          (long long)(hk * rep + (live ? i - tq * rep : 0)) * a.qs[1] + 8 * KW * t;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * w);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 v = unpack2<F16>(live ? u4get(x, e) : 0u);
-        f[4 * w + e] = v;
-        big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
-        sum += v.x + v.y;
+    // B operands of q: this lane has row g of each tile, dims 32 t (16 t) and on
+    uint32_t qb[NT][2 * KW][2];
+    float mul[NT][2], qsum[NT][2];  // of the rows 2 t and 2 t + 1: scores are acc mul s + qsum m
+  #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int i = row0 + nt * 8 + g, tq = sh.by_rep.quot(i);
+      float2 f[4 * KW];
+      float big = 0.f, sum = 0.f;
+      const bool live = nt * 8 + g < nrow;
+      const uint16_t* src = static_cast<const uint16_t*>(a.q) + (long long)(sp.first + (live ? tq : 0)) * a.qs[0] +
+                            (long long)(hk * rep + (live ? i - tq * rep : 0)) * a.qs[1] + 8 * KW * t;
+  #pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const uint4 x = *reinterpret_cast<const uint4*>(src + 8 * w);
+  #pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float2 v = unpack2<F16>(live ? u4get(x, e) : 0u);
+          f[4 * w + e] = v;
+          big = fmaxf(big, fmaxf(fabsf(v.x), fabsf(v.y)));
+          sum += v.x + v.y;
+        }
+      }
+  #pragma unroll
+      for (int d = 1; d < 4; d <<= 1) {
+        big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
+        sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      }
+      // 2^e <= the largest < 2^(e + 1); rows of zeros and below 2^-100 as if it were 2^-100
+      const int e = max((int)((__float_as_uint(big) >> 23) & 255) - 127, -100);
+      const float up = __uint_as_float((uint32_t)(127 + min(13 - e, 127)) << 23), up16 = up * 0.0625f;
+  #pragma unroll
+      for (int w = 0; w < KW; ++w) {
+        const float2* v = f + 4 * w;  // dims 0 1, 2 3, 4 5, 6 7 of the word
+        qb[nt][2 * w][0] = pack2<true>(v[0].x * up, v[2].x * up);
+        qb[nt][2 * w][1] = pack2<true>(v[0].y * up16, v[2].y * up16);
+        qb[nt][2 * w + 1][0] = pack2<true>(v[1].x * up, v[3].x * up);
+        qb[nt][2 * w + 1][1] = pack2<true>(v[1].y * up16, v[3].y * up16);
+      }
+      const float sc = a.scale * kLog2e, back = sc * 16777216.f / up;
+  #pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        mul[nt][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
+        qsum[nt][r] = __shfl_sync(0xffffffffu, sum * sc, (2 * t + r) * 4);
       }
     }
-#pragma unroll
-    for (int d = 1; d < 4; d <<= 1) {
-      big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, d));
-      sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    }
-    // 2^e <= the largest < 2^(e + 1); rows of zeros and below 2^-100 as if it were 2^-100
-    const int e = max((int)((__float_as_uint(big) >> 23) & 255) - 127, -100);
-    const float up = __uint_as_float((uint32_t)(127 + min(13 - e, 127)) << 23), up16 = up * 0.0625f;
-#pragma unroll
-    for (int w = 0; w < KW; ++w) {
-      const float2* v = f + 4 * w;  // dims 0 1, 2 3, 4 5, 6 7 of the word
-      qb[nt][2 * w][0] = pack2<true>(v[0].x * up, v[2].x * up);
-      qb[nt][2 * w][1] = pack2<true>(v[0].y * up16, v[2].y * up16);
-      qb[nt][2 * w + 1][0] = pack2<true>(v[1].x * up, v[3].x * up);
-      qb[nt][2 * w + 1][1] = pack2<true>(v[1].y * up16, v[3].y * up16);
-    }
-    const float sc = a.scale * kLog2e, back = sc * 16777216.f / up;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      mul[nt][r] = __shfl_sync(0xffffffffu, back, (2 * t + r) * 4);
-      qsum[nt][r] = __shfl_sync(0xffffffffu, sum * sc, (2 * t + r) * 4);
-    }
-  }
 
-  auto end_of = [&](int nt, int r) { return old + sh.by_rep.quot(row0 + nt * 8 + 2 * t + r) + 1; };  // keys a row sees
-  float o[NT][HD / 16][4], o8[NT][4];  // sums over codes: dims (rows) g and g + 8 of a tile, query rows 2 t, 2 t + 1
-  float m[NT][2], l[NT][2], z[NT][2];
-  float base[NT][2], rel[NT][2];  // what scores are taken from, pivot(m); 2^(m - M): takes a weight times a step below 2^8
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-    for (int i = 0; i < HD / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
-    o8[nt][0] = o8[nt][1] = o8[nt][2] = o8[nt][3] = 0.f;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      m[nt][r] = -INFINITY;
-      l[nt][r] = z[nt][r] = base[nt][r] = rel[nt][r] = 0.f;
+    auto end_of = [&](int nt, int r) { return old + sh.by_rep.quot(row0 + nt * 8 + 2 * t + r) + 1; };  // keys a row sees
+    float o[NT][HD / 16][4], o8[NT][4];  // sums over codes: dims (rows) g and g + 8 of a tile, query rows 2 t, 2 t + 1
+    float m[NT][2], l[NT][2], z[NT][2];
+    float base[NT][2], rel[NT][2];  // what scores are taken from, pivot(m); 2^(m - M): takes a weight times a step below 2^8
+  #pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+  #pragma unroll
+      for (int i = 0; i < HD / 16; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
+      o8[nt][0] = o8[nt][1] = o8[nt][2] = o8[nt][3] = 0.f;
+  #pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        m[nt][r] = -INFINITY;
+        l[nt][r] = z[nt][r] = base[nt][r] = rel[nt][r] = 0.f;
+      }
     }
-  }
-  // Key of a tile's row g: neighbours swapped in every second pair, so that the
-  // loads of k (rows g, lanes t) and of v (rows 2 t, 2 t + 1, lanes g) both
-  // spread over the banks.
-  const int kg = g ^ ((g >> 1) & 1), ka = (2 * t) ^ (t & 1), kb = ka ^ 1;
-  bool force = true;  // a row has no maximum yet
-  int st = 0, st_in = NST - 1;
-  for (int k = NST - 1, u = u0 + warp; u < units; u += kWarps, ++k) {
-    cp_wait_stages();
-    __syncwarp();  // everybody's copies have landed, and everybody is done with the stage before
-    issue(k, st_in);
-    st_in = st;
-    {
+    // Key of a tile's row g: neighbours swapped in every second pair, so that the
+    // loads of k (rows g, lanes t) and of v (rows 2 t, 2 t + 1, lanes g) both
+    // spread over the banks.
+    const int kg = g ^ ((g >> 1) & 1), ka = (2 * t) ^ (t & 1), kb = ka ^ 1;
+    bool force = true;  // a row has no maximum yet
+    int st = 0, st_in = NST - 1;
+    for (int k = NST - 1, u = u0 + warp; u < units; u += kWarps, ++k) {
+      cp_wait_stages();
+      __syncwarp();  // everybody's copies have landed, and everybody is done with the stage before
+      issue(k, st_in);
+      st_in = st;
       const unsigned char* sk = ring + st * SB;
       const unsigned char* sv = sk + kUnit * HD / 2;
       const uint32_t* sm = reinterpret_cast<const uint32_t*>(sk + kUnit * HD);
@@ -492,98 +497,97 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
         for (int nt = 0; nt < NT; ++nt)
           mma_f16(o8[nt], 0x00080008u, 0x00080008u, 0x00080008u, 0x00080008u, p[q][nt][0], p[q][nt][1]);
       }
+      if (++st == NST) st = 0;
     }
-    if (++st == NST) st = 0;
-  }
 
-  // The warps' states meet in shared memory (each in its own ring, drained):
-  // sums of weighted values, as [R][HD].
-  __syncwarp();
-  float* so = reinterpret_cast<float*>(ring);
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-#pragma unroll
-      for (int d = 4; d < 32; d <<= 1) {
-        l[nt][r] += __shfl_xor_sync(0xffffffffu, l[nt][r], d);
-        z[nt][r] += __shfl_xor_sync(0xffffffffu, z[nt][r], d);
-      }
-      const float f = rel[nt][r] == 0.f ? 0.f : 1048576.f / rel[nt][r];  // 2^20 2^(M - m)
-      const int row = nt * 8 + 2 * t + r;
-#pragma unroll
-      for (int i = 0; i < HD / 16; ++i) {
-        const float even = (o[nt][i][r] - o8[nt][r]) * 16.f, odd = o[nt][i][2 + r] - 16.f * o8[nt][r];
-        *reinterpret_cast<float2*>(so + row * HD + g * (HD / 8) + 2 * i) = make_float2(fmaf(even, f, z[nt][r]), fmaf(odd, f, z[nt][r]));
-      }
-      if (g == 0) {
-        s_m[warp][row] = m[nt][r];
-        s_l[warp][row] = l[nt][r];
-      }
-    }
-  __syncthreads();
-  // The tile's rows, one a warp, lane with dims 2 lane + 64 i: finished here if
-  // all of its units were, else a part.
-  const bool whole = u0 == 0 && u1 == ld.units;
-  float* const part = ws.part + ((long long)blockIdx.x * 2 + !head_part) * kPartFloats<HD, R>;
-  for (int r = warp; r < nrow; r += kWarps) {
-    float top = -INFINITY, sum = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
-    float2 acc[HD / 64];
-#pragma unroll
-    for (int i = 0; i < HD / 64; ++i) acc[i] = make_float2(0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - top);
-      // a state without keys has sum 0 (NaN of NaN scores: kept)
-      sum += s_m[w][r] == -INFINITY ? s_l[w][r] : f * s_l[w][r];
-      const float* src = reinterpret_cast<const float*>(smem + w * NST * SB) + r * HD + 2 * lane;
-      if (f != 0.f) {
-#pragma unroll
-        for (int i = 0; i < HD / 64; ++i) {
-          const float2 v = *reinterpret_cast<const float2*>(src + 64 * i);
-          acc[i].x += f * v.x;
-          acc[i].y += f * v.y;
+    // The warps' states meet in shared memory (each in its own ring, drained):
+    // sums of weighted values, as [R][HD].
+    __syncwarp();
+    float* so = reinterpret_cast<float*>(ring);
+  #pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+  #pragma unroll
+      for (int r = 0; r < 2; ++r) {
+  #pragma unroll
+        for (int d = 4; d < 32; d <<= 1) {
+          l[nt][r] += __shfl_xor_sync(0xffffffffu, l[nt][r], d);
+          z[nt][r] += __shfl_xor_sync(0xffffffffu, z[nt][r], d);
+        }
+        const float f = rel[nt][r] == 0.f ? 0.f : 1048576.f / rel[nt][r];  // 2^20 2^(M - m)
+        const int row = nt * 8 + 2 * t + r;
+  #pragma unroll
+        for (int i = 0; i < HD / 16; ++i) {
+          const float even = (o[nt][i][r] - o8[nt][r]) * 16.f, odd = o[nt][i][2 + r] - 16.f * o8[nt][r];
+          *reinterpret_cast<float2*>(so + row * HD + g * (HD / 8) + 2 * i) = make_float2(fmaf(even, f, z[nt][r]), fmaf(odd, f, z[nt][r]));
+        }
+        if (g == 0) {
+          s_m[warp][row] = m[nt][r];
+          s_l[warp][row] = l[nt][r];
         }
       }
-    }
-    const int i = row0 + r, tq = sh.by_rep.quot(i);
-    const long long n = sp.first + tq, h = hk * rep + i - tq * rep;
-    if (whole) {
-      const float inv = sum == 0.f ? 0.f : 1.f / sum;
-      uint16_t* o = static_cast<uint16_t*>(a.out) + n * a.os[0] + h * a.os[1] + 2 * lane;
-#pragma unroll
-      for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<uint32_t*>(o + 64 * e) = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
-      if (lane == 0 && a.lse) a.lse[n * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-    } else {
-#pragma unroll
-      for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<float2*>(part + r * HD + 2 * lane + 64 * e) = acc[e];
-      if (lane == 0) {
-        part[R * HD + r] = top;
-        part[R * HD + R + r] = sum;
+    __syncthreads();
+    // The tile's rows, one a warp, lane with dims 2 lane + 64 i: finished here if
+    // all of its units were, else a part.
+    const bool whole = u0 == 0 && u1 == ld.units;
+    float* const part = ws.part + ((long long)blockIdx.x * 2 + !head_part) * kPartFloats<HD, R>;
+    for (int r = warp; r < nrow; r += kWarps) {
+      float top = -INFINITY, sum = 0.f;
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+      float2 acc[HD / 64];
+  #pragma unroll
+      for (int i = 0; i < HD / 64; ++i) acc[i] = make_float2(0.f, 0.f);
+  #pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = s_m[w][r] == -INFINITY ? 0.f : ex2(s_m[w][r] - top);
+        // a state without keys has sum 0 (NaN of NaN scores: kept)
+        sum += s_m[w][r] == -INFINITY ? s_l[w][r] : f * s_l[w][r];
+        const float* src = reinterpret_cast<const float*>(smem + w * NST * SB) + r * HD + 2 * lane;
+        if (f != 0.f) {
+  #pragma unroll
+          for (int i = 0; i < HD / 64; ++i) {
+            const float2 v = *reinterpret_cast<const float2*>(src + 64 * i);
+            acc[i].x += f * v.x;
+            acc[i].y += f * v.y;
+          }
+        }
+      }
+      const int i = row0 + r, tq = sh.by_rep.quot(i);
+      const long long n = sp.first + tq, h = hk * rep + i - tq * rep;
+      if (whole) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        uint16_t* o = static_cast<uint16_t*>(a.out) + n * a.os[0] + h * a.os[1] + 2 * lane;
+  #pragma unroll
+        for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<uint32_t*>(o + 64 * e) = pack2<F16>(acc[e].x * inv, acc[e].y * inv);
+        if (lane == 0 && a.lse) a.lse[n * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+      } else {
+  #pragma unroll
+        for (int e = 0; e < HD / 64; ++e) *reinterpret_cast<float2*>(part + r * HD + 2 * lane + 64 * e) = acc[e];
+        if (lane == 0) {
+          part[R * HD + r] = top;
+          part[R * HD + R + r] = sum;
+        }
+      }
+      if (u0 == 0 && lane == 0) {  // (the CTA of unit x is that of the largest i with i all / ctas <= x)
+        const int end_cta = whole ? blockIdx.x : (int)(((s_stop - left + ld.units) * s_ctas - 1) / s_all);
+        ws.where[n * a.Hq + h] = make_int2(blockIdx.x, (end_cta - (int)blockIdx.x) << 6 | !head_part << 5 | r);
       }
     }
-    if (u0 == 0 && lane == 0) {  // (the CTA of unit x is that of the largest i with i all / ctas <= x)
-      const int end_cta = whole ? blockIdx.x : (int)(((s_stop - left + ld.units) * s_ctas - 1) / s_all);
-      ws.where[n * a.Hq + h] = make_int2(blockIdx.x, (end_cta - (int)blockIdx.x) << 6 | !head_part << 5 | r);
+    left -= u1 - u0;
+    if (left <= 0) break;
+    // the next tile: of this sequence, or of the next with any
+    u0 = -kStart;
+    if (++item == ld.tiles * a.Hkv) {
+      item = 0;
+      do ld = seq_load(a, cap, rep, R, ++b);
+      while (ld.tiles == 0 || ld.units == 0);
     }
-  }
-  left -= u1 - u0;
-  if (left <= 0) break;
-  // the next tile: of this sequence, or of the next with any
-  u0 = -kStart;
-  if (++item == ld.tiles * a.Hkv) {
-    item = 0;
-    do ld = seq_load(a, cap, rep, R, ++b);
-    while (ld.tiles == 0 || ld.units == 0);
-  }
-  __syncthreads();  // (the rings are free)
+    __syncthreads();  // (the rings are free)
   }
 }
 
 // A CTA a row and query head: its parts, a warp every fourth; rows without a key.
 template <int HD, bool F16, int R>
-__global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ PackedArgs a, Kv4Ws ws, FastDiv by_heads) {
+__global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ PackedArgs a, Kv4Ws ws, FastDiv by_heads, int ctas) {
   __shared__ float s_m[4], s_l[4], s_o[4][HD];
   const int n = by_heads.quot(blockIdx.x), h = blockIdx.x - n * a.Hq;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -602,9 +606,9 @@ __global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ Packed
     return;
   }
   const int2 where = ws.where[(long long)n * a.Hq + h];
-  const int parts = (where.y >> 6) + 1, r = where.y & 31;
-  if (parts == 1) return;
-  auto at = [&](int i) { return ws.part + ((long long)(where.x + i) * 2 + (i == 0 ? where.y >> 5 & 1 : 0)) * kPartFloats<HD, R>; };
+  const int parts = min((where.y >> 6) + 1, ctas), r = where.y & (R - 1);  // (bounds: nothing was written for starts that overlap)
+  if (parts <= 1) return;
+  auto at = [&](int i) { return ws.part + ((long long)min((unsigned)(where.x + i), (unsigned)ctas - 1) * 2 + (i == 0 ? where.y >> 5 & 1 : 0)) * kPartFloats<HD, R>; };
   float top = -INFINITY, sum = 0.f;
   float2 acc[HD / 64];
 #pragma unroll
@@ -674,6 +678,13 @@ __global__ void __launch_bounds__(128) k_kv4_join(const __grid_constant__ Packed
   if (lane == 0 && a.lse) a.lse[(long long)n * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
+// Units there can be, with row tiles of `rows` rows.
+long long most_units(const PackedArgs& p, const Kv4Args& c, int rows) {
+  const long long units = (((long long)c.width << c.page_log) + kUnit - 1) / kUnit;
+  const long long n = p.start ? min((long long)p.max_rows * p.B, (long long)p.N) : p.B;
+  return ((n * (p.Hq / p.Hkv) + rows - 1) / rows + p.B) * p.Hkv * (units + kStart);
+}
+
 template <int HD, bool F16, int NT>
 cudaError_t launch(const PackedArgs& p, const Kv4Args& c, void* d_ws, cudaStream_t s) {
   int dev = 0, sms = 0;
@@ -695,10 +706,9 @@ cudaError_t launch(const PackedArgs& p, const Kv4Args& c, void* d_ws, cudaStream
   ws.where = static_cast<int2*>(d_ws);
   ws.part = static_cast<float*>(d_ws) + 2ll * p.N * p.Hq;
   // no more CTAs than units there can be
-  const long long units = (((long long)c.width << c.page_log) + kUnit - 1) / kUnit;
-  const long long tiles = ((long long)(p.start ? min((long long)p.max_rows * p.B, (long long)p.N) : p.B) * (p.Hq / p.Hkv) + 8 * NT - 1) / (8 * NT) + p.B;
-  const int grid = (int)min((long long)kResident<NT> * min(sms, kSms), (tiles * p.Hkv * units + kLeast - 1) / kLeast);
-  kern<<<grid, kThreads, kSmem<HD>, s>>>(p, c, Kv4Shape{FastDiv(p.Hkv), FastDiv(p.Hq / p.Hkv)}, ws);
+  const long long most = most_units(p, c, 8 * NT);
+  const int grid = (int)min((long long)kResident<NT> * min(sms, kSms), (most + kLeast - 1) / kLeast);
+  kern<<<grid, kThreads, kSmem<HD>, s>>>(p, c, Kv4Shape{FastDiv(p.Hkv), FastDiv(p.Hq / p.Hkv), most}, ws);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchConfig_t cfg = {};
@@ -710,7 +720,7 @@ cudaError_t launch(const PackedArgs& p, const Kv4Args& c, void* d_ws, cudaStream
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k_kv4_join<HD, F16, 8 * NT>, p, ws, FastDiv(p.Hq));
+  return cudaLaunchKernelEx(&cfg, k_kv4_join<HD, F16, 8 * NT>, p, ws, FastDiv(p.Hq), grid);
 }
 
 // One tile of 8 rows, or two to an operand of codes: with more than 8 rows of a
@@ -723,6 +733,8 @@ cudaError_t launch_rows(const PackedArgs& p, const Kv4Args& c, void* ws, cudaStr
 }
 
 }  // namespace
+
+bool kv4_attention_fits(const PackedArgs& p, const Kv4Args& c) { return most_units(p, c, 8 * row_tiles(p)) <= kMostUnits; }
 
 size_t kv4_attention_ws_bytes(const PackedArgs& p) {
   static_assert(kResident<1> * 8 <= kResident<2> * 16, "the larger of the two forms");
@@ -768,6 +780,7 @@ extern "C" rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, 
   a.start = d_start;
   a.kv_len = d_kv_len;
   a.err = d_err;
+  if (!kv4_attention_fits(a, k)) return op_error(who, RL_ERR_UNSUPPORTED, "rows, table_width and heads make more than 2^38 units of 32 keys");
   const cudaError_t e = launch_kv4_attention(a, k, d_ws, static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return set_error(RL_ERR_CUDA, cudaGetErrorString(e));
   return RL_OK;

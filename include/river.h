@@ -407,7 +407,8 @@ RL_API rl_status rl_kv_timeline(rl_kv* kv, rl_stream_t stream, int64_t cap, uint
  *
  * rl_debug_limit_waits: the waits of the many-row attention kernel (more than
  * 16 query rows a KV head of rl_window_attention, the prefix of
- * rl_shared_prefix_attention, and the model's paths over them) give up after
+ * rl_shared_prefix_attention, the model's paths over them, and
+ * rl_packed_attention) give up after
  * `polls` polls from the next launch on (a captured one keeps its limit),
  * until it is called with a negative value (the default: the kernel's own
  * limit, about a second).  A wait that gives up sets RL_DEVERR_TIMEOUT, and a
@@ -566,9 +567,12 @@ RL_API rl_status rl_shared_prefix_attention(const rl_attn_desc* a, const void* d
  * head_dim 64 or 128, n_q_heads a multiple of n_kv_heads, 16-byte starts,
  * strides whole multiples of 16 bytes, batch at most 2^16, rows 2^27,
  * n_kv_heads 2^10 (RL_ERR_UNSUPPORTED otherwise); what is written has its rows
- * and heads apart (RL_ERR_INVALID_ARG otherwise).  Rows in front of d_start[0] and from d_start[batch] on are left as they were.  An
- * entry of d_start outside [0, rows], or below the one before, sets
- * RL_DEVERR_CAPACITY and is moved there. */
+ * and heads apart (RL_ERR_INVALID_ARG otherwise).  Rows in front of d_start[0]
+ * and from d_start[batch] on are left as they were.  An entry of d_start outside
+ * [0, rows], or below the one before, sets RL_DEVERR_CAPACITY: a sequence then has
+ * the rows between its two entries that are laid out, and the results of rows
+ * that two sequences have, or of all rows where there are more than `rows` in all,
+ * are not defined. */
 typedef struct {
   int32_t dtype;       /* of q, k, v and out: RL_DT_BF16 or RL_DT_F16 */
   int32_t batch, rows; /* sequences; rows laid out */
@@ -657,7 +661,9 @@ RL_API rl_status rl_kv4_read(const rl_kv4* c, const rl_packed_desc* p, const int
  *   d_ws  workspace of rl_kv4_attention_workspace bytes (16-byte aligned), in use
  *         until the call's work on the stream is done: calls that may overlap
  *         need one each
- * RL_ERR_INVALID_ARG also for a workspace too small. */
+ * RL_ERR_INVALID_ARG also for a workspace too small, RL_ERR_UNSUPPORTED for
+ * rows and a table_width that could make more than 2^38 units of 32 keys (of 8 or
+ * 16 rows of a KV head). */
 RL_API rl_status rl_kv4_attention_workspace(const rl_packed_desc* p, uint64_t* bytes);
 RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, const int32_t* d_start,
                                   const int32_t* d_kv_len, const void* d_q, void* d_out, float* d_lse,
@@ -682,8 +688,10 @@ RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, cons
  * how a row is split.  Logits of -infinity are never drawn.  A row with a NaN or
  * +infinity gives the id rl_token_logprobs would put first and logprob NaN, a
  * row of -infinity alone id 0 and NaN; settings of d_ arrays: a temperature
- * not above 0 (or NaN) is 0, a top_k below 1 or from vocab on keeps all, a top_p
- * or min_p that is NaN keeps all.  One launch, no workspace.
+ * not above 0 (or NaN) is 0, an infinite one the largest finite one, a top_k
+ * below 1 or from vocab on keeps all, a top_p or min_p that is NaN keeps all.
+ * A logit whose difference from the largest is beyond fp32 weighs nothing.  One
+ * launch, no workspace.
  * RL_ERR_INVALID_ARG for a missing buffer, a size below 1, row_stride < vocab,
  * a temperature, top_k, top_p or min_p that is negative or not finite, an
  * unknown dtype or misaligned logits; RL_ERR_UNSUPPORTED for a larger vocab. */

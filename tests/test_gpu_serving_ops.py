@@ -389,6 +389,23 @@ def test_kv4_device_errors_and_bounds(river):
         assert (got["out"][r].float() - all_["out"][r].float()).abs().max() < 0.05, r
 
 
+def test_kv4_starts_that_overlap(river):
+    """Reported, and the next call is right: with more units than all rows have (five
+    sequences, three of them of all rows), and with fewer."""
+    rows, lens = [16, 0, 0, 0, 0], [64, 0, 70, 0, 80]
+    cache, table = make_cache(river, [64, 64, 70, 70, 80], 2, 64, 16, BF, 114, width=5)
+    q = rnd(16, 16, 64, dtype=BF, seed=115)
+    want = river.kv4_attention(q, cache, table, i32(lens), start=starts(rows))
+    check_kv4(want, q, cache, table, lens, rows)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for start in ([0, 16, 0, 16, 0, 16], [0, 10, 5, 12, 12, 16]):
+        err.zero_()
+        river.kv4_attention(q, cache, table, i32(lens), start=i32(start), err=err)
+        assert int(err) == river.RL_DEVERR_CAPACITY, start
+        got = river.kv4_attention(q, cache, table, i32(lens), start=starts(rows))
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+
+
 def test_kv4_strides_and_views(river):
     """Heads cut out of a fused projection; the cache one layer of a pool."""
     lens = [100, 47]
@@ -662,6 +679,16 @@ def test_sample_extremes(river):
     check_sample(got, x[6:], u[6:], T=1e-30)
 
 
+def test_sample_temperatures_without_an_end(river):
+    """An infinite one is the largest finite one: every id weighs the same, and is below 1."""
+    x, u = logits(6, 999, F32, 16), uniform(6, 17)
+    T = torch.full((6,), INF, device="cuda")
+    check_sample(call(river, x, u, T=T), x, u, T=torch.finfo(F32).max)
+    check_sample(call(river, x, u, T=T, k=3), x, u, T=torch.finfo(F32).max, k=3)
+    got = call(river, x, u, T=T, mp=1.0)
+    assert torch.equal(got["token"].long(), x.argmax(1)) and (got["logprob"] == 0).all()
+
+
 @pytest.mark.parametrize("dtype", [F32, BF])
 def test_sample_strided_rows_and_odd_starts(river, dtype):
     flat = logits(9, 2011, dtype, 8).view(-1)
@@ -773,6 +800,47 @@ def test_streams_capture_and_repeat(river):
     check_kv4({"out": got[3], "lse": got[4]}, got[0], cache, table, [905, 40, 2011], rows)
     assert all(torch.equal(a, b) for a, b in zip(chain(), got))
     check_sample(gt, x, u, k=50, p=0.9)
+
+
+def test_offsets_past_32_bits(river):
+    """Pages, rows of operands and rows of logits 2^31 bytes and more apart give what compact ones do, bit for bit."""
+    if torch.cuda.get_device_properties(0).total_memory < 1 << 36:
+        pytest.skip("needs 64 GB")
+    lens, rows = [33, 40], [2, 3]
+    small, table = make_cache(river, lens, 2, 128, 16, BF, 131)
+    n, st, pages = i32(lens), starts(rows), small.k_codes.shape[0]
+    cs, ss = (1 << 31) - 4096, (1 << 30) - 4096
+    codes = torch.empty((pages - 1) * cs + 4096, dtype=torch.uint8, device="cuda")
+    scales = torch.empty((pages - 1) * ss + 256, dtype=BF, device="cuda")
+    far = river.KV4Cache(*(b.as_strided(t.shape, (step, *t.stride()[1:]), at) for t, b, step, at in zip(
+        small, (codes, scales) * 2, (cs, ss) * 2, (0, 0, 2048, 128))))
+    for x, y in zip(far, small):
+        x.copy_(y)
+    step = 1 << 30
+    wide = torch.empty(4 * step + 4096, dtype=BF, device="cuda")
+    q, out = (wide.as_strided((5, 8, 128), (step, 128, 1), at) for at in (0, 1024))
+    k, v = (wide.as_strided((5, 2, 128), (step, 128, 1), at) for at in (2048, 2304))
+    for x, seed in ((q, 132), (k, 133), (v, 134)):
+        x.copy_(rnd(*x.shape, dtype=BF, seed=seed))
+    cq, ck, cv = (x.clone(memory_format=torch.contiguous_format) for x in (q, k, v))
+    want = river.kv4_append(small, table, n, ck, cv, q=cq, start=st)["q"]
+    assert torch.equal(river.kv4_append(far, table, n, k, v, q=q, start=st, out={"q": out})["q"], want)
+    assert all(torch.equal(x.contiguous().view(torch.uint8), y.view(torch.uint8)) for x, y in zip(far, small))
+    want = river.kv4_attention(cq, small, table, n, start=st)
+    check_kv4(want, cq, small, table, lens, rows)
+    got = river.kv4_attention(q, far, table, n, start=st, out={"out": out})
+    assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    want = river.packed_attention(cq, ck, cv, st)
+    assert torch.equal(river.packed_attention(q, k, v, st, out={"out": out})["out"], want["out"])
+    want = river.kv4_read(small, table, n, start=st, rows=5)
+    river.kv4_read(far, table, n, start=st, rows=5, out={"k": k, "v": v})
+    assert torch.equal(k, want["k"]) and torch.equal(v, want["v"])
+    del far, codes, scales, q, out, k, v, wide
+    x, u = logits(3, 9001, BF, 135), uniform(3, 136)
+    wide = torch.empty(2 * (1 << 31) + 9001, dtype=BF, device="cuda")
+    y = wide.as_strided(x.shape, (1 << 31, 1))
+    y.copy_(x)
+    assert all(torch.equal(a, b) for a, b in zip(call(river, x, u, p=0.9).values(), call(river, y, u, p=0.9).values()))
 
 
 def test_two_calls_at_once(river):

@@ -99,6 +99,11 @@ def test_operands(river, name, kw, status):
     assert _call(river, name, **kw) == getattr(river, "RL_ERR_" + status), river.rl_last_error()
 
 
+def test_attention_beyond_any_grid(river):
+    kw = dict(rows=1 << 20, n_pages=1, page=256, table_width=1 << 22, table_stride=1 << 22)
+    assert _call(river, "attention", **kw) == river.RL_ERR_UNSUPPORTED and b"2^38" in river._lib.rl_last_error()
+
+
 def _sample(river, **kw):
     a = dict(logits=A, dtype=0, rows=2, vocab=100, stride=100, u=A, set=True, token=A)
     a.update({k: v for k, v in kw.items() if k in a})

@@ -18,13 +18,12 @@
 // no more than half of 64 rows of 128,256 fit the SMs at once: 91 us).  A cut is
 // found a digit of 9 bits at a time from a histogram of the ids that agree in
 // the digits before (counts, or weights in three limbs of 16 bits, whose sums
-// over a part of at most 65,536 ids stay in 32); the
-// digits are those of -log2 of the weight first, in fixed point (even bins where
-// weights matter), then of the logit's bits and of the id, until no more than
-// kList ids are left, which are ordered one against another.  A small top-k
-// needs no histogram of the row: bins of the threads' largest logits give a
-// bound that at least k ids reach and few others, and one CTA finishes with
-// those alone.
+// over a part of at most 65,536 ids stay in 32); the digits are those of -log2 of
+// the weight first, in fixed point (even bins where weights matter), then of the
+// logit's bits and of the id, until no more than kList ids are left, which are
+// ordered one against another.  A small top-k needs no histogram of the row: bins
+// of the threads' largest logits give a bound that at least k ids reach and few
+// others, and one CTA finishes with those alone.
 //
 // What bounds it: instructions, some 75 a logit where weights are summed (the
 // exponential's 45, the histogram's 20), and the chain of a digit: histogram,
@@ -66,7 +65,7 @@ constexpr int kMaxSplit = 16;    // CTAs of a row's cluster
 constexpr int kBins = kThreads;  // of a digit (9 bits), one a thread
 constexpr int kList = 128;       // ids that are ordered one against another
 constexpr int kFew = 96;         // top-k that needs no histogram of the row
-constexpr int kGather = 1024;    // a part's ids of a digit's bin that are brought together before the next 
+constexpr int kGather = 1024;    // a part's ids of a digit's bin that are brought together before the next digit
 constexpr int kMostIds = 65536;  // of a part
 
 __device__ __forceinline__ uint32_t order_bits(float x) {
@@ -151,7 +150,7 @@ struct List {
 struct Shared {
   u64 table[64];
   uint32_t hist[2][4][kBins];  // by a digit's parity: counts, weights' limbs
-  List list[2];             // this part's ids that are ordered one against another: for top-k, for top-p
+  List list[2];                // this part's ids that are ordered one against another: for top-k, for top-p
   u64 key[kList], wt[kList];   // the cluster's, and their weights
   int n_key;
   uint32_t n_few;
@@ -514,10 +513,11 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const float u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604644775390625e-8f);
   // (one thread, in 64 bits, which all threads at once would wait for)
   if (tid == kThreads - 1) {
-    const double c = fmin(1.4426950408889634 / (double)temp, 1e38);  // (finite in fp32)
+    const double t = fmin((double)temp, 3.4028234663852886e38);
+    const double c = fmin(1.4426950408889634 / t, 1e38);  // (finite in fp32)
     s.ch = (float)c;
     s.cl = (float)(c - (double)(float)c);
-    s.span = mp > 0.f ? (double)temp * log((double)mp) : 0.0;
+    s.span = mp > 0.f ? t * log((double)mp) : 0.0;
   }
   __syncthreads();
 

@@ -11,7 +11,9 @@ The ``rl_*`` functions mirror the C ABI in ``include/river.h`` one to one;
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
+import struct
 from typing import Any, NamedTuple
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -825,11 +827,14 @@ def _strides(d, t):
 _PLANS = {}
 
 
+_SHAPE_DTYPE = operator.attrgetter("shape", "dtype")
+
+
 def _plan(name, scale, tensors, make):
     """What ``make()`` derives from the tensors' shapes, strides and types alone
     (their checks, the descriptor, a workspace's size), kept for calls of the
     same layout."""
-    key = (name, scale, *[x for t in tensors for x in (t.shape, t.stride(), t.dtype)])
+    key = (name, scale, *map(_SHAPE_DTYPE, tensors), *map(_torch().Tensor.stride, tensors))
     p = _PLANS.get(key)
     if p is None:
         p = make()
@@ -1010,19 +1015,21 @@ def _kv4_desc(name, cache, table, dtype):
         _refuse(f"{name}: table must be int32 [B][pages] with contiguous rows")
     if max(n, heads, page, *table.shape) > _INT32_MAX:
         _refuse(f"{name}: sizes must be below 2^31", RL_ERR_UNSUPPORTED)
-    c = rl_kv4(n, page)
-    c.code_stride[:] = [t.stride(0) if n > 1 else 0 for t in (kc, vc)]
-    c.scale_stride[:] = [t.stride(0) if n > 1 else 0 for t in (km, vm)]
-    c.table_stride, c.table_width = table.stride(0) if table.shape[0] > 1 else table.shape[1], table.shape[1]
-    return c, heads, 2 * half
+    # (what _kv4_with packs around a call's addresses)
+    fixed = ([t.stride(0) if n > 1 else 0 for t in (kc, vc, km, vm)],
+             table.stride(0) if table.shape[0] > 1 else table.shape[1], table.shape[1])
+    return (n, page, *fixed), heads, 2 * half
+
+
+_KV4_FORM = struct.Struct("@ii4P4qPqi0q")  # rl_kv4
 
 
 def _kv4_with(c, cache, table):
-    """A copy of the descriptor with this call's addresses."""
-    d = rl_kv4.from_buffer_copy(c)
-    d.k_codes, d.k_scale, d.v_codes, d.v_scale = (t.data_ptr() for t in cache)
-    d.d_table = table.data_ptr()
-    return d
+    """rl_kv4 of _kv4_desc's values and this call's addresses."""
+    kc, km, vc, vm = cache
+    n, page, strides, table_stride, width = c
+    return rl_kv4.from_buffer_copy(_KV4_FORM.pack(n, page, kc.data_ptr(), km.data_ptr(), vc.data_ptr(), vm.data_ptr(), *strides,
+                                                  table.data_ptr(), table_stride, width))
 
 
 def _spans(name, start, kv_len, batch, rows, err):
@@ -1047,15 +1054,18 @@ def packed_attention(q, k, v, start, max_rows=None, scale=None, out=None, err=No
     torch = _torch()
     name = "packed_attention"
     dev = _operands(name, (q, k, v, start, err))
-    if q.dim() != 3 or k.dim() != 3 or start.dim() != 1 or q.numel() == 0 or k.numel() == 0 or start.numel() < 2:
-        _refuse(f"{name}: q, k, v must be [N][heads][hd], not empty, start [B + 1]")
     o = dict(out) if out else {}
     res = _buffer(o, "out", q.shape, q, q.dtype, stream, name)
-    B, N = start.numel() - 1, q.shape[0]
-    d = _plan((name, B, max_rows), scale, (q, k, v, res) if out else (q, k, v), lambda: _packed_desc(
-        name, q.dtype, (q.shape[1], k.shape[1], q.shape[2]), B, N, max_rows or 0, scale, q=q, k=k, v=v, out=res))
-    lse = _buffer(o, "lse", (N, q.shape[1]), q, torch.float32, stream, name)
-    _spans(name, start, None, B, N, err)
+    B = start.numel() - 1
+
+    def make():
+        if q.dim() != 3 or k.dim() != 3 or B < 1 or q.numel() == 0 or k.numel() == 0:
+            _refuse(f"{name}: q, k, v must be [N][heads][hd], not empty, start [B + 1]")
+        return _packed_desc(name, q.dtype, (q.shape[1], k.shape[1], q.shape[2]), B, q.shape[0], max_rows or 0, scale, q=q, k=k, v=v, out=res)
+
+    d = _plan((name, B, max_rows), scale, (q, k, v, res) if out else (q, k, v), make)
+    lse = _buffer(o, "lse", (d.rows, d.n_q_heads), q, torch.float32, stream, name)
+    _spans(name, start, None, B, d.rows, err)
     _run(dev, stream, _lib.rl_packed_attention, d, q.data_ptr(), k.data_ptr(), v.data_ptr(), start.data_ptr(), res.data_ptr(),
          lse.data_ptr(), _addr(err))
     return o
@@ -1072,14 +1082,10 @@ def kv4_append(cache, table, kv_len, k, v, q=None, rope=None, start=None, out=No
     torch = _torch()
     name = "kv4_append"
     dev = _operands(name, (k, v, q, table, kv_len, rope, start, err, *cache))
-    if k.dim() != 3 or k.numel() == 0 or kv_len.dim() != 1 or kv_len.numel() == 0:
-        _refuse(f"{name}: k and v must be [N][Hkv][hd], not empty, kv_len [B]")
     o = dict(out) if out else {}
-    B, N = kv_len.numel(), k.shape[0]
+    B = kv_len.numel()
     res = None
     if q is not None:
-        if q.dim() != 3 or q.numel() == 0:
-            _refuse(f"{name}: q must be [N][Hq][hd], not empty")
         res = o.get("q")
         if res is None:
             res = o["q"] = _new(q.shape, q.dtype, q.device, stream)
@@ -1087,15 +1093,19 @@ def kv4_append(cache, table, kv_len, k, v, q=None, rope=None, start=None, out=No
             _operands(name, (k, res))
 
     def make():
+        if k.dim() != 3 or k.numel() == 0 or B < 1:
+            _refuse(f"{name}: k and v must be [N][Hkv][hd], not empty, kv_len [B]")
+        if q is not None and (q.dim() != 3 or q.numel() == 0):
+            _refuse(f"{name}: q must be [N][Hq][hd], not empty")
         c, heads, hd = _kv4_desc(name, cache, table, k.dtype)
-        d = _packed_desc(name, k.dtype, (q.shape[1] if q is not None else heads, heads, hd), B, N, 0, None, q=q, k=k, v=v, out=res)
+        d = _packed_desc(name, k.dtype, (q.shape[1] if q is not None else heads, heads, hd), B, k.shape[0], 0, None, q=q, k=k, v=v, out=res)
+        if table.shape[0] != B:
+            _refuse(f"{name}: table must have a row for each of the {B} sequences")
         return c, d
 
     ts = (*cache, table, k, v) + (() if q is None else (q, res) if out else (q,))
     c, d = _plan((name, B, q is None), None, ts, make)
-    if table.shape[0] != B:
-        _refuse(f"{name}: table must have a row for each of the {B} sequences")
-    _spans(name, start, kv_len, B, N, err)
+    _spans(name, start, kv_len, B, d.rows, err)
     n_rope = 0
     if rope is not None:
         if rope.dtype != torch.float32 or rope.dim() != 3 or rope.shape[0] < 1 or rope.shape[1:] != (d.head_dim // 2, 2) or not rope.is_contiguous():
@@ -1114,28 +1124,32 @@ def kv4_read(cache, table, kv_len, start=None, rows=None, out=None, err=None, st
     ``out`` are used, their rows of no sequence left as they were.  See rl_kv4_read."""
     name = "kv4_read"
     dev = _operands(name, (table, kv_len, start, err, *cache))
-    if kv_len.dim() != 1 or kv_len.numel() == 0:
-        _refuse(f"{name}: kv_len must be [B]")
     B = kv_len.numel()
     if rows is None and start is not None:
         _refuse(f"{name}: start needs rows")
     N = B if rows is None else int(rows)
-    if not 1 <= N <= _INT32_MAX:
-        _refuse(f"{name}: rows must be in [1, 2^31)")
-    c, heads, hd = _plan((name, None), None, (*cache, table), lambda: _kv4_desc(name, cache, table, None))
+
+    def make():
+        if not 1 <= N <= _INT32_MAX or B < 1:
+            _refuse(f"{name}: rows must be in [1, 2^31), kv_len [B]")
+        c, heads, hd = _kv4_desc(name, cache, table, None)
+        if table.shape[0] != B:
+            _refuse(f"{name}: table must have a row for each of the {B} sequences")
+        new = _torch().empty((N, heads, hd), dtype=cache[1].dtype, device="meta")
+        given = {x: new if o.get(x) is None else o[x] for x in ("k", "v")}
+        if any(t.dim() != 3 for t in given.values()):
+            _refuse(f"{name}: k and v must be [{N}][{heads}][{hd}]")
+        return c, new.shape, _packed_desc(name, new.dtype, (heads, heads, hd), B, N, 0, None, **given)
+
     o = dict(out) if out else {}
-    for key in ("k", "v"):
-        if o.get(key) is None:
-            o[key] = _new((N, heads, hd), cache[1].dtype, table.device, stream)
-        else:
-            _operands(name, (table, o[key]))
-            if o[key].dim() != 3:
-                _refuse(f"{name}: out[{key!r}] must be [{N}][{heads}][{hd}]")
+    ts = [o[x] for x in ("k", "v") if o.get(x) is not None]
+    for t in ts:
+        _operands(name, (table, t))
+    c, shape, d = _plan((name, B, N, o.get("k") is None, o.get("v") is None), None, (*cache, table, *ts), make)
+    for x in ("k", "v"):
+        if o.get(x) is None:
+            o[x] = _new(shape, cache[1].dtype, table.device, stream)
     k, v = o["k"], o["v"]
-    d = _plan((name, B, N), None, (*cache[:2], k, v), lambda: _packed_desc(
-        name, cache[1].dtype, (heads, heads, hd), B, N, 0, None, k=k, v=v))
-    if table.shape[0] != B:
-        _refuse(f"{name}: table must have a row for each of the {B} sequences")
     _spans(name, start, kv_len, B, N, err)
     _run(dev, stream, _lib.rl_kv4_read, _kv4_with(c, cache, table), d, _addr(start), kv_len.data_ptr(), k.data_ptr(), v.data_ptr(), _addr(err))
     return o
@@ -1153,22 +1167,22 @@ def kv4_attention(q, cache, table, kv_len, start=None, max_rows=None, scale=None
     torch = _torch()
     name = "kv4_attention"
     dev = _operands(name, (q, table, kv_len, start, workspace, err, *cache))
-    if q.dim() != 3 or q.numel() == 0 or kv_len.dim() != 1 or kv_len.numel() == 0:
-        _refuse(f"{name}: q must be [N][Hq][hd], not empty, kv_len [B]")
     o = dict(out) if out else {}
     res = _buffer(o, "out", q.shape, q, q.dtype, stream, name)
-    B, N = kv_len.numel(), q.shape[0]
+    B = kv_len.numel()
 
     def make():
+        if q.dim() != 3 or q.numel() == 0 or B < 1:
+            _refuse(f"{name}: q must be [N][Hq][hd], not empty, kv_len [B]")
         c, heads, hd = _kv4_desc(name, cache, table, q.dtype)
-        d = _packed_desc(name, q.dtype, (q.shape[1], heads, hd), B, N, max_rows or 0, scale, q=q, out=res)
+        if table.shape[0] != B:
+            _refuse(f"{name}: table must have a row for each of the {B} sequences")
+        d = _packed_desc(name, q.dtype, (q.shape[1], heads, hd), B, q.shape[0], max_rows or 0, scale, q=q, out=res)
         return c, d, rl_kv4_attention_workspace(d)
 
     c, d, need = _plan((name, B, max_rows), scale, (*cache, table, q, res) if out else (*cache, table, q), make)
-    lse = _buffer(o, "lse", (N, q.shape[1]), q, torch.float32, stream, name)
-    if table.shape[0] != B:
-        _refuse(f"{name}: table must have a row for each of the {B} sequences")
-    _spans(name, start, kv_len, B, N, err)
+    lse = _buffer(o, "lse", (d.rows, d.n_q_heads), q, torch.float32, stream, name)
+    _spans(name, start, kv_len, B, d.rows, err)
     if workspace is None:
         workspace = _new((need,), torch.uint8, q.device, stream)
     elif not workspace.is_contiguous():

@@ -30,7 +30,7 @@
 // barrier, the groups' and the bins' sums from the other parts.  64 rows of
 // 128,256 fp32 logits cut at 0.9 of their mass: 71 us (the row's first reading
 // 7, the histogram 16, the next digit 11, the id 5, the rest between them); 500
-// rows of 50,257 bf16 logits, each with settings of its own: 118 us; one row
+// rows of 50,257 bf16 logits, each with settings of its own: 104 us; one row
 // with top-k 50 and top-p 0.95: 14 us.
 #include <float.h>
 #include <math.h>
@@ -67,6 +67,7 @@ constexpr int kList = 128;       // ids that are ordered one against another
 constexpr int kFew = 96;         // top-k that needs no histogram of the row
 constexpr int kGather = 1024;    // a part's ids of a digit's bin that are brought together before the next digit
 constexpr int kMostIds = 65536;  // of a part
+constexpr int kOrder = 2048;     // rows that are put in order of their cost
 
 __device__ __forceinline__ uint32_t order_bits(float x) {
   const uint32_t u = x != x ? 0x7fffffffu : __float_as_uint(x + 0.f);
@@ -164,7 +165,7 @@ struct Shared {
   float lo, hi;             // the logits whose digits so far are the cut's
   u64 cut;
   uint32_t count, own;      // ids of the bin, and this part's
-  int bin;
+  int bin, row;
   float ch, cl, least;      // log2(e) / T in two parts; min-p's logit
   double span;              // T ln min_p
 };
@@ -492,11 +493,55 @@ __device__ __forceinline__ u64 share_up(float p, u64 S) {
   return max(1ull, __umul64hi(f, S) + (f * S != 0));
 }
 
+// Row r's settings.
+struct Set {
+  float temp, tp, mp;
+  int k;
+  __device__ __forceinline__ Set(const SampleArgs& a, int r) {
+    temp = a.set.d_temperature ? a.set.d_temperature[r] : a.set.temperature;
+    k = a.set.d_top_k ? a.set.d_top_k[r] : a.set.top_k;
+    tp = a.set.d_top_p ? a.set.d_top_p[r] : a.set.top_p;
+    mp = a.set.d_min_p ? a.set.d_min_p[r] : a.set.min_p;
+  }
+  // 0: one or two readings of the row, 1: its weights too, 2: cuts by digits
+  __device__ __forceinline__ int cost(int V) const {
+    const bool has_k = k >= 1 && k < V;
+    return !(temp > 0.f) || (has_k && k <= kFew) ? 0 : has_k || tp < 1.f ? 2 : 1;
+  }
+};
+
+// The i-th row when those that cost most come first (of one cost: by threads).
+__device__ int costly_first(const SampleArgs& a, Shared& s, int i, int tid) {
+  const int lane = tid & 31, warp = tid >> 5;
+  u64 mine = 0;  // rows of this thread by cost, 20 bits each, the costliest lowest
+  for (int r = tid; r < a.rows; r += kThreads) mine += 1ull << (20 * (2 - Set(a, r).cost(a.V)));
+  const u64 upto = warp_scan64(mine, lane);
+  if (lane == 31) s.red[warp] = upto;
+  __syncthreads();
+  u64 all = 0, front = upto - mine;
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp) front += s.red[w];
+    all += s.red[w];
+  }
+  auto of = [](u64 x, int c) { return (int)(x >> (20 * c) & 0xfffff); };
+  int c = 0;
+  while (c < 2 && i >= of(all, c)) i -= of(all, c++);
+  i -= of(front, c);
+  if (i >= 0 && i < of(mine, c))
+    for (int r = tid; r < a.rows; r += kThreads)
+      if (2 - Set(a, r).cost(a.V) == c && i-- == 0) s.bin = r;
+  __syncthreads();
+  return s.bin;
+}
+
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ SampleArgs a, const __grid_constant__ Pow2Table pow2, int split) {
+__global__ void __launch_bounds__(kThreads, 2)
+    k_sample(const __grid_constant__ SampleArgs a, const __grid_constant__ Pow2Table pow2, int split, bool order) {
   __shared__ Shared s;
-  const int row = blockIdx.x / split, part = blockIdx.x - row * split;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = a.V;
+  const int place = blockIdx.x / split, part = blockIdx.x - place * split;
+  const int row = order ? costly_first(a, s, place, tid) : place;
+  if (tid == 0) s.row = row;  // (read from here on: a register less)
 
   // this part's ids, in whole vectors of 16 bytes
   constexpr int VE = Vec<T>::kN;
@@ -507,9 +552,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   if (tid < 64) s.table[tid] = pow2.t[tid];
   if (tid < 2) s.list[tid].n = 0;
   if (tid == 0) s.mass = 0;
-  const float temp = a.set.d_temperature ? a.set.d_temperature[row] : a.set.temperature;
-  const int k = a.set.d_top_k ? a.set.d_top_k[row] : a.set.top_k;
-  const float tp = a.set.d_top_p ? a.set.d_top_p[row] : a.set.top_p, mp = a.set.d_min_p ? a.set.d_min_p[row] : a.set.min_p;
+  const Set set(a, row);
+  const float temp = set.temp, tp = set.tp, mp = set.mp;
+  const int k = set.k;
   const float u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604644775390625e-8f);
   // (one thread, in 64 bits, which all threads at once would wait for)
   if (tid == kThreads - 1) {
@@ -551,8 +596,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const float m = value_of((uint32_t)(best >> 32));
   if (!(fabsf(m) < INFINITY) || !(temp > 0.f)) {
     if (part == 0 && tid == 0) {
-      a.token[row] = m == -INFINITY ? 0 : (int)(0xffffffffu - (uint32_t)best);
-      if (a.logprob) a.logprob[row] = fabsf(m) < INFINITY ? 0.f : NAN;
+      a.token[s.row] = m == -INFINITY ? 0 : (int)(0xffffffffu - (uint32_t)best);
+      if (a.logprob) a.logprob[s.row] = fabsf(m) < INFINITY ? 0.f : NAN;
     }
     if (split > 1) cluster_barrier();
     return;
@@ -624,8 +669,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
           }
           const u64 goal = share(u, total);
           if (keep && upto <= goal && goal < upto + v) {
-            a.token[row] = (int)(0xffffffffu - id);
-            if (a.logprob) a.logprob[row] = logf((float)v / (float)total);
+            a.token[s.row] = (int)(0xffffffffu - id);
+            if (a.logprob) a.logprob[s.row] = logf((float)v / (float)total);
           }
         }
       }
@@ -680,7 +725,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   const int owner = __ffs(__ballot_sync(0xffffffffu, lane < split && upto > goal)) - 1;
   u64 front = __shfl_sync(0xffffffffu, upto - of_part, owner);
   const int o0 = (int)((long long)V * owner / split), o1 = (int)((long long)V * (owner + 1) / split);
-  const T* osrc = static_cast<const T*>(a.x) + (long long)row * a.ld + o0;
+  const T* osrc = static_cast<const T*>(a.x) + (long long)s.row * a.ld + o0;
   const int ooff = (int)((reinterpret_cast<uintptr_t>(osrc) & 15) / sizeof(T)), ovec = (ooff + o1 - o0 + VE - 1) / VE;
   r.x = osrc - ooff;
   r.off = ooff;
@@ -742,8 +787,8 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
             u64 weight = w[0];
 #pragma unroll
             for (int j = 1; j < VE; ++j) weight = j == pick ? w[j] : weight;
-            a.token[row] = r.id(i + lane, pick);
-            if (a.logprob) a.logprob[row] = logf((float)weight / (float)all);
+            a.token[s.row] = r.id(i + lane, pick);
+            if (a.logprob) a.logprob[s.row] = logf((float)weight / (float)all);
           }
           break;
         }
@@ -754,13 +799,24 @@ __global__ void __launch_bounds__(kThreads, 2) k_sample(const __grid_constant__ 
   if (split > 1) cluster_barrier();  // nobody leaves while its shared memory may still be read
 }
 
+// Settings that differ from row to row.
+bool of_each(const rl_sampling& s) { return s.d_temperature || s.d_top_k || s.d_top_p || s.d_min_p; }
+
 // CTAs a row is split over: as many as its parts' sums need, and more while all
-// rows' are at work at once (two an SM) and have 4096 ids at least (64 rows of
-// 128,256 cut by mass: 71 us in 4 parts, 91 in 8, 167 in 16; one row: 14.4 us in
-// 16; 500 rows of 50,257: 118 us whole, 125 in halves).
-int pick_split(int rows, int V, int sms) {
+// rows' are at work at once and have 4096 ids at least: with one an SM (64 rows of
+// 128,256 cut by mass: 71 us in 4 parts, 88 in 2, 91 in 8; 500 of 50,257: 211 whole,
+// 207 in halves; one row: 14.4 us in 16), or two where rows' settings differ and
+// the costliest take the time (48 rows of 50,257: 39 us in 8, 44 in 4; 200: 58 in
+// halves, 112 whole; 64 of 128,256: 48 in 8, 55 in 4), and halves of long rows up
+// to four (320 of 50,257: 72 us, 98 whole; 500: 104 and 110; 608: 124 and 121; of
+// 20,011 ids 400 are slower so, 63 and 55).
+int pick_split(int rows, int V, bool each, int sms) {
   int s = 1;
-  while (s < kMaxSplit && (V > kMostIds * s || ((long long)rows * s <= sms && V > 4096 * s))) s *= 2;
+  auto more = [&] {
+    const long long ctas = (long long)rows * s;
+    return V > 4096 * s && ctas <= (each ? s == 1 && V > 32768 ? 4ll : 2ll : 1ll) * sms;
+  };
+  while (s < kMaxSplit && (V > kMostIds * s || more())) s *= 2;
   return s;
 }
 
@@ -781,7 +837,7 @@ cudaError_t launch(const SampleArgs& a, const Pow2Table& table, cudaStream_t st)
       done[dev] = true;
     }
   }
-  const int split = pick_split(a.rows, a.V, sms);
+  const int split = pick_split(a.rows, a.V, of_each(a.set), sms);
   if ((long long)a.rows * split >= 1ll << 31) return cudaErrorInvalidValue;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)a.rows * split);
@@ -793,7 +849,11 @@ cudaError_t launch(const SampleArgs& a, const Pow2Table& table, cudaStream_t st)
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, a, table, split);
+  // Rows of different cost that do not all fit at once: the last to start should
+  // be the shortest (500 of 50,257 in halves: 104 us, 116 as they come; 500 of
+  // 128,256: 168 and 221; 600 of 9,001: 59 and 52, so rows of some length only).
+  const bool order = of_each(a.set) && a.V > 16384 && a.rows <= kOrder && (long long)a.rows * split > 2ll * sms;
+  return cudaLaunchKernelEx(&cfg, kern, a, table, split, order);
 }
 
 }  // namespace
@@ -829,6 +889,9 @@ extern "C" rl_status rl_sample(const void* d_logits, int32_t dtype, int32_t rows
   if ((!s.d_temperature && !(s.temperature >= 0.f && s.temperature < INFINITY)) || (!s.d_top_k && s.top_k < 0) ||
       (!s.d_top_p && !(s.top_p >= 0.f && s.top_p < INFINITY)) || (!s.d_min_p && !(s.min_p >= 0.f && s.min_p < INFINITY)))
     return bad(RL_ERR_INVALID_ARG, "temperature, top_k, top_p and min_p must not be negative, nor NaN or infinite");
+  const void* in[] = {d_logits, d_u, s.d_temperature, s.d_top_k, s.d_top_p, s.d_min_p};
+  for (const void* x : in)
+    if (x && (x == d_token || x == d_logprob)) return bad(RL_ERR_INVALID_ARG, "an output overlaps an input");
   if (reinterpret_cast<uintptr_t>(d_logits) % (dtype == RL_DT_F32 ? 4 : 2)) return bad(RL_ERR_INVALID_ARG, "logits off their element's alignment");
   SampleArgs a = {};
   a.x = d_logits;

@@ -641,7 +641,8 @@ RL_API rl_status rl_kv4_append(const rl_kv4* c, const rl_packed_desc* p, const i
 
 /* rl_kv4_read: what the cache holds for rows, as values: the last
  * d_start[b + 1] - d_start[b] of sequence b's d_kv_len[b] rows, to k and v
- * (k_stride, v_stride), m + s c in fp32 rounded once to dtype.  A prompt's
+ * (k_stride, v_stride), m + s c in fp32 rounded once to dtype (infinite beyond
+ * its range, which a row that spans nearly all of it can reach).  A prompt's
  * attention over these sees what later steps will see.  Positions outside the
  * sequence's pages set RL_DEVERR_CAPACITY, their rows are left as they were. */
 RL_API rl_status rl_kv4_read(const rl_kv4* c, const rl_packed_desc* p, const int32_t* d_start,
@@ -692,9 +693,10 @@ RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, cons
  * below 1 or from vocab on keeps all, a top_p or min_p that is NaN keeps all.
  * A logit whose difference from the largest is beyond fp32 weighs nothing.  One
  * launch, no workspace.
- * RL_ERR_INVALID_ARG for a missing buffer, a size below 1, row_stride < vocab,
- * a temperature, top_k, top_p or min_p that is negative or not finite, an
- * unknown dtype or misaligned logits; RL_ERR_UNSUPPORTED for a larger vocab. */
+ * RL_ERR_INVALID_ARG for a missing buffer, an output in an input's place (rows'
+ * settings are read by all), a size below 1, row_stride < vocab, a temperature,
+ * top_k, top_p or min_p that is negative or not finite, an unknown dtype or
+ * misaligned logits; RL_ERR_UNSUPPORTED for a larger vocab. */
 typedef struct {
   float temperature;
   int32_t top_k;

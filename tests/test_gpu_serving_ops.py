@@ -637,6 +637,26 @@ def test_sample_settings_of_each_row(river):
     check_sample(got, x, u, T, k, p, mp)
 
 
+@pytest.mark.parametrize("R", [305, 1500, 2048, 2049])
+def test_sample_many_rows_of_their_own_settings(river, R):
+    """Rows in whatever order give what a few of them alone do; only the costliest, or none of a kind, too."""
+    V = 16501  # (longer rows are put in order of their cost)
+    x, u = logits(R, V, F32, 21), uniform(R, 22)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(23)
+    T = torch.rand(R, device="cuda", generator=g) + 0.3
+    T[torch.rand(R, device="cuda", generator=g) < 0.2] = 0
+    k = torch.randint(-150, 200, (R,), device="cuda", generator=g).to(torch.int32)
+    p = torch.rand(R, device="cuda", generator=g) * 1.6
+    full = torch.full((R,), 0.9, device="cuda")
+    for s in (dict(T=T, k=k, p=p), dict(T=torch.zeros_like(T), k=k), dict(T=T), dict(p=full), dict(k=k, mp=0.01)):
+        whole = call(river, x, u, **s)
+        for i in range(0, R, 250):
+            few = call(river, x[i:i + 250], u[i:i + 250], **{n: v[i:i + 250] if torch.is_tensor(v) else v for n, v in s.items()})
+            assert torch.equal(whole["token"][i:i + 250], few["token"]) and torch.equal(whole["logprob"][i:i + 250], few["logprob"])
+        check_sample({n: t[:60] for n, t in whole.items()}, x[:60], u[:60], **{n: v[:60] if torch.is_tensor(v) else v for n, v in s.items()})
+
+
 @pytest.mark.parametrize("R,V", [(2, 40009), (40, 4003)])
 def test_sample_orders_and_ties(river, R, V):
     """Ties at every border, all logits equal, sorted rows."""

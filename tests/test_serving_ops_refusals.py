@@ -112,6 +112,19 @@ def _sample(river, **kw):
                                 P(a["token"]), None, None)
 
 
+@pytest.mark.parametrize("key", ["d_temperature", "d_top_k", "d_top_p", "d_min_p", "u", "logits"])
+@pytest.mark.parametrize("out", ["token", "logprob"])
+def test_sample_outputs_in_inputs_places(river, key, out):
+    at = dict(logits=A, u=A + 4096, token=A + 8192, logprob=A + 12288)
+    s = river.rl_sampling(1.0, 0, 1.0, 0.0)
+    if key in at:
+        at[out] = at[key]
+    else:
+        setattr(s, key, at[out])
+    assert river._lib.rl_sample(P(at["logits"]), 0, 2, 100, 100, P(at["u"]), ctypes.byref(s), P(at["token"]), P(at["logprob"]),
+                                None) == river.RL_ERR_INVALID_ARG and b"overlaps" in river._lib.rl_last_error()
+
+
 @pytest.mark.parametrize("kw,status", [
     (dict(logits=None), "INVALID_ARG"), (dict(u=None), "INVALID_ARG"), (dict(set=False), "INVALID_ARG"), (dict(token=None), "INVALID_ARG"),
     (dict(dtype=3), "INVALID_ARG"), (dict(rows=0), "INVALID_ARG"), (dict(vocab=0), "INVALID_ARG"), (dict(stride=99), "INVALID_ARG"),

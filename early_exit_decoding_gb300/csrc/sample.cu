@@ -28,7 +28,7 @@
 // What bounds it: instructions, some 75 a logit where weights are summed (the
 // exponential's 45, the histogram's 20), and the chain of a digit: histogram,
 // barrier, the groups' and the bins' sums from the other parts.  64 rows of
-// 128,256 fp32 logits cut at 0.9 of their mass: 71 us (the row's first reading
+// 128,256 fp32 logits cut at 0.9 of their mass: 72 us (the row's first reading
 // 7, the histogram 16, the next digit 11, the id 5, the rest between them); 500
 // rows of 50,257 bf16 logits, each with settings of its own: 104 us; one row
 // with top-k 50 and top-p 0.95: 14 us.
@@ -804,7 +804,7 @@ bool of_each(const rl_sampling& s) { return s.d_temperature || s.d_top_k || s.d_
 
 // CTAs a row is split over: as many as its parts' sums need, and more while all
 // rows' are at work at once and have 4096 ids at least: with one an SM (64 rows of
-// 128,256 cut by mass: 71 us in 4 parts, 88 in 2, 91 in 8; 500 of 50,257: 211 whole,
+// 128,256 cut by mass: 72 us in 4 parts, 88 in 2, 91 in 8; 500 of 50,257: 211 whole,
 // 207 in halves; one row: 14.4 us in 16), or two where rows' settings differ and
 // the costliest take the time (48 rows of 50,257: 39 us in 8, 44 in 4; 200: 58 in
 // halves, 112 whole; 64 of 128,256: 48 in 8, 55 in 4), and halves of long rows up

@@ -413,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
             const float mn = fmaxf(m[nt][r], x + base[nt][r]), to = mn == -INFINITY ? 0.f : mn, f = ex2(m[nt][r] - to);
             const float M = rel[nt][r] == 0.f ? -INFINITY : base[nt][r] - log2f(rel[nt][r]);
             float Mn = fmaxf(M, y + base[nt][r]);
-            if (Mn != -INFINITY) Mn = fmaxf(Mn, to - 100.f);  // (2^-100 of the largest weight: as good as nothing)
+            // at least 2^-100 of the largest weight: as good as nothing, and a start while all steps so far are 0
+            if (mn != -INFINITY) Mn = fmaxf(Mn, to - 100.f);
             fo[r] = M == -INFINITY ? 0.f : ex2(M - Mn);
             l[nt][r] *= f;
             z[nt][r] *= f;

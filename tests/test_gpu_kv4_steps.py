@@ -1,0 +1,66 @@
+"""kv4_attention where the steps of the values differ from key to key: zeros in
+front of, between and behind ordinary ones.  Tolerances as in test_gpu_serving_ops (which count steps by their size)."""
+import pytest
+
+from tests.test_gpu_attention_ops import rnd, river  # noqa: F401
+from tests.test_gpu_serving_ops import check_kv4, i32, make_cache, starts
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+BF, FP = torch.bfloat16, torch.float16
+
+
+def set_steps(cache, table, b, positions, value, minimum=None):
+    """v's steps (and minima) of a sequence's positions, in every head."""
+    page = cache.v_codes.shape[2]
+    pos = torch.tensor(list(positions), dtype=torch.int64, device="cuda")
+    cache.v_scale[table[b, pos // page].long(), :, pos % page, 0] = value
+    if minimum is not None:
+        cache.v_scale[table[b, pos // page].long(), :, pos % page, 1] = minimum
+
+
+ZEROS = [range(32), range(128), range(256), range(1, 33), range(700), range(300, 700), [*range(64), *range(500, 900)], range(1000)]
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D,Hq,rows", [(64, 4, 1), (128, 8, 1), (64, 4, 5), (128, 8, 4), (128, 32, 1)])
+@pytest.mark.parametrize("zeros", ZEROS, ids=lambda z: f"{z[0]}-{z[-1]}-{len(z)}")
+def test_steps_of_zero_beside_others(river, dtype, D, Hq, rows, zeros):  # noqa: F811
+    """Flat scores, so that nothing else makes the kernel scale anew."""
+    lens = [1024, 33, 1001]
+    cache, table = make_cache(river, lens, 2, D, 16, dtype, 11)
+    cache.k_scale.mul_(0.02)
+    for b, n in enumerate(lens):
+        set_steps(cache, table, b, [p for p in zeros if p < n], 0.0)
+    q = rnd(3 * rows, Hq, D, dtype=dtype, seed=12)
+    args = dict(start=starts([rows] * 3), max_rows=rows) if rows > 1 else {}
+    check_kv4(river.kv4_attention(q, cache, table, i32(lens), **args), q, cache, table, lens, [rows] * 3)
+    # rows of zeros as an append leaves them
+    for b, n in enumerate(lens):
+        set_steps(cache, table, b, [p for p in zeros if p < n], 0.0, 0.0)
+    check_kv4(river.kv4_attention(q, cache, table, i32(lens), **args), q, cache, table, lens, [rows] * 3)
+
+
+@pytest.mark.parametrize("rows", [1, 9])
+def test_shares_that_start_among_steps_of_zero(river, rows):  # noqa: F811
+    lens = [20000, 700, 9000]
+    cache, table = make_cache(river, lens, 2, 128, 64, BF, 21)
+    cache.k_scale.mul_(0.02)
+    for b, n in enumerate(lens):
+        set_steps(cache, table, b, [p for p in range(n) if p % 3000 < 1500], 0.0)
+    q = rnd(3 * rows, 4, 128, dtype=BF, seed=22)
+    got = river.kv4_attention(q, cache, table, i32(lens), start=starts([rows] * 3), max_rows=rows)
+    check_kv4(got, q, cache, table, lens, [rows] * 3, most=3)
+
+
+def test_zeros_first_give_what_they_give_last(river):  # noqa: F811
+    """A sequence's output does not hang on what else is in the call."""
+    lens = [640] + [100] * 40
+    cache, table = make_cache(river, lens, 2, 64, 32, BF, 31)
+    cache.k_scale.mul_(0.02)
+    set_steps(cache, table, 0, range(320), 0.0)
+    q = rnd(len(lens), 8, 64, dtype=BF, seed=32)
+    alone = river.kv4_attention(q[:1], cache, table[:1].contiguous(), i32(lens[:1]))
+    check_kv4(alone, q[:1], cache, table, lens[:1], [1])
+    check_kv4(river.kv4_attention(q, cache, table, i32(lens)), q, cache, table, lens, [1] * len(lens))

@@ -514,11 +514,11 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
           l[nt][r] += __shfl_xor_sync(0xffffffffu, l[nt][r], d);
           z[nt][r] += __shfl_xor_sync(0xffffffffu, z[nt][r], d);
         }
-        const float f = rel[nt][r] == 0.f ? 0.f : 1048576.f / rel[nt][r];  // 2^20 2^(M - m)
+        const float f = rel[nt][r] == 0.f ? 0.f : 1.f / rel[nt][r];  // 2^(M - m): steps of 2^124 leave it finite
         const int row = nt * 8 + 2 * t + r;
   #pragma unroll
         for (int i = 0; i < HD / 16; ++i) {
-          const float even = (o[nt][i][r] - o8[nt][r]) * 16.f, odd = o[nt][i][2 + r] - 16.f * o8[nt][r];
+          const float even = (o[nt][i][r] - o8[nt][r]) * 16777216.f, odd = (o[nt][i][2 + r] - 16.f * o8[nt][r]) * 1048576.f;
           *reinterpret_cast<float2*>(so + row * HD + g * (HD / 8) + 2 * i) = make_float2(fmaf(even, f, z[nt][r]), fmaf(odd, f, z[nt][r]));
         }
         if (g == 0) {

@@ -1,5 +1,6 @@
 """kv4_attention where the steps of the values differ from key to key: zeros in
-front of, between and behind ordinary ones.  Tolerances as in test_gpu_serving_ops (which count steps by their size)."""
+front of, between and behind ordinary ones, and the
+largest there are.  Tolerances as in test_gpu_serving_ops (which count steps by their size)."""
 import pytest
 
 from tests.test_gpu_attention_ops import rnd, river  # noqa: F401
@@ -64,3 +65,35 @@ def test_zeros_first_give_what_they_give_last(river):  # noqa: F811
     alone = river.kv4_attention(q[:1], cache, table[:1].contiguous(), i32(lens[:1]))
     check_kv4(alone, q[:1], cache, table, lens[:1], [1])
     check_kv4(river.kv4_attention(q, cache, table, i32(lens)), q, cache, table, lens, [1] * len(lens))
+
+
+@pytest.mark.parametrize("big", [1e33, 1e35, 1e36])
+@pytest.mark.parametrize("rows", [1, 6])
+def test_the_largest_steps(river, big, rows):  # noqa: F811
+    """Values up to 15 times `big`, whose weighted sums stay in fp32's range (41 keys: 41 x 15 x 1e35; 9 with 1e36)."""
+    lens = [41, 17, 9] if big < 1e36 else [9, 9, 3]
+    lens = [max(n, rows) for n in lens]
+    cache, table = make_cache(river, lens, 2, 64, 16, BF, 41)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(42)
+    s = (torch.rand(cache.v_scale.shape[:3], device="cuda", generator=g) * 0.9 + 0.1) * big
+    cache.v_scale[..., 0] = s.to(BF)
+    cache.v_scale[..., 1] = (-7.0 * s * torch.rand(s.shape, device="cuda", generator=g)).to(BF)
+    q = rnd(3 * rows, 4, 64, dtype=BF, seed=43)
+    args = dict(start=starts([rows] * 3), max_rows=rows) if rows > 1 else {}
+    got = river.kv4_attention(q, cache, table, i32(lens), **args)
+    assert torch.isfinite(got["out"]).all()
+    check_kv4(got, q, cache, table, lens, [rows] * 3)
+
+
+def test_a_row_over_the_types_whole_range(river):  # noqa: F811
+    """The largest steps an append can leave, one key a sequence."""
+    cache, table = make_cache(river, [1, 1], 2, 64, 16, BF, 51)
+    k = rnd(2, 2, 64, dtype=BF, seed=52)
+    v = (rnd(2, 2, 64, dtype=torch.float32, seed=53).tanh() * 1.6e38).to(BF)
+    v[..., 0], v[..., 1] = -1.69e38, 1.69e38
+    river.kv4_append(cache, table, i32([1, 1]), k, v)
+    q = rnd(2, 4, 64, dtype=BF, seed=54)
+    got = river.kv4_attention(q, cache, table, i32([1, 1]))
+    assert torch.isfinite(got["out"]).all()
+    check_kv4(got, q, cache, table, [1, 1], [1, 1])

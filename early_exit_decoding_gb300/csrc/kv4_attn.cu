@@ -385,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
             for (int e = 0; e < 4; ++e) {
               w[q][nt][e] = ex2(s[q][nt][e]);
               ws_[q][nt][e] = w[q][nt][e] * rel[nt][e & 1] * vs[q][e >> 1];  // (in this order nothing overflows that the result holds)
-              most = fmaxf(most, fmaxf(w[q][nt][e], ws_[q][nt][e]));
+              most = fmaxf(most, fmaxf(w[q][nt][e], fabsf(ws_[q][nt][e])));  // (a step may be below 0)
             }
       };
       weigh();

@@ -1,10 +1,12 @@
 """kv4_attention where the steps of the values differ from key to key: zeros in
-front of, between and behind ordinary ones, and the
-largest there are.  Tolerances as in test_gpu_serving_ops (which count steps by their size)."""
+front of, between and behind ordinary ones, the largest there are, negative
+ones.  Tolerances as in test_gpu_serving_ops (which count steps by their size)."""
+import math
+
 import pytest
 
-from tests.test_gpu_attention_ops import rnd, river  # noqa: F401
-from tests.test_gpu_serving_ops import check_kv4, i32, make_cache, starts
+from tests.test_gpu_attention_ops import compare, rnd, river  # noqa: F401
+from tests.test_gpu_serving_ops import check_kv4, held, i32, kv4_ref, make_cache, starts
 
 torch = pytest.importorskip("torch")
 pytestmark = pytest.mark.gpu
@@ -97,3 +99,24 @@ def test_a_row_over_the_types_whole_range(river):  # noqa: F811
     got = river.kv4_attention(q, cache, table, i32([1, 1]))
     assert torch.isfinite(got["out"]).all()
     check_kv4(got, q, cache, table, [1, 1], [1, 1])
+
+
+@pytest.mark.parametrize("dtype", [BF, FP])
+@pytest.mark.parametrize("D,Hq,rows", [(64, 4, 1), (128, 8, 4)])
+def test_steps_below_zero(river, dtype, D, Hq, rows):  # noqa: F811
+    """A cache whose rows count down from their largest value, the sizes of the steps growing on the way."""
+    lens = [600, 41]
+    cache, table = make_cache(river, lens, 2, D, 16, dtype, 61)
+    cache.k_scale.mul_(0.02)
+    for b, n in enumerate(lens):
+        set_steps(cache, table, b, range(0, n), -0.4)
+        set_steps(cache, table, b, range(0, n // 2), -1e-4)
+        set_steps(cache, table, b, range(n * 3 // 4, n), -300.0, 4000.0)
+    q = rnd(2 * rows, Hq, D, dtype=dtype, seed=62)
+    args = dict(start=starts([rows] * 2), max_rows=rows) if rows > 1 else {}
+    got = river.kv4_attention(q, cache, table, i32(lens), **args)
+    for b, n in enumerate(lens):
+        (k, ks), (v, vs) = held(cache, table, b, n)
+        refs = [kv4_ref(q[b * rows + t], [(k[:, : n - rows + t + 1], ks[:, : n - rows + t + 1]), (v[:, : n - rows + t + 1], vs[:, : n - rows + t + 1].abs())],
+                        1 / math.sqrt(D)) for t in range(rows)]
+        compare(got["out"][b * rows:(b + 1) * rows], got["lse"][b * rows:(b + 1) * rows], refs, f"sequence {b}")

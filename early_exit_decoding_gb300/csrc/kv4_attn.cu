@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
   int left = (int)(stop_at - at);  // units of the share to come
   // the sequence, tile and head, and unit it starts with
   int b = 0, item = 0, u0 = 0;
-  Load ld;
+  Load ld{0, 0};
   {
     long long before = 0;
     for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -580,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, kResident<NT>)
     if (++item == ld.tiles * a.Hkv) {
       item = 0;
       do ld = seq_load(a, cap, rep, R, ++b);
-      while (ld.tiles == 0 || ld.units == 0);
+      while (b < a.B && (ld.tiles == 0 || ld.units == 0));  // (the end: only if lengths change meanwhile)
     }
     __syncthreads();  // (the rings are free)
   }

@@ -41,6 +41,7 @@
 
 #include "dev_common.cuh"
 #include "internal.h"
+#include "sample_weight.h"
 
 namespace river {
 
@@ -78,36 +79,20 @@ __device__ __forceinline__ float value_of(uint32_t o) {
 }
 __device__ __forceinline__ u64 key_of(float x, int id) { return ((u64)order_bits(x) << 32) | (0xffffffffu - (uint32_t)id); }
 
-// 2^(-j / 64) 2^45, j < 64.
 struct Pow2Table {
-  u64 t[64];
+  u64 t[64];  // weight::entry
 };
 
-// exp((x - m) / T) 2^44, rounded: 2^-y with y = (m - x) c, c = log2(e) / T.
+// A logit's weight (sample_weight.h), with the row's largest logit and rate.
 struct Weight {
-  float m, ch, cl;  // c = ch + cl
-  uint32_t table;   // Pow2Table in shared memory
+  float m, ch, cl;
+  uint32_t table;  // Pow2Table in shared memory
   __device__ __forceinline__ u64 operator()(float x) const {
-    // y = p + e: the difference and the product exact in two parts each
-    const float d = m - x, b = d - m, dl = (m - (d - b)) - (x + b);
-    const float p = d * ch;
-    if (!(p < 46.f)) return 0;  // (below half a unit; x = -infinity, or c 0 times infinity)
-    const float e = fmaf(dl, ch, fmaf(d, cl, fmaf(d, ch, -p)));
-    // y = k / 64 + r, |r| <= 1 / 128
-    const float big = 196608.f;  // 1.5 2^17: its sums are whole multiples of 1 / 64
-    const float s = p + big, r = p - (s - big);
-    const uint32_t k = __float_as_uint(s) - __float_as_uint(big);
-    // 2^-r = 1 - a + a^2 / 2 - a^3 / 6 + a^4 / 24 (the next term is below 2^-44), a = ln 2 (r + e) = ah + al
-    const float lh = 0.693147182464599609375f, ll = -1.904654323148236017e-9f;  // ln 2 in two parts
-    const float ah = r * lh, al = fmaf(e, lh, fmaf(r, ll, fmaf(r, lh, -ah)));
-    const float v = fmaf(-ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al);  // 1 - 2^-r = ah + v
-    // times 2^38, to whole numbers (v's is below 2^22: by a sum with 1.5 2^23)
-    const float unit = 274877906944.f, round = 12582912.f;
-    const int w = __float2int_rn(ah * unit) + ((int)__float_as_uint(fmaf(v, unit, round)) - (int)__float_as_uint(round));
-    u64 t;
-    asm("ld.shared.u64 %0, [%1];" : "=l"(t) : "r"(table + (k & 63) * 8));
-    const u64 f = t - (u64)(((long long)(int)(t >> 15) * w) >> 23);
-    return ((f >> (k >> 6)) + 1) >> 1;
+    return weight::of(x, m, weight::Rate{ch, cl}, [&](uint32_t j) {
+      u64 t;
+      asm("ld.shared.u64 %0, [%1];" : "=l"(t) : "r"(table + j * 8));
+      return t;
+    });
   }
 };
 
@@ -558,11 +543,10 @@ __global__ void __launch_bounds__(kThreads, 2)
   const float u = fminf(fmaxf(a.u[row], 0.f), 1.f - 5.9604644775390625e-8f);
   // (one thread, in 64 bits, which all threads at once would wait for)
   if (tid == kThreads - 1) {
-    const double t = fmin((double)temp, 3.4028234663852886e38);
-    const double c = fmin(1.4426950408889634 / t, 1e38);  // (finite in fp32)
-    s.ch = (float)c;
-    s.cl = (float)(c - (double)(float)c);
-    s.span = mp > 0.f ? t * log((double)mp) : 0.0;
+    const weight::Rate c = weight::rate_of(temp);
+    s.ch = c.h;
+    s.cl = c.l;
+    s.span = mp > 0.f ? fmin((double)temp, 3.4028234663852886e38) * log((double)mp) : 0.0;
   }
   __syncthreads();
 
@@ -861,7 +845,7 @@ cudaError_t launch(const SampleArgs& a, const Pow2Table& table, cudaStream_t st)
 cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
   static const Pow2Table table = [] {
     Pow2Table t;
-    for (int j = 0; j < 64; ++j) t.t[j] = (u64)llrint(exp2(45.0 - j / 64.0));
+    for (int j = 0; j < 64; ++j) t.t[j] = weight::entry(j);
     return t;
   }();
   if (a.dtype == RL_DT_F32) return launch<float>(a, table, s);

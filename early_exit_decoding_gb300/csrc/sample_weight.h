@@ -74,8 +74,10 @@ RIVER_WEIGHT_FN uint64_t of(float x, float m, Rate c, Table table) {
   const float lh = 0.693147182464599609375f, ll = -1.904654323148236017e-9f;  // ln 2 in two parts
   const float ah = r * lh, al = fmaf(e, lh, fmaf(r, ll, fmaf(r, lh, -ah)));
   const float v = fmaf(-ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al);  // 1 - 2^-r = ah + v
-  // times 2^38, to whole numbers (v's is below 2^22: by a sum with 1.5 2^23)
-  const float unit = 274877906944.f, round = 12582912.f;
+  // times 2^38, to whole numbers.  v's is in (-5.6e6, 1.5e6): -a^2 / 2 reaches -4.03e6, and al, ln 2 times half a
+  // unit of p in its last place and the roundings of d and c, 5.2e-6 at y 46; so its sum with 1.75 2^23 is in
+  // [2^23, 2^24), where bits are units.
+  const float unit = 274877906944.f, round = 14680064.f;
   const int w = whole(ah * unit) + ((int)bits(fmaf(v, unit, round)) - (int)bits(round));
   const uint64_t t = table(k & 63);
   const uint64_t f = t - (uint64_t)(((long long)(int)(t >> 15) * w) >> 23);

@@ -9,9 +9,10 @@
 // sums in the order of ids.
 //
 // A weight is a 64-bit whole number, exp((x - max) / T) 2^44 rounded: sums are
-// exact whatever their order, and with exponentials good to 2^-38 a token
-// differs from that of exact weights only where u is that near a border (fp32
-// sums: 1 in 50 rows of 128,256 logits with a long tail).
+// exact whatever their order, and with exponentials good to 2^-35 of themselves
+// (sample_weight.h; measured 2^-36.2) a token differs from that of exact weights
+// only where u is that near a border (fp32 sums: 1 in 50 rows of 128,256 logits
+// with a long tail).
 //
 // A cluster of CTAs takes a row, each a part whose warps have contiguous
 // segments, and reads it from HBM once and then from L2 (held in shared memory

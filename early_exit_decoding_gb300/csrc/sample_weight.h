@@ -70,10 +70,12 @@ RIVER_WEIGHT_FN uint64_t of(float x, float m, Rate c, Table table) {
   const float big = 196608.f;  // 1.5 2^17: its sums are whole multiples of 1 / 64
   const float s = p + big, r = p - (s - big);
   const uint32_t k = bits(s) - bits(big);
-  // 2^-r = 1 - a + a^2 / 2 - a^3 / 6 + a^4 / 24 (the next term is below 2^-44), a = ln 2 (r + e) = ah + al
+  // 2^-r = exp(-a), a = ln 2 (r + e) = ah + al: 1 - exp(-ah) = q = ah - ah^2 / 2 + ah^3 / 6 - ah^4 / 24 (the next term
+  // is below 2^-44), and (1 - q) (1 - exp(-al)) more, of which al^2 / 2 is left out (2^-36 at y 46, 2^-39 at 16)
   const float lh = 0.693147182464599609375f, ll = -1.904654323148236017e-9f;  // ln 2 in two parts
   const float ah = r * lh, al = fmaf(e, lh, fmaf(r, ll, fmaf(r, lh, -ah)));
-  const float v = fmaf(-ah * ah, fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), al);  // 1 - 2^-r = ah + v
+  const float sq = -ah * ah, h = fmaf(ah, fmaf(ah, 1.f / 24.f, -1.f / 6.f), 0.5f), q = fmaf(sq, h, ah);
+  const float v = fmaf(-q, al, fmaf(sq, h, al));  // 1 - 2^-r = ah + v
   // times 2^38, to whole numbers.  v's is in (-5.6e6, 1.5e6): -a^2 / 2 reaches -4.03e6, and al, ln 2 times half a
   // unit of p in its last place and the roundings of d and c, 5.2e-6 at y 46; so its sum with 1.75 2^23 is in
   // [2^23, 2^24), where bits are units.

@@ -684,9 +684,9 @@ RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, cons
  *   settings  of all rows, or (a pointer that is not NULL) one a row
  *   d_token   [rows] int32
  *   d_logprob [rows] fp32, may be NULL: ln of the token's share of the kept weights
- * Weights are whole multiples of 2^-44 (their exponentials are good to
- * 2^-38), sums are exact, so results repeat bit for bit and do not depend on
- * how a row is split.  Logits of -infinity are never drawn.  A row with a NaN or
+ * Weights are whole multiples of 2^-44, each within 2^-35 of itself and half of
+ * that (temperatures from 2^-125 to 2^110), sums are exact, so results repeat
+ * bit for bit and do not depend on how a row is split.  Logits of -infinity are never drawn.  A row with a NaN or
  * +infinity gives the id rl_token_logprobs would put first and logprob NaN, a
  * row of -infinity alone id 0 and NaN; settings of d_ arrays: a temperature
  * not above 0 (or NaN) is 0, an infinite one the largest finite one, a top_k

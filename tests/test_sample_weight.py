@@ -27,3 +27,24 @@ def test_whole_numbers_far_from_the_largest(host, m, T):
     Bound: ah al <= 2^-7.5 2^-17.5 of the weight, the other terms together below 2^-35 of it."""
     rel, _ = host.errors(grid(m, T, 200000, 1, least=8.0), m, T)
     assert rel.max() <= 2.0 ** -24.9, np.log2(rel.max())
+
+
+@pytest.mark.parametrize("m,T", SETTINGS)
+def test_weights_are_good_to_their_bound(host, m, T):
+    """Within 2^-35 of themselves and half a unit, wherever they are.
+
+    Of the weight: the table's 15 low bits left out times |1 - 2^-r| < 2^-7.5: 2^-36.5; two whole numbers rounded, 2^-38;
+    fp32 roundings of v (below 2^-15.5), 2^-39; al^2 / 2, 2^-36.2; what is left of the series, the shift and the table's
+    own rounding, below 2^-43 together."""
+    rel, exact = host.errors(grid(m, T, 500000, 2), m, T)
+    assert rel.max() <= 2.0 ** -35, np.log2(rel.max())
+    assert (rel * exact).max() <= 2.0 ** (44 - 36), np.log2((rel * exact).max())  # of the largest weight, where al is small
+
+
+def test_weights_at_the_ends(host):
+    """The largest itself, what is below half a unit, infinite and huge differences."""
+    w = host.weights([2.0, 2.0 - 31.5, -1e30, -np.inf, -3.4e38], 2.0, 1.0)
+    assert w.tolist() == [1 << 44, 0, 0, 0, 0]
+    assert host.weights([3.3e38, -3.3e38], 3.3e38, 1.0).tolist() == [1 << 44, 0]
+    assert host.weights([0.0, 1.0], 1.0, 3e38).tolist() == [1 << 44, 1 << 44]
+    assert host.weights([1.0, np.nextafter(np.float32(1), np.float32(0))], 1.0, 1e-30).tolist() == [1 << 44, 0]

@@ -771,6 +771,17 @@ def _int32(name, key, t, shape):
         _refuse(f"{name}: {key} must be contiguous int32 {shape}")
 
 
+def _whole(name, key, x):
+    """x as an int; refused where it is none (a fraction is not cut off)."""
+    try:
+        n = int(x)
+        if n == x:
+            return n
+    except (TypeError, ValueError, OverflowError):
+        pass
+    _refuse(f"{name}: {key} must be a whole number (found {x!r})")
+
+
 def _addr(t):
     return None if t is None else t.data_ptr()
 
@@ -984,7 +995,7 @@ def _packed_desc(name, dtype, heads, batch, rows, max_rows, scale, **tensors):
         _refuse(f"{name}: sizes must be below 2^31", RL_ERR_UNSUPPORTED)
     if scale is not None and not scale > 0.0:
         _refuse(f"{name}: scale must be above 0")
-    d.dtype, d.batch, d.rows, d.max_rows, d.n_q_heads, d.n_kv_heads, d.head_dim = code, batch, rows, _int32_of(max_rows), n_q, n_kv, hd
+    d.dtype, d.batch, d.rows, d.max_rows, d.n_q_heads, d.n_kv_heads, d.head_dim = code, batch, rows, _int32_of(_whole(name, "max_rows", max_rows)), n_q, n_kv, hd
     d.scale = 0.0 if scale is None else scale
     if scale is not None and d.scale == 0.0:  # (which would stand for the default)
         _refuse(f"{name}: scale {scale} is 0 in fp32")
@@ -1127,7 +1138,7 @@ def kv4_read(cache, table, kv_len, start=None, rows=None, out=None, err=None, st
     B = kv_len.numel()
     if rows is None and start is not None:
         _refuse(f"{name}: start needs rows")
-    N = B if rows is None else int(rows)
+    N = B if rows is None else _whole(name, "rows", rows)
 
     def make():
         if not 1 <= N <= _INT32_MAX or B < 1:
@@ -1215,7 +1226,7 @@ def sample(logits, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, out=None, 
             setattr(s, "d_" + key, x.data_ptr())
             given.append(x)
         else:
-            setattr(s, key, _int32_of(int(x)) if key == "top_k" else float(x))
+            setattr(s, key, _int32_of(_whole(name, key, x)) if key == "top_k" else float(x))
     dev = _operands(name, (logits, u, *given))
     if u.dtype != torch.float32 or u.shape != (R,) or not u.is_contiguous():
         _refuse(f"{name}: u must be contiguous fp32 ({R},)")

@@ -207,3 +207,21 @@ def test_rope_table_is_the_model_rotation(river):
     c, s = tab[None, :, None, :, 0], tab[None, :, None, :, 1]
     want = rope(x, np.arange(7), 10000.0)
     assert np.abs(np.concatenate([a * c - b * s, b * c + a * s], -1) - want).max() < 1e-5
+
+
+@pytest.mark.parametrize("bad", [0.5, 2.25, float("nan"), float("inf"), "3"])
+def test_fractions_for_whole_numbers(river, monkeypatch, bad):
+    """A count is never cut to the whole number below it (top_k 0.5 would keep every id); whole floats are counts."""
+    monkeypatch.setattr(river, "_operands", lambda name, tensors: -1)
+    monkeypatch.setattr(river, "_run", lambda *a: pytest.fail("reached the library"))
+    t = _tensors(river)
+    q, k, c, tab, n, st = (t[x] for x in ("q", "k", "cache", "table", "n", "start"))
+    for call in (lambda: river.sample(torch.zeros((2, 9)), torch.zeros(2), top_k=bad), lambda: river.kv4_read(c, tab, n, start=st, rows=bad),
+                 lambda: river.packed_attention(q, k, k, st, max_rows=bad), lambda: river.kv4_attention(q, c, tab, n, start=st, max_rows=bad)):
+        with pytest.raises(river.RiverError) as e:
+            call()
+        assert e.value.status == river.RL_ERR_INVALID_ARG and "whole" in str(e.value)
+    seen = []
+    monkeypatch.setattr(river, "_run", lambda dev, stream, fn, *a: seen.append(a))
+    river.sample(torch.zeros((2, 9)), torch.zeros(2), top_k=7.0)
+    assert seen[0][6].top_k == 7

@@ -858,6 +858,14 @@ cudaError_t launch_sample(const SampleArgs& a, cudaStream_t s) {
 
 using namespace river;
 
+// Whether n bytes from p on meet one of `rows` rows of `len` bytes, `step` apart, from x on.
+static bool meets(const void* p, uint64_t n, const void* x, int rows, uint64_t len, uint64_t step) {
+  const uint64_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(x);
+  if (a < b) return n > b - a;
+  const uint64_t row = (a - b) / step, in = (a - b) % step;
+  return row < (uint64_t)rows && (in < len || (row + 1 < (uint64_t)rows && n > step - in));
+}
+
 extern "C" rl_status rl_sample(const void* d_logits, int32_t dtype, int32_t rows, int32_t vocab, int64_t row_stride,
                                const float* d_u, const rl_sampling* settings, int32_t* d_token, float* d_logprob,
                                rl_stream_t stream) {
@@ -874,9 +882,14 @@ extern "C" rl_status rl_sample(const void* d_logits, int32_t dtype, int32_t rows
   if ((!s.d_temperature && !(s.temperature >= 0.f && s.temperature < INFINITY)) || (!s.d_top_k && s.top_k < 0) ||
       (!s.d_top_p && !(s.top_p >= 0.f && s.top_p < INFINITY)) || (!s.d_min_p && !(s.min_p >= 0.f && s.min_p < INFINITY)))
     return bad(RL_ERR_INVALID_ARG, "temperature, top_k, top_p and min_p must not be negative, nor NaN or infinite");
-  const void* in[] = {d_logits, d_u, s.d_temperature, s.d_top_k, s.d_top_p, s.d_min_p};
-  for (const void* x : in)
-    if (x && (x == d_token || x == d_logprob)) return bad(RL_ERR_INVALID_ARG, "an output overlaps an input");
+  const uint64_t n = 4ull * rows, width = dtype == RL_DT_F32 ? 4 : 2, apart = (uint64_t)row_stride < 1ull << 60 ? row_stride : 1ull << 60;
+  for (const void* out : {(const void*)d_token, (const void*)d_logprob}) {
+    bool hit = out && meets(out, n, d_logits, rows, width * vocab, width * apart);
+    for (const void* x : {(const void*)d_u, (const void*)s.d_temperature, (const void*)s.d_top_k, (const void*)s.d_top_p, (const void*)s.d_min_p})
+      hit = hit || (out && x && meets(out, n, x, 1, n, n));
+    if (hit) return bad(RL_ERR_INVALID_ARG, "an output overlaps an input");
+  }
+  if (d_logprob && meets(d_token, n, d_logprob, 1, n, n)) return bad(RL_ERR_INVALID_ARG, "the outputs overlap");
   if (reinterpret_cast<uintptr_t>(d_logits) % (dtype == RL_DT_F32 ? 4 : 2)) return bad(RL_ERR_INVALID_ARG, "logits off their element's alignment");
   SampleArgs a = {};
   a.x = d_logits;

@@ -693,10 +693,11 @@ RL_API rl_status rl_kv4_attention(const rl_kv4* c, const rl_packed_desc* p, cons
  * below 1 or from vocab on keeps all, a top_p or min_p that is NaN keeps all.
  * A logit whose difference from the largest is beyond fp32 weighs nothing.  One
  * launch, no workspace.
- * RL_ERR_INVALID_ARG for a missing buffer, an output in an input's place (rows'
- * settings are read by all), a size below 1, row_stride < vocab, a temperature,
- * top_k, top_p or min_p that is negative or not finite, an unknown dtype or
- * misaligned logits; RL_ERR_UNSUPPORTED for a larger vocab. */
+ * RL_ERR_INVALID_ARG for a missing buffer, an output that overlaps an input (rows'
+ * logits and settings are read more than once) or the other output, a size below
+ * 1, row_stride < vocab, a temperature, top_k, top_p or min_p that is negative or
+ * not finite, an unknown dtype or misaligned logits; RL_ERR_UNSUPPORTED for a
+ * larger vocab. */
 typedef struct {
   float temperature;
   int32_t top_k;

@@ -225,3 +225,20 @@ def test_fractions_for_whole_numbers(river, monkeypatch, bad):
     monkeypatch.setattr(river, "_run", lambda dev, stream, fn, *a: seen.append(a))
     river.sample(torch.zeros((2, 9)), torch.zeros(2), top_k=7.0)
     assert seen[0][6].top_k == 7
+
+
+@pytest.mark.parametrize("out", ["token", "logprob"])
+@pytest.mark.parametrize("key,by", [("d_temperature", 4), ("d_top_k", -4), ("d_top_p", 8), ("d_min_p", -8), ("u", 8), ("u", -8), ("logits", -8), ("logits", 396),
+                                    ("logits", 480), ("logits", 872), ("other", 4), ("other", 0), ("other", -8)])
+def test_sample_outputs_that_overlap_in_part(river, key, by, out):
+    """Three rows: an output that starts `by` bytes from an input, or from the other output (rows of logits are 400 bytes, 480 apart)."""
+    at = dict(logits=A, u=A + 4096, token=A + 8192, logprob=A + 12288)
+    s = river.rl_sampling(1.0, 0, 1.0, 0.0)
+    if key == "other":
+        at[out] = at["logprob" if out == "token" else "token"] + by
+    elif key in at:
+        at[out] = at[key] + by
+    else:
+        setattr(s, key, at[out] - by)
+    assert river._lib.rl_sample(P(at["logits"]), 0, 3, 100, 120, P(at["u"]), ctypes.byref(s), P(at["token"]), P(at["logprob"]),
+                                None) == river.RL_ERR_INVALID_ARG and b"overlap" in river._lib.rl_last_error()

@@ -390,10 +390,13 @@ struct Row {
       } else {
         // few ids, brought together first (a weight takes a warp the same time for one lane's)
         each<2>(i0, i1, [&](float v, int i) {
-          if (agrees(v, i, level)) s.few[atomicAdd(&s.n_few, 1u)] = key_of(v, i);  // (no more than were counted)
+          if (agrees(v, i, level)) {
+            const uint32_t at = atomicAdd(&s.n_few, 1u);
+            if (at < kGather) s.few[at] = key_of(v, i);  // (no more than were counted, if logits stay as they are)
+          }
         });
         __syncthreads();
-        for (int i = tid; i < (int)s.n_few; i += kThreads) {
+        for (int i = tid; i < (int)min(s.n_few, (uint32_t)kGather); i += kThreads) {
           const Cut c = cut_of(s.few[i]);
           add(c.v, (int)c.id);
         }
@@ -517,7 +520,7 @@ __device__ int costly_first(const SampleArgs& a, Shared& s, int i, int tid) {
     for (int r = tid; r < a.rows; r += kThreads)
       if (2 - Set(a, r).cost(a.V) == c && i-- == 0) s.bin = r;
   __syncthreads();
-  return s.bin;
+  return (int)min((unsigned)s.bin, (unsigned)a.rows - 1u);
 }
 
 template <typename T>
@@ -707,7 +710,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const u64 t = __shfl_up_sync(0xffffffffu, upto, o);
     if (lane >= o) upto += t;
   }
-  const int owner = __ffs(__ballot_sync(0xffffffffu, lane < split && upto > goal)) - 1;
+  const int owner = max(__ffs(__ballot_sync(0xffffffffu, lane < split && upto > goal)), 1) - 1;
   u64 front = __shfl_sync(0xffffffffu, upto - of_part, owner);
   const int o0 = (int)((long long)V * owner / split), o1 = (int)((long long)V * (owner + 1) / split);
   const T* osrc = static_cast<const T*>(a.x) + (long long)s.row * a.ld + o0;
@@ -736,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     // the segment it is in, then the sixteenth of that, then the id
     const int step = width / kWarps;
     int ow = 0;
-    while (front + s.sums[ow] <= goal) front += s.sums[ow++];
+    while (ow < kWarps - 1 && front + s.sums[ow] <= goal) front += s.sums[ow++];
     const int s0 = min(ovec, base + ow * step), s1 = min(ovec, s0 + step), sub = (s1 - s0 + kWarps - 1) / kWarps;
     auto range = [&](int j, int* b, int* e) {
       *b = min(s1, s0 + j * sub);
@@ -748,7 +751,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     if (lane == 0) s.red[warp] = sum;
     __syncthreads();
     int os = 0;
-    while (front + s.red[os] <= goal) front += s.red[os++];
+    while (os < kWarps - 1 && front + s.red[os] <= goal) front += s.red[os++];
     if (warp == 0) {
       range(os, &b, &e);
       for (int i = b; i < e; i += 32) {

@@ -591,7 +591,9 @@ typedef struct {
  * roundings; keys a row does not see have no part in its result, whatever they
  * hold.  A sequence of more than max_rows rows sets RL_DEVERR_CAPACITY and has
  * its first max_rows rows computed, the others are left as they were.  One
- * launch, no workspace, results repeat bit for bit. */
+ * launch, no workspace, results repeat bit for bit.  Every CTA reads all of
+ * d_start: set-up grows with batch squared (8 KV heads: 0.7 ms for 1,024
+ * sequences of a row, 6.8 for 4,096, 155 for 16,384, 2.4 s for 2^16). */
 RL_API rl_status rl_packed_attention(const rl_packed_desc* p, const void* d_q, const void* d_k,
                                      const void* d_v, const int32_t* d_start, void* d_out, float* d_lse,
                                      int32_t* d_err, rl_stream_t stream);

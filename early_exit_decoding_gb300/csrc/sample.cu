@@ -262,7 +262,7 @@ struct Row {
     return sum;
   }
   __device__ __forceinline__ uint32_t place_q(float v) const {
-    const float y = (m - v) * w.ch;
+    const float y = weight::product(m - v, w.ch);
     return y >= 0.f ? ~__float2uint_rz(y * 67108864.f) : 0u;  // 2^26; saturates (NaN: 0 times infinity)
   }
   __device__ __forceinline__ void barrier() const {
@@ -355,7 +355,7 @@ struct Row {
     auto agrees = [&](float v, int i, int level) {
       if (!(v >= lo && v <= hi) || !least.takes(v, i)) return false;
       // (what fills the vectors is nobody's; weights of 0 would only crowd the others)
-      if (MASS ? !((m - v) * w.ch < 46.f) : i < id0 || i >= id1) return false;
+      if (MASS ? !(weight::product(m - v, w.ch) < 46.f) : i < id0 || i >= id1) return false;
       return level < 5 || !(((order_bits(v) ^ want.o) & mask.o) | (((0xfffffu - (uint32_t)i) ^ want.i) & mask.i));
     };
     int level = 0;
@@ -381,7 +381,7 @@ struct Row {
       };
       if (MASS && level == 0 && least.v == -INFINITY) {  // (every id)
         each<1>(i0, i1, [&](float v, int i) {
-          if ((m - v) * w.ch < 46.f) add(v, i);
+          if (weight::product(m - v, w.ch) < 46.f) add(v, i);
         });
       } else if (level == 0 || s.own > kGather) {
         each<1>(i0, i1, [&](float v, int i) {

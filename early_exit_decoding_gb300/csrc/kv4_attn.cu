@@ -14,12 +14,15 @@
 // own: a 16-byte load of k gives it 32 of a key's dims, 8 bytes of v 16 dims
 // of a key.
 //
-// Numbers: q is scaled by a power of two a row (its largest to 2^13), exact in
-// fp16 but for what is 2^-37 below the largest.  The weights times s go to fp16
+// Numbers: q is scaled by a power of two a row (its largest to 2^13, for odd dims,
+// whose codes stand for 16 times theirs, to 2^9), exact in fp16 but for what is
+// 2^-37 (odd dims: 2^-33) below the largest.  The weights times s go to fp16
 // relative to the largest of them so far, 2^M, apart from the softmax's own
-// maximum m: steps may be of any size.  That rounding (2^-12 of a weight) meets
-// c - 8, as the sum of the rounded weights comes from the same products (a row
-// of eights beside the codes).  Scores, sums and statistics are fp32.  Maxima
+// maximum m: steps may be of any size and sign, 0 among them (M is at least
+// m - 100, so that it has a value while all steps so far are 0).  That rounding
+// (2^-12 of a weight) meets c - 8, as the sum of the rounded weights comes from
+// the same products (a row of eights beside the codes); weights times steps
+// below 2^-25 of the largest have no part in it.  Scores, sums and statistics are fp32.  Maxima
 // follow lazily: everything is rescaled only when one grew by more than 2^8.
 //
 // Work is counted in units of 32 keys of a row tile and KV head, over the whole
@@ -31,13 +34,15 @@
 // warps take the units in turn, each with a ring of its own filled by
 // asynchronous copies.
 //
-// What bounds it: instructions.  A unit of 32 keys of head_dim 128 is 4352 bytes
-// (186 clocks of an SM's share of HBM) and takes 34 products and some 520
-// instructions a warp, 220 of them masks, shifts and permutes that make
-// operands of codes, on a pipe that takes two clocks each.  64 sequences of 130
-// to 8191 positions, 8 KV heads: 69 us for 291 MB, 4.2 TB/s (0.63 of a measured
-// copy); two of 99,999 and 131,072: 58 us, 4.4 TB/s.  One sequence of 1001: 11 us
-// and 5 for the join, a chain of latencies.
+// What bounds it: the chain inside a warp, with three warps a scheduler.  A unit
+// of 32 keys of head_dim 128 is 4352 bytes (186 clocks of an SM's share of HBM)
+// and takes 34 products and some 520 instructions a warp one after another:
+// loads from shared memory, masks (220 with shifts and permutes, on a pipe that
+// takes two clocks each), products, exponentials, products.  No unit is at its
+// peak: issue slots 52 %, that pipe 51 %, tensor pipe 27 %, DRAM 0.71 of a
+// measured copy within the kernel.  64 sequences of 130 to 8191 positions, 8 KV
+// heads: 69 us for 291 MB, 4.2 TB/s (0.63 of a copy); two of 99,999 and 131,072:
+// 58 us, 4.4 TB/s.  One sequence of 1001: 9.5 us and 6 for the join, latencies.
 #include <float.h>
 #include <math.h>
 

@@ -8,11 +8,13 @@
 // largest values half a step of s at most (2^-9 of the range in bf16).
 //
 // What bounds it: instructions, then HBM.  8169 rows of 32 + 2 x 8 heads of 128:
-// append 48 us for 170 MB (0.5 of a measured copy; 25 M warp instructions, a
-// third of them the rotation's conversions, a third the codes), reading back 16.
-// (Packed fp32 products and sums would halve the rotation's, but they came out
-// fused, one rounding short, and codes must not depend on that.)  A decode
-// step's rows: 8 us and 6, launches and chains of loads.
+// append 42 us for 170 MB (0.6 of a measured copy; 26 M warp instructions, a
+// third of them the rotation's conversions, a third the codes), reading back 16
+// (16-byte stores 32 bytes apart: half of every sector an instruction).
+// (Packed fp32 products and sums would halve the rotation's, but written as they
+// are they came out fused, one rounding short, and codes must not depend on that;
+// sums as fma by a 1 that the compiler cannot see have not been tried.)  A decode
+// step's rows: 7 us and 6, launches and chains of loads.
 #include <float.h>
 #include <math.h>
 #include <stdio.h>

@@ -26,13 +26,14 @@
 // of the threads' largest logits give a bound that at least k ids reach and few
 // others, and one CTA finishes with those alone.
 //
-// What bounds it: instructions, some 75 a logit where weights are summed (the
-// exponential's 45, the histogram's 20), and the chain of a digit: histogram,
-// barrier, the groups' and the bins' sums from the other parts.  64 rows of
-// 128,256 fp32 logits cut at 0.9 of their mass: 72 us (the row's first reading
-// 7, the histogram 16, the next digit 11, the id 5, the rest between them); 500
-// rows of 50,257 bf16 logits, each with settings of its own: 104 us; one row
-// with top-k 50 and top-p 0.95: 14 us.
+// What bounds it: the chain of a digit (histogram, barrier, the groups' and the
+// bins' sums from the other parts: three block and one cluster barrier), and
+// instructions, some 77 a logit where weights are summed (the exponential's 47,
+// the histogram's 20).  64 rows of 128,256 fp32 logits cut at 0.9 of their mass:
+// 74 us, 45 M warp instructions (the row's first reading 7 us, the histogram 16,
+// the next digit 11, the id 5, the rest between them); 500 rows of 50,257 bf16
+// logits, each with settings of its own: 104 us, 65 M; one row with top-k 50 and
+// top-p 0.95: 14 us.
 #include <float.h>
 #include <math.h>
 #include <stdio.h>
@@ -790,14 +791,16 @@ __global__ void __launch_bounds__(kThreads, 2)
 // Settings that differ from row to row.
 bool of_each(const rl_sampling& s) { return s.d_temperature || s.d_top_k || s.d_top_p || s.d_min_p; }
 
-// CTAs a row is split over: as many as its parts' sums need, and more while all
-// rows' are at work at once and have 4096 ids at least: with one an SM (64 rows of
+// CTAs a row is split over: as many as its parts' sums need, and twice as many
+// while, before that, they are no more than the SMs and a part keeps 4096 ids (so up
+// to two CTAs an SM, which all are at work at once: 64 rows of
 // 128,256 cut by mass: 72 us in 4 parts, 88 in 2, 91 in 8; 500 of 50,257: 211 whole,
-// 207 in halves; one row: 14.4 us in 16), or two where rows' settings differ and
-// the costliest take the time (48 rows of 50,257: 39 us in 8, 44 in 4; 200: 58 in
-// halves, 112 whole; 64 of 128,256: 48 in 8, 55 in 4), and halves of long rows up
-// to four (320 of 50,257: 72 us, 98 whole; 500: 104 and 110; 608: 124 and 121; of
-// 20,011 ids 400 are slower so, 63 and 55).
+// 207 in halves; one row: 14.4 us in 16); while they are no more than twice the
+// SMs where rows' settings differ and the costliest take the time (48 rows of
+// 50,257: 39 us in 8, 44 in 4; 200: 58 in halves, 112 whole; 64 of 128,256: 48 in
+// 8, 55 in 4); and halves of long rows while there are no more than four rows an
+// SM, which start in turn (320 of 50,257: 72 us, 98 whole; 500: 104 and 110; even
+// at the end, 608: 124 and 121; of 20,011 ids 400 are slower so, 63 and 55).
 int pick_split(int rows, int V, bool each, int sms) {
   int s = 1;
   auto more = [&] {

@@ -657,10 +657,13 @@ RL_API rl_status rl_kv4_read(const rl_kv4* c, const rl_packed_desc* p, const int
  * length outside [0, table_width * page] sets RL_DEVERR_CAPACITY and is
  * clamped; rows past max_rows of a sequence set it and are left as they were.
  * Positions from d_kv_len[b] on have no part in any result, whatever their
- * pages hold.  Scores, sums and statistics are fp32; q is scaled by a power
- * of two a row and rounded to fp16 (exact but for what is 2^-37 below the row's
- * largest), weights times v's steps are rounded to fp16.  Two launches, results
- * repeat bit for bit.  d_start NULL: one row each (rows == batch).
+ * pages hold.  Scores, sums and statistics are fp32 (sums of weights times values
+ * that pass its range, and queries whose largest value times scale passes 2^115,
+ * come out infinite or NaN); q is scaled by a power of two a row and rounded to
+ * fp16 (exact but for what is 2^-37, in odd dims 2^-33, below the row's largest);
+ * weights times v's steps are rounded to fp16, those below 2^-25 of the largest
+ * to 0 (their values then count as those of code 8).
+ * Two launches, results repeat bit for bit.  d_start NULL: one row each (rows == batch).
  *   d_ws  workspace of rl_kv4_attention_workspace bytes (16-byte aligned), in use
  *         until the call's work on the stream is done: calls that may overlap
  *         need one each

@@ -32,7 +32,7 @@
 // the histogram's 20).  64 rows of 128,256 fp32 logits cut at 0.9 of their mass:
 // 74 us, 45 M warp instructions (the row's first reading 7 us, the histogram 16,
 // the next digit 11, the id 5, the rest between them); 500 rows of 50,257 bf16
-// logits, each with settings of its own: 104 us, 65 M; one row with top-k 50 and
+// logits, each with settings of its own: 104 us, 64 M; one row with top-k 50 and
 // top-p 0.95: 14 us.
 #include <float.h>
 #include <math.h>
